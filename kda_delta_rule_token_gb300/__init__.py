@@ -19,12 +19,15 @@ __all__ = [
     "kda_launch_count", "kda_bind_lowrank", "kda_lowrank", "kda_lowrank_workspace_bytes",
     "kda_decode_step_lowrank", "kda_decode_lowrank_workspace_bytes", "kda_lowrank_noalloc",
     "LOWRANK_NOALLOC_SCRATCH_BYTES", "kda_bind_projections", "kda_project_qkvg", "kda_project_o",
-    "kda_project_o_workspace_bytes", "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_ALIGNMENT",
+    "kda_project_o_workspace_bytes", "kda_attn_create", "kda_attn_destroy", "kda_attn_bind_cache",
+    "kda_attn_plan", "kda_attn_append", "kda_attn_workspace_bytes", "kda_attn_decode", "kda_attn_prefill",
+    "kda_attn_sync_status", "KDA_CACHE_BF16", "KDA_CACHE_E4M3", "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_ALIGNMENT",
     "KDA_ERR_UNSUPPORTED", "KDA_ERR_CUDA", "KDA_ERR_TIMEOUT", "HEAD_DIM", "CHUNK",
 ]
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_ALIGNMENT, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, \
     KDA_ERR_TIMEOUT = range(6)
+KDA_CACHE_BF16, KDA_CACHE_E4M3 = range(2)
 HEAD_DIM = 128
 CHUNK = 64
 LOWRANK_NOALLOC_SCRATCH_BYTES = 4 << 20   # KDA_LOWRANK_NOALLOC_SCRATCH_BYTES of include/kda.h
@@ -47,6 +50,13 @@ class _Config(ctypes.Structure):
     _fields_ = [("num_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
                 ("chunk_size", ctypes.c_int), ("l2_eps", ctypes.c_float),
                 ("rms_eps", ctypes.c_float)]
+
+
+class _AttnConfig(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int), ("cache_type", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("rope_interleaved", ctypes.c_int),
+                ("rms_eps", ctypes.c_float), ("softmax_scale", ctypes.c_float)]
 
 
 def library_path() -> str:
@@ -107,6 +117,26 @@ def load(path: str | None = None):
     lib.kda_project_o_workspace_bytes.restype = sz
     lib.kda_project_o.argtypes = [vp, i32, vp, vp, vp, sz, vp]
     lib.kda_project_o.restype = i32
+    i64 = ctypes.c_longlong
+    lib.kda_attn_create.argtypes = [ctypes.POINTER(_AttnConfig), ctypes.POINTER(ctypes.c_double),
+                                    vp, vp, vp, vp, ctypes.POINTER(vp)]
+    lib.kda_attn_create.restype = i32
+    lib.kda_attn_destroy.argtypes = [vp]
+    lib.kda_attn_destroy.restype = None
+    lib.kda_attn_bind_cache.argtypes = [vp, i32, vp, vp]
+    lib.kda_attn_bind_cache.restype = i32
+    lib.kda_attn_plan.argtypes = [vp, i32, i32, vp, vp, vp, i32, vp, vp, i32] + [vp] * 6
+    lib.kda_attn_plan.restype = i32
+    lib.kda_attn_append.argtypes = [vp, i32, vp, i64, vp, i64, vp, i64] + [vp] * 4
+    lib.kda_attn_append.restype = i32
+    lib.kda_attn_workspace_bytes.argtypes = [vp]
+    lib.kda_attn_workspace_bytes.restype = sz
+    lib.kda_attn_decode.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.kda_attn_decode.restype = i32
+    lib.kda_attn_prefill.argtypes = [vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.kda_attn_prefill.restype = i32
+    lib.kda_attn_sync_status.argtypes = [vp, vp]
+    lib.kda_attn_sync_status.restype = i32
     lib.kda_testing_bounded_wait.argtypes = [vp, ctypes.c_uint, vp]
     lib.kda_testing_bounded_wait.restype = i32
     _lib = lib
@@ -260,6 +290,95 @@ def kda_project_o(ctx, N, o, y, workspace, workspace_bytes=0, stream=None) -> No
 def kda_sync_status(ctx, stream=None) -> int:
     """Synchronise and return the status code (does not raise)."""
     return int(load().kda_sync_status(ctx, _stream(stream)))
+
+
+def kda_attn_create(num_q_heads, num_kv_heads, *, page_size, cache_type=KDA_CACHE_BF16,
+                    rotary_dim=HEAD_DIM, rope_interleaved=False, inv_freq=None, q_gamma=None,
+                    k_gamma=None, k_scale=None, v_scale=None, rms_eps=1e-6,
+                    softmax_scale=HEAD_DIM ** -0.5, head_dim=HEAD_DIM) -> int:
+    """Returns an opaque handle (int) of one softmax-attention layer (kda_attn.h).
+    inv_freq: a sequence of rotary_dim / 2 radians per position (host numbers,
+    copied).  The device tensors are borrowed."""
+    freqs = None
+    if inv_freq is not None:
+        freqs = [float(f) for f in inv_freq]
+        if len(freqs) != int(rotary_dim) // 2:
+            raise ValueError(f"inv_freq has {len(freqs)} values, rotary_dim {rotary_dim} needs {int(rotary_dim) // 2}")
+        freqs = (ctypes.c_double * max(1, len(freqs)))(*freqs)
+    cfg = _AttnConfig(int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size), int(cache_type),
+                      int(rotary_dim), 1 if rope_interleaved else 0, float(rms_eps), float(softmax_scale))
+    out = ctypes.c_void_p()
+    _check(load().kda_attn_create(ctypes.byref(cfg), freqs, _p(q_gamma), _p(k_gamma), _p(k_scale),
+                                  _p(v_scale), ctypes.byref(out)), "kda_attn_create")
+    return out.value
+
+
+def kda_attn_destroy(attn: int) -> None:
+    load().kda_attn_destroy(attn)
+
+
+def kda_attn_bind_cache(attn, num_pages, k_cache, v_cache) -> None:
+    """Caches [num_pages, kv heads, page_size, 128]: bf16 or e4m3 tensors (or their raw views)."""
+    _check(load().kda_attn_bind_cache(attn, int(num_pages), _p(k_cache), _p(v_cache)), "kda_attn_bind_cache")
+
+
+def _pitch(table, given):
+    """Row length of a block table: given, or the tensor's."""
+    return int(given) if given is not None else table.stride(0)
+
+
+def kda_attn_plan(attn, B, N, cache_lens, new_lens, free_pages, free_count, block_table, cu_new, kv_lens,
+                  positions, slots, info, *, free_capacity=None, max_pages=None, stream=None) -> None:
+    cap = free_pages.numel() if free_capacity is None else int(free_capacity)
+    _check(load().kda_attn_plan(attn, B, N, _p(cache_lens), _p(new_lens), _p(free_pages), cap,
+                                _p(free_count), _p(block_table), _pitch(block_table, max_pages), _p(cu_new),
+                                _p(kv_lens), _p(positions), _p(slots), _p(info), _stream(stream)),
+           "kda_attn_plan")
+
+
+def _token_stride(t, given):
+    """Elements from one token's heads to the next's: given, or the [N, heads, 128] tensor's."""
+    if given is not None:
+        return int(given)
+    st = t.stride()
+    if st[-1] != 1 or st[-2] != HEAD_DIM:
+        raise ValueError(f"heads must be dense rows of {HEAD_DIM} elements: strides {tuple(st)}")
+    return st[0]
+
+
+def kda_attn_append(attn, N, q, k, v, positions, slots, q_out, *, q_stride=None, k_stride=None,
+                    v_stride=None, stream=None) -> None:
+    _check(load().kda_attn_append(attn, N, _p(q), _token_stride(q, q_stride), _p(k), _token_stride(k, k_stride),
+                                  _p(v), _token_stride(v, v_stride), _p(positions), _p(slots), _p(q_out),
+                                  _stream(stream)), "kda_attn_append")
+
+
+def kda_attn_workspace_bytes(attn) -> int:
+    return int(load().kda_attn_workspace_bytes(attn))
+
+
+def _is_f32(o, given):
+    return int(bool(given)) if given is not None else int(o.element_size() == 4)
+
+
+def kda_attn_decode(attn, B, q, block_table, kv_lens, o, workspace, *, max_pages=None, gate_logit=None,
+                    o_f32=None, lse=None, workspace_bytes=0, stream=None) -> None:
+    _check(load().kda_attn_decode(attn, B, _p(q), _p(block_table), _pitch(block_table, max_pages), _p(kv_lens),
+                                  _p(gate_logit), _p(o), _is_f32(o, o_f32), _p(lse), _p(workspace),
+                                  _nbytes(workspace, workspace_bytes), _stream(stream)), "kda_attn_decode")
+
+
+def kda_attn_prefill(attn, B, N, cu_new, q, block_table, kv_lens, o, workspace, *, max_pages=None,
+                     gate_logit=None, o_f32=None, lse=None, workspace_bytes=0, stream=None) -> None:
+    _check(load().kda_attn_prefill(attn, B, N, _p(cu_new), _p(q), _p(block_table),
+                                   _pitch(block_table, max_pages), _p(kv_lens), _p(gate_logit), _p(o),
+                                   _is_f32(o, o_f32), _p(lse), _p(workspace),
+                                   _nbytes(workspace, workspace_bytes), _stream(stream)), "kda_attn_prefill")
+
+
+def kda_attn_sync_status(attn, stream=None) -> int:
+    """Synchronise and return the status code (does not raise)."""
+    return int(load().kda_attn_sync_status(attn, _stream(stream)))
 
 
 def kda_testing_bounded_wait(ctx, limit_us, stream=None) -> None:

@@ -1,0 +1,90 @@
+// Internal declarations of the paged softmax-attention operators
+// (include/kda_attn.h): what the host side hands to their kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_attn.h"
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// Error-word bits of the attention context beside the bounded-wait ones of
+// ptx.cuh: a page id or slot outside the cache was met (and not accessed).
+constexpr int kErrAttnIndex = 1 << 16;
+
+// One layer as its kernels see it.
+struct AttnLayer {
+    int Hq, Hkv, G;          // G = Hq / Hkv
+    int page_size, page_shift;
+    int e4m3;
+    int rotary, interleaved;
+    float rms_eps, softmax_scale;
+    const float* q_gamma;    // may be null
+    const float* k_gamma;    // may be null
+    const float* k_scale;    // e4m3 only
+    const float* v_scale;    // e4m3 only
+    int num_pages;           // 0: no cache bound
+    void* k_cache;
+    void* v_cache;
+};
+
+// Rotation steps: pair i advances by turn[i] / 2^64 of a full turn per
+// position, so position * turn[i] modulo 2^64 is the exact fraction of a turn.
+struct RopeTurns {
+    uint64_t turn[kHeadDim / 2];
+};
+
+struct AttnPlanIO {
+    int B, N;
+    const int* cache_lens;
+    const int* new_lens;
+    const int* free_pages;
+    int free_capacity;
+    const int* free_count;
+    int* block_table;
+    int max_pages;
+    int* cu_new;
+    int* kv_lens;
+    int* positions;
+    long long* slots;
+    int* info;
+};
+
+struct AttnAppendIO {
+    int N;
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    long long q_stride, k_stride, v_stride;
+    const int* positions;
+    const long long* slots;
+    uint16_t* q_out;
+};
+
+struct AttnIO {
+    int B, N;                // decode: N = B
+    const int* cu_new;       // prefill; null for decode (one token each)
+    const uint16_t* q;
+    const int* block_table;
+    int max_pages;
+    const int* kv_lens;
+    const float* gate;       // may be null
+    void* o;
+    int o_f32;
+    float* lse;              // may be null
+    void* workspace;
+};
+
+cudaError_t launch_attn_plan(const AttnLayer& l, const AttnPlanIO& io, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_attn_append(const AttnLayer& l, const RopeTurns& turns, const AttnAppendIO& io,
+                               const DeviceInfo& dev, int* err_word, cudaStream_t stream);
+size_t attn_workspace_bytes(const AttnLayer& l, const DeviceInfo& dev);
+cudaError_t launch_attn_decode(const AttnLayer& l, const AttnIO& io, const DeviceInfo& dev, int* err_word,
+                               cudaStream_t stream);
+cudaError_t launch_attn_prefill(const AttnLayer& l, const AttnIO& io, const DeviceInfo& dev, int* err_word,
+                                cudaStream_t stream);
+
+}  // namespace kda

@@ -17,6 +17,7 @@
 // or empty: no injection.
 #include <atomic>
 #include <cmath>
+#include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -114,6 +115,32 @@ void set_launch_detail(const kda_ctx* ctx, unsigned what, const char* name, cuda
 
 void count_launches(uint64_t n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
+void set_error_text(const char* format, ...) {
+    va_list args;
+    va_start(args, format);
+    std::vsnprintf(g_detail, sizeof(g_detail), format, args);
+    va_end(args);
+}
+
+kda_status query_device(DeviceInfo& dev) {
+    cudaError_t e = cudaGetDevice(&dev.device);
+    if (e != cudaSuccess) { set_detail("cudaGetDevice", e); return KDA_ERR_CUDA; }
+    int major = 0, minor = 0;
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev.device)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev.device)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&dev.sm_count, cudaDevAttrMultiProcessorCount, dev.device)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&dev.max_smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin,
+                                    dev.device)) != cudaSuccess) {
+        set_detail("cudaDeviceGetAttribute", e);
+        return KDA_ERR_CUDA;
+    }
+    if (major != 10 || minor != 3) {
+        set_error_text("device %d is sm_%d%d; this library is built for sm_103a only", dev.device, major, minor);
+        return KDA_ERR_UNSUPPORTED;
+    }
+    return KDA_OK;
+}
+
 }  // namespace kda
 
 using kda::aligned16;
@@ -151,23 +178,7 @@ kda_status kda_create(const kda_config* cfg, const float* conv_w, const float* d
         return KDA_ERR_ALIGNMENT;
 
     kda::DeviceInfo dev{};
-    cudaError_t e = cudaGetDevice(&dev.device);
-    if (e != cudaSuccess) { kda::set_detail("cudaGetDevice", e); return KDA_ERR_CUDA; }
-    int major = 0, minor = 0;
-    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev.device)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev.device)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&dev.sm_count, cudaDevAttrMultiProcessorCount, dev.device)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&dev.max_smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin,
-                                    dev.device)) != cudaSuccess) {
-        kda::set_detail("cudaDeviceGetAttribute", e);
-        return KDA_ERR_CUDA;
-    }
-    if (major != 10 || minor != 3) {
-        std::snprintf(kda::g_detail, sizeof(kda::g_detail),
-                      "device %d is sm_%d%d; this library is built for sm_103a only", dev.device,
-                      major, minor);
-        return KDA_ERR_UNSUPPORTED;
-    }
+    if (const kda_status d = kda::query_device(dev); d != KDA_OK) return d;
     kda_ctx* c = new (std::nothrow) kda_ctx{};
     if (!c) {
         std::snprintf(kda::g_detail, sizeof(kda::g_detail), "host allocation of the context failed");
@@ -178,7 +189,8 @@ kda_status kda_create(const kda_config* cfg, const float* conv_w, const float* d
     c->chunk = cfg->chunk_size;
     c->dev = dev;
     c->inject = kda::parse_inject(std::getenv("KDA_FAULT_INJECT"));
-    if ((e = cudaMalloc(&c->err_word, 16)) != cudaSuccess) {
+    cudaError_t e = cudaMalloc(&c->err_word, 16);
+    if (e != cudaSuccess) {
         kda::set_detail("cudaMalloc(error word)", e);
         delete c;
         return KDA_ERR_CUDA;

@@ -154,4 +154,10 @@ int project_o_ksplit(int hidden, int N, int HD, int sm_count);
 // Counts kernel launches made by the library (for benchmark accounting).
 void count_launches(uint64_t n);
 
+// Host-side helpers of the C ABI's translation units: the text that
+// kda_last_error_detail returns (per thread, printf form), and the facts of
+// the current device (KDA_ERR_UNSUPPORTED unless it is sm_103).
+void set_error_text(const char* format, ...) __attribute__((format(printf, 1, 2)));
+kda_status query_device(DeviceInfo& dev);
+
 }  // namespace kda
