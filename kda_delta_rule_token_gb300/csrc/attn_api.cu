@@ -16,6 +16,7 @@
 
 struct kda_attn_ctx {
     kda::AttnLayer layer;
+    kda::AttnMaps maps;
     kda::RopeTurns turns;
     kda::DeviceInfo dev;
     int* err_word;
@@ -81,6 +82,8 @@ kda_status need_cache(const kda_attn_ctx* ctx) {
     return KDA_ERR_INVALID_ARG;
 }
 
+size_t workspace_bytes_of(const kda_attn_ctx* ctx) { return attn_decode_workspace_bytes(ctx->dev); }
+
 // What kda_attn_decode and kda_attn_prefill check alike.
 kda_status check_attend(const kda_attn_ctx* ctx, const AttnIO& io, size_t workspace_bytes) {
     if (!io.q || !io.block_table || io.max_pages < 1 || !io.kv_lens || !io.o || !io.workspace)
@@ -88,13 +91,13 @@ kda_status check_attend(const kda_attn_ctx* ctx, const AttnIO& io, size_t worksp
     if (!aligned(io.q, 16) || !aligned(io.o, 16) || !aligned(io.gate, 16) || !aligned(io.workspace, 16) ||
         !aligned(io.block_table, 4) || !aligned(io.kv_lens, 4) || !aligned(io.lse, 4) || !aligned(io.cu_new, 4))
         return KDA_ERR_ALIGNMENT;
-    if ((long long)io.max_pages * ctx->layer.page_size > 0x7fffffffLL) {
-        set_error_text("max_pages (%d) pages of %d tokens exceed 2^31 - 1 keys", io.max_pages, ctx->layer.page_size);
+    if ((long long)io.max_pages * ctx->layer.page_size > 0x7fff0000LL) {   // tile ends stay within an int
+        set_error_text("max_pages (%d) pages of %d tokens exceed 2^31 - 2^16 keys", io.max_pages, ctx->layer.page_size);
         return KDA_ERR_INVALID_ARG;
     }
-    if (workspace_bytes < attn_workspace_bytes(ctx->layer, ctx->dev)) {
+    if (workspace_bytes < workspace_bytes_of(ctx)) {
         set_error_text("workspace of %zu bytes, %zu needed", workspace_bytes,
-                       attn_workspace_bytes(ctx->layer, ctx->dev));
+                       workspace_bytes_of(ctx));
         return KDA_ERR_INVALID_ARG;
     }
     return need_cache(ctx);
@@ -204,9 +207,17 @@ kda_status kda_attn_bind_cache(kda_attn_ctx* ctx, int num_pages, void* k_cache, 
         return KDA_ERR_INVALID_ARG;
     }
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return KDA_ERR_ALIGNMENT;
-    ctx->layer.num_pages = num_pages;
-    ctx->layer.k_cache = k_cache;
-    ctx->layer.v_cache = v_cache;
+    kda::AttnLayer l = ctx->layer;
+    l.num_pages = num_pages;
+    l.k_cache = k_cache;
+    l.v_cache = v_cache;
+    kda::AttnMaps maps;
+    if (!kda::attn_prepare_cache(l, maps)) {
+        kda::set_error_text("cuTensorMapEncodeTiled failed for the cache");
+        return KDA_ERR_CUDA;
+    }
+    ctx->layer = l;
+    ctx->maps = maps;
     return KDA_OK;
 }
 
@@ -264,7 +275,7 @@ kda_status kda_attn_append(kda_attn_ctx* ctx, int N, const uint16_t* q, long lon
 }
 
 size_t kda_attn_workspace_bytes(const kda_attn_ctx* ctx) {
-    return ctx ? kda::attn_workspace_bytes(ctx->layer, ctx->dev) : 0;
+    return ctx ? kda::workspace_bytes_of(ctx) : 0;
 }
 
 kda_status kda_attn_decode(kda_attn_ctx* ctx, int B, const uint16_t* q, const int32_t* block_table, int max_pages,
@@ -275,7 +286,8 @@ kda_status kda_attn_decode(kda_attn_ctx* ctx, int B, const uint16_t* q, const in
     const kda::AttnIO io{B, B, nullptr, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace};
     if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectDecode, "attn_decode launch", [&] {
-        return kda::launch_attn_decode(ctx->layer, io, ctx->dev, ctx->err_word, static_cast<cudaStream_t>(stream));
+        return kda::launch_attn_decode(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word,
+                                       static_cast<cudaStream_t>(stream));
     });
 }
 

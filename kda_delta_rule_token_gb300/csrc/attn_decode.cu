@@ -1,0 +1,727 @@
+// Attention of one new token per request over a paged cache.
+//
+//   o = softmax(scale * q K^T) V,   per request and query head
+//
+// Every cached byte of a request is read once for each key head and takes part
+// in 2 G operations (G query heads share a key head), so the call is bound by
+// HBM.  The kernel is built around keeping enough bytes in flight on every SM:
+//
+//  * Work is cut into units of 8 warp tiles (128 keys in bf16, 256 in e4m3) of
+//    one request and key head, numbered request-major.  Each CTA (one per SM)
+//    takes an equal, contiguous range of units, whatever the lengths are: it
+//    finds its first request by a prefix sum over the lengths.  A request
+//    whose units lie in several CTAs leaves one partial result (weighted sum,
+//    maximum, sum) per CTA, joined in a fixed order by a second, dependent
+//    launch, so the result does not depend on scheduling.
+//  * Inside a CTA each warp streams its own tiles: lane 0 copies the tile's
+//    pages of K and V (4 KiB each) with TMA into the warp's private ring of
+//    kStages stages, running ahead across the ends of requests, and the warp
+//    consumes them by itself.  No warp waits for another before the end of a
+//    request's part, where the eight partial results meet in shared memory.
+//  * The G query heads are the rows of a 16-row mma.sync tile (two tiles from
+//    17 heads on, several passes beyond 32).  The softmax keeps a reference
+//    (not the exact maximum) per row and rescales only when a logit passes it
+//    by more than kLimit powers of two: the result is the same, the rescaling
+//    almost never runs.
+//  * bf16: the weights enter the second product as the sum of two bf16 parts
+//    (error 2^-17; one part alone would add 2^-9 per weight, as much as the
+//    rounding of the output, and the pipe is idle anyway).  e4m3: keys, values
+//    and weights are f16 (keys and values exactly, weights to 2^-12, kept
+//    within 2^15 of the row's reference), q is scaled by a power of two per row.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "attn_internal.cuh"
+#include "attn_mma.cuh"
+#include "attn_tma.cuh"
+#include "ptx.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;
+constexpr uint32_t kTileBytes = 4096;            // keys (or values) of one warp tile
+constexpr uint32_t kStageBytes = 2 * kTileBytes;
+constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kMergeCols = 64;                   // channels merged at a time
+constexpr uint32_t kMergeBytes = kWarps * 16 * kMergeCols * 4;
+constexpr int kMaxRows = 32;                     // query heads of one pass
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoRef = -3e38f;                // reference before the first finite logit
+
+struct Smem {
+    uint8_t ring[kRingBytes];
+    float merge[kMergeBytes / 4];
+    float ref[kWarps][kMaxRows];
+    float sum[kWarps][kMaxRows];
+    uint64_t full[kWarps][kStages];
+    long long scan[kWarps];
+    long long total, first_unit;
+    int first_b;
+    int dead;
+};
+
+struct DecodeArgs {
+    AttnIO io;
+    int Hq, Hkv, G;
+    int passes, rows;        // head groups of a key head, and query heads of a group
+    int page_shift, num_pages;
+    float scale;             // softmax scale * log2(e)
+    const float* k_scale;
+    const float* v_scale;
+};
+
+// What a CTA leaves for the join: the request and (virtual) head whose first
+// part it holds and that goes on in the next CTAs, up to CTA last.  b < 0: none.
+struct JoinDesc {
+    int b, vh, last, slot;
+};
+
+// Workspace: a descriptor per CTA, then two slots per CTA of partial results,
+// rows x (128 weighted sums, then reference and sum).
+constexpr int kSlotFloats = kMaxRows * (kHeadDim + 2);
+
+__host__ __device__ constexpr size_t desc_bytes(int ctas) { return ((size_t)ctas * sizeof(JoinDesc) + 255) & ~size_t(255); }
+
+__device__ __forceinline__ JoinDesc* descs(void* ws) { return static_cast<JoinDesc*>(ws); }
+__device__ __forceinline__ float* slot_at(void* ws, int ctas, int slot) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + desc_bytes(ctas)) + (size_t)slot * kSlotFloats;
+}
+
+// Four consecutive channels of one head's output row.
+__device__ __forceinline__ void store4(const AttnIO& io, size_t at, float4 v) {
+    if (io.gate) {
+        const float4 g = *reinterpret_cast<const float4*>(io.gate + at);
+        v.x /= 1.f + mma::exp2_approx(-g.x * kLog2e);
+        v.y /= 1.f + mma::exp2_approx(-g.y * kLog2e);
+        v.z /= 1.f + mma::exp2_approx(-g.z * kLog2e);
+        v.w /= 1.f + mma::exp2_approx(-g.w * kLog2e);
+    }
+    if (io.o_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(io.o) + at) = v;
+    else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(io.o) + at) =
+            make_uint2(mma::pack_bf16(v.x, v.y), mma::pack_bf16(v.z, v.w));
+}
+
+__device__ __forceinline__ int clamped_len(const DecodeArgs& a, int b) {
+    return min(max(a.io.kv_lens[b], 0), a.io.max_pages << a.page_shift);
+}
+
+// A position in the CTA's range of units.
+struct Walk {
+    long long left;   // units of the range not yet passed, this one included
+    int b, vh, u;     // request, virtual head, unit of it
+    int len, units;   // of request b
+};
+
+template <int kTile>
+__device__ __forceinline__ int units_of(int len) { return (int)(((long long)len + kWarps * kTile - 1) / (kWarps * kTile)); }
+
+// To the next unit (of the next request with any, at the end of one).
+template <int kTile>
+__device__ __forceinline__ void step(const DecodeArgs& a, Walk& w) {
+    --w.left;
+    if (++w.u < w.units) return;
+    w.u = 0;
+    if (++w.vh < a.Hkv * a.passes) return;
+    w.vh = 0;
+    if (w.left <= 0) return;
+    do {
+        w.len = clamped_len(a, ++w.b);
+        w.units = units_of<kTile>(w.len);
+    } while (w.units == 0);
+}
+
+template <bool kE4m3, int kMT>
+__global__ void __launch_bounds__(kThreads, 1)
+kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, int* err) {
+    constexpr int kTile = kE4m3 ? 32 : 16;       // keys of a warp tile
+    constexpr int kNT = kTile / 8;               // 8-key column tiles of the logits
+    constexpr float kOffset = kE4m3 ? 10.f : 0.f;
+    constexpr float kLimit = kE4m3 ? 15.f : 8.f;
+    extern __shared__ __align__(1024) uint8_t sm_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(sm_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+
+    ptx::griddep_launch_dependents();
+    if (lane == 0)
+        for (int s = 0; s < kStages; ++s) ptx::mbar_init(&sm.full[warp][s], 1);
+    if (tid == 0) {
+        sm.dead = 0;
+        descs(a.io.workspace)[blockIdx.x].b = -1;
+    }
+    ptx::fence_mbar_init();
+
+    // The CTA's range of units.
+    const int heads = a.Hkv * a.passes;
+    const int per = (a.io.B + kThreads - 1) / kThreads;
+    const int b0 = min(a.io.B, tid * per), b1 = min(a.io.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units_of<kTile>(clamped_len(a, b));
+    mine *= heads;
+    long long upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+    }
+    if (lane == 31) sm.scan[warp] = upto;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) upto += sm.scan[w];
+        total += sm.scan[w];
+    }
+    const long long ctas = min((long long)gridDim.x, total);
+    const bool works = blockIdx.x < ctas;
+    const long long from = works ? total * blockIdx.x / ctas : 0, to = works ? total * (blockIdx.x + 1) / ctas : 0;
+    if (works && upto - mine <= from && from < upto) {
+        long long at = upto - mine;
+        for (int b = b0;; ++b) {
+            const long long n = (long long)units_of<kTile>(clamped_len(a, b)) * heads;
+            if (from < at + n) {
+                sm.first_b = b;
+                sm.first_unit = from - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    // Requests without keys: zero rows.
+    for (int b = blockIdx.x; b < a.io.B; b += gridDim.x)
+        if (clamped_len(a, b) == 0) {
+            for (int i = tid; i < a.Hq * (kHeadDim / 4); i += kThreads)
+                store4(a.io, (size_t)b * a.Hq * kHeadDim + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+            if (a.io.lse)
+                for (int i = tid; i < a.Hq; i += kThreads) a.io.lse[(size_t)b * a.Hq + i] = -INFINITY;
+        }
+    __syncthreads();
+    if (!works) return;
+
+    Walk cur;
+    cur.left = to - from;
+    cur.b = sm.first_b;
+    cur.len = clamped_len(a, cur.b);
+    cur.units = units_of<kTile>(cur.len);
+    cur.vh = (int)(sm.first_unit / cur.units);
+    cur.u = (int)(sm.first_unit % cur.units);
+
+    // Producer: lane 0 issues the warp's tiles; the page ids of the next tile
+    // are loaded one issue ahead of their use.
+    const int boxes = max(1, kTile >> a.page_shift), box_rows = kTile / boxes;
+    const int page_mask = (1 << a.page_shift) - 1;
+    Walk ahead = cur;
+    int ids[kTile / 16];
+    auto fetch_ids = [&]() {   // to the warp's next tile, if there is one
+        while (ahead.left > 0 && (ahead.u * kWarps + warp) * kTile >= ahead.len) step<kTile>(a, ahead);
+        if (ahead.left <= 0) return;
+        const int key = (ahead.u * kWarps + warp) * kTile;
+        const int* t = a.io.block_table + (size_t)ahead.b * a.io.max_pages + (key >> a.page_shift);
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+            if (i < boxes) ids[i] = key + i * box_rows < ahead.len ? t[i] : ids[0];
+    };
+    int issued = 0;
+    auto issue = [&]() {
+        if (ahead.left <= 0) return;
+        if (lane == 0) {
+            const int s = issued % kStages;
+            uint8_t* st = sm.ring + (warp * kStages + s) * kStageBytes;
+            const int row = (ahead.u * kWarps + warp) * kTile & page_mask;
+            const int h = ahead.vh / a.passes;
+            ptx::mbar_arrive_expect_tx(&sm.full[warp][s], kStageBytes);
+#pragma unroll
+            for (int i = 0; i < kTile / 16; ++i)
+                if (i < boxes) {
+                    const bool in = ids[i] >= 0 && ids[i] < a.num_pages;
+                    if (!in) atomicOr(err, kErrAttnIndex);
+                    // A page outside the cache: a box outside the tensor, which reads as zeros.
+                    const int ph = (in ? ids[i] : a.num_pages) * a.Hkv + (in ? h : 0);
+                    const uint32_t off = i * (kTileBytes / boxes);
+                    ptx::tma_load_4d(st + off, &kmap, 0, row, 0, ph, &sm.full[warp][s]);
+                    ptx::tma_load_4d(st + kTileBytes + off, &vmap, 0, row, 0, ph, &sm.full[warp][s]);
+                }
+        }
+        ++issued;
+        step<kTile>(a, ahead);
+        fetch_ids();
+    };
+    fetch_ids();
+    for (int s = 0; s < kStages; ++s) issue();
+
+    int used = 0;
+    bool ok = true;
+    while (cur.left > 0) {
+        // One request and head (or the part of it in this CTA's range).
+        const int h = cur.vh / a.passes, pass = cur.vh % a.passes;
+        const int row0 = pass * a.rows, nrows = min(a.rows, a.G - row0);
+        const size_t head0 = (size_t)cur.b * a.Hq + h * a.G + row0;   // output row of query row 0
+        const int u0 = cur.u, u1 = (int)min((long long)cur.units, u0 + cur.left);
+
+        // Query rows into A fragments.
+        uint32_t qf[kMT][8][4];
+        float fac[kMT][2];   // logit -> power of two
+        const float base = a.scale * (kE4m3 ? a.k_scale[h] : 1.f);
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = t * 16 + half * 8 + g;
+                const uint16_t* q = a.io.q + (head0 + r) * kHeadDim;
+                fac[t][half] = base;
+                if (!kE4m3) {
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) {
+                        qf[t][s][half] = r < nrows ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * c) : 0u;
+                        qf[t][s][half + 2] = r < nrows ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * c + 8) : 0u;
+                    }
+                } else {
+                    // Channels in the order in which the keys are read: step s takes
+                    // 16 c + 4 s + {0, 1 | 2, 3} of the lower half, then of the upper.
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < nrows) v = *reinterpret_cast<const uint4*>(q + (i >> 1) * 64 + 16 * c + (i & 1) * 8);
+                        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+                    }
+                    float top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // q * 2^(14 - e) with 2^e <= top < 2^(e+1): exact in f16 down to 2^-28 of the row's largest.
+                    const int e = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
+                    const float up = exp2f((float)(14 - e));
+                    fac[t][half] = base * exp2f((float)(e - 14));
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t v = w[2 * s + x];
+                            qf[t][s][half + 2 * x] =
+                                mma::pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+                        }
+                }
+            }
+
+        float acc[kMT][16][4], ref[kMT][2], sum[kMT][2];
+#pragma unroll
+        for (int t = 0; t < kMT; ++t) {
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][n][e] = 0.f;
+            ref[t][0] = ref[t][1] = kNoRef;
+            sum[t][0] = sum[t][1] = 0.f;
+        }
+
+        for (int u = u0; u < u1 && ok; ++u) {
+            const int key0 = (u * kWarps + warp) * kTile;
+            if (key0 >= cur.len) break;
+            const int s = used % kStages;
+            ok = ptx::mbar_wait_timed(&sm.full[warp][s], (uint32_t)(used / kStages) & 1u, &sm.dead);
+            if (!ok) {
+                sm.dead = 1;
+                atomicOr(err, ptx::kErrAttnWait);
+                break;
+            }
+            ++used;
+            const uint32_t ks = ptx::smem_u32(sm.ring + (warp * kStages + s) * kStageBytes), vs = ks + kTileBytes;
+            const int valid = cur.len - key0;   // keys of the tile, if below kTile
+            if (valid < kTile) {
+                // Values past the request's end may be anything, NaN too: their weight is 0, make them 0.
+                for (int i = lane; i < (int)kTileBytes / 16; i += 32) {
+                    const int row = kE4m3 ? i >> 3 : (i >> 3) & 15;
+                    if (row >= valid) *reinterpret_cast<uint4*>(sm.ring + (warp * kStages + s) * kStageBytes + kTileBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            }
+
+            // Logits: rows = query heads, columns = keys.
+            float sc[kMT][kNT][4];
+#pragma unroll
+            for (int t = 0; t < kMT; ++t)
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[t][n][e] = 0.f;
+            if (!kE4m3) {
+                const int key = (lane & 7) + ((lane >> 4) << 3), odd = (lane >> 3) & 1;
+#pragma unroll
+                for (int st = 0; st < 8; ++st) {
+                    const int ch = 2 * st + odd;   // 16-byte chunk of the key's row
+                    uint32_t b[4];
+                    mma::ldmatrix4(b, ks + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+#pragma unroll
+                    for (int t = 0; t < kMT; ++t) {
+                        mma::m16n8k16<false>(sc[t][0], qf[t][st], b[0], b[1]);
+                        mma::m16n8k16<false>(sc[t][1], qf[t][st], b[2], b[3]);
+                    }
+                }
+            } else {
+                // Column n of a tile is key 4 (n % 2) + n / 2 of its eight, so
+                // that the two rows that a quarter warp reads lie in different banks.
+                const int kr = ((g & 1) << 2) | (g >> 1);
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) {
+                    const uint32_t rowp = ks + (n * 8 + kr) * 128;
+                    const uint4 lo = mma::lds128(rowp + ((c ^ kr) << 4)), hi = mma::lds128(rowp + (((c + 4) ^ kr) << 4));
+                    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                    for (int st = 0; st < 8; ++st) {
+                        const uint32_t x0 = mma::e4m3x2_f16x2(w[st]), x1 = mma::e4m3x2_f16x2(w[st] >> 16);
+#pragma unroll
+                        for (int t = 0; t < kMT; ++t) mma::m16n8k16<true>(sc[t][n], qf[t][st], x0, x1);
+                    }
+                }
+            }
+            if (valid < kTile) {
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k = n * 8 + (kE4m3 ? c + 4 * e : 2 * c + e);
+                        if (k >= valid)
+#pragma unroll
+                            for (int t = 0; t < kMT; ++t) sc[t][n][e] = sc[t][n][e + 2] = -INFINITY;
+                    }
+            }
+
+            // Softmax weights against the row's reference.
+            uint32_t hi[kMT][kNT][2], lo[kMT][kNT][2];   // A fragments of the weights, rows g and g + 8
+#pragma unroll
+            for (int t = 0; t < kMT; ++t) {
+                float top[2];
+                bool raise = false;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n) m = fmaxf(m, fmaxf(sc[t][n][2 * half], sc[t][n][2 * half + 1]));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    top[half] = m * fac[t][half];
+                    raise |= top[half] > ref[t][half] + kLimit;
+                }
+                if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (top[half] > ref[t][half] + kLimit) {
+                            const float to_ref = top[half] - kOffset;
+                            const float f = mma::exp2_approx(ref[t][half] - to_ref);
+                            ref[t][half] = to_ref;
+                            sum[t][half] *= f;
+#pragma unroll
+                            for (int n = 0; n < 16; ++n) {
+                                acc[t][n][2 * half] *= f;
+                                acc[t][n][2 * half + 1] *= f;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n) {
+                        const float p0 = mma::exp2_approx(fmaf(sc[t][n][2 * half], fac[t][half], -ref[t][half]));
+                        const float p1 = mma::exp2_approx(fmaf(sc[t][n][2 * half + 1], fac[t][half], -ref[t][half]));
+                        sum[t][half] += p0 + p1;
+                        if (kE4m3) {
+                            hi[t][n][half] = mma::pack_f16(p0, p1);
+                        } else {
+                            const uint32_t p = mma::pack_bf16(p0, p1);
+                            hi[t][n][half] = p;
+                            lo[t][n][half] = mma::pack_bf16(p0 - __uint_as_float(p << 16), p1 - __uint_as_float(p & 0xffff0000u));
+                        }
+                    }
+            }
+
+            // Weighted values.
+            if (!kE4m3) {
+                const int key = (lane & 7) + (((lane >> 3) & 1) << 3), odd = lane >> 4;
+                uint32_t ah[kMT][4], al[kMT][4];
+#pragma unroll
+                for (int t = 0; t < kMT; ++t) {
+                    ah[t][0] = hi[t][0][0]; ah[t][1] = hi[t][0][1]; ah[t][2] = hi[t][1][0]; ah[t][3] = hi[t][1][1];
+                    al[t][0] = lo[t][0][0]; al[t][1] = lo[t][0][1]; al[t][2] = lo[t][1][0]; al[t][3] = lo[t][1][1];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int ch = 2 * j + odd;
+                    uint32_t b[4];
+                    mma::ldmatrix4_trans(b, vs + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+#pragma unroll
+                    for (int t = 0; t < kMT; ++t) {
+                        mma::m16n8k16<false>(acc[t][2 * j], ah[t], b[0], b[1]);
+                        mma::m16n8k16<false>(acc[t][2 * j + 1], ah[t], b[2], b[3]);
+                        mma::m16n8k16<false>(acc[t][2 * j], al[t], b[0], b[1]);
+                        mma::m16n8k16<false>(acc[t][2 * j + 1], al[t], b[2], b[3]);
+                    }
+                }
+            } else {
+                // Rows of the transposed 8 x 8 loads in the weights' key order; a
+                // 16-bit column holds channels 2 n and 2 n + 1 of its chunk, which
+                // are split into two column tiles.
+                const int i = lane & 7, kr = ((i & 1) << 2) | (i >> 1);
+                const int key8 = ((lane >> 3) & 1) << 3, odd = lane >> 4;
+#pragma unroll
+                for (int k2 = 0; k2 < kTile / 16; ++k2) {
+                    uint32_t ap[kMT][4];
+#pragma unroll
+                    for (int t = 0; t < kMT; ++t) {
+                        ap[t][0] = hi[t][2 * k2][0]; ap[t][1] = hi[t][2 * k2][1];
+                        ap[t][2] = hi[t][2 * k2 + 1][0]; ap[t][3] = hi[t][2 * k2 + 1][1];
+                    }
+                    const uint32_t rowp = vs + (k2 * 16 + key8 + kr) * 128;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t b[4];
+                        mma::ldmatrix4_trans(b, rowp + (((2 * j + odd) ^ kr) << 4));
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {   // chunk 2 j + x
+                            const uint32_t y0 = __byte_perm(b[2 * x], 0, 0x3120), y1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
+                            const uint32_t e0 = mma::e4m3x2_f16x2(y0), e1 = mma::e4m3x2_f16x2(y1);
+                            const uint32_t o0 = mma::e4m3x2_f16x2(y0 >> 16), o1 = mma::e4m3x2_f16x2(y1 >> 16);
+#pragma unroll
+                            for (int t = 0; t < kMT; ++t) {
+                                mma::m16n8k16<true>(acc[t][4 * j + 2 * x], ap[t], e0, e1);
+                                mma::m16n8k16<true>(acc[t][4 * j + 2 * x + 1], ap[t], o0, o1);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();   // every lane has read the stage: it may be filled again
+            issue();
+        }
+        if (__syncthreads_or(!ok)) {
+            ok = false;
+            break;
+        }
+
+        // The eight warps' partial results meet.
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float l = sum[t][half];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                if (c == 0) {
+                    sm.ref[warp][t * 16 + half * 8 + g] = ref[t][half];
+                    sm.sum[warp][t * 16 + half * 8 + g] = l;
+                }
+            }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == cur.units;
+        const bool at_start = cur.left == to - from;   // the CTA's first segment
+        float* part = whole ? nullptr : slot_at(a.io.workspace, gridDim.x, 2 * blockIdx.x + (at_start ? 0 : 1));
+        const float vscale = kE4m3 ? a.v_scale[h] : 1.f;
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
+#pragma unroll
+            for (int cols = 0; cols < 2; ++cols) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int r = half * 8 + g;
+                    float top = sm.ref[0][t * 16 + r];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.ref[w][t * 16 + r]);
+                    const float f = mma::exp2_approx(ref[t][half] - top);
+                    float* m = sm.merge + (warp * 16 + r) * kMergeCols;
+                    const int flip = (r & 3) << 3;
+#pragma unroll
+                    for (int n = 0; n < 8; n += kE4m3 ? 2 : 1) {
+                        const float* x = acc[t][cols * 8 + n];
+                        if (!kE4m3) {
+                            *reinterpret_cast<float2*>(m + ((8 * n + 2 * c) ^ flip)) = make_float2(x[2 * half] * f, x[2 * half + 1] * f);
+                        } else {
+                            const float* y = acc[t][cols * 8 + n + 1];
+                            *reinterpret_cast<float4*>(m + ((8 * n + 4 * c) ^ flip)) =
+                                make_float4(x[2 * half] * f, y[2 * half] * f, x[2 * half + 1] * f, y[2 * half + 1] * f);
+                        }
+                    }
+                }
+                __syncthreads();
+                {
+                    const int r = tid >> 4, q = (tid & 15) * 4, row = t * 16 + r;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float top = -INFINITY, l = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float4 x = *reinterpret_cast<const float4*>(sm.merge + (w * 16 + r) * kMergeCols + (q ^ ((r & 3) << 3)));
+                        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+                        top = fmaxf(top, sm.ref[w][row]);
+                    }
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) l += sm.sum[w][row] * mma::exp2_approx(sm.ref[w][row] - top);
+                    if (row < nrows) {
+                        const int col = cols * kMergeCols + q;
+                        if (whole) {
+                            const float n = vscale / l;
+                            store4(a.io, (head0 + row) * kHeadDim + col, make_float4(v.x * n, v.y * n, v.z * n, v.w * n));
+                            if (a.io.lse && col == 0) a.io.lse[head0 + row] = (top + log2f(l)) / kLog2e;
+                        } else {
+                            *reinterpret_cast<float4*>(part + row * kHeadDim + col) = v;
+                            if (col == 0) {
+                                part[kMaxRows * kHeadDim + 2 * row] = top;
+                                part[kMaxRows * kHeadDim + 2 * row + 1] = l;
+                            }
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+        // The CTA that holds the first part of a request that goes on says up to where.
+        if (tid == 0 && u0 == 0 && u1 < cur.units) {
+            const long long last = to - 1 + (cur.units - u1);   // its last unit
+            const int slot = 2 * (int)blockIdx.x + (at_start ? 0 : 1);
+            // The CTA whose range [total i / ctas, total (i + 1) / ctas) holds it.
+            descs(a.io.workspace)[blockIdx.x] = JoinDesc{cur.b, cur.vh, (int)(((last + 1) * ctas - 1) / total), slot};
+        }
+        const int passed = u1 - u0;
+        cur.left -= passed - 1;
+        cur.u = u1 - 1;
+        step<kTile>(a, cur);
+    }
+    if (!ok) {
+        // Give-up path: the copies this warp issued complete (bounded waits) before its shared memory is released.
+        for (int i = used; i < issued; ++i) ptx::mbar_wait_timed(&sm.full[warp][i % kStages], (uint32_t)(i / kStages) & 1u);
+        __syncthreads();
+    }
+}
+
+// Joins the parts of a request and head that lie in several CTAs: one CTA per
+// part-holding CTA and query row, eight warps over the parts, four channels per lane.
+__global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, int ctas) {
+    __shared__ float4 s_acc[8][32];
+    __shared__ float s_ref[8], s_sum[8];
+    ptx::griddep_wait();
+    const JoinDesc d = descs(a.io.workspace)[blockIdx.x];
+    if (d.b < 0) return;
+    const int h = d.vh / a.passes, pass = d.vh % a.passes;
+    const int row = blockIdx.y, row0 = pass * a.rows;
+    if (row >= min(a.rows, a.G - row0)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = d.last - (int)blockIdx.x + 1;
+    float ref = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = warp; i < parts; i += 8) {
+        const float* p = slot_at(a.io.workspace, ctas, i == 0 ? d.slot : 2 * ((int)blockIdx.x + i));
+        const float r = p[kMaxRows * kHeadDim + 2 * row], l = p[kMaxRows * kHeadDim + 2 * row + 1];
+        const float4 v = *reinterpret_cast<const float4*>(p + row * kHeadDim + 4 * lane);
+        const float to = fmaxf(ref, r);
+        const float f = mma::exp2_approx(ref - to), e = mma::exp2_approx(r - to);
+        ref = to;
+        sum = sum * f + l * e;
+        acc.x = acc.x * f + v.x * e;
+        acc.y = acc.y * f + v.y * e;
+        acc.z = acc.z * f + v.z * e;
+        acc.w = acc.w * f + v.w * e;
+    }
+    s_acc[warp][lane] = acc;
+    if (lane == 0) {
+        s_ref[warp] = ref;
+        s_sum[warp] = sum;
+    }
+    __syncthreads();
+    if (warp) return;
+    float top = s_ref[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = fmaxf(top, s_ref[w]);
+    sum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const float e = mma::exp2_approx(s_ref[w] - top);
+        const float4 v = s_acc[w][lane];
+        sum += s_sum[w] * e;
+        acc.x += v.x * e;
+        acc.y += v.y * e;
+        acc.z += v.z * e;
+        acc.w += v.w * e;
+    }
+    const float n = (a.v_scale ? a.v_scale[h] : 1.f) / sum;
+    const size_t head = (size_t)d.b * a.Hq + h * a.G + row0 + row;
+    store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
+    if (a.io.lse && lane == 0) a.io.lse[head] = (top + log2f(sum)) / kLog2e;
+}
+
+std::atomic<bool> g_attr_done[64];
+
+template <bool kE4m3, int kMT>
+cudaError_t set_smem() {
+    return cudaFuncSetAttribute(kda_attn_decode_kernel<kE4m3, kMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(Smem));
+}
+
+}  // namespace
+
+bool attn_prepare_cache(const AttnLayer& l, AttnMaps& maps) {
+    const int tile = l.e4m3 ? 32 : 16;
+    const int rows = l.page_size < tile ? l.page_size : tile;
+    return make_cache_map(&maps.k_decode, l, l.k_cache, rows, l.e4m3 ? 1 : 2) &&
+           make_cache_map(&maps.v_decode, l, l.v_cache, rows, l.e4m3 ? 1 : 2);
+}
+
+size_t attn_decode_workspace_bytes(const DeviceInfo& dev) {
+    return desc_bytes(dev.sm_count) + (size_t)dev.sm_count * 2 * kSlotFloats * sizeof(float);
+}
+
+cudaError_t launch_attn_decode(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
+                               int* err_word, cudaStream_t stream) {
+    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+    if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
+        cudaError_t e = set_smem<false, 1>();
+        if (e == cudaSuccess) e = set_smem<false, 2>();
+        if (e == cudaSuccess) e = set_smem<true, 1>();
+        if (e == cudaSuccess) e = set_smem<true, 2>();
+        if (e != cudaSuccess) return e;
+        g_attr_done[dev.device].store(true, std::memory_order_release);
+    }
+    DecodeArgs a{};
+    a.io = io;
+    a.Hq = l.Hq;
+    a.Hkv = l.Hkv;
+    a.G = l.G;
+    a.passes = (l.G + kMaxRows - 1) / kMaxRows;
+    a.rows = (l.G + a.passes - 1) / a.passes;
+    a.page_shift = l.page_shift;
+    a.num_pages = l.num_pages;
+    a.scale = l.softmax_scale * kLog2e;
+    a.k_scale = l.k_scale;
+    a.v_scale = l.v_scale;
+    // Never more CTAs than the longest table allows units.
+    const int tile = kWarps * (l.e4m3 ? 32 : 16);
+    const long long most = (long long)io.B * l.Hkv * a.passes * ((((long long)io.max_pages << l.page_shift) + tile - 1) / tile);
+    const int grid = (int)(most < dev.sm_count ? most : dev.sm_count);
+    auto kernel = l.e4m3 ? (a.rows <= 16 ? kda_attn_decode_kernel<true, 1> : kda_attn_decode_kernel<true, 2>)
+                         : (a.rows <= 16 ? kda_attn_decode_kernel<false, 1> : kda_attn_decode_kernel<false, 2>);
+    kernel<<<grid, kThreads, sizeof(Smem), stream>>>(a, maps.k_decode, maps.v_decode, err_word);
+    count_launches(1);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || grid == 1) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)a.rows);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kda_attn_join_kernel, a, grid);
+    count_launches(1);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kda

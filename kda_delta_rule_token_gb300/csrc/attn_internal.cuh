@@ -31,6 +31,11 @@ struct AttnLayer {
     void* v_cache;
 };
 
+// Tensor maps of the bound cache (attn_tma.cuh): boxes of the decode's warp tiles.
+struct AttnMaps {
+    CUtensorMap k_decode, v_decode;
+};
+
 // Rotation steps: pair i advances by turn[i] / 2^64 of a full turn per
 // position, so position * turn[i] modulo 2^64 is the exact fraction of a turn.
 struct RopeTurns {
@@ -81,9 +86,11 @@ struct AttnIO {
 cudaError_t launch_attn_plan(const AttnLayer& l, const AttnPlanIO& io, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_attn_append(const AttnLayer& l, const RopeTurns& turns, const AttnAppendIO& io,
                                const DeviceInfo& dev, int* err_word, cudaStream_t stream);
-size_t attn_workspace_bytes(const AttnLayer& l, const DeviceInfo& dev);
-cudaError_t launch_attn_decode(const AttnLayer& l, const AttnIO& io, const DeviceInfo& dev, int* err_word,
-                               cudaStream_t stream);
+// Encodes the bound cache's tensor maps; false if it cannot.
+bool attn_prepare_cache(const AttnLayer& l, AttnMaps& maps);
+size_t attn_decode_workspace_bytes(const DeviceInfo& dev);
+cudaError_t launch_attn_decode(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
+                               int* err_word, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const AttnLayer& l, const AttnIO& io, const DeviceInfo& dev, int* err_word,
                                 cudaStream_t stream);
 

@@ -95,13 +95,6 @@ cudaError_t launch_rows(const AttnLayer& l, const AttnIO& io, int* err_word, cud
 
 }  // namespace
 
-size_t attn_workspace_bytes(const AttnLayer&, const DeviceInfo&) { return 16; }
-
-cudaError_t launch_attn_decode(const AttnLayer& l, const AttnIO& io, const DeviceInfo&, int* err_word,
-                               cudaStream_t stream) {
-    return launch_rows(l, io, err_word, stream);
-}
-
 cudaError_t launch_attn_prefill(const AttnLayer& l, const AttnIO& io, const DeviceInfo&, int* err_word,
                                 cudaStream_t stream) {
     return launch_rows(l, io, err_word, stream);

@@ -16,6 +16,7 @@ constexpr int kErrPrefillWait = 1 << 1;
 constexpr int kErrTestingWait = 1 << 2;
 constexpr int kErrLowrankWait = 1 << 3;
 constexpr int kErrProjWait = 1 << 4;
+constexpr int kErrAttnWait = 1 << 5;
 
 // Longest a kernel waits on one barrier phase before it reports an error.
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;   // 1 s
