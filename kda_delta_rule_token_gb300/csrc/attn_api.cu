@@ -82,7 +82,10 @@ kda_status need_cache(const kda_attn_ctx* ctx) {
     return KDA_ERR_INVALID_ARG;
 }
 
-size_t workspace_bytes_of(const kda_attn_ctx* ctx) { return attn_decode_workspace_bytes(ctx->dev); }
+// The two attention kernels' shares, the few-row one's first.
+size_t workspace_bytes_of(const kda_attn_ctx* ctx) {
+    return attn_decode_workspace_bytes(ctx->dev) + attn_prefill_workspace_bytes(ctx->dev);
+}
 
 // What kda_attn_decode and kda_attn_prefill check alike.
 kda_status check_attend(const kda_attn_ctx* ctx, const AttnIO& io, size_t workspace_bytes) {
@@ -212,7 +215,7 @@ kda_status kda_attn_bind_cache(kda_attn_ctx* ctx, int num_pages, void* k_cache, 
     l.k_cache = k_cache;
     l.v_cache = v_cache;
     kda::AttnMaps maps;
-    if (!kda::attn_prepare_cache(l, maps)) {
+    if (!kda::attn_decode_maps(l, maps) || !kda::attn_prefill_maps(l, maps)) {
         kda::set_error_text("cuTensorMapEncodeTiled failed for the cache");
         return KDA_ERR_CUDA;
     }
@@ -286,8 +289,8 @@ kda_status kda_attn_decode(kda_attn_ctx* ctx, int B, const uint16_t* q, const in
     const kda::AttnIO io{B, B, nullptr, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace};
     if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectDecode, "attn_decode launch", [&] {
-        return kda::launch_attn_decode(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word,
-                                       static_cast<cudaStream_t>(stream));
+        return kda::launch_attn_few_rows(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word,
+                                         static_cast<cudaStream_t>(stream));
     });
 }
 
@@ -301,7 +304,12 @@ kda_status kda_attn_prefill(kda_attn_ctx* ctx, int B, int N, const int32_t* cu_n
     const kda::AttnIO io{B, N, cu_new, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace};
     if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectPrefill, "attn_prefill launch", [&] {
-        return kda::launch_attn_prefill(ctx->layer, io, ctx->dev, ctx->err_word, static_cast<cudaStream_t>(stream));
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        cudaError_t e = kda::launch_attn_few_rows(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word, st);
+        if (e != cudaSuccess || kda::attn_few_rows(N, ctx->layer.G)) return e;   // no request can have more rows
+        kda::AttnIO many = io;
+        many.workspace = static_cast<uint8_t*>(workspace) + kda::attn_decode_workspace_bytes(ctx->dev);
+        return kda::launch_attn_many_rows(ctx->layer, ctx->maps, many, ctx->dev, ctx->err_word, st);
     });
 }
 

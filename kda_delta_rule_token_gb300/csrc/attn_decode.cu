@@ -1,10 +1,13 @@
-// Attention of one new token per request over a paged cache.
+// Attention of one new token, or of a few, per request over a paged cache.
 //
-//   o = softmax(scale * q K^T) V,   per request and query head
+//   o = softmax(scale * q K^T) V,   per request, query head and token
 //
-// Every cached byte of a request is read once for each key head and takes part
-// in 2 G operations (G query heads share a key head), so the call is bound by
-// HBM.  The kernel is built around keeping enough bytes in flight on every SM:
+// The rows of a key head are its G query heads, times n for n new tokens
+// (token i of them sees the keys up to its own); this file takes requests of
+// one token, and of n * G <= 32 rows.  Every cached byte of a request is then
+// read once for each key head and takes part in 2 n G operations, so the call
+// is bound by HBM.  The kernel is built around keeping enough bytes in flight
+// on every SM:
 //
 //  * Work is cut into units of 8 warp tiles (128 keys in bf16, 256 in e4m3) of
 //    one request and key head, numbered request-major.  Each CTA (one per SM)
@@ -18,8 +21,8 @@
 //    kStages stages, running ahead across the ends of requests, and the warp
 //    consumes them by itself.  No warp waits for another before the end of a
 //    request's part, where the eight partial results meet in shared memory.
-//  * The G query heads are the rows of a 16-row mma.sync tile (two tiles from
-//    17 heads on, several passes beyond 32).  The softmax keeps a reference
+//  * The rows are those of a 16-row mma.sync tile (two tiles from 17 rows on,
+//    several passes beyond 32 query heads of one token).  The softmax keeps a reference
 //    (not the exact maximum) per row and rescales only when a logit passes it
 //    by more than kLimit powers of two: the result is the same, the rescaling
 //    almost never runs.
@@ -48,9 +51,7 @@ constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kMergeCols = 64;                   // channels merged at a time
 constexpr uint32_t kMergeBytes = kWarps * 16 * kMergeCols * 4;
-constexpr int kMaxRows = 32;                     // query heads of one pass
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNoRef = -3e38f;                // reference before the first finite logit
+constexpr int kMaxRows = kAttnFewRows;           // rows of one pass
 
 struct Smem {
     uint8_t ring[kRingBytes];
@@ -78,6 +79,7 @@ struct DecodeArgs {
 // part it holds and that goes on in the next CTAs, up to CTA last.  b < 0: none.
 struct JoinDesc {
     int b, vh, last, slot;
+    int tok0, n;
 };
 
 // Workspace: a descriptor per CTA, then two slots per CTA of partial results,
@@ -91,24 +93,19 @@ __device__ __forceinline__ float* slot_at(void* ws, int ctas, int slot) {
     return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + desc_bytes(ctas)) + (size_t)slot * kSlotFloats;
 }
 
-// Four consecutive channels of one head's output row.
-__device__ __forceinline__ void store4(const AttnIO& io, size_t at, float4 v) {
-    if (io.gate) {
-        const float4 g = *reinterpret_cast<const float4*>(io.gate + at);
-        v.x /= 1.f + mma::exp2_approx(-g.x * kLog2e);
-        v.y /= 1.f + mma::exp2_approx(-g.y * kLog2e);
-        v.z /= 1.f + mma::exp2_approx(-g.z * kLog2e);
-        v.w /= 1.f + mma::exp2_approx(-g.w * kLog2e);
-    }
-    if (io.o_f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(io.o) + at) = v;
-    else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(io.o) + at) =
-            make_uint2(mma::pack_bf16(v.x, v.y), mma::pack_bf16(v.z, v.w));
-}
+// Request b as this file sees it: its new tokens, and its cached keys (0 where
+// it has no rows here).
+struct Request {
+    int tok0, n, len;
+};
 
-__device__ __forceinline__ int clamped_len(const DecodeArgs& a, int b) {
-    return min(max(a.io.kv_lens[b], 0), a.io.max_pages << a.page_shift);
+__device__ __forceinline__ Request request(const DecodeArgs& a, int b) {
+    Request r{b, 1, attn_kv_len(a.io, b, a.page_shift)};
+    if (a.io.cu_new) {
+        attn_tokens(a.io, b, r.tok0, r.n);
+        if (r.n == 0 || !attn_few_rows(r.n, a.G)) r.len = 0;
+    }
+    return r;
 }
 
 // A position in the CTA's range of units.
@@ -116,6 +113,7 @@ struct Walk {
     long long left;   // units of the range not yet passed, this one included
     int b, vh, u;     // request, virtual head, unit of it
     int len, units;   // of request b
+    int tok0, n;
 };
 
 template <int kTile>
@@ -131,7 +129,10 @@ __device__ __forceinline__ void step(const DecodeArgs& a, Walk& w) {
     w.vh = 0;
     if (w.left <= 0) return;
     do {
-        w.len = clamped_len(a, ++w.b);
+        const Request r = request(a, ++w.b);
+        w.len = r.len;
+        w.tok0 = r.tok0;
+        w.n = r.n;
         w.units = units_of<kTile>(w.len);
     } while (w.units == 0);
 }
@@ -162,7 +163,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     const int per = (a.io.B + kThreads - 1) / kThreads;
     const int b0 = min(a.io.B, tid * per), b1 = min(a.io.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units_of<kTile>(clamped_len(a, b));
+    for (int b = b0; b < b1; ++b) mine += units_of<kTile>(request(a, b).len);
     mine *= heads;
     long long upto = mine;
 #pragma unroll
@@ -184,7 +185,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     if (works && upto - mine <= from && from < upto) {
         long long at = upto - mine;
         for (int b = b0;; ++b) {
-            const long long n = (long long)units_of<kTile>(clamped_len(a, b)) * heads;
+            const long long n = (long long)units_of<kTile>(request(a, b).len) * heads;
             if (from < at + n) {
                 sm.first_b = b;
                 sm.first_unit = from - at;
@@ -195,11 +196,13 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     }
     // Requests without keys: zero rows.
     for (int b = blockIdx.x; b < a.io.B; b += gridDim.x)
-        if (clamped_len(a, b) == 0) {
-            for (int i = tid; i < a.Hq * (kHeadDim / 4); i += kThreads)
-                store4(a.io, (size_t)b * a.Hq * kHeadDim + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+        if (attn_kv_len(a.io, b, a.page_shift) == 0) {
+            const Request r = request(a, b);
+            const long long rows = (long long)r.n * a.Hq;
+            for (long long i = tid; i < rows * (kHeadDim / 4); i += kThreads)
+                mma::store4(a.io, (size_t)r.tok0 * a.Hq * kHeadDim + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
             if (a.io.lse)
-                for (int i = tid; i < a.Hq; i += kThreads) a.io.lse[(size_t)b * a.Hq + i] = -INFINITY;
+                for (long long i = tid; i < rows; i += kThreads) a.io.lse[(size_t)r.tok0 * a.Hq + i] = -INFINITY;
         }
     __syncthreads();
     if (!works) return;
@@ -207,7 +210,12 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     Walk cur;
     cur.left = to - from;
     cur.b = sm.first_b;
-    cur.len = clamped_len(a, cur.b);
+    {
+        const Request r = request(a, cur.b);
+        cur.len = r.len;
+        cur.tok0 = r.tok0;
+        cur.n = r.n;
+    }
     cur.units = units_of<kTile>(cur.len);
     cur.vh = (int)(sm.first_unit / cur.units);
     cur.u = (int)(sm.first_unit % cur.units);
@@ -260,21 +268,26 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     while (cur.left > 0) {
         // One request and head (or the part of it in this CTA's range).
         const int h = cur.vh / a.passes, pass = cur.vh % a.passes;
-        const int row0 = pass * a.rows, nrows = min(a.rows, a.G - row0);
-        const size_t head0 = (size_t)cur.b * a.Hq + h * a.G + row0;   // output row of query row 0
+        // Row r is query head r % G of token r / G (one pass), or head row0 + r of the only token.
+        const int row0 = pass * a.rows, nrows = cur.n > 1 ? cur.n * a.G : min(a.rows, a.G - row0);
+        const size_t head0 = (size_t)cur.tok0 * a.Hq + h * a.G + row0;
+        auto head_of = [&](int r) { return cur.n > 1 ? head0 + (size_t)(r / a.G) * a.Hq + r % a.G : head0 + r; };
         const int u0 = cur.u, u1 = (int)min((long long)cur.units, u0 + cur.left);
 
         // Query rows into A fragments.
         uint32_t qf[kMT][8][4];
         float fac[kMT][2];   // logit -> power of two
+        int sees[kMT][2];
         const float base = a.scale * (kE4m3 ? a.k_scale[h] : 1.f);
 #pragma unroll
         for (int t = 0; t < kMT; ++t)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int r = t * 16 + half * 8 + g;
-                const uint16_t* q = a.io.q + (head0 + r) * kHeadDim;
+                const uint16_t* q = a.io.q + head_of(r) * kHeadDim;
                 fac[t][half] = base;
+                // Keys that the row sees (all of them where there is one token).
+                sees[t][half] = cur.n > 1 && r < nrows ? cur.len - cur.n + 1 + r / a.G : cur.len;
                 if (!kE4m3) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
@@ -384,15 +397,17 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
                     }
                 }
             }
-            if (valid < kTile) {
+            if (valid - (cur.n - 1) < kTile) {
 #pragma unroll
                 for (int n = 0; n < kNT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int k = n * 8 + (kE4m3 ? c + 4 * e : 2 * c + e);
-                        if (k >= valid)
+                        const int k = key0 + n * 8 + (kE4m3 ? c + 4 * e : 2 * c + e);
 #pragma unroll
-                            for (int t = 0; t < kMT; ++t) sc[t][n][e] = sc[t][n][e + 2] = -INFINITY;
+                        for (int t = 0; t < kMT; ++t) {
+                            if (k >= sees[t][0]) sc[t][n][e] = -INFINITY;
+                            if (k >= sees[t][1]) sc[t][n][e + 2] = -INFINITY;
+                        }
                     }
             }
 
@@ -567,9 +582,10 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
                     if (row < nrows) {
                         const int col = cols * kMergeCols + q;
                         if (whole) {
-                            const float n = vscale / l;
-                            store4(a.io, (head0 + row) * kHeadDim + col, make_float4(v.x * n, v.y * n, v.z * n, v.w * n));
-                            if (a.io.lse && col == 0) a.io.lse[head0 + row] = (top + log2f(l)) / kLog2e;
+                            const float n = l > 0.f ? vscale / l : 0.f;   // 0: the row sees no key
+                            const size_t at = head_of(row);
+                            mma::store4(a.io, at * kHeadDim + col, make_float4(v.x * n, v.y * n, v.z * n, v.w * n));
+                            if (a.io.lse && col == 0) a.io.lse[at] = (top + log2f(l)) / kLog2e;
                         } else {
                             *reinterpret_cast<float4*>(part + row * kHeadDim + col) = v;
                             if (col == 0) {
@@ -586,7 +602,8 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
             const long long last = to - 1 + (cur.units - u1);   // its last unit
             const int slot = 2 * (int)blockIdx.x + (at_start ? 0 : 1);
             // The CTA whose range [total i / ctas, total (i + 1) / ctas) holds it.
-            descs(a.io.workspace)[blockIdx.x] = JoinDesc{cur.b, cur.vh, (int)(((last + 1) * ctas - 1) / total), slot};
+            descs(a.io.workspace)[blockIdx.x] =
+                JoinDesc{cur.b, cur.vh, (int)(((last + 1) * ctas - 1) / total), slot, cur.tok0, cur.n};
         }
         const int passed = u1 - u0;
         cur.left -= passed - 1;
@@ -610,7 +627,7 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
     if (d.b < 0) return;
     const int h = d.vh / a.passes, pass = d.vh % a.passes;
     const int row = blockIdx.y, row0 = pass * a.rows;
-    if (row >= min(a.rows, a.G - row0)) return;
+    if (row >= (d.n > 1 ? d.n * a.G : min(a.rows, a.G - row0))) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = d.last - (int)blockIdx.x + 1;
     float ref = -INFINITY, sum = 0.f;
@@ -650,9 +667,9 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
         acc.z += v.z * e;
         acc.w += v.w * e;
     }
-    const float n = (a.v_scale ? a.v_scale[h] : 1.f) / sum;
-    const size_t head = (size_t)d.b * a.Hq + h * a.G + row0 + row;
-    store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
+    const float n = sum > 0.f ? (a.v_scale ? a.v_scale[h] : 1.f) / sum : 0.f;
+    const size_t head = ((size_t)d.tok0 + (d.n > 1 ? row / a.G : 0)) * a.Hq + h * a.G + (d.n > 1 ? row % a.G : row0 + row);
+    mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
     if (a.io.lse && lane == 0) a.io.lse[head] = (top + log2f(sum)) / kLog2e;
 }
 
@@ -666,7 +683,7 @@ cudaError_t set_smem() {
 
 }  // namespace
 
-bool attn_prepare_cache(const AttnLayer& l, AttnMaps& maps) {
+bool attn_decode_maps(const AttnLayer& l, AttnMaps& maps) {
     const int tile = l.e4m3 ? 32 : 16;
     const int rows = l.page_size < tile ? l.page_size : tile;
     return make_cache_map(&maps.k_decode, l, l.k_cache, rows, l.e4m3 ? 1 : 2) &&
@@ -677,8 +694,8 @@ size_t attn_decode_workspace_bytes(const DeviceInfo& dev) {
     return desc_bytes(dev.sm_count) + (size_t)dev.sm_count * 2 * kSlotFloats * sizeof(float);
 }
 
-cudaError_t launch_attn_decode(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
-                               int* err_word, cudaStream_t stream) {
+cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
+                                 int* err_word, cudaStream_t stream) {
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
         cudaError_t e = set_smem<false, 1>();
@@ -700,18 +717,20 @@ cudaError_t launch_attn_decode(const AttnLayer& l, const AttnMaps& maps, const A
     a.scale = l.softmax_scale * kLog2e;
     a.k_scale = l.k_scale;
     a.v_scale = l.v_scale;
+    // A call with a token per request has G rows at most; else any count up to 32 may occur.
+    const int most_rows = io.cu_new && l.G < kMaxRows ? kMaxRows : a.rows;
     // Never more CTAs than the longest table allows units.
     const int tile = kWarps * (l.e4m3 ? 32 : 16);
     const long long most = (long long)io.B * l.Hkv * a.passes * ((((long long)io.max_pages << l.page_shift) + tile - 1) / tile);
     const int grid = (int)(most < dev.sm_count ? most : dev.sm_count);
-    auto kernel = l.e4m3 ? (a.rows <= 16 ? kda_attn_decode_kernel<true, 1> : kda_attn_decode_kernel<true, 2>)
-                         : (a.rows <= 16 ? kda_attn_decode_kernel<false, 1> : kda_attn_decode_kernel<false, 2>);
+    auto kernel = l.e4m3 ? (most_rows <= 16 ? kda_attn_decode_kernel<true, 1> : kda_attn_decode_kernel<true, 2>)
+                         : (most_rows <= 16 ? kda_attn_decode_kernel<false, 1> : kda_attn_decode_kernel<false, 2>);
     kernel<<<grid, kThreads, sizeof(Smem), stream>>>(a, maps.k_decode, maps.v_decode, err_word);
     count_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)a.rows);
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)most_rows);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

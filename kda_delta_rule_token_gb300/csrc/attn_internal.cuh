@@ -31,9 +31,11 @@ struct AttnLayer {
     void* v_cache;
 };
 
-// Tensor maps of the bound cache (attn_tma.cuh): boxes of the decode's warp tiles.
+// Tensor maps of the bound cache (attn_tma.cuh): boxes of the decode's warp
+// tiles, and of one 128-byte column block for prompts.
 struct AttnMaps {
     CUtensorMap k_decode, v_decode;
+    CUtensorMap k_prefill, v_prefill;
 };
 
 // Rotation steps: pair i advances by turn[i] / 2^64 of a full turn per
@@ -86,12 +88,37 @@ struct AttnIO {
 cudaError_t launch_attn_plan(const AttnLayer& l, const AttnPlanIO& io, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_attn_append(const AttnLayer& l, const RopeTurns& turns, const AttnAppendIO& io,
                                const DeviceInfo& dev, int* err_word, cudaStream_t stream);
-// Encodes the bound cache's tensor maps; false if it cannot.
-bool attn_prepare_cache(const AttnLayer& l, AttnMaps& maps);
+// The bound cache's tensor maps; false if they cannot be encoded.
+bool attn_decode_maps(const AttnLayer& l, AttnMaps& maps);
+bool attn_prefill_maps(const AttnLayer& l, AttnMaps& maps);
+// attn_decode.cu: every request of one token (cu_new null), or those of
+// attn_few_rows (the others are left alone), and the zero rows of requests
+// without keys.  attn_prefill.cu: the remaining requests of a call.
 size_t attn_decode_workspace_bytes(const DeviceInfo& dev);
-cudaError_t launch_attn_decode(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
-                               int* err_word, cudaStream_t stream);
-cudaError_t launch_attn_prefill(const AttnLayer& l, const AttnIO& io, const DeviceInfo& dev, int* err_word,
-                                cudaStream_t stream);
+size_t attn_prefill_workspace_bytes(const DeviceInfo& dev);
+cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
+                                 int* err_word, cudaStream_t stream);
+cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
+                                  int* err_word, cudaStream_t stream);
+
+// Which of the two takes a request of n new tokens and G query heads per key
+// head: up to 32 rows fit two 16-row warp tiles, whose kernel streams the
+// cache at HBM rate; 128-row tensor-memory tiles pay from there on.
+constexpr int kAttnFewRows = 32;
+__host__ __device__ __forceinline__ bool attn_few_rows(int n, int G) {
+    return n <= 1 || (long long)n * G <= kAttnFewRows;
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ int attn_kv_len(const AttnIO& io, int b, int page_shift) {
+    return min(max(io.kv_lens[b], 0), io.max_pages << page_shift);
+}
+
+// Request b's rows of the packed inputs (offsets clamped to the N rows there are).
+__device__ __forceinline__ void attn_tokens(const AttnIO& io, int b, int& tok0, int& n) {
+    tok0 = min(max(io.cu_new[b], 0), io.N);
+    n = max(min(max(io.cu_new[b + 1], 0), io.N) - tok0, 0);
+}
+#endif
 
 }  // namespace kda

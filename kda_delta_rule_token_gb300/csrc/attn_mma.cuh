@@ -1,5 +1,5 @@
-// Warp-level pieces of the paged attention kernels: mma.sync with bf16 or f16
-// operands, ldmatrix, and the conversions of e4m3 values.
+// Pieces of the paged attention kernels: mma.sync with bf16 or f16 operands,
+// ldmatrix, conversions of e4m3 values, packed fp32, and the output's store.
 //
 // One new token's query heads of one key head are at most a few rows, and a
 // byte of the cache takes part in 2 * rows operations: the tensor pipe idles
@@ -11,7 +11,13 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "attn_internal.cuh"
+
 namespace kda {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoRef = -3e38f;   // a softmax row's reference before its first finite logit
+
 namespace mma {
 
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8).  Lane (g, c) = (lane / 4, lane %
@@ -59,6 +65,29 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// Packed pairs of fp32.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pk(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void upk(f32x2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -67,6 +96,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Four consecutive channels of one head's output row.
+__device__ __forceinline__ void store4(const AttnIO& io, size_t at, float4 v) {
+    if (io.gate) {
+        const float4 g = *reinterpret_cast<const float4*>(io.gate + at);
+        v.x /= 1.f + exp2_approx(-g.x * kLog2e);
+        v.y /= 1.f + exp2_approx(-g.y * kLog2e);
+        v.z /= 1.f + exp2_approx(-g.z * kLog2e);
+        v.w /= 1.f + exp2_approx(-g.w * kLog2e);
+    }
+    if (io.o_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(io.o) + at) = v;
+    else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(io.o) + at) =
+            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
 }  // namespace mma
