@@ -43,22 +43,24 @@
 namespace kda {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
+constexpr int kCtasPerSm = 2;
+constexpr int kStages = 2;
 constexpr uint32_t kTileBytes = 4096;            // keys (or values) of one warp tile
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
-constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kMergeCols = 64;                   // channels merged at a time
-constexpr uint32_t kMergeBytes = kWarps * 16 * kMergeCols * 4;
+constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;   // whatever the number of warps to a tile
+constexpr uint32_t kMergeBytes = kWarps * 16 * kHeadDim * 4;
+constexpr int kPartCost = 1;
 constexpr int kMaxRows = kAttnFewRows;           // rows of one pass
 
 struct Smem {
     uint8_t ring[kRingBytes];
     float merge[kMergeBytes / 4];
-    float ref[kWarps][kMaxRows];
-    float sum[kWarps][kMaxRows];
-    uint64_t full[kWarps][kStages];
+    float ref[2][kWarps * 16];
+    float sum[2][kWarps * 16];
+    uint64_t full[kWarps * kStages];
+    uint64_t empty[kWarps * kStages];
     long long scan[kWarps];
     long long total, first_unit;
     int first_b;
@@ -108,23 +110,31 @@ __device__ __forceinline__ Request request(const DecodeArgs& a, int b) {
     return r;
 }
 
-// A position in the CTA's range of units.
+// A position in the CTA's range.  The range also counts kPartCost units for
+// each request and head before its first unit: what starting and ending one
+// costs, as measured, so that ranges of many short requests are not longer
+// than ranges of one long one.
 struct Walk {
-    long long left;   // units of the range not yet passed, this one included
+    long long left;   // units of the range not yet passed, this one included; none if <= 0
     int b, vh, u;     // request, virtual head, unit of it
     int len, units;   // of request b
     int tok0, n;
 };
 
-template <int kTile>
-__device__ __forceinline__ int units_of(int len) { return (int)(((long long)len + kWarps * kTile - 1) / (kWarps * kTile)); }
+// Units of a request and head, and those with its cost.
+template <int kUnit>
+__device__ __forceinline__ int units_of(int len) { return (int)(((long long)len + kUnit - 1) / kUnit); }
+
+template <int kUnit>
+__device__ __forceinline__ long long cost_of(int len) { return len ? units_of<kUnit>(len) + kPartCost : 0; }
 
 // To the next unit (of the next request with any, at the end of one).
-template <int kTile>
+template <int kUnit>
 __device__ __forceinline__ void step(const DecodeArgs& a, Walk& w) {
     --w.left;
     if (++w.u < w.units) return;
     w.u = 0;
+    w.left -= kPartCost;
     if (++w.vh < a.Hkv * a.passes) return;
     w.vh = 0;
     if (w.left <= 0) return;
@@ -133,25 +143,36 @@ __device__ __forceinline__ void step(const DecodeArgs& a, Walk& w) {
         w.len = r.len;
         w.tok0 = r.tok0;
         w.n = r.n;
-        w.units = units_of<kTile>(w.len);
+        w.units = units_of<kUnit>(w.len);
     } while (w.units == 0);
 }
 
-template <bool kE4m3, int kMT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool kE4m3, int kRowTiles>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
 kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, int* err) {
     constexpr int kTile = kE4m3 ? 32 : 16;       // keys of a warp tile
     constexpr int kNT = kTile / 8;               // 8-key column tiles of the logits
+    constexpr int kGroups = kWarps / kRowTiles;  // groups of warps that share a tile
+    constexpr int kUnit = kGroups * kTile;       // keys of a unit
+    constexpr int kDepth = kStages * kRowTiles;  // stages of a group's ring
     constexpr float kOffset = kE4m3 ? 10.f : 0.f;
     constexpr float kLimit = kE4m3 ? 15.f : 8.f;
     extern __shared__ __align__(1024) uint8_t sm_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(sm_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int group = warp / kRowTiles, row_tile = warp % kRowTiles;
+    const bool lead = row_tile == 0;             // the group's copying warp
+    uint64_t* full = sm.full + group * kDepth;
+    uint64_t* empty = sm.empty + group * kDepth; // the group's other warp has read the stage
+    uint8_t* ring = sm.ring + group * kDepth * kStageBytes;
 
     ptx::griddep_launch_dependents();
-    if (lane == 0)
-        for (int s = 0; s < kStages; ++s) ptx::mbar_init(&sm.full[warp][s], 1);
+    if (lane == 0 && lead)
+        for (int s = 0; s < kDepth; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
     if (tid == 0) {
         sm.dead = 0;
         descs(a.io.workspace)[blockIdx.x].b = -1;
@@ -163,7 +184,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     const int per = (a.io.B + kThreads - 1) / kThreads;
     const int b0 = min(a.io.B, tid * per), b1 = min(a.io.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units_of<kTile>(request(a, b).len);
+    for (int b = b0; b < b1; ++b) mine += cost_of<kUnit>(request(a, b).len);
     mine *= heads;
     long long upto = mine;
 #pragma unroll
@@ -185,7 +206,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     if (works && upto - mine <= from && from < upto) {
         long long at = upto - mine;
         for (int b = b0;; ++b) {
-            const long long n = (long long)units_of<kTile>(request(a, b).len) * heads;
+            const long long n = cost_of<kUnit>(request(a, b).len) * heads;
             if (from < at + n) {
                 sm.first_b = b;
                 sm.first_unit = from - at;
@@ -216,9 +237,13 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         cur.tok0 = r.tok0;
         cur.n = r.n;
     }
-    cur.units = units_of<kTile>(cur.len);
-    cur.vh = (int)(sm.first_unit / cur.units);
-    cur.u = (int)(sm.first_unit % cur.units);
+    cur.units = units_of<kUnit>(cur.len);
+    cur.vh = (int)(sm.first_unit / (cur.units + kPartCost));
+    cur.u = (int)(sm.first_unit % (cur.units + kPartCost)) - kPartCost;
+    if (cur.u < 0) {
+        cur.left += cur.u;
+        cur.u = 0;
+    }
 
     // Producer: lane 0 issues the warp's tiles; the page ids of the next tile
     // are loaded one issue ahead of their use.
@@ -227,23 +252,26 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     Walk ahead = cur;
     int ids[kTile / 16];
     auto fetch_ids = [&]() {   // to the warp's next tile, if there is one
-        while (ahead.left > 0 && (ahead.u * kWarps + warp) * kTile >= ahead.len) step<kTile>(a, ahead);
+        while (ahead.left > 0 && (ahead.u * kGroups + group) * kTile >= ahead.len) step<kUnit>(a, ahead);
         if (ahead.left <= 0) return;
-        const int key = (ahead.u * kWarps + warp) * kTile;
+        const int key = (ahead.u * kGroups + group) * kTile;
         const int* t = a.io.block_table + (size_t)ahead.b * a.io.max_pages + (key >> a.page_shift);
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i)
             if (i < boxes) ids[i] = key + i * box_rows < ahead.len ? t[i] : ids[0];
     };
     int issued = 0;
-    auto issue = [&]() {
+    bool ok = true;
+    auto issue = [&]() {   // the lead warp
         if (ahead.left <= 0) return;
-        if (lane == 0) {
-            const int s = issued % kStages;
-            uint8_t* st = sm.ring + (warp * kStages + s) * kStageBytes;
-            const int row = (ahead.u * kWarps + warp) * kTile & page_mask;
+        const int s = issued % kDepth;
+        if (kRowTiles > 1 && issued >= kDepth)
+            ok = ptx::mbar_wait_timed(&empty[s], (uint32_t)(issued / kDepth - 1) & 1u, &sm.dead);
+        if (lane == 0 && ok) {
+            uint8_t* st = ring + s * kStageBytes;
+            const int row = (ahead.u * kGroups + group) * kTile & page_mask;
             const int h = ahead.vh / a.passes;
-            ptx::mbar_arrive_expect_tx(&sm.full[warp][s], kStageBytes);
+            ptx::mbar_arrive_expect_tx(&full[s], kStageBytes);
 #pragma unroll
             for (int i = 0; i < kTile / 16; ++i)
                 if (i < boxes) {
@@ -252,121 +280,150 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
                     // A page outside the cache: a box outside the tensor, which reads as zeros.
                     const int ph = (in ? ids[i] : a.num_pages) * a.Hkv + (in ? h : 0);
                     const uint32_t off = i * (kTileBytes / boxes);
-                    ptx::tma_load_4d(st + off, &kmap, 0, row, 0, ph, &sm.full[warp][s]);
-                    ptx::tma_load_4d(st + kTileBytes + off, &vmap, 0, row, 0, ph, &sm.full[warp][s]);
+                    ptx::tma_load_4d(st + off, &kmap, 0, row, 0, ph, &full[s]);
+                    ptx::tma_load_4d(st + kTileBytes + off, &vmap, 0, row, 0, ph, &full[s]);
                 }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+            sm.dead = 1;
+            atomicOr(err, ptx::kErrAttnWait);
+            return;
         }
         ++issued;
-        step<kTile>(a, ahead);
+        step<kUnit>(a, ahead);
         fetch_ids();
     };
-    fetch_ids();
-    for (int s = 0; s < kStages; ++s) issue();
+    if (lead) {
+        fetch_ids();
+        for (int s = 0; s < kDepth; ++s) issue();
+    }
 
-    int used = 0;
-    bool ok = true;
-    while (cur.left > 0) {
-        // One request and head (or the part of it in this CTA's range).
-        const int h = cur.vh / a.passes, pass = cur.vh % a.passes;
-        // Row r is query head r % G of token r / G (one pass), or head row0 + r of the only token.
-        const int row0 = pass * a.rows, nrows = cur.n > 1 ? cur.n * a.G : min(a.rows, a.G - row0);
-        const size_t head0 = (size_t)cur.tok0 * a.Hq + h * a.G + row0;
-        auto head_of = [&](int r) { return cur.n > 1 ? head0 + (size_t)(r / a.G) * a.Hq + r % a.G : head0 + r; };
-        const int u0 = cur.u, u1 = (int)min((long long)cur.units, u0 + cur.left);
-
-        // Query rows into A fragments.
-        uint32_t qf[kMT][8][4];
-        float fac[kMT][2];   // logit -> power of two
-        int sees[kMT][2];
-        const float base = a.scale * (kE4m3 ? a.k_scale[h] : 1.f);
+    // Row r of a request and head: query head r % G of token r / G (one pass),
+    // or head row0 + r of the only token.
+    struct Rows {
+        int h, row0, n;
+        size_t head0;
+    };
+    auto rows_of = [&](const Walk& w) {
+        Rows x;
+        x.h = w.vh / a.passes;
+        x.row0 = w.vh % a.passes * a.rows;
+        x.n = w.n > 1 ? w.n * a.G : min(a.rows, a.G - x.row0);
+        x.head0 = (size_t)w.tok0 * a.Hq + x.h * a.G + x.row0;
+        return x;
+    };
+    auto head_of = [&](const Walk& w, const Rows& x, int r) {
+        return w.n > 1 ? x.head0 + (size_t)(r / a.G) * a.Hq + r % a.G : x.head0 + r;
+    };
+    // The query rows' words that this lane's A fragments are made of, loaded
+    // before the partial results of the request before meet.  e4m3: channels in the
+    // order in which the keys are read, step s takes 16 c + 4 s + {0, 1 | 2, 3}
+    // of the lower half, then of the upper.
+    uint32_t raw[2][16];
+    auto load_rows = [&](const Walk& w) {
+        const Rows x = rows_of(w);
 #pragma unroll
-        for (int t = 0; t < kMT; ++t)
+        for (int half = 0; half < 2; ++half) {
+            const int r = row_tile * 16 + half * 8 + g;
+            const uint16_t* q = a.io.q + head_of(w, x, r) * kHeadDim;
+            if (!kE4m3) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int r = t * 16 + half * 8 + g;
-                const uint16_t* q = a.io.q + head_of(r) * kHeadDim;
-                fac[t][half] = base;
-                // Keys that the row sees (all of them where there is one token).
-                sees[t][half] = cur.n > 1 && r < nrows ? cur.len - cur.n + 1 + r / a.G : cur.len;
-                if (!kE4m3) {
+                for (int s = 0; s < 16; ++s)
+                    raw[half][s] = r < x.n ? *reinterpret_cast<const uint32_t*>(q + 8 * s + 2 * c) : 0u;
+            } else {
 #pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        qf[t][s][half] = r < nrows ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * c) : 0u;
-                        qf[t][s][half + 2] = r < nrows ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * c + 8) : 0u;
-                    }
-                } else {
-                    // Channels in the order in which the keys are read: step s takes
-                    // 16 c + 4 s + {0, 1 | 2, 3} of the lower half, then of the upper.
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < nrows) v = *reinterpret_cast<const uint4*>(q + (i >> 1) * 64 + 16 * c + (i & 1) * 8);
-                        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-                    }
-                    float top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // q * 2^(14 - e) with 2^e <= top < 2^(e+1): exact in f16 down to 2^-28 of the row's largest.
-                    const int e = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
-                    const float up = exp2f((float)(14 - e));
-                    fac[t][half] = base * exp2f((float)(e - 14));
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t v = w[2 * s + x];
-                            qf[t][s][half + 2 * x] =
-                                mma::pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
-                        }
+                for (int i = 0; i < 4; ++i) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < x.n) v = *reinterpret_cast<const uint4*>(q + (i >> 1) * 64 + 16 * c + (i & 1) * 8);
+                    raw[half][4 * i] = v.x; raw[half][4 * i + 1] = v.y;
+                    raw[half][4 * i + 2] = v.z; raw[half][4 * i + 3] = v.w;
                 }
             }
+        }
+    };
 
-        float acc[kMT][16][4], ref[kMT][2], sum[kMT][2];
+    int used = 0, parity = 0;
+    bool at_start = true;   // in the CTA's first request and head
+    if (cur.left > 0) load_rows(cur);
+    while (cur.left > 0) {
+        // One request and head (or the part of it in this CTA's range).
+        const Rows rw = rows_of(cur);
+        const int h = rw.h, nrows = rw.n;
+        const int u0 = cur.u, u1 = (int)min((long long)cur.units, u0 + cur.left);
+
+        uint32_t qf[8][4];   // A fragments
+        float fac[2];        // logit -> power of two
+        int sees[2];         // keys that the row sees (all of them where there is one token)
+        const float base = a.scale * (kE4m3 ? a.k_scale[h] : 1.f);
 #pragma unroll
-        for (int t = 0; t < kMT; ++t) {
+        for (int half = 0; half < 2; ++half) {
+            const int r = row_tile * 16 + half * 8 + g;
+            const uint32_t (&w)[16] = raw[half];
+            fac[half] = base;
+            sees[half] = cur.n > 1 && r < nrows ? cur.len - cur.n + 1 + r / a.G : cur.len;
+            float up = 1.f;
+            if (kE4m3) {
+                float top = 0.f;
 #pragma unroll
-            for (int n = 0; n < 16; ++n)
+                for (int i = 0; i < 16; ++i)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // q * 2^(14 - e) with 2^e <= top < 2^(e+1): exact in f16 down to 2^-28 of the row's largest.
+                const int e = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
+                up = exp2f((float)(14 - e));
+                fac[half] = base * exp2f((float)(e - 14));
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][n][e] = 0.f;
-            ref[t][0] = ref[t][1] = kNoRef;
-            sum[t][0] = sum[t][1] = 0.f;
+            for (int s = 0; s < 8; ++s)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t v = w[2 * s + x];
+                    qf[s][half + 2 * x] = !kE4m3 ? v : mma::pack_f16(__uint_as_float(v << 16) * up,
+                                                                       __uint_as_float(v & 0xffff0000u) * up);
+                }
         }
 
+        float acc[16][4], ref[2], sum[2];
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+        ref[0] = ref[1] = kNoRef;
+        sum[0] = sum[1] = 0.f;
+
         for (int u = u0; u < u1 && ok; ++u) {
-            const int key0 = (u * kWarps + warp) * kTile;
+            const int key0 = (u * kGroups + group) * kTile;
             if (key0 >= cur.len) break;
-            const int s = used % kStages;
-            ok = ptx::mbar_wait_timed(&sm.full[warp][s], (uint32_t)(used / kStages) & 1u, &sm.dead);
+            const int s = used % kDepth;
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait_timed(&full[s], (uint32_t)(used / kDepth) & 1u, &sm.dead));
             if (!ok) {
                 sm.dead = 1;
                 atomicOr(err, ptx::kErrAttnWait);
                 break;
             }
             ++used;
-            const uint32_t ks = ptx::smem_u32(sm.ring + (warp * kStages + s) * kStageBytes), vs = ks + kTileBytes;
+            uint8_t* stage = ring + s * kStageBytes;
+            const uint32_t ks = ptx::smem_u32(stage), vs = ks + kTileBytes;
             const int valid = cur.len - key0;   // keys of the tile, if below kTile
             if (valid < kTile) {
-                // Values past the request's end may be anything, NaN too: their weight is 0, make them 0.
+                // Values past the request's end may be anything, NaN too: their
+                // weight is 0, make them 0 (every warp of the group writes the same).
                 for (int i = lane; i < (int)kTileBytes / 16; i += 32) {
                     const int row = kE4m3 ? i >> 3 : (i >> 3) & 15;
-                    if (row >= valid) *reinterpret_cast<uint4*>(sm.ring + (warp * kStages + s) * kStageBytes + kTileBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    if (row >= valid) *reinterpret_cast<uint4*>(stage + kTileBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             }
 
             // Logits: rows = query heads, columns = keys.
-            float sc[kMT][kNT][4];
+            float sc[kNT][4];
 #pragma unroll
-            for (int t = 0; t < kMT; ++t)
+            for (int n = 0; n < kNT; ++n)
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[t][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
             if (!kE4m3) {
                 const int key = (lane & 7) + ((lane >> 4) << 3), odd = (lane >> 3) & 1;
 #pragma unroll
@@ -374,11 +431,8 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
                     const int ch = 2 * st + odd;   // 16-byte chunk of the key's row
                     uint32_t b[4];
                     mma::ldmatrix4(b, ks + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
-#pragma unroll
-                    for (int t = 0; t < kMT; ++t) {
-                        mma::m16n8k16<false>(sc[t][0], qf[t][st], b[0], b[1]);
-                        mma::m16n8k16<false>(sc[t][1], qf[t][st], b[2], b[3]);
-                    }
+                    mma::m16n8k16<false>(sc[0], qf[st], b[0], b[1]);
+                    mma::m16n8k16<false>(sc[1], qf[st], b[2], b[3]);
                 }
             } else {
                 // Column n of a tile is key 4 (n % 2) + n / 2 of its eight, so
@@ -392,8 +446,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
 #pragma unroll
                     for (int st = 0; st < 8; ++st) {
                         const uint32_t x0 = mma::e4m3x2_f16x2(w[st]), x1 = mma::e4m3x2_f16x2(w[st] >> 16);
-#pragma unroll
-                        for (int t = 0; t < kMT; ++t) mma::m16n8k16<true>(sc[t][n], qf[t][st], x0, x1);
+                        mma::m16n8k16<true>(sc[n], qf[st], x0, x1);
                     }
                 }
             }
@@ -403,83 +456,82 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int k = key0 + n * 8 + (kE4m3 ? c + 4 * e : 2 * c + e);
-#pragma unroll
-                        for (int t = 0; t < kMT; ++t) {
-                            if (k >= sees[t][0]) sc[t][n][e] = -INFINITY;
-                            if (k >= sees[t][1]) sc[t][n][e + 2] = -INFINITY;
-                        }
+                        if (k >= sees[0]) sc[n][e] = -INFINITY;
+                        if (k >= sees[1]) sc[n][e + 2] = -INFINITY;
                     }
             }
 
             // Softmax weights against the row's reference.
-            uint32_t hi[kMT][kNT][2], lo[kMT][kNT][2];   // A fragments of the weights, rows g and g + 8
+            uint32_t hi[kNT][2], lo[kNT][2];   // A fragments of the weights, rows g and g + 8
+            // A row is looked at as a whole only when one of its logits passes the reference.
+            float top[2];
+            bool raise = false;
 #pragma unroll
-            for (int t = 0; t < kMT; ++t) {
-                float top[2];
-                bool raise = false;
+            for (int half = 0; half < 2; ++half) {
+                float m = fmaxf(sc[0][2 * half], sc[0][2 * half + 1]);
+#pragma unroll
+                for (int n = 1; n < kNT; ++n) m = mma::max3(m, sc[n][2 * half], sc[n][2 * half + 1]);
+                top[half] = m * fac[half];
+                raise |= top[half] > ref[half] + kLimit;
+            }
+            if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    float m = -INFINITY;
-#pragma unroll
-                    for (int n = 0; n < kNT; ++n) m = fmaxf(m, fmaxf(sc[t][n][2 * half], sc[t][n][2 * half + 1]));
+                    float m = top[half];
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    top[half] = m * fac[t][half];
-                    raise |= top[half] > ref[t][half] + kLimit;
-                }
-                if (__any_sync(0xffffffffu, raise)) {
+                    if (m > ref[half] + kLimit) {
+                        const float to_ref = m - kOffset;
+                        const float f = mma::exp2_approx(ref[half] - to_ref);
+                        ref[half] = to_ref;
+                        sum[half] *= f;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (top[half] > ref[t][half] + kLimit) {
-                            const float to_ref = top[half] - kOffset;
-                            const float f = mma::exp2_approx(ref[t][half] - to_ref);
-                            ref[t][half] = to_ref;
-                            sum[t][half] *= f;
-#pragma unroll
-                            for (int n = 0; n < 16; ++n) {
-                                acc[t][n][2 * half] *= f;
-                                acc[t][n][2 * half + 1] *= f;
-                            }
+                        for (int n = 0; n < 16; ++n) {
+                            acc[n][2 * half] *= f;
+                            acc[n][2 * half + 1] *= f;
                         }
                     }
                 }
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int n = 0; n < kNT; ++n) {
-                        const float p0 = mma::exp2_approx(fmaf(sc[t][n][2 * half], fac[t][half], -ref[t][half]));
-                        const float p1 = mma::exp2_approx(fmaf(sc[t][n][2 * half + 1], fac[t][half], -ref[t][half]));
-                        sum[t][half] += p0 + p1;
-                        if (kE4m3) {
-                            hi[t][n][half] = mma::pack_f16(p0, p1);
-                        } else {
-                            const uint32_t p = mma::pack_bf16(p0, p1);
-                            hi[t][n][half] = p;
-                            lo[t][n][half] = mma::pack_bf16(p0 - __uint_as_float(p << 16), p1 - __uint_as_float(p & 0xffff0000u));
-                        }
-                    }
             }
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) {
+                    const float p0 = mma::exp2_approx(fmaf(sc[n][2 * half], fac[half], -ref[half]));
+                    const float p1 = mma::exp2_approx(fmaf(sc[n][2 * half + 1], fac[half], -ref[half]));
+                    sum[half] += p0 + p1;
+                    if (kE4m3) {
+                        hi[n][half] = mma::pack_f16(p0, p1);
+                    } else {
+                        const uint32_t p = mma::pack_bf16(p0, p1);
+                        hi[n][half] = p;
+                        lo[n][half] = mma::pack_bf16(p0 - __uint_as_float(p << 16), p1 - __uint_as_float(p & 0xffff0000u));
+                    }
+                }
 
             // Weighted values.
             if (!kE4m3) {
                 const int key = (lane & 7) + (((lane >> 3) & 1) << 3), odd = lane >> 4;
-                uint32_t ah[kMT][4], al[kMT][4];
+                uint32_t ah[4], al[4];
+                ah[0] = hi[0][0]; ah[1] = hi[0][1]; ah[2] = hi[1][0]; ah[3] = hi[1][1];
+                al[0] = lo[0][0]; al[1] = lo[0][1]; al[2] = lo[1][0]; al[3] = lo[1][1];
 #pragma unroll
-                for (int t = 0; t < kMT; ++t) {
-                    ah[t][0] = hi[t][0][0]; ah[t][1] = hi[t][0][1]; ah[t][2] = hi[t][1][0]; ah[t][3] = hi[t][1][1];
-                    al[t][0] = lo[t][0][0]; al[t][1] = lo[t][0][1]; al[t][2] = lo[t][1][0]; al[t][3] = lo[t][1][1];
-                }
+                for (int j = 0; j < 8; j += 4) {
+                    uint32_t b[4][4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int ch = 2 * j + odd;
-                    uint32_t b[4];
-                    mma::ldmatrix4_trans(b, vs + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+                    for (int i = 0; i < 4; ++i) {
+                        const int ch = 2 * (j + i) + odd;
+                        mma::ldmatrix4_trans(b[i], vs + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+                    }
 #pragma unroll
-                    for (int t = 0; t < kMT; ++t) {
-                        mma::m16n8k16<false>(acc[t][2 * j], ah[t], b[0], b[1]);
-                        mma::m16n8k16<false>(acc[t][2 * j + 1], ah[t], b[2], b[3]);
-                        mma::m16n8k16<false>(acc[t][2 * j], al[t], b[0], b[1]);
-                        mma::m16n8k16<false>(acc[t][2 * j + 1], al[t], b[2], b[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        mma::m16n8k16<false>(acc[2 * (j + i)], ah, b[i][0], b[i][1]);
+                        mma::m16n8k16<false>(acc[2 * (j + i) + 1], ah, b[i][2], b[i][3]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mma::m16n8k16<false>(acc[2 * (j + i)], al, b[i][0], b[i][1]);
+                        mma::m16n8k16<false>(acc[2 * (j + i) + 1], al, b[i][2], b[i][3]);
                     }
                 }
             } else {
@@ -490,12 +542,9 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
                 const int key8 = ((lane >> 3) & 1) << 3, odd = lane >> 4;
 #pragma unroll
                 for (int k2 = 0; k2 < kTile / 16; ++k2) {
-                    uint32_t ap[kMT][4];
-#pragma unroll
-                    for (int t = 0; t < kMT; ++t) {
-                        ap[t][0] = hi[t][2 * k2][0]; ap[t][1] = hi[t][2 * k2][1];
-                        ap[t][2] = hi[t][2 * k2 + 1][0]; ap[t][3] = hi[t][2 * k2 + 1][1];
-                    }
+                    uint32_t ap[4];
+                    ap[0] = hi[2 * k2][0]; ap[1] = hi[2 * k2][1];
+                    ap[2] = hi[2 * k2 + 1][0]; ap[3] = hi[2 * k2 + 1][1];
                     const uint32_t rowp = vs + (k2 * 16 + key8 + kr) * 128;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -506,97 +555,92 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
                             const uint32_t y0 = __byte_perm(b[2 * x], 0, 0x3120), y1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
                             const uint32_t e0 = mma::e4m3x2_f16x2(y0), e1 = mma::e4m3x2_f16x2(y1);
                             const uint32_t o0 = mma::e4m3x2_f16x2(y0 >> 16), o1 = mma::e4m3x2_f16x2(y1 >> 16);
-#pragma unroll
-                            for (int t = 0; t < kMT; ++t) {
-                                mma::m16n8k16<true>(acc[t][4 * j + 2 * x], ap[t], e0, e1);
-                                mma::m16n8k16<true>(acc[t][4 * j + 2 * x + 1], ap[t], o0, o1);
-                            }
+                            mma::m16n8k16<true>(acc[4 * j + 2 * x], ap, e0, e1);
+                            mma::m16n8k16<true>(acc[4 * j + 2 * x + 1], ap, o0, o1);
                         }
                     }
                 }
             }
             __syncwarp();   // every lane has read the stage: it may be filled again
-            issue();
+            if (lead) issue();
+            else if (lane == 0) ptx::mbar_arrive(&empty[s]);
+        }
+        Walk next = cur;
+        next.left -= u1 - u0 - 1;
+        next.u = u1 - 1;
+        step<kUnit>(a, next);
+        if (next.left > 0) load_rows(next);
+
+        // The warps' partial results meet.  The buffers of references and
+        // sums alternate: a warp may be a request ahead of another's reading.
+        float* s_ref = sm.ref[parity];
+        float* s_sum = sm.sum[parity];
+        parity ^= 1;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float l = sum[half];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if (c == 0) {
+                s_ref[warp * 16 + half * 8 + g] = ref[half];
+                s_sum[warp * 16 + half * 8 + g] = l;
+            }
         }
         if (__syncthreads_or(!ok)) {
             ok = false;
             break;
         }
-
-        // The eight warps' partial results meet.
+        constexpr int kRowsAll = 16 * kRowTiles;   // rows of a group
 #pragma unroll
-        for (int t = 0; t < kMT; ++t)
+        for (int half = 0; half < 2; ++half) {
+            const int r = row_tile * 16 + half * 8 + g;
+            float top = s_ref[r];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float l = sum[t][half];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                if (c == 0) {
-                    sm.ref[warp][t * 16 + half * 8 + g] = ref[t][half];
-                    sm.sum[warp][t * 16 + half * 8 + g] = l;
+            for (int w = 1; w < kGroups; ++w) top = fmaxf(top, s_ref[w * kRowsAll + r]);
+            const float f = mma::exp2_approx(ref[half] - top);
+            float* m = sm.merge + (group * kRowsAll + r) * kHeadDim;
+            const int flip = (r & 3) << 3;
+#pragma unroll
+            for (int n = 0; n < 16; n += kE4m3 ? 2 : 1) {
+                const float* x = acc[n];
+                if (!kE4m3) {
+                    *reinterpret_cast<float2*>(m + ((8 * n + 2 * c) ^ flip)) = make_float2(x[2 * half] * f, x[2 * half + 1] * f);
+                } else {
+                    const float* y = acc[n + 1];
+                    *reinterpret_cast<float4*>(m + ((8 * n + 4 * c) ^ flip)) =
+                        make_float4(x[2 * half] * f, y[2 * half] * f, x[2 * half + 1] * f, y[2 * half + 1] * f);
                 }
             }
+        }
         __syncthreads();
         const bool whole = u0 == 0 && u1 == cur.units;
-        const bool at_start = cur.left == to - from;   // the CTA's first segment
         float* part = whole ? nullptr : slot_at(a.io.workspace, gridDim.x, 2 * blockIdx.x + (at_start ? 0 : 1));
         const float vscale = kE4m3 ? a.v_scale[h] : 1.f;
+        for (int i = tid; i < nrows * (kHeadDim / 4); i += kThreads) {
+            const int row = i / (kHeadDim / 4), col = i % (kHeadDim / 4) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            float top = kNoRef, l = 0.f;
 #pragma unroll
-        for (int t = 0; t < kMT; ++t)
-#pragma unroll
-            for (int cols = 0; cols < 2; ++cols) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int r = half * 8 + g;
-                    float top = sm.ref[0][t * 16 + r];
-#pragma unroll
-                    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.ref[w][t * 16 + r]);
-                    const float f = mma::exp2_approx(ref[t][half] - top);
-                    float* m = sm.merge + (warp * 16 + r) * kMergeCols;
-                    const int flip = (r & 3) << 3;
-#pragma unroll
-                    for (int n = 0; n < 8; n += kE4m3 ? 2 : 1) {
-                        const float* x = acc[t][cols * 8 + n];
-                        if (!kE4m3) {
-                            *reinterpret_cast<float2*>(m + ((8 * n + 2 * c) ^ flip)) = make_float2(x[2 * half] * f, x[2 * half + 1] * f);
-                        } else {
-                            const float* y = acc[t][cols * 8 + n + 1];
-                            *reinterpret_cast<float4*>(m + ((8 * n + 4 * c) ^ flip)) =
-                                make_float4(x[2 * half] * f, y[2 * half] * f, x[2 * half + 1] * f, y[2 * half + 1] * f);
-                        }
-                    }
-                }
-                __syncthreads();
-                {
-                    const int r = tid >> 4, q = (tid & 15) * 4, row = t * 16 + r;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float top = -INFINITY, l = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        const float4 x = *reinterpret_cast<const float4*>(sm.merge + (w * 16 + r) * kMergeCols + (q ^ ((r & 3) << 3)));
-                        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-                        top = fmaxf(top, sm.ref[w][row]);
-                    }
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) l += sm.sum[w][row] * mma::exp2_approx(sm.ref[w][row] - top);
-                    if (row < nrows) {
-                        const int col = cols * kMergeCols + q;
-                        if (whole) {
-                            const float n = l > 0.f ? vscale / l : 0.f;   // 0: the row sees no key
-                            const size_t at = head_of(row);
-                            mma::store4(a.io, at * kHeadDim + col, make_float4(v.x * n, v.y * n, v.z * n, v.w * n));
-                            if (a.io.lse && col == 0) a.io.lse[at] = (top + log2f(l)) / kLog2e;
-                        } else {
-                            *reinterpret_cast<float4*>(part + row * kHeadDim + col) = v;
-                            if (col == 0) {
-                                part[kMaxRows * kHeadDim + 2 * row] = top;
-                                part[kMaxRows * kHeadDim + 2 * row + 1] = l;
-                            }
-                        }
-                    }
-                }
-                __syncthreads();
+            for (int w = 0; w < kGroups; ++w) {
+                const float4 x = *reinterpret_cast<const float4*>(sm.merge + (w * kRowsAll + row) * kHeadDim + (col ^ ((row & 3) << 3)));
+                v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+                top = fmaxf(top, s_ref[w * kRowsAll + row]);
             }
+#pragma unroll
+            for (int w = 0; w < kGroups; ++w) l += s_sum[w * kRowsAll + row] * mma::exp2_approx(s_ref[w * kRowsAll + row] - top);
+            if (whole) {
+                const float n = l > 0.f ? vscale / l : 0.f;   // 0: the row sees no key
+                const size_t at = head_of(cur, rw, row);
+                mma::store4(a.io, at * kHeadDim + col, make_float4(v.x * n, v.y * n, v.z * n, v.w * n));
+                if (a.io.lse && col == 0) a.io.lse[at] = (top + log2f(l)) / kLog2e;
+            } else {
+                *reinterpret_cast<float4*>(part + row * kHeadDim + col) = v;
+                if (col == 0) {
+                    part[kMaxRows * kHeadDim + 2 * row] = top;
+                    part[kMaxRows * kHeadDim + 2 * row + 1] = l;
+                }
+            }
+        }
         // The CTA that holds the first part of a request that goes on says up to where.
         if (tid == 0 && u0 == 0 && u1 < cur.units) {
             const long long last = to - 1 + (cur.units - u1);   // its last unit
@@ -605,14 +649,12 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
             descs(a.io.workspace)[blockIdx.x] =
                 JoinDesc{cur.b, cur.vh, (int)(((last + 1) * ctas - 1) / total), slot, cur.tok0, cur.n};
         }
-        const int passed = u1 - u0;
-        cur.left -= passed - 1;
-        cur.u = u1 - 1;
-        step<kTile>(a, cur);
+        cur = next;
+        at_start = false;
     }
     if (!ok) {
         // Give-up path: the copies this warp issued complete (bounded waits) before its shared memory is released.
-        for (int i = used; i < issued; ++i) ptx::mbar_wait_timed(&sm.full[warp][i % kStages], (uint32_t)(i / kStages) & 1u);
+        for (int i = used; i < issued; ++i) ptx::mbar_wait_timed(&full[i % kDepth], (uint32_t)(i / kDepth) & 1u);
         __syncthreads();
     }
 }
@@ -675,9 +717,9 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
 
 std::atomic<bool> g_attr_done[64];
 
-template <bool kE4m3, int kMT>
+template <bool kE4m3, int kRowTiles>
 cudaError_t set_smem() {
-    return cudaFuncSetAttribute(kda_attn_decode_kernel<kE4m3, kMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(kda_attn_decode_kernel<kE4m3, kRowTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)sizeof(Smem));
 }
 
@@ -691,7 +733,8 @@ bool attn_decode_maps(const AttnLayer& l, AttnMaps& maps) {
 }
 
 size_t attn_decode_workspace_bytes(const DeviceInfo& dev) {
-    return desc_bytes(dev.sm_count) + (size_t)dev.sm_count * 2 * kSlotFloats * sizeof(float);
+    const int ctas = dev.sm_count * kCtasPerSm;
+    return desc_bytes(ctas) + (size_t)ctas * 2 * kSlotFloats * sizeof(float);
 }
 
 cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
@@ -720,9 +763,10 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
     // A call with a token per request has G rows at most; else any count up to 32 may occur.
     const int most_rows = io.cu_new && l.G < kMaxRows ? kMaxRows : a.rows;
     // Never more CTAs than the longest table allows units.
-    const int tile = kWarps * (l.e4m3 ? 32 : 16);
+    const int tile = (most_rows <= 16 ? kWarps : kWarps / 2) * (l.e4m3 ? 32 : 16);
     const long long most = (long long)io.B * l.Hkv * a.passes * ((((long long)io.max_pages << l.page_shift) + tile - 1) / tile);
-    const int grid = (int)(most < dev.sm_count ? most : dev.sm_count);
+    const int ctas = dev.sm_count * kCtasPerSm;
+    const int grid = (int)(most < ctas ? most : ctas);
     auto kernel = l.e4m3 ? (most_rows <= 16 ? kda_attn_decode_kernel<true, 1> : kda_attn_decode_kernel<true, 2>)
                          : (most_rows <= 16 ? kda_attn_decode_kernel<false, 1> : kda_attn_decode_kernel<false, 2>);
     kernel<<<grid, kThreads, sizeof(Smem), stream>>>(a, maps.k_decode, maps.v_decode, err_word);
