@@ -51,7 +51,7 @@ constexpr uint32_t kTileBytes = 4096;            // keys (or values) of one warp
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;   // whatever the number of warps to a tile
 constexpr uint32_t kMergeBytes = kWarps * 16 * kHeadDim * 4;
-constexpr int kPartCost = 1;
+constexpr int kJoinRows = 8;                     // CTAs of the join per part, over rows
 constexpr int kMaxRows = kAttnFewRows;           // rows of one pass
 
 struct Smem {
@@ -126,10 +126,10 @@ template <int kUnit>
 __device__ __forceinline__ int units_of(int len) { return (int)(((long long)len + kUnit - 1) / kUnit); }
 
 template <int kUnit>
-__device__ __forceinline__ long long cost_of(int len) { return len ? units_of<kUnit>(len) + kPartCost : 0; }
+__device__ __forceinline__ long long cost_of(int len, int part_cost) { return len ? units_of<kUnit>(len) + part_cost : 0; }
 
 // To the next unit (of the next request with any, at the end of one).
-template <int kUnit>
+template <int kUnit, int kPartCost>
 __device__ __forceinline__ void step(const DecodeArgs& a, Walk& w) {
     --w.left;
     if (++w.u < w.units) return;
@@ -155,6 +155,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     constexpr int kNT = kTile / 8;               // 8-key column tiles of the logits
     constexpr int kGroups = kWarps / kRowTiles;  // groups of warps that share a tile
     constexpr int kUnit = kGroups * kTile;       // keys of a unit
+    constexpr int kPartCost = kRowTiles;         // units that a request and head costs beside its own
     constexpr int kDepth = kStages * kRowTiles;  // stages of a group's ring
     constexpr float kOffset = kE4m3 ? 10.f : 0.f;
     constexpr float kLimit = kE4m3 ? 15.f : 8.f;
@@ -184,7 +185,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     const int per = (a.io.B + kThreads - 1) / kThreads;
     const int b0 = min(a.io.B, tid * per), b1 = min(a.io.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += cost_of<kUnit>(request(a, b).len);
+    for (int b = b0; b < b1; ++b) mine += cost_of<kUnit>(request(a, b).len, kPartCost);
     mine *= heads;
     long long upto = mine;
 #pragma unroll
@@ -206,7 +207,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     if (works && upto - mine <= from && from < upto) {
         long long at = upto - mine;
         for (int b = b0;; ++b) {
-            const long long n = cost_of<kUnit>(request(a, b).len) * heads;
+            const long long n = cost_of<kUnit>(request(a, b).len, kPartCost) * heads;
             if (from < at + n) {
                 sm.first_b = b;
                 sm.first_unit = from - at;
@@ -252,7 +253,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     Walk ahead = cur;
     int ids[kTile / 16];
     auto fetch_ids = [&]() {   // to the warp's next tile, if there is one
-        while (ahead.left > 0 && (ahead.u * kGroups + group) * kTile >= ahead.len) step<kUnit>(a, ahead);
+        while (ahead.left > 0 && (ahead.u * kGroups + group) * kTile >= ahead.len) step<kUnit, kPartCost>(a, ahead);
         if (ahead.left <= 0) return;
         const int key = (ahead.u * kGroups + group) * kTile;
         const int* t = a.io.block_table + (size_t)ahead.b * a.io.max_pages + (key >> a.page_shift);
@@ -291,7 +292,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
             return;
         }
         ++issued;
-        step<kUnit>(a, ahead);
+        step<kUnit, kPartCost>(a, ahead);
         fetch_ids();
     };
     if (lead) {
@@ -568,7 +569,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         Walk next = cur;
         next.left -= u1 - u0 - 1;
         next.u = u1 - 1;
-        step<kUnit>(a, next);
+        step<kUnit, kPartCost>(a, next);
         if (next.left > 0) load_rows(next);
 
         // The warps' partial results meet.  The buffers of references and
@@ -659,60 +660,66 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     }
 }
 
-// Joins the parts of a request and head that lie in several CTAs: one CTA per
-// part-holding CTA and query row, eight warps over the parts, four channels per lane.
+// Joins the parts of a request and head that lie in several CTAs: blockIdx.x
+// the CTA that holds the first part, blockIdx.y over query rows, eight warps
+// over the parts, four channels per lane.
 __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, int ctas) {
     __shared__ float4 s_acc[8][32];
     __shared__ float s_ref[8], s_sum[8];
+    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const JoinDesc d = descs(a.io.workspace)[blockIdx.x];
     if (d.b < 0) return;
-    const int h = d.vh / a.passes, pass = d.vh % a.passes;
-    const int row = blockIdx.y, row0 = pass * a.rows;
-    if (row >= (d.n > 1 ? d.n * a.G : min(a.rows, a.G - row0))) return;
+    const int h = d.vh / a.passes, row0 = d.vh % a.passes * a.rows;
+    const int rows = d.n > 1 ? d.n * a.G : min(a.rows, a.G - row0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = d.last - (int)blockIdx.x + 1;
-    float ref = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = warp; i < parts; i += 8) {
-        const float* p = slot_at(a.io.workspace, ctas, i == 0 ? d.slot : 2 * ((int)blockIdx.x + i));
-        const float r = p[kMaxRows * kHeadDim + 2 * row], l = p[kMaxRows * kHeadDim + 2 * row + 1];
-        const float4 v = *reinterpret_cast<const float4*>(p + row * kHeadDim + 4 * lane);
-        const float to = fmaxf(ref, r);
-        const float f = mma::exp2_approx(ref - to), e = mma::exp2_approx(r - to);
-        ref = to;
-        sum = sum * f + l * e;
-        acc.x = acc.x * f + v.x * e;
-        acc.y = acc.y * f + v.y * e;
-        acc.z = acc.z * f + v.z * e;
-        acc.w = acc.w * f + v.w * e;
-    }
-    s_acc[warp][lane] = acc;
-    if (lane == 0) {
-        s_ref[warp] = ref;
-        s_sum[warp] = sum;
-    }
-    __syncthreads();
-    if (warp) return;
-    float top = s_ref[0];
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        float ref = kNoRef, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = warp; i < parts; i += 8) {
+            const float* p = slot_at(a.io.workspace, ctas, i == 0 ? d.slot : 2 * ((int)blockIdx.x + i));
+            const float2 rl = *reinterpret_cast<const float2*>(p + kMaxRows * kHeadDim + 2 * row);
+            const float4 v = *reinterpret_cast<const float4*>(p + row * kHeadDim + 4 * lane);
+            const float to = fmaxf(ref, rl.x);
+            const float f = mma::exp2_approx(ref - to), e = mma::exp2_approx(rl.x - to);
+            ref = to;
+            sum = sum * f + rl.y * e;
+            acc.x = acc.x * f + v.x * e;
+            acc.y = acc.y * f + v.y * e;
+            acc.z = acc.z * f + v.z * e;
+            acc.w = acc.w * f + v.w * e;
+        }
+        s_acc[warp][lane] = acc;
+        if (lane == 0) {
+            s_ref[warp] = ref;
+            s_sum[warp] = sum;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            float top = s_ref[0];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) top = fmaxf(top, s_ref[w]);
-    sum = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 1; w < 8; ++w) top = fmaxf(top, s_ref[w]);
+            sum = 0.f;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        const float e = mma::exp2_approx(s_ref[w] - top);
-        const float4 v = s_acc[w][lane];
-        sum += s_sum[w] * e;
-        acc.x += v.x * e;
-        acc.y += v.y * e;
-        acc.z += v.z * e;
-        acc.w += v.w * e;
+            for (int w = 0; w < 8; ++w) {
+                const float e = mma::exp2_approx(s_ref[w] - top);
+                const float4 v = s_acc[w][lane];
+                sum += s_sum[w] * e;
+                acc.x += v.x * e;
+                acc.y += v.y * e;
+                acc.z += v.z * e;
+                acc.w += v.w * e;
+            }
+            const float n = sum > 0.f ? (a.v_scale ? a.v_scale[h] : 1.f) / sum : 0.f;
+            const size_t head = ((size_t)d.tok0 + (d.n > 1 ? row / a.G : 0)) * a.Hq + h * a.G + (d.n > 1 ? row % a.G : row0 + row);
+            mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
+            if (a.io.lse && lane == 0) a.io.lse[head] = sum > 0.f ? (top + log2f(sum)) / kLog2e : -INFINITY;
+        }
+        __syncthreads();
     }
-    const float n = sum > 0.f ? (a.v_scale ? a.v_scale[h] : 1.f) / sum : 0.f;
-    const size_t head = ((size_t)d.tok0 + (d.n > 1 ? row / a.G : 0)) * a.Hq + h * a.G + (d.n > 1 ? row % a.G : row0 + row);
-    mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
-    if (a.io.lse && lane == 0) a.io.lse[head] = (top + log2f(sum)) / kLog2e;
 }
 
 std::atomic<bool> g_attr_done[64];
@@ -774,7 +781,7 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)most_rows);
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(most_rows < kJoinRows ? most_rows : kJoinRows));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

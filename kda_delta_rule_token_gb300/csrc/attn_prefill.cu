@@ -227,7 +227,17 @@ __device__ __forceinline__ int scan_inclusive(int v, int* s_warp, int* total) {
 
 constexpr int kWarpMma = 8, kWarpTma = 9, kWarpConvert = 12;
 template <bool kE4m3>
-constexpr int threads_of() { return kE4m3 ? 512 : 320; }
+constexpr int threads_of() { return kE4m3 ? 512 : 384; }
+// Registers: the launch's share of each thread, and what the softmax
+// warpgroups (0, 1) and the other ones change to; the sum stays within the
+// launch's (checked against the compiled kernel before its first launch).
+template <bool kE4m3>
+constexpr int regs_launch() { return kE4m3 ? 128 : 168; }
+template <bool kE4m3>
+constexpr int regs_softmax() { return kE4m3 ? 176 : 208; }
+constexpr int kRegsOther = 80;
+static_assert(256 * regs_softmax<false>() + 128 * kRegsOther <= 384 * regs_launch<false>(), "registers");
+static_assert(256 * regs_softmax<true>() + 256 * kRegsOther <= 512 * regs_launch<true>(), "registers");
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(threads_of<kE4m3>(), 1)
@@ -292,10 +302,11 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     tc::fence_after();
     const uint32_t tm = ctl.tmem;
 
-    Part p;
-    int k = 0;
     if (warp == kWarpTma) {
         // ---- copies
+        tc::reg_dec<kRegsOther>();
+        Part p;
+        int k = 0;
         const int rows = min(1 << a.page_shift, kKeys), boxes = kKeys / rows;   // rows of a box, pages of a tile
         const int is_v = lane >> 4;
         const int pg = kE4m3 ? lane & 15 : (lane & 15) >> 1, block = kE4m3 ? 0 : lane & 1;
@@ -370,7 +381,10 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     copies_done:;
     } else if (warp == kWarpMma) {
         // ---- MMAs, one thread
+        tc::reg_dec<kRegsOther>();
         if (lane == 0) {
+            Part p;
+            int k = 0;
             constexpr uint32_t id_s = tc::idesc_f16kind(kRows, kKeys, !kE4m3, false);
             constexpr uint32_t id_o = tc::idesc_f16kind(kRows, kHeadDim, !kE4m3, true);
             const uint32_t base = ptx::smem_u32(sm);
@@ -431,6 +445,9 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         }
     } else if (kE4m3 && warp >= kWarpConvert) {
         // ---- e4m3 -> f16, one key per thread
+        tc::reg_dec<kRegsOther>();
+        Part p;
+        int k = 0;
         const int row = tid - 32 * kWarpConvert;
         int it = 0;
         bool ok = true;
@@ -468,6 +485,9 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             }
     } else if (warp < 8) {
         // ---- softmax, one thread per row of tile x
+        tc::reg_inc<regs_softmax<kE4m3>()>();
+        Part p;
+        int k = 0;
         const int x = warp >> 2, r = tid & (kRows - 1);
         const int i_row = r / a.G, g_row = r % a.G;
         const uint32_t ts = tc::taddr(tm, warp, kColS + 128 * x), to = tc::taddr(tm, warp, kColO + 128 * x);
@@ -547,14 +567,14 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                         sum *= f;
                         if (j > p.j0) {
                             // S_x(j) is complete, so P_x(j - 1) V is too: O_x is at rest.
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t o[32];
-                                tc::ld32(to + 32 * c, o);
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t o[16];
+                                tc::ld16(to + 16 * c, o);
                                 tc::wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tc::st32(to + 32 * c, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tc::st16(to + 16 * c, o);
                             }
                         }
                     }
@@ -623,6 +643,8 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                     PrefillJoin{p.s.tok, p.s.m, p.s.h, (int)(((last + 1) * sc.ctas - 1) / sc.units), p.slot, {0, 0, 0}};
             }
         }
+    } else {
+        tc::reg_dec<kRegsOther>();
     }
 
     tc::fence_before();
@@ -644,6 +666,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     }
     __syncthreads();
     if (warp == kWarpMma) tc::dealloc(tm, 512);
+    ptx::griddep_wait();   // ends after the few-row kernels launched before it
 }
 
 // Joins the parts of segments cut between CTAs: blockIdx.x the CTA that holds
@@ -684,6 +707,16 @@ __global__ void __launch_bounds__(256) kda_attn_prefill_join_kernel(const Prefil
 
 std::atomic<bool> g_attr_done[64];
 
+template <bool kE4m3>
+cudaError_t prepare_kernel() {
+    cudaFuncAttributes f{};
+    cudaError_t e = cudaFuncGetAttributes(&f, kda_attn_prefill_kernel<kE4m3>);
+    if (e != cudaSuccess) return e;
+    if (f.numRegs < regs_launch<kE4m3>()) return cudaErrorLaunchOutOfResources;   // the splits would never be met
+    return cudaFuncSetAttribute(kda_attn_prefill_kernel<kE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)smem_bytes<kE4m3>());
+}
+
 }  // namespace
 
 bool attn_prefill_maps(const AttnLayer& l, AttnMaps& maps) {
@@ -699,11 +732,8 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
                                   int* err_word, cudaStream_t stream) {
     if (dev.device < 0 || dev.device >= 64 || dev.sm_count > kMaxCtas) return cudaErrorInvalidDevice;
     if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(kda_attn_prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem_bytes<false>());
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kda_attn_prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)smem_bytes<true>());
+        cudaError_t e = prepare_kernel<false>();
+        if (e == cudaSuccess) e = prepare_kernel<true>();
         if (e != cudaSuccess) return e;
         g_attr_done[dev.device].store(true, std::memory_order_release);
     }
@@ -718,23 +748,27 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
     a.scale = l.softmax_scale * kLog2e;
     a.k_scale = l.k_scale;
     a.v_scale = l.v_scale;
-    const int grid = dev.sm_count;
-    if (l.e4m3)
-        kda_attn_prefill_kernel<true><<<grid, threads_of<true>(), smem_bytes<true>(), stream>>>(a, maps.k_prefill, maps.v_prefill, err_word);
-    else
-        kda_attn_prefill_kernel<false><<<grid, threads_of<false>(), smem_bytes<false>(), stream>>>(a, maps.k_prefill, maps.v_prefill, err_word);
-    count_launches(1);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, 16);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
+    // Both launches are programmatic: the first may start beside the few-row
+    // kernels launched before it (it shares nothing with them but their
+    // inputs, and waits for them before it ends), the join waits for the first.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    const int grid = dev.sm_count;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(l.e4m3 ? threads_of<true>() : threads_of<false>());
+    cfg.dynamicSmemBytes = l.e4m3 ? smem_bytes<true>() : smem_bytes<false>();
+    cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, l.e4m3 ? kda_attn_prefill_kernel<true> : kda_attn_prefill_kernel<false>,
+                                       a, maps.k_prefill, maps.v_prefill, err_word);
+    count_launches(1);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)grid, 16);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, kda_attn_prefill_join_kernel, a, grid);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
