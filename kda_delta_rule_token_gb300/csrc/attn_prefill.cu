@@ -34,6 +34,7 @@
 // range of (segment, key tile) units and leaves partial results, joined in a
 // fixed order by a dependent launch.
 #include <atomic>
+#include <type_traits>
 
 #include "attn_internal.cuh"
 #include "attn_mma.cuh"
@@ -57,7 +58,7 @@ constexpr uint32_t kColS = 0, kColO = 256;     // TMEM columns, + 128 X
 
 struct Ctl {
     uint64_t kfull[2], kempty[2], vfull[2], vempty[2], vraw;
-    uint64_t qfull[2], sfull[2], pfull[2], ofull[2];
+    uint64_t qfull[2], sfull[2], pfull[2][2], ofull[2];   // pfull: by tile and half of its keys
     uint64_t ckfull, ckempty, cvfull, cvempty;   // e4m3 staging
     uint64_t drain;
     uint32_t tmem;
@@ -197,7 +198,6 @@ __device__ __forceinline__ bool next_part(const PrefillArgs& a, const Ctl& ctl, 
 }
 
 __device__ __forceinline__ bool pwait(uint64_t* bar, uint32_t parity, int* dead, int* err) {
-    if (*(volatile int*)dead) return false;
     if (ptx::mbar_wait_timed(bar, parity, dead)) return true;
     *(volatile int*)dead = 1;
     atomicOr(err, ptx::kErrAttnWait);
@@ -259,7 +259,8 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             ptx::mbar_init(&ctl.vempty[i], 1);
             ptx::mbar_init(&ctl.qfull[i], kRows);
             ptx::mbar_init(&ctl.sfull[i], 1);
-            ptx::mbar_init(&ctl.pfull[i], kRows);
+            ptx::mbar_init(&ctl.pfull[i][0], kRows);
+            ptx::mbar_init(&ctl.pfull[i][1], kRows);
             ptx::mbar_init(&ctl.ofull[i], 1);
         }
         ptx::mbar_init(&ctl.vraw, 1);
@@ -300,7 +301,11 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tm = ctl.tmem;
+    constexpr uint32_t tm = 0;   // all 512 columns are this CTA's, so they start at 0
+    if (tid == 0 && ctl.tmem != tm) {
+        ctl.dead = 1;
+        atomicOr(err, ptx::kErrAttnWait);
+    }
 
     if (warp == kWarpTma) {
         // ---- copies
@@ -380,69 +385,96 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         }
     copies_done:;
     } else if (warp == kWarpMma) {
-        // ---- MMAs, one thread
+        // ---- MMAs.  The warp runs the loop together and one lane issues.
+        // The issuing lane shares its scheduler with two softmax warps, and
+        // operands that have to be moved to uniform registers first made it
+        // the slowest part of the loop (110 cycles per MMA, of which the
+        // pipe needs 64): the slots' code is therefore written out for both
+        // parities, with every operand a constant but the shared-memory base.
         tc::reg_dec<kRegsOther>();
-        if (lane == 0) {
-            Part p;
-            int k = 0;
-            constexpr uint32_t id_s = tc::idesc_f16kind(kRows, kKeys, !kE4m3, false);
-            constexpr uint32_t id_o = tc::idesc_f16kind(kRows, kHeadDim, !kE4m3, true);
-            const uint32_t base = ptx::smem_u32(sm);
-            const uint64_t dq = tc::desc_sw128(base + kOffQ), dk = tc::desc_sw128(base + kOffK);
-            const uint64_t dv = tc::desc_sw128_mn(base + kOffV, kBlock);
-            uint32_t qpar[2] = {0u, 0u}, ppar[2] = {0u, 0u};
-            int it = 0;
-            bool ok = true;
-            auto mma_s = [&](int x, int slot) {   // S_x = Q_x K^T
-                const uint64_t q = tc::desc_add(dq, x * kOperand), kk = tc::desc_add(dk, slot * kOperand);
+        Part p;
+        int k = 0;
+        constexpr uint32_t id_s = tc::idesc_f16kind(kRows, kKeys, !kE4m3, false);
+        constexpr uint32_t id_o = tc::idesc_f16kind(kRows, kHeadDim, !kE4m3, true);
+        const uint32_t base = ptx::smem_u32(sm);
+        const uint64_t dq = tc::desc_sw128(base + kOffQ), dk = tc::desc_sw128(base + kOffK);
+        const uint64_t dv = tc::desc_sw128_mn(base + kOffV, kBlock);
+        const bool issuer = tc::elect_one();
+        uint32_t qpar = 0u, ppar = 0u;   // bit x: tile x
+        int it = 0;
+        bool ok = true;
+        auto mma_s = [&](auto tile, auto slot) {   // S_x = Q_x K^T
+            constexpr int x = decltype(tile)::value, sl = decltype(slot)::value;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    tc::mma_ss_bf16(tm + kColS + 128 * x, tc::desc_add(q, (i >> 2) * kBlock + (i & 3) * 32),
-                                    tc::desc_add(kk, (i >> 2) * kBlock + (i & 3) * 32), id_s, i > 0);
+            for (int i = 0; i < 8; ++i)
+                tc::mma_ss_bf16(kColS + 128 * x, tc::desc_add(dq, x * kOperand + (i >> 2) * kBlock + (i & 3) * 32),
+                                tc::desc_add(dk, sl * kOperand + (i >> 2) * kBlock + (i & 3) * 32), id_s, i > 0);
+        };
+        auto first_s = [&](auto tile, auto slot) {
+            constexpr int x = decltype(tile)::value;
+            if (p.cnt[x] <= 0) return;
+            ok = ok && pwait(&ctl.qfull[x], (qpar >> x) & 1u, dead, err);
+            qpar ^= 1u << x;
+            tc::fence_after();
+            if (issuer && ok) {
+                mma_s(tile, slot);
                 tc::commit(&ctl.sfull[x]);
-            };
-            while (ok && next_part(a, ctl, sc, k, p)) {
-                ok = pwait(&ctl.kfull[it & 1], (uint32_t)(it >> 1) & 1u, dead, err);
-                for (int x = 0; x < 2 && ok; ++x)
-                    if (p.cnt[x] > 0) {
-                        ok = pwait(&ctl.qfull[x], qpar[x], dead, err);
-                        qpar[x] ^= 1u;
-                        tc::fence_after();
-                        if (ok) mma_s(x, it & 1);
-                    }
-                tc::commit(&ctl.kempty[it & 1]);
-                for (int j = 0; j < p.n && ok; ++j, ++it) {
-                    const int s = it & 1, next = (it + 1) & 1;
-                    const int last = j < p.cnt[1] ? 1 : 0;   // the last tile that uses V_j
-                    bool have_v = false, have_k = false;
-                    for (int x = 0; x < 2 && ok; ++x) {
-                        if (j >= p.cnt[x]) continue;
-                        ok = pwait(&ctl.pfull[x], ppar[x], dead, err);
-                        ppar[x] ^= 1u;
-                        if (ok && !have_v) ok = pwait(&ctl.vfull[s], (uint32_t)(it >> 1) & 1u, dead, err);
-                        have_v = true;
-                        tc::fence_after();
-                        if (!ok) break;
-                        const uint64_t v = tc::desc_add(dv, s * kOperand);
+            }
+        };
+        // O_x += P_x(j) V_j from this slot, S_x(j + 1) from the other one.
+        auto tile_step = [&](auto tile, auto slot, int j) {
+            constexpr int x = decltype(tile)::value, sl = decltype(slot)::value;
+            if (j >= p.cnt[x]) return;
+            const uint32_t par = (ppar >> x) & 1u;
+            ppar ^= 1u << x;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            tc::mma_ts_f16kind(tm + kColO + 128 * x, tm + kColS + 128 * x + 8 * i,
-                                               tc::desc_add(v, i * 2048), id_o, j > 0 || i > 0);
-                        if (x == last) tc::commit(&ctl.vempty[s]);
-                        if (j + 1 < p.cnt[x]) {
-                            if (!have_k) ok = pwait(&ctl.kfull[next], (uint32_t)((it + 1) >> 1) & 1u, dead, err);
-                            have_k = true;
-                            tc::fence_after();
-                            if (ok) mma_s(x, next);
-                        } else {
-                            tc::commit(&ctl.ofull[x]);
-                        }
-                    }
-                    if (have_k) tc::commit(&ctl.kempty[next]);
+            for (int half = 0; half < 2; ++half) {
+                ok = ok && pwait(&ctl.pfull[x][half], par, dead, err);
+                tc::fence_after();
+                if (issuer && ok) {
+#pragma unroll
+                    for (int i = 4 * half; i < 4 * half + 4; ++i)
+                        tc::mma_ts_f16kind(kColO + 128 * x, kColS + 128 * x + 8 * i,
+                                           tc::desc_add(dv, sl * kOperand + i * 2048), id_o, i > 0 ? 1u : (uint32_t)(j > 0));
                 }
             }
-            tc::commit(&ctl.drain);
+            if (issuer && ok) {
+                if (x == 1 || j >= p.cnt[1]) tc::commit(&ctl.vempty[sl]);
+                if (j + 1 < p.cnt[x]) {
+                    mma_s(tile, std::integral_constant<int, 1 - sl>());
+                    tc::commit(&ctl.sfull[x]);
+                } else {
+                    tc::commit(&ctl.ofull[x]);
+                }
+            }
+        };
+        auto both = [&](auto slot, int j) {
+            constexpr int sl = decltype(slot)::value;
+            // Normally there already: waited for while the pipe works on S_1(j).
+            ok = ok && pwait(&ctl.vfull[sl], (uint32_t)(it >> 1) & 1u, dead, err);
+            if (j + 1 < p.n) ok = ok && pwait(&ctl.kfull[1 - sl], (uint32_t)((it + 1) >> 1) & 1u, dead, err);
+            tile_step(std::integral_constant<int, 0>(), slot, j);
+            tile_step(std::integral_constant<int, 1>(), slot, j);
+            if (j + 1 < p.n && issuer && ok) tc::commit(&ctl.kempty[1 - sl]);
+        };
+        using Slot0 = std::integral_constant<int, 0>;
+        using Slot1 = std::integral_constant<int, 1>;
+        while (ok && next_part(a, ctl, sc, k, p)) {
+            ok = pwait(&ctl.kfull[it & 1], (uint32_t)(it >> 1) & 1u, dead, err);
+            if (it & 1) {
+                first_s(Slot0(), Slot1());
+                first_s(Slot1(), Slot1());
+            } else {
+                first_s(Slot0(), Slot0());
+                first_s(Slot1(), Slot0());
+            }
+            if (issuer && ok) tc::commit(&ctl.kempty[it & 1]);
+            for (int j = 0; j < p.n && ok; ++j, ++it) {
+                if (it & 1) both(Slot1(), j);
+                else both(Slot0(), j);
+            }
         }
+        if (issuer) tc::commit(&ctl.drain);   // completes once every MMA that it issued has
     } else if (kE4m3 && warp >= kWarpConvert) {
         // ---- e4m3 -> f16, one key per thread
         tc::reg_dec<kRegsOther>();
@@ -593,10 +625,12 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                             pk[e] = kE4m3 ? mma::pack_f16(u, v) : mma::pack_bf16(u, v);
                         }
                         tc::st16(ts + 16 * c, pk);
+                        if (c & 1) {
+                            tc::wait_st();
+                            tc::fence_before();
+                            ptx::mbar_arrive(&ctl.pfull[x][c >> 1]);
+                        }
                     }
-                    tc::wait_st();
-                    tc::fence_before();
-                    ptx::mbar_arrive(&ctl.pfull[x]);
                     float u, v;
                     mma::upk(mma::add2(sum2[0], sum2[1]), u, v);
                     sum += u + v;
