@@ -50,39 +50,13 @@ constexpr int kKeys = 128;                     // keys of a tile
 constexpr uint32_t kOperand = 32768;           // a 128 x 128 16-bit operand
 constexpr uint32_t kBlock = 16384;             // one 64-channel block of it
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffStage = 6 * kOperand;
-constexpr int kScan = 256;                     // threads of the prefix sums
+constexpr int kScan = 128;                     // threads of the prefix sums
 constexpr int kMaxCtas = 256;
-constexpr int kSplitGain = 6;                  // key tiles that splitting has to save on the longest segment
+constexpr int kPartCost = 2;                   // key tiles that starting and ending a segment costs beside its own
+constexpr int kSplitGain = 4;                  // key tiles that cutting has to save on the busiest CTA
+constexpr int kMostWeighed = 32;               // segments per CTA up to which their load is worked out
 
 constexpr uint32_t kColS = 0, kColO = 256;     // TMEM columns, + 128 X
-
-struct Ctl {
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], vraw;
-    uint64_t qfull[2], sfull[2], pfull[2][2], ofull[2];   // pfull: by tile and half of its keys
-    uint64_t ckfull, ckempty, cvfull, cvempty;   // e4m3 staging
-    uint64_t drain;
-    uint32_t tmem;
-    int dead;
-    int longest;
-    int kissued, vissued;
-    int warp_sum[8];
-    int pre[kScan];          // tiles of tokens before the requests of scan thread t
-    int seg_pre[kMaxCtas];   // split: units before segment s
-};
-
-template <bool kE4m3>
-constexpr uint32_t smem_bytes() { return kOffStage + (kE4m3 ? 2 * kBlock : 0) + (uint32_t)sizeof(Ctl); }
-static_assert(kOffStage + 2 * kBlock + sizeof(Ctl) <= 232448, "shared memory");
-
-struct PrefillArgs {
-    AttnIO io;
-    int Hq, Hkv, G;
-    int tokens;              // of a tile: 128 / G
-    int page_shift, num_pages;
-    float scale;             // softmax scale * log2(e)
-    const float* k_scale;
-    const float* v_scale;
-};
 
 // Up to 2 * tokens consecutive new tokens of one request with one key head.
 struct Segment {
@@ -103,17 +77,49 @@ struct Segment {
 // What a CTA does next: key tiles [j0, j0 + n) of a segment, cnt[x] of them for tile x.
 struct Part {
     Segment s;
-    int j0, n, cnt[2];
-    bool whole, first;       // the whole segment; the segment's first key tile is in it
-    int slot;                // of the partial result, if not whole
+    int j0, n, cnt[2];       // n == 0: no more parts
+    int slot;                // of the partial result, -1 if the part is the whole segment
+    int last;                // the segment's first part, if it goes on: up to this CTA; else -1
+};
+
+struct Ctl {
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], vraw;
+    uint64_t qfull[2], sfull[2], pfull[2][2], ofull[2];   // pfull: by tile and half of its keys
+    uint64_t ckfull, ckempty, cvfull, cvempty;            // e4m3 staging
+    uint64_t partfull[2], partempty[2];
+    uint64_t drain;
+    Part part[2];            // from the copying warp to the others
+    uint32_t tmem;
+    int dead;
+    int busiest;
+    int kissued, vissued;
+    int warp_sum[kScan / 32];
+    int pre[kScan];          // pairs of token tiles before the requests of scan thread t
+    int units[kScan];        // key tiles and costs before the segments of scan thread t
+    int load[kMaxCtas];      // of each CTA, were the segments dealt whole
+};
+
+template <bool kE4m3>
+constexpr uint32_t smem_bytes() { return kOffStage + (kE4m3 ? 2 * kBlock : 0) + (uint32_t)sizeof(Ctl); }
+static_assert(kOffStage + 2 * kBlock + sizeof(Ctl) <= 232448, "shared memory");
+
+struct PrefillArgs {
+    AttnIO io;
+    int Hq, Hkv, G;
+    int tokens;              // of a tile: 128 / G
+    int page_shift, num_pages;
+    float scale;             // softmax scale * log2(e)
+    const float* k_scale;
+    const float* v_scale;
 };
 
 struct Sched {
-    int total;               // token tiles (pairs) of all requests
+    int total;               // pairs of token tiles of all requests
     int per;                 // requests of a scan thread
     long long segments;
+    int chunk;               // segments of a scan thread
     bool split;
-    int units, ctas;         // split: key tiles of all segments, CTAs that share them
+    int units, ctas;         // split: key tiles and costs of all segments, CTAs that share them
 };
 
 struct PrefillJoin {
@@ -160,41 +166,62 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
     return g;
 }
 
-// The k-th part of this CTA; false past the last.
-__device__ __forceinline__ bool next_part(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, int& k, Part& p) {
+// Where a CTA is in its work (the copying warp's).
+struct Cursor {
+    long long k;             // whole segments: rounds dealt; cut: the next segment, -1 before the first
+    int at;                  // cut: units before segment k
+    bool begun;              // cut: a part was found
+};
+
+// The next part of this CTA; p.n = 0 past the last.
+__device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, Cursor& c, Part& p) {
+    p.n = 0;
     if (!sc.split) {
-        for (;; ++k) {
-            const long long base = (long long)k * gridDim.x;
-            if (base >= sc.segments) return false;
-            const long long s = base + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        for (;; ++c.k) {
+            const long long base = c.k * gridDim.x;
+            if (base >= sc.segments) return;
+            const long long s = base + ((c.k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             if (s >= sc.segments) continue;
             p.s = find_segment(a, ctl, sc, s);
             break;
         }
-        ++k;
+        ++c.k;
         p.j0 = 0;
         p.n = p.s.tiles_all(a.tokens);
         p.cnt[0] = p.s.tiles(0, a.tokens);
         p.cnt[1] = p.s.tiles(1, a.tokens);
-        p.whole = p.first = true;
-        return true;
+        p.slot = p.last = -1;
+        return;
     }
-    if ((int)blockIdx.x >= sc.ctas) return false;
+    if ((int)blockIdx.x >= sc.ctas) return;
     const int from = (int)((long long)sc.units * blockIdx.x / sc.ctas), to = (int)((long long)sc.units * (blockIdx.x + 1) / sc.ctas);
-    int s = k;
-    if (k == 0)
-        while (s + 1 < sc.segments && ctl.seg_pre[s + 1] <= from) ++s;
-    if (s >= sc.segments || ctl.seg_pre[s] >= to) return false;
-    p.s = find_segment(a, ctl, sc, s);
-    const int all = p.s.tiles_all(a.tokens), at = ctl.seg_pre[s];
-    p.j0 = max(from - at, 0);
-    p.n = min(to - at, all) - p.j0;
-    for (int x = 0; x < 2; ++x) p.cnt[x] = min(max(p.s.tiles(x, a.tokens) - p.j0, 0), p.n);
-    p.whole = p.n == all;
-    p.first = p.j0 == 0;
-    p.slot = 2 * (int)blockIdx.x + (at <= from ? 0 : 1);
-    k = s + 1;
-    return true;
+    if (c.k < 0) {
+        int lo = 0, hi = kScan - 1;   // the last scan thread whose segments begin at or before `from`
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (ctl.units[mid] <= from) lo = mid; else hi = mid - 1;
+        }
+        c.k = (long long)lo * sc.chunk;
+        c.at = ctl.units[lo];
+    }
+    while (c.k < sc.segments && c.at < to) {
+        p.s = find_segment(a, ctl, sc, c.k);
+        const int tiles = p.s.tiles_all(a.tokens), at = c.at;
+        ++c.k;
+        c.at += tiles + kPartCost;
+        // A segment's first kPartCost units stand for its cost, the others for its tiles.
+        const int j0 = max(from - at - kPartCost, 0), j1 = min(to - at - kPartCost, tiles);
+        if (j1 <= j0) continue;
+        p.j0 = j0;
+        p.n = j1 - j0;
+        for (int x = 0; x < 2; ++x) p.cnt[x] = min(max(p.s.tiles(x, a.tokens) - j0, 0), p.n);
+        const bool whole = p.n == tiles;
+        p.slot = whole ? -1 : 2 * (int)blockIdx.x + (c.begun ? 1 : 0);
+        // The CTA whose range [units i / ctas, units (i + 1) / ctas) holds the segment's last unit.
+        p.last = whole || j0 > 0 ? -1 : (int)(((long long)c.at * sc.ctas - 1) / sc.units);
+        c.begun = true;
+        return;
+    }
 }
 
 __device__ __forceinline__ bool pwait(uint64_t* bar, uint32_t parity, int* dead, int* err) {
@@ -204,7 +231,17 @@ __device__ __forceinline__ bool pwait(uint64_t* bar, uint32_t parity, int* dead,
     return false;
 }
 
-// Inclusive prefix of v over the first kScan threads; all of them call it.
+// The next part, as the copying warp found it; false past the last (or if the CTA gave up).
+__device__ __forceinline__ bool take_part(Ctl& ctl, int& np, Part& p, int* dead, int* err) {
+    if (!__all_sync(0xffffffffu, pwait(&ctl.partfull[np & 1], (uint32_t)(np >> 1) & 1u, dead, err))) return false;
+    p = ctl.part[np & 1];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&ctl.partempty[np & 1]);
+    ++np;
+    return p.n > 0;
+}
+
+// Inclusive prefix of v over the first kScan threads; all threads of the CTA call it.
 __device__ __forceinline__ int scan_inclusive(int v, int* s_warp, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -212,11 +249,11 @@ __device__ __forceinline__ int scan_inclusive(int v, int* s_warp, int* total) {
         const int y = __shfl_up_sync(0xffffffffu, v, d);
         if (lane >= d) v += y;
     }
-    if (lane == 31 && warp < 8) s_warp[warp] = v;
+    if (lane == 31 && warp < kScan / 32) s_warp[warp] = v;
     __syncthreads();
     int all = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < kScan / 32; ++w) {
         if (w < warp) v += s_warp[w];
         all += s_warp[w];
     }
@@ -262,6 +299,8 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             ptx::mbar_init(&ctl.pfull[i][0], kRows);
             ptx::mbar_init(&ctl.pfull[i][1], kRows);
             ptx::mbar_init(&ctl.ofull[i], 1);
+            ptx::mbar_init(&ctl.partfull[i], 1);
+            ptx::mbar_init(&ctl.partempty[i], kE4m3 ? 13 : 9);   // warps that take parts
         }
         ptx::mbar_init(&ctl.vraw, 1);
         ptx::mbar_init(&ctl.ckfull, 1);
@@ -271,7 +310,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         ptx::mbar_init(&ctl.drain, 1);
         ptx::fence_mbar_init();
         ctl.dead = 0;
-        ctl.longest = 0;
+        ctl.busiest = 0;
         ctl.kissued = ctl.vissued = 0;
         joins(a.io.workspace)[blockIdx.x].m = 0;
     }
@@ -288,15 +327,29 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     __syncthreads();
     sc.segments = (long long)sc.total * a.Hkv;
     sc.split = false;
-    sc.units = sc.ctas = 0;
-    if (sc.segments < gridDim.x && sc.segments > 0) {   // and so at most kScan - 1
-        int n = 0;
-        if (tid < sc.segments) n = find_segment(a, ctl, sc, tid).tiles_all(a.tokens);
-        if (n) atomicMax(&ctl.longest, n);
-        const int u = scan_inclusive(n, ctl.warp_sum, &sc.units);
-        if (tid < sc.segments) ctl.seg_pre[tid] = u - n;
+    sc.units = sc.ctas = sc.chunk = 0;
+    if (sc.segments > 0 && sc.segments <= (long long)kMostWeighed * gridDim.x) {
+        // The load of every CTA if whole segments are dealt, against equal shares of key tiles.
+        for (int i = tid; i < kMaxCtas; i += blockDim.x) ctl.load[i] = 0;
+        __syncthreads();
+        const int n = (int)sc.segments;
+        sc.chunk = (n + kScan - 1) / kScan;
+        long long sum = 0;
+        if (tid < kScan)
+            for (int s = tid * sc.chunk, end = min(n, s + sc.chunk), u = -1; s < end; ++s) {
+                if (u < 0 || s % a.Hkv == 0)   // the heads of a pair of token tiles are alike
+                    u = find_segment(a, ctl, sc, s).tiles_all(a.tokens) + kPartCost;
+                sum += u;
+                const int round = s / (int)gridDim.x, r = s % (int)gridDim.x;
+                atomicAdd(&ctl.load[(round & 1) ? gridDim.x - 1 - r : r], u);
+            }
+        const int u = (int)min(sum, (long long)(0x7fffffff / kScan));   // beyond that, shares are not worth cutting for
+        const int to = scan_inclusive(u, ctl.warp_sum, &sc.units);
+        if (tid < kScan) ctl.units[tid] = to - u;
+        for (int i = tid; i < (int)gridDim.x; i += blockDim.x) atomicMax(&ctl.busiest, ctl.load[i]);
+        const bool fits = !__syncthreads_or(tid < kScan && (long long)u != sum);
         sc.ctas = min((int)gridDim.x, sc.units);
-        sc.split = ctl.longest > (sc.units + sc.ctas - 1) / sc.ctas + kSplitGain;
+        sc.split = fits && ctl.busiest > (sc.units + sc.ctas - 1) / sc.ctas + kSplitGain;
     }
     tc::fence_before();
     __syncthreads();
@@ -311,12 +364,20 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         // ---- copies
         tc::reg_dec<kRegsOther>();
         Part p;
-        int k = 0;
+        Cursor cur{sc.split ? -1 : 0, 0, false};
         const int rows = min(1 << a.page_shift, kKeys), boxes = kKeys / rows;   // rows of a box, pages of a tile
         const int is_v = lane >> 4;
         const int pg = kE4m3 ? lane & 15 : (lane & 15) >> 1, block = kE4m3 ? 0 : lane & 1;
         int it = 0, raws = 0;
-        while (next_part(a, ctl, sc, k, p)) {
+        for (int np = 0;; ++np) {
+            next_part(a, ctl, sc, cur, p);
+            if (np >= 2 && !__all_sync(0xffffffffu, pwait(&ctl.partempty[np & 1], (uint32_t)((np >> 1) - 1) & 1u, dead, err)))
+                break;
+            if (lane == 0) {
+                ctl.part[np & 1] = p;
+                ptx::mbar_arrive(&ctl.partfull[np & 1]);
+            }
+            if (p.n == 0) break;
             const int* table = a.io.block_table + (size_t)p.s.b * a.io.max_pages;
             auto page_of = [&](int j) {
                 const int key = j * kKeys + pg * rows;
@@ -385,105 +446,119 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         }
     copies_done:;
     } else if (warp == kWarpMma) {
-        // ---- MMAs.  The warp runs the loop together and one lane issues.
-        // The issuing lane shares its scheduler with two softmax warps, and
-        // operands that have to be moved to uniform registers first made it
-        // the slowest part of the loop (110 cycles per MMA, of which the
-        // pipe needs 64): the slots' code is therefore written out for both
-        // parities, with every operand a constant but the shared-memory base.
+        // ---- MMAs, issued by one thread.  The pipe holds about two MMAs
+        // beyond the one it works on (some 130 cycles), while a wait on a
+        // barrier that is long complete takes as much, and operands that
+        // have to be moved to uniform registers nearly as much per MMA.  So
+        // the loop is written out for both slots, with every operand a
+        // constant but the shared-memory base, and each barrier is tested
+        // before the batch of MMAs that precedes its use: only one that was
+        // not complete by then is waited for.
         tc::reg_dec<kRegsOther>();
         Part p;
-        int k = 0;
+        int np = 0;
         constexpr uint32_t id_s = tc::idesc_f16kind(kRows, kKeys, !kE4m3, false);
         constexpr uint32_t id_o = tc::idesc_f16kind(kRows, kHeadDim, !kE4m3, true);
         const uint32_t base = ptx::smem_u32(sm);
         const uint64_t dq = tc::desc_sw128(base + kOffQ), dk = tc::desc_sw128(base + kOffK);
         const uint64_t dv = tc::desc_sw128_mn(base + kOffV, kBlock);
-        const bool issuer = tc::elect_one();
         uint32_t qpar = 0u, ppar = 0u;   // bit x: tile x
         int it = 0;
         bool ok = true;
+        // A barrier's phase: tested now, waited for where it is needed.
+        struct Test {
+            bool done;
+            uint64_t* bar;
+            uint32_t par;
+        };
+        auto test = [&](uint64_t* bar, uint32_t par) { return Test{ptx::mbar_test(bar, par), bar, par}; };
+        auto need = [&](const Test& t) {
+            if (!t.done) ok = ok && pwait(t.bar, t.par, dead, err);
+            tc::fence_after();
+        };
         auto mma_s = [&](auto tile, auto slot) {   // S_x = Q_x K^T
             constexpr int x = decltype(tile)::value, sl = decltype(slot)::value;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 tc::mma_ss_bf16(kColS + 128 * x, tc::desc_add(dq, x * kOperand + (i >> 2) * kBlock + (i & 3) * 32),
                                 tc::desc_add(dk, sl * kOperand + (i >> 2) * kBlock + (i & 3) * 32), id_s, i > 0);
+            tc::commit(&ctl.sfull[x]);
         };
         auto first_s = [&](auto tile, auto slot) {
             constexpr int x = decltype(tile)::value;
             if (p.cnt[x] <= 0) return;
-            ok = ok && pwait(&ctl.qfull[x], (qpar >> x) & 1u, dead, err);
+            need(test(&ctl.qfull[x], (qpar >> x) & 1u));
             qpar ^= 1u << x;
-            tc::fence_after();
-            if (issuer && ok) {
-                mma_s(tile, slot);
-                tc::commit(&ctl.sfull[x]);
-            }
+            if (ok) mma_s(tile, slot);
         };
+        auto p_test = [&](int x, int half) { return test(&ctl.pfull[x][half], (ppar >> x) & 1u); };
         // O_x += P_x(j) V_j from this slot, S_x(j + 1) from the other one.
-        auto tile_step = [&](auto tile, auto slot, int j) {
+        // `mine`: the test of P_x(j)'s first half; returns that of the tile after this one.
+        auto tile_step = [&](auto tile, auto slot, int j, const Test& mine) -> Test {
             constexpr int x = decltype(tile)::value, sl = decltype(slot)::value;
-            if (j >= p.cnt[x]) return;
-            const uint32_t par = (ppar >> x) & 1u;
+            const bool more = j + 1 < p.cnt[x];
+            const bool last = x == 1 || j >= p.cnt[1];          // the last tile that uses V_j
+            const bool firstk = x == 0 || j >= p.cnt[0];        // the first that uses K_(j + 1)
+            const uint32_t npar = (uint32_t)((it + 1) >> 1) & 1u;
+            const Test upper = p_test(x, 1);
+            need(mine);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i == 4) need(upper);
+                if (ok)
+                    tc::mma_ts_f16kind(kColO + 128 * x, kColS + 128 * x + 8 * i,
+                                       tc::desc_add(dv, sl * kOperand + i * 2048), id_o, i > 0 ? 1u : (uint32_t)(j > 0));
+            }
             ppar ^= 1u << x;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                ok = ok && pwait(&ctl.pfull[x][half], par, dead, err);
-                tc::fence_after();
-                if (issuer && ok) {
-#pragma unroll
-                    for (int i = 4 * half; i < 4 * half + 4; ++i)
-                        tc::mma_ts_f16kind(kColO + 128 * x, kColS + 128 * x + 8 * i,
-                                           tc::desc_add(dv, sl * kOperand + i * 2048), id_o, i > 0 ? 1u : (uint32_t)(j > 0));
-                }
+            if (ok && last) tc::commit(&ctl.vempty[sl]);
+            if (j + 1 < p.n) {
+                if (firstk) need(test(&ctl.kfull[1 - sl], npar));
+                if (last) need(test(&ctl.vfull[1 - sl], npar));
             }
-            if (issuer && ok) {
-                if (x == 1 || j >= p.cnt[1]) tc::commit(&ctl.vempty[sl]);
-                if (j + 1 < p.cnt[x]) {
-                    mma_s(tile, std::integral_constant<int, 1 - sl>());
-                    tc::commit(&ctl.sfull[x]);
-                } else {
-                    tc::commit(&ctl.ofull[x]);
-                }
-            }
+            // The tile after this one: the other one of this j, or the first one of the next.
+            const int nx = x == 0 && j < p.cnt[1] ? 1 : j + 1 < p.cnt[0] ? 0 : 1;
+            const Test next = p_test(nx, 0);
+            if (ok && more) mma_s(tile, std::integral_constant<int, 1 - sl>());
+            if (ok && !more) tc::commit(&ctl.ofull[x]);
+            return next;
         };
-        auto both = [&](auto slot, int j) {
+        using Zero = std::integral_constant<int, 0>;
+        using One = std::integral_constant<int, 1>;
+        auto both = [&](auto slot, int j, Test t) {
             constexpr int sl = decltype(slot)::value;
-            // Normally there already: waited for while the pipe works on S_1(j).
-            ok = ok && pwait(&ctl.vfull[sl], (uint32_t)(it >> 1) & 1u, dead, err);
-            if (j + 1 < p.n) ok = ok && pwait(&ctl.kfull[1 - sl], (uint32_t)((it + 1) >> 1) & 1u, dead, err);
-            tile_step(std::integral_constant<int, 0>(), slot, j);
-            tile_step(std::integral_constant<int, 1>(), slot, j);
-            if (j + 1 < p.n && issuer && ok) tc::commit(&ctl.kempty[1 - sl]);
+            if (j < p.cnt[0]) t = tile_step(Zero(), slot, j, t);
+            if (j < p.cnt[1]) t = tile_step(One(), slot, j, t);
+            if (j + 1 < p.n && ok) tc::commit(&ctl.kempty[1 - sl]);
+            return t;
         };
-        using Slot0 = std::integral_constant<int, 0>;
-        using Slot1 = std::integral_constant<int, 1>;
-        while (ok && next_part(a, ctl, sc, k, p)) {
-            ok = pwait(&ctl.kfull[it & 1], (uint32_t)(it >> 1) & 1u, dead, err);
-            if (it & 1) {
-                first_s(Slot0(), Slot1());
-                first_s(Slot1(), Slot1());
-            } else {
-                first_s(Slot0(), Slot0());
-                first_s(Slot1(), Slot0());
+        const bool issuer = tc::elect_one();
+        while (take_part(ctl, np, p, dead, err)) {
+            if (issuer && ok) {
+                need(test(&ctl.kfull[it & 1], (uint32_t)(it >> 1) & 1u));
+                if (it & 1) {
+                    first_s(Zero(), One());
+                    first_s(One(), One());
+                } else {
+                    first_s(Zero(), Zero());
+                    first_s(One(), Zero());
+                }
+                if (ok) tc::commit(&ctl.kempty[it & 1]);
+                need(test(&ctl.vfull[it & 1], (uint32_t)(it >> 1) & 1u));
+                Test t = p_test(p.cnt[0] > 0 ? 0 : 1, 0);
+                for (int j = 0; j < p.n && ok; ++j, ++it) t = (it & 1) ? both(One(), j, t) : both(Zero(), j, t);
             }
-            if (issuer && ok) tc::commit(&ctl.kempty[it & 1]);
-            for (int j = 0; j < p.n && ok; ++j, ++it) {
-                if (it & 1) both(Slot1(), j);
-                else both(Slot0(), j);
-            }
+            __syncwarp();
         }
         if (issuer) tc::commit(&ctl.drain);   // completes once every MMA that it issued has
     } else if (kE4m3 && warp >= kWarpConvert) {
         // ---- e4m3 -> f16, one key per thread
         tc::reg_dec<kRegsOther>();
         Part p;
-        int k = 0;
+        int np = 0;
         const int row = tid - 32 * kWarpConvert;
         int it = 0;
         bool ok = true;
-        while (ok && next_part(a, ctl, sc, k, p))
+        while (ok && take_part(ctl, np, p, dead, err))
             for (int j = p.j0; j < p.j0 + p.n && ok; ++j, ++it) {
                 const int s = it & 1;
                 const uint32_t par = (uint32_t)((it >> 1) - 1) & 1u;
@@ -519,47 +594,65 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         // ---- softmax, one thread per row of tile x
         tc::reg_inc<regs_softmax<kE4m3>()>();
         Part p;
-        int k = 0;
+        int np = 0;
         const int x = warp >> 2, r = tid & (kRows - 1);
         const int i_row = r / a.G, g_row = r % a.G;
         const uint32_t ts = tc::taddr(tm, warp, kColS + 128 * x), to = tc::taddr(tm, warp, kColO + 128 * x);
         uint32_t spar = 0u, opar = 0u;
         bool ok = true;
-        while (ok && next_part(a, ctl, sc, k, p)) {
+        const int chunk = lane & 15;                       // 16 bytes of a row, as rows are copied two at a time
+        uint8_t* rows_x = sm + kOffQ + x * kOperand + (warp & 3) * 32 * 128;   // the warp's rows: two blocks of 128 bytes each
+        auto place = [&](int row, int c) { return rows_x + (c >> 3) * kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
+        while (ok && take_part(ctl, np, p, dead, err)) {
             const int tokens = p.s.tokens_of(x, a.tokens);
             const int tok = p.s.tok + x * a.tokens + i_row;
             const bool live = i_row < tokens;
             const size_t head = (size_t)tok * a.Hq + p.s.h * a.G + g_row;
+            // The head of the row that this lane copies in round i, and whether it has a token.
+            auto head_of = [&](int i) { return (size_t)__shfl_sync(0xffffffffu, (unsigned long long)head, 2 * i + (lane >> 4)); };
+            const uint32_t lives = __ballot_sync(0xffffffffu, live);
             float ref = kNoRef, sum = 0.f;
             const int cnt = p.cnt[x];
             if (cnt > 0) {
-                // Q row into shared memory (swizzled as TMA would).
+                // Q rows into shared memory (swizzled as TMA would), two per
+                // round.  The loops that run once per part stay rolled: their
+                // instructions come from L2 each time.
                 float fac = a.scale;
-                uint32_t w[64];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (live) v = *reinterpret_cast<const uint4*>(a.io.q + head * kHeadDim + 8 * c);
-                    w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+#pragma unroll 2
+                for (int i = 0; i < 16; ++i) {
+                    const int row = 2 * i + (lane >> 4);
+                    const size_t h = head_of(i);
+                    ptx::cp_async16(place(row, chunk), a.io.q + h * kHeadDim + 8 * chunk, lives >> row & 1u);
                 }
+                ptx::cp_async_commit();
+                ptx::cp_async_wait_all();
+                __syncwarp();
                 if (kE4m3) {
+                    // To f16, each lane its row: q * 2^(14 - e) with 2^e <= the row's
+                    // largest < 2^(e+1), exact down to 2^-28 of it.
                     float top = 0.f;
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(place(lane, c));
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[c] << 16)), fabsf(__uint_as_float(w[c] & 0xffff0000u))));
-                    // q * 2^(14 - e) with 2^e <= top < 2^(e+1): exact in f16 down to 2^-28 of the row's largest.
-                    const int e = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
-                    const float up = exp2f((float)(14 - e));
-                    fac = a.scale * a.k_scale[p.s.h] * exp2f((float)(e - 14));
+                        for (int e = 0; e < 4; ++e)
+                            top = mma::max3(top, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
+                    }
+                    const int ex = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
+                    const float up = exp2f((float)(14 - ex));
+                    fac = a.scale * a.k_scale[p.s.h] * exp2f((float)(ex - 14));
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c) {
+                        uint4* at = reinterpret_cast<uint4*>(place(lane, c));
+                        const uint4 v = *at;
+                        uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        w[c] = mma::pack_f16(__uint_as_float(w[c] << 16) * up, __uint_as_float(w[c] & 0xffff0000u) * up);
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = mma::pack_f16(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
+                        *at = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
                 }
-                uint8_t* qd = sm + kOffQ + x * kOperand + r * 128;
-#pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    *reinterpret_cast<uint4*>(qd + (c >> 3) * kBlock + (((c & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
                 ptx::fence_proxy_async_smem();
                 tc::fence_before();
                 ptx::mbar_arrive(&ctl.qfull[x]);
@@ -641,41 +734,71 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 tc::fence_after();
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             }
-            // The row's result, or its part of one.
-            float* part = p.whole ? nullptr : slot_at(a.io.workspace, gridDim.x, p.slot) + (size_t)(x * kRows + r) * kHeadDim;
+            // The rows' results, or this part's share of them, through shared
+            // memory (Q_x is not read any more) so that whole rows are
+            // stored together: 64 channels at a time.
+            const bool whole = p.slot < 0;
+            float* part = whole ? nullptr : slot_at(a.io.workspace, gridDim.x, p.slot);
             if (cnt > 0) {
-                const float n = !p.whole ? 1.f : sum > 0.f ? (kE4m3 ? a.v_scale[p.s.h] : 1.f) / sum : 0.f;
+                const float n = !whole ? 1.f : sum > 0.f ? (kE4m3 ? a.v_scale[p.s.h] : 1.f) / sum : 0.f;
+                const bool plain = whole && !a.io.gate && !a.io.o_f32;   // bf16, all channels at once
+                if (plain) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tc::ld32(to + 32 * c, o);
+                        tc::wait_ld();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tc::ld32(to + 32 * c, o);
-                    tc::wait_ld();
-                    if (live) {
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(place(lane, 4 * c + (e >> 3))) = make_uint4(
+                                mma::pack_bf16(__uint_as_float(o[e]) * n, __uint_as_float(o[e + 1]) * n),
+                                mma::pack_bf16(__uint_as_float(o[e + 2]) * n, __uint_as_float(o[e + 3]) * n),
+                                mma::pack_bf16(__uint_as_float(o[e + 4]) * n, __uint_as_float(o[e + 5]) * n),
+                                mma::pack_bf16(__uint_as_float(o[e + 6]) * n, __uint_as_float(o[e + 7]) * n));
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = 0; i < 16; ++i) {
+                        const int row = 2 * i + (lane >> 4);
+                        const size_t h = head_of(i);
+                        const uint4 v = *reinterpret_cast<const uint4*>(place(row, chunk));
+                        if (lives >> row & 1u) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.io.o) + h * kHeadDim + 8 * chunk) = v;
+                    }
+                    __syncwarp();
+                }
+#pragma unroll 1
+                for (int half = plain ? 2 : 0; half < 2; ++half) {
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t o[32];
+                        tc::ld32(to + 64 * half + 32 * c, o);
+                        tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 v = make_float4(__uint_as_float(o[e]) * n, __uint_as_float(o[e + 1]) * n,
-                                                         __uint_as_float(o[e + 2]) * n, __uint_as_float(o[e + 3]) * n);
-                            if (p.whole) mma::store4(a.io, head * kHeadDim + 32 * c + e, v);
-                            else *reinterpret_cast<float4*>(part + 32 * c + e) = v;
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(place(lane, 8 * c + (e >> 2))) =
+                                make_float4(__uint_as_float(o[e]) * n, __uint_as_float(o[e + 1]) * n,
+                                            __uint_as_float(o[e + 2]) * n, __uint_as_float(o[e + 3]) * n);
+                    }
+                    __syncwarp();
+#pragma unroll 2
+                    for (int i = 0; i < 16; ++i) {
+                        const int row = 2 * i + (lane >> 4);
+                        const size_t h = head_of(i);
+                        const float4 v = *reinterpret_cast<const float4*>(place(row, chunk));
+                        if (lives >> row & 1u) {
+                            if (whole) mma::store4(a.io, h * kHeadDim + 64 * half + 4 * chunk, v);
+                            else *reinterpret_cast<float4*>(part + (size_t)((warp & 7) * 32 + row) * kHeadDim + 64 * half + 4 * chunk) = v;
                         }
                     }
-                    __syncwarp();   // the warp reads TMEM together
+                    __syncwarp();
                 }
                 tc::fence_before();
             }
-            if (live && p.whole && a.io.lse) a.io.lse[head] = sum > 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
-            if (live && !p.whole) {
-                float* ls = slot_at(a.io.workspace, gridDim.x, p.slot) + (size_t)2 * kRows * kHeadDim + 2 * (x * kRows + r);
-                ls[0] = ref;
-                ls[1] = sum;
-            }
-            if (tid == 0 && !p.whole && p.first) {
-                // The first part of a segment that goes on: up to the CTA that holds its last unit.
-                const int s = k - 1;
-                const long long last = ctl.seg_pre[s] + p.s.tiles_all(a.tokens) - 1;
-                joins(a.io.workspace)[blockIdx.x] =
-                    PrefillJoin{p.s.tok, p.s.m, p.s.h, (int)(((last + 1) * sc.ctas - 1) / sc.units), p.slot, {0, 0, 0}};
-            }
+            if (live && whole && a.io.lse) a.io.lse[head] = sum > 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
+            if (live && !whole)
+                *reinterpret_cast<float2*>(part + (size_t)2 * kRows * kHeadDim + 2 * (x * kRows + r)) = make_float2(ref, sum);
+            if (tid == 0 && p.last >= 0)
+                joins(a.io.workspace)[blockIdx.x] = PrefillJoin{p.s.tok, p.s.m, p.s.h, p.last, p.slot, {0, 0, 0}};
         }
     } else {
         tc::reg_dec<kRegsOther>();
