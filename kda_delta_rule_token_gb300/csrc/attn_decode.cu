@@ -45,22 +45,28 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 2;
-constexpr int kStages = 2;
+// By the warps that share a tile (row tiles).  One: two CTAs per SM, each warp
+// with two stages.  Two: a tile takes twice the work, so three CTAs, which the
+// registers allow without loading a request's rows ahead.
+template <int kRowTiles>
+constexpr int ctas_per_sm() { return kRowTiles == 1 ? 2 : 3; }
+template <int kRowTiles>
+constexpr int stages_per_warp() { return kRowTiles == 1 ? 2 : 1; }
+constexpr int kMostCtasPerSm = 3;
 constexpr uint32_t kTileBytes = 4096;            // keys (or values) of one warp tile
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
-constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;   // whatever the number of warps to a tile
 constexpr uint32_t kMergeBytes = kWarps * 16 * kHeadDim * 4;
 constexpr int kJoinRows = 8;                     // CTAs of the join per part, over rows
 constexpr int kMaxRows = kAttnFewRows;           // rows of one pass
 
+template <int kRowTiles>
 struct Smem {
-    uint8_t ring[kRingBytes];
+    uint8_t ring[kWarps * stages_per_warp<kRowTiles>() * kStageBytes];
     float merge[kMergeBytes / 4];
     float ref[2][kWarps * 16];
     float sum[2][kWarps * 16];
-    uint64_t full[kWarps * kStages];
-    uint64_t empty[kWarps * kStages];
+    uint64_t full[kWarps * stages_per_warp<kRowTiles>()];
+    uint64_t empty[kWarps * stages_per_warp<kRowTiles>()];
     long long scan[kWarps];
     long long total, first_unit;
     int first_b;
@@ -148,7 +154,7 @@ __device__ __forceinline__ void step(const DecodeArgs& a, Walk& w) {
 }
 
 template <bool kE4m3, int kRowTiles>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<kRowTiles>())
 kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, int* err) {
     constexpr int kTile = kE4m3 ? 32 : 16;       // keys of a warp tile
@@ -156,11 +162,11 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     constexpr int kGroups = kWarps / kRowTiles;  // groups of warps that share a tile
     constexpr int kUnit = kGroups * kTile;       // keys of a unit
     constexpr int kPartCost = kRowTiles;         // units that a request and head costs beside its own
-    constexpr int kDepth = kStages * kRowTiles;  // stages of a group's ring
+    constexpr int kDepth = stages_per_warp<kRowTiles>() * kRowTiles;  // stages of a group's ring
     constexpr float kOffset = kE4m3 ? 10.f : 0.f;
     constexpr float kLimit = kE4m3 ? 15.f : 8.f;
     extern __shared__ __align__(1024) uint8_t sm_raw[];
-    Smem& sm = *reinterpret_cast<Smem*>(sm_raw);
+    auto& sm = *reinterpret_cast<Smem<kRowTiles>*>(sm_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int group = warp / kRowTiles, row_tile = warp % kRowTiles;
     const bool lead = row_tile == 0;             // the group's copying warp
@@ -346,9 +352,10 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
 
     int used = 0, parity = 0;
     bool at_start = true;   // in the CTA's first request and head
-    if (cur.left > 0) load_rows(cur);
+    if (kRowTiles == 1 && cur.left > 0) load_rows(cur);
     while (cur.left > 0) {
         // One request and head (or the part of it in this CTA's range).
+        if (kRowTiles > 1) load_rows(cur);
         const Rows rw = rows_of(cur);
         const int h = rw.h, nrows = rw.n;
         const int u0 = cur.u, u1 = (int)min((long long)cur.units, u0 + cur.left);
@@ -570,7 +577,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         next.left -= u1 - u0 - 1;
         next.u = u1 - 1;
         step<kUnit, kPartCost>(a, next);
-        if (next.left > 0) load_rows(next);
+        if (kRowTiles == 1 && next.left > 0) load_rows(next);
 
         // The warps' partial results meet.  The buffers of references and
         // sums alternate: a warp may be a request ahead of another's reading.
@@ -727,7 +734,7 @@ std::atomic<bool> g_attr_done[64];
 template <bool kE4m3, int kRowTiles>
 cudaError_t set_smem() {
     return cudaFuncSetAttribute(kda_attn_decode_kernel<kE4m3, kRowTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(Smem));
+                                (int)sizeof(Smem<kRowTiles>));
 }
 
 }  // namespace
@@ -740,7 +747,7 @@ bool attn_decode_maps(const AttnLayer& l, AttnMaps& maps) {
 }
 
 size_t attn_decode_workspace_bytes(const DeviceInfo& dev) {
-    const int ctas = dev.sm_count * kCtasPerSm;
+    const int ctas = dev.sm_count * kMostCtasPerSm;
     return desc_bytes(ctas) + (size_t)ctas * 2 * kSlotFloats * sizeof(float);
 }
 
@@ -772,11 +779,12 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
     // Never more CTAs than the longest table allows units.
     const int tile = (most_rows <= 16 ? kWarps : kWarps / 2) * (l.e4m3 ? 32 : 16);
     const long long most = (long long)io.B * l.Hkv * a.passes * ((((long long)io.max_pages << l.page_shift) + tile - 1) / tile);
-    const int ctas = dev.sm_count * kCtasPerSm;
+    const bool two = most_rows > 16;
+    const int ctas = dev.sm_count * (two ? ctas_per_sm<2>() : ctas_per_sm<1>());
     const int grid = (int)(most < ctas ? most : ctas);
-    auto kernel = l.e4m3 ? (most_rows <= 16 ? kda_attn_decode_kernel<true, 1> : kda_attn_decode_kernel<true, 2>)
-                         : (most_rows <= 16 ? kda_attn_decode_kernel<false, 1> : kda_attn_decode_kernel<false, 2>);
-    kernel<<<grid, kThreads, sizeof(Smem), stream>>>(a, maps.k_decode, maps.v_decode, err_word);
+    auto kernel = l.e4m3 ? (two ? kda_attn_decode_kernel<true, 2> : kda_attn_decode_kernel<true, 1>)
+                         : (two ? kda_attn_decode_kernel<false, 2> : kda_attn_decode_kernel<false, 1>);
+    kernel<<<grid, kThreads, two ? sizeof(Smem<2>) : sizeof(Smem<1>), stream>>>(a, maps.k_decode, maps.v_decode, err_word);
     count_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;
