@@ -290,7 +290,7 @@ kda_status kda_attn_decode(kda_attn_ctx* ctx, int B, const uint16_t* q, const in
     if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectDecode, "attn_decode launch", [&] {
         return kda::launch_attn_few_rows(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word,
-                                         static_cast<cudaStream_t>(stream));
+                                         static_cast<cudaStream_t>(stream), false);
     });
 }
 
@@ -305,11 +305,14 @@ kda_status kda_attn_prefill(kda_attn_ctx* ctx, int B, int N, const int32_t* cu_n
     if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectPrefill, "attn_prefill launch", [&] {
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
-        cudaError_t e = kda::launch_attn_few_rows(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word, st);
-        if (e != cudaSuccess || kda::attn_few_rows(N, ctx->layer.G)) return e;   // no request can have more rows
-        kda::AttnIO many = io;
-        many.workspace = static_cast<uint8_t*>(workspace) + kda::attn_decode_workspace_bytes(ctx->dev);
-        return kda::launch_attn_many_rows(ctx->layer, ctx->maps, many, ctx->dev, ctx->err_word, st);
+        const bool many = !kda::attn_few_rows(N, ctx->layer.G);   // else no request can have more rows
+        if (many) {
+            kda::AttnIO m = io;
+            m.workspace = static_cast<uint8_t*>(workspace) + kda::attn_decode_workspace_bytes(ctx->dev);
+            const cudaError_t e = kda::launch_attn_many_rows(ctx->layer, ctx->maps, m, ctx->dev, ctx->err_word, st);
+            if (e != cudaSuccess) return e;
+        }
+        return kda::launch_attn_few_rows(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word, st, many);
     });
 }
 

@@ -233,7 +233,10 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
                 for (long long i = tid; i < rows; i += kThreads) a.io.lse[(size_t)r.tok0 * a.Hq + i] = -INFINITY;
         }
     __syncthreads();
-    if (!works) return;
+    if (!works) {
+        ptx::griddep_wait();
+        return;
+    }
 
     Walk cur;
     cur.left = to - from;
@@ -665,6 +668,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         for (int i = used; i < issued; ++i) ptx::mbar_wait_timed(&full[i % kDepth], (uint32_t)(i / kDepth) & 1u);
         __syncthreads();
     }
+    ptx::griddep_wait();   // launched beside other kernels: ends after them
 }
 
 // Joins the parts of a request and head that lie in several CTAs: blockIdx.x
@@ -673,7 +677,6 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
 __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, int ctas) {
     __shared__ float4 s_acc[8][32];
     __shared__ float s_ref[8], s_sum[8];
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const JoinDesc d = descs(a.io.workspace)[blockIdx.x];
     if (d.b < 0) return;
@@ -752,7 +755,7 @@ size_t attn_decode_workspace_bytes(const DeviceInfo& dev) {
 }
 
 cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
-                                 int* err_word, cudaStream_t stream) {
+                                 int* err_word, cudaStream_t stream, bool beside) {
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
         cudaError_t e = set_smem<false, 1>();
@@ -784,18 +787,22 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
     const int grid = (int)(most < ctas ? most : ctas);
     auto kernel = l.e4m3 ? (two ? kda_attn_decode_kernel<true, 2> : kda_attn_decode_kernel<true, 1>)
                          : (two ? kda_attn_decode_kernel<false, 2> : kda_attn_decode_kernel<false, 1>);
-    kernel<<<grid, kThreads, two ? sizeof(Smem<2>) : sizeof(Smem<1>), stream>>>(a, maps.k_decode, maps.v_decode, err_word);
-    count_launches(1);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || grid == 1) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(most_rows < kJoinRows ? most_rows : kJoinRows));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = two ? sizeof(Smem<2>) : sizeof(Smem<1>);
+    cfg.stream = stream;
     cfg.attrs = attr;
+    cfg.numAttrs = beside ? 1 : 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, maps.k_decode, maps.v_decode, err_word);
+    count_launches(1);
+    if (e != cudaSuccess || grid == 1) return e;   // one CTA leaves no parts
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(most_rows < kJoinRows ? most_rows : kJoinRows));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kda_attn_join_kernel, a, grid);
     count_launches(1);

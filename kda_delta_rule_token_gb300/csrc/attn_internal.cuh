@@ -96,8 +96,11 @@ bool attn_prefill_maps(const AttnLayer& l, AttnMaps& maps);
 // without keys.  attn_prefill.cu: the remaining requests of a call.
 size_t attn_decode_workspace_bytes(const DeviceInfo& dev);
 size_t attn_prefill_workspace_bytes(const DeviceInfo& dev);
+// `beside`: the few-row kernel may start beside the launches before it, the
+// many-row ones of the same call (it shares nothing with them but their inputs,
+// and ends after them).
 cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
-                                 int* err_word, cudaStream_t stream);
+                                 int* err_word, cudaStream_t stream, bool beside);
 cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
                                   int* err_word, cudaStream_t stream);
 

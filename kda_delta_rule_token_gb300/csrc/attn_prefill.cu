@@ -314,8 +314,6 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         ctl.kissued = ctl.vissued = 0;
         joins(a.io.workspace)[blockIdx.x].m = 0;
     }
-    if (warp == kWarpMma) tc::alloc(&ctl.tmem, 512);
-
     // Segments of all requests.
     Sched sc;
     sc.per = (a.io.B + kScan - 1) / kScan;
@@ -323,6 +321,8 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     if (tid < kScan)
         for (int b = min(a.io.B, tid * sc.per), end = min(a.io.B, b + sc.per); b < end; ++b) mine += pairs_of(a, b);
     const int upto = scan_inclusive(mine, ctl.warp_sum, &sc.total);
+    if (sc.total == 0) return;   // every request has few rows
+    if (warp == kWarpMma) tc::alloc(&ctl.tmem, 512);
     if (tid < kScan) ctl.pre[tid] = upto - mine;
     __syncthreads();
     sc.segments = (long long)sc.total * a.Hkv;
@@ -823,12 +823,12 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     }
     __syncthreads();
     if (warp == kWarpMma) tc::dealloc(tm, 512);
-    ptx::griddep_wait();   // ends after the few-row kernels launched before it
 }
 
 // Joins the parts of segments cut between CTAs: blockIdx.x the CTA that holds
 // the first part, a warp per row, four channels per lane.
 __global__ void __launch_bounds__(256) kda_attn_prefill_join_kernel(const PrefillArgs a, int ctas) {
+    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const PrefillJoin d = joins(a.io.workspace)[blockIdx.x];
     if (d.m == 0) return;
@@ -905,20 +905,12 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
     a.scale = l.softmax_scale * kLog2e;
     a.k_scale = l.k_scale;
     a.v_scale = l.v_scale;
-    // Both launches are programmatic: the first may start beside the few-row
-    // kernels launched before it (it shares nothing with them but their
-    // inputs, and waits for them before it ends), the join waits for the first.
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     const int grid = dev.sm_count;
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(l.e4m3 ? threads_of<true>() : threads_of<false>());
     cfg.dynamicSmemBytes = l.e4m3 ? smem_bytes<true>() : smem_bytes<false>();
     cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, l.e4m3 ? kda_attn_prefill_kernel<true> : kda_attn_prefill_kernel<false>,
                                        a, maps.k_prefill, maps.v_prefill, err_word);
     count_launches(1);
@@ -926,6 +918,11 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
     cfg.gridDim = dim3((unsigned)grid, 16);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kda_attn_prefill_join_kernel, a, grid);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
