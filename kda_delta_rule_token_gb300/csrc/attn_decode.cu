@@ -56,7 +56,7 @@ constexpr int kMostCtasPerSm = 3;
 constexpr uint32_t kTileBytes = 4096;            // keys (or values) of one warp tile
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kMergeBytes = kWarps * 16 * kHeadDim * 4;
-constexpr int kJoinRows = 8;                     // CTAs of the join per part, over rows
+constexpr int kJoinRows = 4;                     // CTAs of the join per part, over rows
 constexpr int kMaxRows = kAttnFewRows;           // rows of one pass
 
 template <int kRowTiles>
@@ -672,8 +672,8 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
 }
 
 // Joins the parts of a request and head that lie in several CTAs: blockIdx.x
-// the CTA that holds the first part, blockIdx.y over query rows, eight warps
-// over the parts, four channels per lane.
+// the CTA that holds the first part, blockIdx.y over query rows, four channels
+// per lane.  Few parts: a warp per row.  Many: the eight warps share a row's.
 __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, int ctas) {
     __shared__ float4 s_acc[8][32];
     __shared__ float s_ref[8], s_sum[8];
@@ -684,23 +684,45 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
     const int rows = d.n > 1 ? d.n * a.G : min(a.rows, a.G - row0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = d.last - (int)blockIdx.x + 1;
-    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-        float ref = kNoRef, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = warp; i < parts; i += 8) {
+
+    float ref, sum;
+    float4 acc;
+    auto add = [&](float r, float l, float4 v) {
+        const float to = fmaxf(ref, r);
+        const float f = mma::exp2_approx(ref - to), e = mma::exp2_approx(r - to);
+        ref = to;
+        sum = sum * f + l * e;
+        acc.x = acc.x * f + v.x * e;
+        acc.y = acc.y * f + v.y * e;
+        acc.z = acc.z * f + v.z * e;
+        acc.w = acc.w * f + v.w * e;
+    };
+    auto add_parts = [&](int row, int first, int step) {
+        ref = kNoRef;
+        sum = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = first; i < parts; i += step) {
             const float* p = slot_at(a.io.workspace, ctas, i == 0 ? d.slot : 2 * ((int)blockIdx.x + i));
             const float2 rl = *reinterpret_cast<const float2*>(p + kMaxRows * kHeadDim + 2 * row);
-            const float4 v = *reinterpret_cast<const float4*>(p + row * kHeadDim + 4 * lane);
-            const float to = fmaxf(ref, rl.x);
-            const float f = mma::exp2_approx(ref - to), e = mma::exp2_approx(rl.x - to);
-            ref = to;
-            sum = sum * f + rl.y * e;
-            acc.x = acc.x * f + v.x * e;
-            acc.y = acc.y * f + v.y * e;
-            acc.z = acc.z * f + v.z * e;
-            acc.w = acc.w * f + v.w * e;
+            add(rl.x, rl.y, *reinterpret_cast<const float4*>(p + row * kHeadDim + 4 * lane));
         }
+    };
+    auto finish = [&](int row) {
+        const float n = sum > 0.f ? (a.v_scale ? a.v_scale[h] : 1.f) / sum : 0.f;
+        const size_t head = ((size_t)d.tok0 + (d.n > 1 ? row / a.G : 0)) * a.Hq + h * a.G + (d.n > 1 ? row % a.G : row0 + row);
+        mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
+        if (a.io.lse && lane == 0) a.io.lse[head] = sum > 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
+    };
+    if (parts <= 8) {
+        for (int row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
+            add_parts(row, 0, 1);
+            finish(row);
+        }
+        return;
+    }
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        add_parts(row, warp, 8);
         s_acc[warp][lane] = acc;
         if (lane == 0) {
             s_ref[warp] = ref;
@@ -708,25 +730,9 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
         }
         __syncthreads();
         if (warp == 0) {
-            float top = s_ref[0];
 #pragma unroll
-            for (int w = 1; w < 8; ++w) top = fmaxf(top, s_ref[w]);
-            sum = 0.f;
-            acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const float e = mma::exp2_approx(s_ref[w] - top);
-                const float4 v = s_acc[w][lane];
-                sum += s_sum[w] * e;
-                acc.x += v.x * e;
-                acc.y += v.y * e;
-                acc.z += v.z * e;
-                acc.w += v.w * e;
-            }
-            const float n = sum > 0.f ? (a.v_scale ? a.v_scale[h] : 1.f) / sum : 0.f;
-            const size_t head = ((size_t)d.tok0 + (d.n > 1 ? row / a.G : 0)) * a.Hq + h * a.G + (d.n > 1 ? row % a.G : row0 + row);
-            mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
-            if (a.io.lse && lane == 0) a.io.lse[head] = sum > 0.f ? (top + log2f(sum)) / kLog2e : -INFINITY;
+            for (int w = 1; w < 8; ++w) add(s_ref[w], s_sum[w], s_acc[w][lane]);
+            finish(row);
         }
         __syncthreads();
     }
