@@ -446,14 +446,14 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         }
     copies_done:;
     } else if (warp == kWarpMma) {
-        // ---- MMAs, issued by one thread.  The pipe holds about two MMAs
-        // beyond the one it works on (some 130 cycles), while a wait on a
-        // barrier that is long complete takes as much, and operands that
-        // have to be moved to uniform registers nearly as much per MMA.  So
-        // the loop is written out for both slots, with every operand a
-        // constant but the shared-memory base, and each barrier is tested
-        // before the batch of MMAs that precedes its use: only one that was
-        // not complete by then is waited for.
+        // ---- MMAs, issued by one thread.  It shares its scheduler with two
+        // softmax warps, and the pipe holds only about two MMAs beyond the
+        // one it works on, so every instruction between two MMAs counts:
+        //  * the step of a key tile that both tiles go on from is written out
+        //    for either slot, all operands constants but the shared-memory base;
+        //  * each barrier is tested before the batch of MMAs that precedes its
+        //    use, and waited for only if it was not complete by then;
+        //  * giving up leaves the loop from the waits, the MMAs carry no condition.
         tc::reg_dec<kRegsOther>();
         Part p;
         int np = 0;
@@ -462,91 +462,103 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         const uint32_t base = ptx::smem_u32(sm);
         const uint64_t dq = tc::desc_sw128(base + kOffQ), dk = tc::desc_sw128(base + kOffK);
         const uint64_t dv = tc::desc_sw128_mn(base + kOffV, kBlock);
-        uint32_t qpar = 0u, ppar = 0u;   // bit x: tile x
+        uint32_t qpar[2] = {0u, 0u}, ppar[2] = {0u, 0u};
         int it = 0;
-        bool ok = true;
-        // A barrier's phase: tested now, waited for where it is needed.
-        struct Test {
-            bool done;
-            uint64_t* bar;
-            uint32_t par;
-        };
-        auto test = [&](uint64_t* bar, uint32_t par) { return Test{ptx::mbar_test(bar, par), bar, par}; };
-        auto need = [&](const Test& t) {
-            if (!t.done) ok = ok && pwait(t.bar, t.par, dead, err);
-            tc::fence_after();
-        };
-        auto mma_s = [&](auto tile, auto slot) {   // S_x = Q_x K^T
-            constexpr int x = decltype(tile)::value, sl = decltype(slot)::value;
+        // S_x = Q_x K^T and four of the eight MMAs of O_x += P_x V; slots by byte offset.
+        auto mma_s = [&](int x, uint32_t slot) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 tc::mma_ss_bf16(kColS + 128 * x, tc::desc_add(dq, x * kOperand + (i >> 2) * kBlock + (i & 3) * 32),
-                                tc::desc_add(dk, sl * kOperand + (i >> 2) * kBlock + (i & 3) * 32), id_s, i > 0);
+                                tc::desc_add(dk, slot + (i >> 2) * kBlock + (i & 3) * 32), id_s, i > 0);
             tc::commit(&ctl.sfull[x]);
         };
-        auto first_s = [&](auto tile, auto slot) {
-            constexpr int x = decltype(tile)::value;
-            if (p.cnt[x] <= 0) return;
-            need(test(&ctl.qfull[x], (qpar >> x) & 1u));
-            qpar ^= 1u << x;
-            if (ok) mma_s(tile, slot);
-        };
-        auto p_test = [&](int x, int half) { return test(&ctl.pfull[x][half], (ppar >> x) & 1u); };
-        // O_x += P_x(j) V_j from this slot, S_x(j + 1) from the other one.
-        // `mine`: the test of P_x(j)'s first half; returns that of the tile after this one.
-        auto tile_step = [&](auto tile, auto slot, int j, const Test& mine) -> Test {
-            constexpr int x = decltype(tile)::value, sl = decltype(slot)::value;
-            const bool more = j + 1 < p.cnt[x];
-            const bool last = x == 1 || j >= p.cnt[1];          // the last tile that uses V_j
-            const bool firstk = x == 0 || j >= p.cnt[0];        // the first that uses K_(j + 1)
-            const uint32_t npar = (uint32_t)((it + 1) >> 1) & 1u;
-            const Test upper = p_test(x, 1);
-            need(mine);
+        auto mma_pv = [&](int x, uint32_t slot, int half, uint32_t add) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (i == 4) need(upper);
-                if (ok)
-                    tc::mma_ts_f16kind(kColO + 128 * x, kColS + 128 * x + 8 * i,
-                                       tc::desc_add(dv, sl * kOperand + i * 2048), id_o, i > 0 ? 1u : (uint32_t)(j > 0));
-            }
-            ppar ^= 1u << x;
-            if (ok && last) tc::commit(&ctl.vempty[sl]);
-            if (j + 1 < p.n) {
-                if (firstk) need(test(&ctl.kfull[1 - sl], npar));
-                if (last) need(test(&ctl.vfull[1 - sl], npar));
-            }
-            // The tile after this one: the other one of this j, or the first one of the next.
-            const int nx = x == 0 && j < p.cnt[1] ? 1 : j + 1 < p.cnt[0] ? 0 : 1;
-            const Test next = p_test(nx, 0);
-            if (ok && more) mma_s(tile, std::integral_constant<int, 1 - sl>());
-            if (ok && !more) tc::commit(&ctl.ofull[x]);
-            return next;
+            for (int i = 4 * half; i < 4 * half + 4; ++i)
+                tc::mma_ts_f16kind(kColO + 128 * x, kColS + 128 * x + 8 * i, tc::desc_add(dv, slot + i * 2048), id_o,
+                                   i > 0 ? 1u : add);
         };
-        using Zero = std::integral_constant<int, 0>;
-        using One = std::integral_constant<int, 1>;
-        auto both = [&](auto slot, int j, Test t) {
-            constexpr int sl = decltype(slot)::value;
-            if (j < p.cnt[0]) t = tile_step(Zero(), slot, j, t);
-            if (j < p.cnt[1]) t = tile_step(One(), slot, j, t);
-            if (j + 1 < p.n && ok) tc::commit(&ctl.kempty[1 - sl]);
-            return t;
+        // The rest of a wait whose barrier was tested before.
+        auto need = [&](bool done, uint64_t* bar, uint32_t par) { return done || pwait(bar, par, dead, err); };
+        // One key tile of both tiles, with another one after it for both.
+        // `ready`: the test of P_0's first half, on return that of the next one's.
+        auto full_step = [&](auto slot_index, bool& ready, uint32_t add) -> bool {
+            constexpr int sl = decltype(slot_index)::value;
+            constexpr uint32_t here = sl * kOperand, there = (1 - sl) * kOperand;
+            const uint32_t npar = (uint32_t)((it + 1) >> 1) & 1u;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (!need(ready, &ctl.pfull[x][0], ppar[x])) return false;
+                tc::fence_after();
+                bool t = ptx::mbar_test(&ctl.pfull[x][1], ppar[x]);
+                mma_pv(x, here, 0, add);
+                if (!need(t, &ctl.pfull[x][1], ppar[x])) return false;
+                tc::fence_after();
+                uint64_t* kv = x ? &ctl.vfull[1 - sl] : &ctl.kfull[1 - sl];
+                t = ptx::mbar_test(kv, npar);
+                mma_pv(x, here, 1, 1u);
+                ppar[x] ^= 1u;
+                if (x) tc::commit(&ctl.vempty[sl]);
+                if (!need(t, kv, npar)) return false;
+                ready = ptx::mbar_test(&ctl.pfull[1 - x][0], ppar[1 - x]);
+                mma_s(x, there);
+            }
+            tc::commit(&ctl.kempty[1 - sl]);
+            return true;
+        };
+        // The same for any state of the two tiles.
+        auto any_step = [&](int j) -> bool {
+            const int sl = it & 1;
+            const uint32_t here = sl * kOperand, there = (1 - sl) * kOperand, npar = (uint32_t)((it + 1) >> 1) & 1u;
+            for (int x = 0; x < 2; ++x) {
+                if (j >= p.cnt[x]) continue;
+                for (int half = 0; half < 2; ++half) {
+                    if (!pwait(&ctl.pfull[x][half], ppar[x], dead, err)) return false;
+                    tc::fence_after();
+                    mma_pv(x, here, half, half || j > 0);
+                }
+                ppar[x] ^= 1u;
+                if (x || j >= p.cnt[1]) tc::commit(&ctl.vempty[sl]);
+                if (j + 1 < p.cnt[x]) {
+                    if (!pwait(&ctl.kfull[1 - sl], npar, dead, err)) return false;
+                    mma_s(x, there);
+                } else {
+                    tc::commit(&ctl.ofull[x]);
+                }
+            }
+            if (j + 1 < p.n) {
+                tc::commit(&ctl.kempty[1 - sl]);
+                if (!pwait(&ctl.vfull[1 - sl], npar, dead, err)) return false;
+            }
+            return true;
+        };
+        auto part = [&]() -> bool {
+            if (!pwait(&ctl.kfull[it & 1], (uint32_t)(it >> 1) & 1u, dead, err)) return false;
+            for (int x = 0; x < 2; ++x) {
+                if (p.cnt[x] <= 0) continue;
+                if (!pwait(&ctl.qfull[x], qpar[x], dead, err)) return false;
+                qpar[x] ^= 1u;
+                tc::fence_after();
+                mma_s(x, (it & 1) * kOperand);
+            }
+            tc::commit(&ctl.kempty[it & 1]);
+            if (!pwait(&ctl.vfull[it & 1], (uint32_t)(it >> 1) & 1u, dead, err)) return false;
+            int j = 0;
+            const int both = min(p.cnt[0], p.cnt[1]) - 1;   // steps that both tiles go on from
+            bool ready = false;
+            for (; j < both; ++j, ++it) {
+                const bool ok = (it & 1) ? full_step(std::integral_constant<int, 1>(), ready, j > 0)
+                                         : full_step(std::integral_constant<int, 0>(), ready, j > 0);
+                if (!ok) return false;
+            }
+            for (; j < p.n; ++j, ++it)
+                if (!any_step(j)) return false;
+            return true;
         };
         const bool issuer = tc::elect_one();
+        bool ok = true;
         while (take_part(ctl, np, p, dead, err)) {
-            if (issuer && ok) {
-                need(test(&ctl.kfull[it & 1], (uint32_t)(it >> 1) & 1u));
-                if (it & 1) {
-                    first_s(Zero(), One());
-                    first_s(One(), One());
-                } else {
-                    first_s(Zero(), Zero());
-                    first_s(One(), Zero());
-                }
-                if (ok) tc::commit(&ctl.kempty[it & 1]);
-                need(test(&ctl.vfull[it & 1], (uint32_t)(it >> 1) & 1u));
-                Test t = p_test(p.cnt[0] > 0 ? 0 : 1, 0);
-                for (int j = 0; j < p.n && ok; ++j, ++it) t = (it & 1) ? both(One(), j, t) : both(Zero(), j, t);
-            }
+            if (issuer && ok) ok = part();
             __syncwarp();
         }
         if (issuer) tc::commit(&ctl.drain);   // completes once every MMA that it issued has
