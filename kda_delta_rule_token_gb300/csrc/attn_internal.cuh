@@ -32,7 +32,7 @@ struct AttnLayer {
 };
 
 // Tensor maps of the bound cache (attn_tma.cuh): boxes of the decode's warp
-// tiles, and of one 128-byte column block for prompts.
+// tiles, and of whole pages for prompts.
 struct AttnMaps {
     CUtensorMap k_decode, v_decode;
     CUtensorMap k_prefill, v_prefill;

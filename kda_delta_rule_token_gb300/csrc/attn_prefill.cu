@@ -12,8 +12,8 @@
 // works on a segment of two such tiles (consecutive tokens), X = 0 and 1, at a
 // time:
 //
-//  * one warp copies K and V pages with TMA (128-byte swizzle, a box per page
-//    and 64-channel block) into two slots each;
+//  * one warp copies K and V pages with TMA (128-byte swizzle, a box per page)
+//    into two slots each;
 //  * one thread issues the MMAs: S_X(j) = Q_X K_j^T into TMEM, and
 //    O_X += P_X(j) V_j with P_X read from TMEM.  While the softmax of one
 //    tile runs, the MMAs of the other one do;
@@ -48,7 +48,9 @@ namespace {
 constexpr int kRows = 128;                     // rows of a tile
 constexpr int kKeys = 128;                     // keys of a tile
 constexpr uint32_t kOperand = 32768;           // a 128 x 128 16-bit operand
-constexpr uint32_t kBlock = 16384;             // one 64-channel block of it
+constexpr uint32_t kBlock = 16384;             // Q: one 64-channel block of it; e4m3: a tile as copied
+// K and V tiles: each eight keys are two swizzled 1024-byte atoms, channels 0-63 and 64-127.
+constexpr uint32_t kAtom = 1024, kEight = 2 * kAtom;
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffStage = 6 * kOperand;
 constexpr int kScan = 128;                     // threads of the prefix sums
 constexpr int kMaxCtas = 256;
@@ -367,7 +369,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         Cursor cur{sc.split ? -1 : 0, 0, false};
         const int rows = min(1 << a.page_shift, kKeys), boxes = kKeys / rows;   // rows of a box, pages of a tile
         const int is_v = lane >> 4;
-        const int pg = kE4m3 ? lane & 15 : (lane & 15) >> 1, block = kE4m3 ? 0 : lane & 1;
+        const int pg = lane & 15;
         int it = 0, raws = 0;
         for (int np = 0;; ++np) {
             next_part(a, ctl, sc, cur, p);
@@ -410,18 +412,18 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                         ptx::tma_load_4d(sm + kOffStage + kBlock + pg * rows * 128, &vmap, 0, 0, 0, ph, &ctl.cvfull);
                     if (ok) ctl.vissued = it + 1;
                 } else {
-                    uint8_t* kd = sm + kOffK + s * kOperand + block * kBlock + pg * rows * 128;
-                    uint8_t* vd = sm + kOffV + s * kOperand + block * kBlock + pg * rows * 128;
+                    uint8_t* kd = sm + kOffK + s * kOperand + pg * rows * 256;
+                    uint8_t* vd = sm + kOffV + s * kOperand + pg * rows * 256;
                     if (it >= 2) ok = pwait(&ctl.kempty[s], par, dead, err);
                     if (ok && lane == 0) ptx::mbar_arrive_expect_tx(&ctl.kfull[s], (uint32_t)(pages * rows * 256));
                     __syncwarp();
-                    if (ok && mine_box && !is_v) ptx::tma_load_4d(kd, &kmap, 0, 0, block, ph, &ctl.kfull[s]);
+                    if (ok && mine_box && !is_v) ptx::tma_load_5d(kd, &kmap, 0, 0, 0, 0, ph, &ctl.kfull[s]);
                     if (ok) ctl.kissued = it + 1;
                     if (ok && it >= 2) ok = pwait(&ctl.vempty[s], par, dead, err);
                     uint64_t* bar = raw ? &ctl.vraw : &ctl.vfull[s];
                     if (ok && lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(pages * rows * 256));
                     __syncwarp();
-                    if (ok && mine_box && is_v) ptx::tma_load_4d(vd, &vmap, 0, 0, block, ph, bar);
+                    if (ok && mine_box && is_v) ptx::tma_load_5d(vd, &vmap, 0, 0, 0, 0, ph, bar);
                     if (ok && !raw) ctl.vissued = it + 1;
                 }
                 if (!__all_sync(0xffffffffu, ok)) goto copies_done;
@@ -433,7 +435,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                     ++raws;
                     for (int i = lane; i < (kKeys - valid) * 16; i += 32) {
                         const int row = valid + (i >> 4), ch = i & 15;
-                        *reinterpret_cast<uint4*>(sm + kOffV + s * kOperand + (ch >> 3) * kBlock + row * 128 + (ch & 7) * 16) =
+                        *reinterpret_cast<uint4*>(sm + kOffV + s * kOperand + (row >> 3) * kEight + (ch >> 3) * kAtom + (row & 7) * 128 + (ch & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     }
                     ptx::fence_proxy_async_smem();
@@ -460,8 +462,8 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         constexpr uint32_t id_s = tc::idesc_f16kind(kRows, kKeys, !kE4m3, false);
         constexpr uint32_t id_o = tc::idesc_f16kind(kRows, kHeadDim, !kE4m3, true);
         const uint32_t base = ptx::smem_u32(sm);
-        const uint64_t dq = tc::desc_sw128(base + kOffQ), dk = tc::desc_sw128(base + kOffK);
-        const uint64_t dv = tc::desc_sw128_mn(base + kOffV, kBlock);
+        const uint64_t dq = tc::desc_sw128(base + kOffQ), dk = tc::desc_sw128(base + kOffK, kEight);
+        const uint64_t dv = tc::desc_sw128_mn(base + kOffV, kAtom, kEight);
         uint32_t qpar[2] = {0u, 0u}, ppar[2] = {0u, 0u};
         int it = 0;
         // S_x = Q_x K^T and four of the eight MMAs of O_x += P_x V; slots by byte offset.
@@ -469,13 +471,13 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 tc::mma_ss_bf16(kColS + 128 * x, tc::desc_add(dq, x * kOperand + (i >> 2) * kBlock + (i & 3) * 32),
-                                tc::desc_add(dk, slot + (i >> 2) * kBlock + (i & 3) * 32), id_s, i > 0);
+                                tc::desc_add(dk, slot + (i >> 2) * kAtom + (i & 3) * 32), id_s, i > 0);
             tc::commit(&ctl.sfull[x]);
         };
         auto mma_pv = [&](int x, uint32_t slot, int half, uint32_t add) {
 #pragma unroll
             for (int i = 4 * half; i < 4 * half + 4; ++i)
-                tc::mma_ts_f16kind(kColO + 128 * x, kColS + 128 * x + 8 * i, tc::desc_add(dv, slot + i * 2048), id_o,
+                tc::mma_ts_f16kind(kColO + 128 * x, kColS + 128 * x + 8 * i, tc::desc_add(dv, slot + i * 2 * kEight), id_o,
                                    i > 0 ? 1u : add);
         };
         // The rest of a wait whose barrier was tested before.
@@ -581,7 +583,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                     if (ok && it >= 2) ok = pwait(v ? &ctl.vempty[s] : &ctl.kempty[s], par, dead, err);
                     if (!ok) break;
                     const uint8_t* src = sm + kOffStage + v * kBlock + row * 128;
-                    uint8_t* dst = sm + (v ? kOffV : kOffK) + s * kOperand + row * 128;
+                    uint8_t* dst = sm + (v ? kOffV : kOffK) + s * kOperand + (row >> 3) * kEight + (row & 7) * 128;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
@@ -593,7 +595,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                             f[2 * i] = mma::e4m3x2_f16x2(u[i]);
                             f[2 * i + 1] = mma::e4m3x2_f16x2(u[i] >> 16);
                         }
-                        uint8_t* d = dst + (c >> 2) * kBlock;
+                        uint8_t* d = dst + (c >> 2) * kAtom;
                         *reinterpret_cast<uint4*>(d + ((((2 * c) & 7) ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
                         *reinterpret_cast<uint4*>(d + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
                     }
@@ -890,7 +892,9 @@ cudaError_t prepare_kernel() {
 
 bool attn_prefill_maps(const AttnLayer& l, AttnMaps& maps) {
     const int rows = l.page_size < kKeys ? l.page_size : kKeys;
-    return make_cache_map(&maps.k_prefill, l, l.k_cache, rows, 1) && make_cache_map(&maps.v_prefill, l, l.v_cache, rows, 1);
+    if (l.e4m3)
+        return make_cache_map(&maps.k_prefill, l, l.k_cache, rows, 1) && make_cache_map(&maps.v_prefill, l, l.v_cache, rows, 1);
+    return make_cache_map_atoms(&maps.k_prefill, l, l.k_cache, rows) && make_cache_map_atoms(&maps.v_prefill, l, l.v_cache, rows);
 }
 
 size_t attn_prefill_workspace_bytes(const DeviceInfo& dev) {

@@ -37,6 +37,12 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// The same with 8-row atoms `eight` bytes apart.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t eight) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(eight >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
 // The descriptor of the operand `off` bytes (a multiple of 16) past the one
 // `d` describes.  The start-address field holds bits 4..17 of the
 // shared-memory address and every operand lies below 256 KiB, so the sum
@@ -53,10 +59,10 @@ __host__ __device__ constexpr uint32_t idesc_tf32(int M, int N) {
 }
 
 // Shared-memory matrix descriptor of an MN-major SW128 operand: rows of 128
-// bytes (64 16-bit elements of MN) for consecutive K, 8-row atoms 1024 B apart
-// along K, further blocks of 64 elements of MN `block` bytes on.
-__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t block) {
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+// bytes (64 16-bit elements of MN) for consecutive K, 8-row atoms `eight` bytes
+// apart along K, further blocks of 64 elements of MN `block` bytes on.
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t block, uint32_t eight) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(eight >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
