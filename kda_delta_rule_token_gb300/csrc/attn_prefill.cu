@@ -54,8 +54,7 @@ constexpr uint32_t kAtom = 1024, kEight = 2 * kAtom;
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffStage = 6 * kOperand;
 constexpr int kScan = 128;                     // threads of the prefix sums
 constexpr int kMaxCtas = 256;
-constexpr int kPartCost = 2;                   // key tiles that starting and ending a segment costs beside its own
-constexpr int kSplitGain = 4;                  // key tiles that cutting has to save on the busiest CTA
+constexpr int kJoinCost = 8;                   // key tiles that writing and joining partial results takes (11 us)
 constexpr int kMostWeighed = 32;               // segments per CTA up to which their load is worked out
 
 constexpr uint32_t kColS = 0, kColO = 256;     // TMEM columns, + 128 X
@@ -109,6 +108,8 @@ struct PrefillArgs {
     AttnIO io;
     int Hq, Hkv, G;
     int tokens;              // of a tile: 128 / G
+    int part_cost;           // key tiles that starting and ending a segment costs beside its own, as measured:
+                             // 3.8 us of 1.35 us tiles in bf16, 5.3 us of 1.5 us in e4m3
     int page_shift, num_pages;
     float scale;             // softmax scale * log2(e)
     const float* k_scale;
@@ -118,7 +119,7 @@ struct PrefillArgs {
 struct Sched {
     int total;               // pairs of token tiles of all requests
     int per;                 // requests of a scan thread
-    long long segments;
+    int segments;            // pairs * key heads (fewer than the query rows, whose memory bounds them)
     int chunk;               // segments of a scan thread
     bool split;
     int units, ctas;         // split: key tiles and costs of all segments, CTAs that share them
@@ -143,8 +144,8 @@ __device__ __forceinline__ int pairs_of(const PrefillArgs& a, int b) {
     return (n + 2 * a.tokens - 1) / (2 * a.tokens);
 }
 
-__device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, long long s) {
-    const int pair = (int)(s / a.Hkv);
+__device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, int s) {
+    const int pair = (int)((unsigned)s / (unsigned)a.Hkv);
     int lo = 0, hi = kScan - 1;   // the last scan thread with pre <= pair
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -157,7 +158,7 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
     }
     Segment g;
     g.b = b;
-    g.h = (int)(s % a.Hkv);
+    g.h = s - pair * a.Hkv;
     int tok0, tokens;
     attn_tokens(a.io, b, tok0, tokens);
     const int i0 = (n - 1 - (pair - at)) * 2 * a.tokens;   // the longest first
@@ -168,11 +169,18 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
     return g;
 }
 
+// The segment after segment s - 1, which g holds: the next head of its pair, or the next pair.
+__device__ __forceinline__ void next_segment(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, int s, Segment& g) {
+    if (g.h + 1 < a.Hkv) ++g.h;
+    else if (s < sc.segments) g = find_segment(a, ctl, sc, s);
+}
+
 // Where a CTA is in its work (the copying warp's).
 struct Cursor {
-    long long k;             // whole segments: rounds dealt; cut: the next segment, -1 before the first
+    int k;                   // whole segments: rounds dealt; cut: the next segment, -1 before the first
     int at;                  // cut: units before segment k
     bool begun;              // cut: a part was found
+    Segment s;               // cut: segment k
 };
 
 // The next part of this CTA; p.n = 0 past the last.
@@ -180,9 +188,9 @@ __device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, 
     p.n = 0;
     if (!sc.split) {
         for (;; ++c.k) {
-            const long long base = c.k * gridDim.x;
+            const long long base = (long long)c.k * gridDim.x;
             if (base >= sc.segments) return;
-            const long long s = base + ((c.k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            const int s = (int)(base + ((c.k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
             if (s >= sc.segments) continue;
             p.s = find_segment(a, ctl, sc, s);
             break;
@@ -203,16 +211,18 @@ __device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, 
             const int mid = (lo + hi + 1) >> 1;
             if (ctl.units[mid] <= from) lo = mid; else hi = mid - 1;
         }
-        c.k = (long long)lo * sc.chunk;
+        c.k = lo * sc.chunk;
         c.at = ctl.units[lo];
+        if (c.k < sc.segments) c.s = find_segment(a, ctl, sc, c.k);
     }
     while (c.k < sc.segments && c.at < to) {
-        p.s = find_segment(a, ctl, sc, c.k);
+        p.s = c.s;
         const int tiles = p.s.tiles_all(a.tokens), at = c.at;
         ++c.k;
-        c.at += tiles + kPartCost;
-        // A segment's first kPartCost units stand for its cost, the others for its tiles.
-        const int j0 = max(from - at - kPartCost, 0), j1 = min(to - at - kPartCost, tiles);
+        next_segment(a, ctl, sc, c.k, c.s);
+        c.at += tiles + a.part_cost;
+        // A segment's first part_cost units stand for its cost, the others for its tiles.
+        const int j0 = max(from - at - a.part_cost, 0), j1 = min(to - at - a.part_cost, tiles);
         if (j1 <= j0) continue;
         p.j0 = j0;
         p.n = j1 - j0;
@@ -327,31 +337,39 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     if (warp == kWarpMma) tc::alloc(&ctl.tmem, 512);
     if (tid < kScan) ctl.pre[tid] = upto - mine;
     __syncthreads();
-    sc.segments = (long long)sc.total * a.Hkv;
+    sc.segments = sc.total * a.Hkv;
     sc.split = false;
     sc.units = sc.ctas = sc.chunk = 0;
-    if (sc.segments > 0 && sc.segments <= (long long)kMostWeighed * gridDim.x) {
-        // The load of every CTA if whole segments are dealt, against equal shares of key tiles.
+    if (sc.segments > 0 && sc.segments <= kMostWeighed * (int)gridDim.x) {
+        // The load of every CTA if whole segments are dealt, against equal
+        // shares of key tiles, which cost up to two more parts per CTA and the join.
         for (int i = tid; i < kMaxCtas; i += blockDim.x) ctl.load[i] = 0;
         __syncthreads();
-        const int n = (int)sc.segments;
-        sc.chunk = (n + kScan - 1) / kScan;
+        const int n = sc.segments;
+        sc.chunk = (sc.total + kScan - 1) / kScan * a.Hkv;   // whole pairs, so that the threads find theirs together
         long long sum = 0;
-        if (tid < kScan)
-            for (int s = tid * sc.chunk, end = min(n, s + sc.chunk), u = -1; s < end; ++s) {
-                if (u < 0 || s % a.Hkv == 0)   // the heads of a pair of token tiles are alike
-                    u = find_segment(a, ctl, sc, s).tiles_all(a.tokens) + kPartCost;
+        if (tid < kScan && tid * sc.chunk < n) {
+            int s = tid * sc.chunk;
+            Segment g = find_segment(a, ctl, sc, s);
+            int round = s / (int)gridDim.x, r = s - round * (int)gridDim.x;
+            for (const int end = min(n, s + sc.chunk); s < end;) {
+                const int u = g.tiles_all(a.tokens) + a.part_cost;
                 sum += u;
-                const int round = s / (int)gridDim.x, r = s % (int)gridDim.x;
                 atomicAdd(&ctl.load[(round & 1) ? gridDim.x - 1 - r : r], u);
+                if (++r == (int)gridDim.x) {
+                    r = 0;
+                    ++round;
+                }
+                next_segment(a, ctl, sc, ++s, g);
             }
+        }
         const int u = (int)min(sum, (long long)(0x7fffffff / kScan));   // beyond that, shares are not worth cutting for
         const int to = scan_inclusive(u, ctl.warp_sum, &sc.units);
         if (tid < kScan) ctl.units[tid] = to - u;
         for (int i = tid; i < (int)gridDim.x; i += blockDim.x) atomicMax(&ctl.busiest, ctl.load[i]);
         const bool fits = !__syncthreads_or(tid < kScan && (long long)u != sum);
         sc.ctas = min((int)gridDim.x, sc.units);
-        sc.split = fits && ctl.busiest > (sc.units + sc.ctas - 1) / sc.ctas + kSplitGain;
+        sc.split = fits && ctl.busiest > (sc.units + sc.ctas - 1) / sc.ctas + 2 * a.part_cost + kJoinCost;
     }
     tc::fence_before();
     __syncthreads();
@@ -366,7 +384,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         // ---- copies
         tc::reg_dec<kRegsOther>();
         Part p;
-        Cursor cur{sc.split ? -1 : 0, 0, false};
+        Cursor cur{sc.split ? -1 : 0, 0, false, {}};
         const int rows = min(1 << a.page_shift, kKeys), boxes = kKeys / rows;   // rows of a box, pages of a tile
         const int is_v = lane >> 4;
         const int pg = lane & 15;
@@ -916,6 +934,7 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
     a.Hkv = l.Hkv;
     a.G = l.G;
     a.tokens = kRows / l.G;
+    a.part_cost = l.e4m3 ? 4 : 3;
     a.page_shift = l.page_shift;
     a.num_pages = l.num_pages;
     a.scale = l.softmax_scale * kLog2e;
