@@ -415,6 +415,35 @@ def test_prefill_long_prompt():
     layer.done()
 
 
+@pytest.mark.parametrize("new,kv,hq,hkv,page,e4m3", [
+    # more (token tile, key head) segments than SMs: dealt in rounds
+    ([2500], [2500], 32, 16, 16, False),
+    ([900, 40, 700, 1, 1100], [900, 3000, 800, 2000, 1300], 16, 8, 64, True),
+    # one long segment among many short ones: the keys are cut
+    ([64, 300, 300], [20000, 300, 400], 8, 4, 32, False),
+    ([40] * 12 + [70], [300] * 12 + [17000], 8, 4, 16, True),
+    # more requests than threads look at once, small and large chunks mixed
+    ([(7 * i) % 50 for i in range(300)], [(7 * i) % 50 + (13 * i) % 200 for i in range(300)], 4, 1, 16, False),
+])
+def test_prefill_schedules(new, kv, hq, hkv, page, e4m3):
+    layer = Layer(hq, hkv, page, e4m3, seed=len(new))
+    layer.fill(kv)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    verify(layer, queries(layer, cu[-1]), kv, cu)
+    layer.done()
+
+
+def test_prefill_more_segments_than_are_weighed():
+    """64 query heads to a key head: four tokens to a segment, 5000 segments."""
+    new = [500] * 40
+    layer = Layer(64, 1, 16)
+    layer.fill(new)
+    verify(layer, queries(layer, 20000), new, [500 * i for i in range(41)])
+    layer.done()
+
+
 def test_prefill_of_single_tokens_is_decode():
     """Both entry points on the same tokens, within both bounds of the same exact value."""
     lens = [400, 1, 77]
