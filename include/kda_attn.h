@@ -26,7 +26,10 @@
  * on the caller's stream, no allocation and no synchronisation per call,
  * arguments checked on the host before any launch, one host thread per context
  * at a time, bounded waits, KDA_FAULT_INJECT (names "attn_plan",
- * "attn_append", "attn_decode", "attn_prefill"; "all" includes them).
+ * "attn_append", "attn_decode", "attn_prefill"; "all" includes them; the name
+ * "attn_drop", not part of "all", makes every CTA of the attention kernels leave
+ * out its first copy of keys: the bounded waits on it run out and
+ * kda_attn_sync_status reports KDA_ERR_TIMEOUT).
  *
  * What only the device knows (lengths, page ids, slots) is checked by the
  * kernels: nothing is read or written outside the buffers, and the cases that

@@ -5,7 +5,10 @@
 //
 // KDA_FAULT_INJECT, read once by kda_attn_create, replaces the launches of
 // the entry points it names ("attn_plan", "attn_append", "attn_decode",
-// "attn_prefill", or "all") by the error cudaErrorLaunchFailure.
+// "attn_prefill", or "all") by the error cudaErrorLaunchFailure.  The name
+// "attn_drop" (not part of "all") instead makes every CTA of the attention
+// kernels leave out its first copy of keys, so that a bounded wait inside the
+// kernel runs out.
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -26,7 +29,7 @@ struct kda_attn_ctx {
 namespace kda {
 namespace {
 
-constexpr unsigned kInjectPlan = 1u, kInjectAppend = 2u, kInjectDecode = 4u, kInjectPrefill = 8u;
+constexpr unsigned kInjectPlan = 1u, kInjectAppend = 2u, kInjectDecode = 4u, kInjectPrefill = 8u, kInjectDrop = 16u;
 
 unsigned parse_inject(const char* v) {
     unsigned m = 0u;
@@ -39,6 +42,7 @@ unsigned parse_inject(const char* v) {
         else if (is("attn_append")) m |= kInjectAppend;
         else if (is("attn_decode")) m |= kInjectDecode;
         else if (is("attn_prefill")) m |= kInjectPrefill;
+        else if (is("attn_drop")) m |= kInjectDrop;
         else if (is("all")) m |= kInjectPlan | kInjectAppend | kInjectDecode | kInjectPrefill;
         p = *e ? e + 1 : e;
     }
@@ -286,7 +290,8 @@ kda_status kda_attn_decode(kda_attn_ctx* ctx, int B, const uint16_t* q, const in
                            void* workspace, size_t workspace_bytes, void* stream) {
     if (!ctx || B < 0) return KDA_ERR_INVALID_ARG;
     if (B == 0) return KDA_OK;
-    const kda::AttnIO io{B, B, nullptr, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace};
+    const kda::AttnIO io{B, B, nullptr, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace,
+                         (ctx->inject & kda::kInjectDrop) ? 1 : 0};
     if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectDecode, "attn_decode launch", [&] {
         return kda::launch_attn_few_rows(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word,
@@ -301,7 +306,8 @@ kda_status kda_attn_prefill(kda_attn_ctx* ctx, int B, int N, const int32_t* cu_n
     if (!ctx || B < 0 || N < 0) return KDA_ERR_INVALID_ARG;
     if (B == 0 || N == 0) return KDA_OK;
     if (!cu_new) return KDA_ERR_INVALID_ARG;
-    const kda::AttnIO io{B, N, cu_new, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace};
+    const kda::AttnIO io{B, N, cu_new, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace,
+                         (ctx->inject & kda::kInjectDrop) ? 1 : 0};
     if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectPrefill, "attn_prefill launch", [&] {
         const cudaStream_t st = static_cast<cudaStream_t>(stream);

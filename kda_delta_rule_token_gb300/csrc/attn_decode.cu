@@ -277,7 +277,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         const int s = issued % kDepth;
         if (kRowTiles > 1 && issued >= kDepth)
             ok = ptx::mbar_wait_timed(&empty[s], (uint32_t)(issued / kDepth - 1) & 1u, &sm.dead);
-        if (lane == 0 && ok) {
+        if (lane == 0 && ok && !(a.io.drop && group == 0 && issued == 0)) {
             uint8_t* st = ring + s * kStageBytes;
             const int row = (ahead.u * kGroups + group) * kTile & page_mask;
             const int h = ahead.vh / a.passes;

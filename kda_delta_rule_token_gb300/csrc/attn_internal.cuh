@@ -83,6 +83,9 @@ struct AttnIO {
     int o_f32;
     float* lse;              // may be null
     void* workspace;
+    // Test injection (KDA_FAULT_INJECT "attn_drop"): every CTA leaves out
+    // its first copy of keys, so that a bounded wait runs out.
+    int drop;
 };
 
 cudaError_t launch_attn_plan(const AttnLayer& l, const AttnPlanIO& io, const DeviceInfo& dev, cudaStream_t stream);

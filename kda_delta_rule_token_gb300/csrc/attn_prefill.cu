@@ -93,7 +93,7 @@ struct Ctl {
     uint32_t tmem;
     int dead;
     int busiest;
-    int kissued, vissued;
+    int kissued, vissued, raws;   // copies issued (raws: of values whose request ends in the tile)
     int warp_sum[kScan / 32];
     int pre[kScan];          // pairs of token tiles before the requests of scan thread t
     int units[kScan];        // key tiles and costs before the segments of scan thread t
@@ -323,7 +323,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         ptx::fence_mbar_init();
         ctl.dead = 0;
         ctl.busiest = 0;
-        ctl.kissued = ctl.vissued = 0;
+        ctl.kissued = ctl.vissued = ctl.raws = 0;
         joins(a.io.workspace)[blockIdx.x].m = 0;
     }
     // Segments of all requests.
@@ -414,13 +414,14 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 if (mine_box && !in) atomicOr(err, kErrAttnIndex);
                 const int ph = (in ? id : a.num_pages) * a.Hkv + (in ? p.s.h : 0);
                 const bool raw = !kE4m3 && valid < kKeys;   // values past the end have to be cleared
+                const bool drop = a.io.drop && it == 0;
                 bool ok = true;
                 if (kE4m3) {
                     // Staging: one buffer each, emptied by the converting warps.
                     if (it > 0) ok = pwait(&ctl.ckempty, (uint32_t)(it - 1) & 1u, dead, err);
-                    if (ok && lane == 0) ptx::mbar_arrive_expect_tx(&ctl.ckfull, (uint32_t)(pages * rows * 128));
+                    if (ok && lane == 0 && !drop) ptx::mbar_arrive_expect_tx(&ctl.ckfull, (uint32_t)(pages * rows * 128));
                     __syncwarp();
-                    if (ok && mine_box && !is_v)
+                    if (ok && mine_box && !is_v && !drop)
                         ptx::tma_load_4d(sm + kOffStage + pg * rows * 128, &kmap, 0, 0, 0, ph, &ctl.ckfull);
                     if (ok) ctl.kissued = it + 1;
                     if (ok && it > 0) ok = pwait(&ctl.cvempty, (uint32_t)(it - 1) & 1u, dead, err);
@@ -433,9 +434,9 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                     uint8_t* kd = sm + kOffK + s * kOperand + pg * rows * 256;
                     uint8_t* vd = sm + kOffV + s * kOperand + pg * rows * 256;
                     if (it >= 2) ok = pwait(&ctl.kempty[s], par, dead, err);
-                    if (ok && lane == 0) ptx::mbar_arrive_expect_tx(&ctl.kfull[s], (uint32_t)(pages * rows * 256));
+                    if (ok && lane == 0 && !drop) ptx::mbar_arrive_expect_tx(&ctl.kfull[s], (uint32_t)(pages * rows * 256));
                     __syncwarp();
-                    if (ok && mine_box && !is_v) ptx::tma_load_5d(kd, &kmap, 0, 0, 0, 0, ph, &ctl.kfull[s]);
+                    if (ok && mine_box && !is_v && !drop) ptx::tma_load_5d(kd, &kmap, 0, 0, 0, 0, ph, &ctl.kfull[s]);
                     if (ok) ctl.kissued = it + 1;
                     if (ok && it >= 2) ok = pwait(&ctl.vempty[s], par, dead, err);
                     uint64_t* bar = raw ? &ctl.vraw : &ctl.vfull[s];
@@ -443,6 +444,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                     __syncwarp();
                     if (ok && mine_box && is_v) ptx::tma_load_5d(vd, &vmap, 0, 0, 0, 0, ph, bar);
                     if (ok && !raw) ctl.vissued = it + 1;
+                    if (ok && raw) ctl.raws = raws + 1;
                 }
                 if (!__all_sync(0xffffffffu, ok)) goto copies_done;
                 if (j + 1 < p.j0 + p.n) id = page_of(j + 1);
@@ -850,6 +852,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                     ptx::mbar_wait_timed(&ctl.kfull[i & 1], (uint32_t)(i >> 1) & 1u);
                 for (int i = max(0, ctl.vissued - 2); i < ctl.vissued; ++i)
                     ptx::mbar_wait_timed(&ctl.vfull[i & 1], (uint32_t)(i >> 1) & 1u);
+                if (ctl.raws) ptx::mbar_wait_timed(&ctl.vraw, (uint32_t)(ctl.raws - 1) & 1u);
             }
         }
     }

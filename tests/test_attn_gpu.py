@@ -606,6 +606,27 @@ def test_refusals_with_a_context():
     layer.done()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_a_copy_that_never_comes(prefill, e4m3, monkeypatch):
+    """The bounded waits on it run out: reported once, nothing written outside, and the device works on."""
+    lens, cu = [700, 300], [0, 90, 130] if prefill else None
+    monkeypatch.setenv("KDA_FAULT_INJECT", "attn_drop")
+    layer = Layer(8, 2, 16, e4m3)
+    monkeypatch.delenv("KDA_FAULT_INJECT")
+    layer.fill(lens)
+    q = queries(layer, 130 if prefill else 2)
+    o, lse = run_attend(layer, q, lens, cu)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_ERR_TIMEOUT
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    assert o.intact() and lse.intact()
+    layer.done()
+    again = Layer(8, 2, 16, e4m3)
+    again.fill(lens)
+    verify(again, queries(again, 130 if prefill else 2), lens, cu)
+    again.done()
+
+
 @pytest.mark.parametrize("name", ["attn_plan", "attn_append", "attn_decode", "attn_prefill", "all"])
 def test_injected_launch_failure(name, monkeypatch):
     monkeypatch.setenv("KDA_FAULT_INJECT", name)
