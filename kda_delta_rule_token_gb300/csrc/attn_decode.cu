@@ -161,7 +161,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     constexpr int kNT = kTile / 8;               // 8-key column tiles of the logits
     constexpr int kGroups = kWarps / kRowTiles;  // groups of warps that share a tile
     constexpr int kUnit = kGroups * kTile;       // keys of a unit
-    constexpr int kPartCost = kRowTiles;         // units that a request and head costs beside its own
+    constexpr int kPartCost = kRowTiles == 1 ? 1 : 3;   // units that a request and head costs beside its own
     constexpr int kDepth = stages_per_warp<kRowTiles>() * kRowTiles;  // stages of a group's ring
     constexpr float kOffset = kE4m3 ? 10.f : 0.f;
     constexpr float kLimit = kE4m3 ? 15.f : 8.f;

@@ -55,6 +55,7 @@ constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffSt
 constexpr int kScan = 128;                     // threads of the prefix sums
 constexpr int kMaxCtas = 256;
 constexpr int kJoinCost = 8;                   // key tiles that writing and joining partial results takes (11 us)
+constexpr int kJoinCtas = 8;                   // CTAs of the join per SM (fewer leave its loads waiting, more cost calls without cut keys)
 constexpr int kMostWeighed = 32;               // segments per CTA up to which their load is worked out
 
 constexpr uint32_t kColS = 0, kColO = 256;     // TMEM columns, + 128 X
@@ -860,24 +861,45 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     if (warp == kWarpMma) tc::dealloc(tm, 512);
 }
 
-// Joins the parts of segments cut between CTAs: blockIdx.x the CTA that holds
-// the first part, a warp per row, four channels per lane.
+// Joins the parts of segments cut between CTAs, a warp per row, four channels
+// per lane; the rows of all cut segments are shared out evenly.
 __global__ void __launch_bounds__(256) kda_attn_prefill_join_kernel(const PrefillArgs a, int ctas) {
+    __shared__ int s_end[kMaxCtas], s_warp[8];   // rows up to and with the segment that CTA i begins
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const PrefillJoin d = joins(a.io.workspace)[blockIdx.x];
-    if (d.m == 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int parts = d.last - (int)blockIdx.x + 1;
-    const int rows = d.m * a.G;
-    for (int row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int end = tid < ctas ? joins(a.io.workspace)[tid].m * a.G : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, end, d);
+        if (lane >= d) end += y;
+    }
+    if (lane == 31) s_warp[warp] = end;
+    __syncthreads();
+    int rows = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) end += s_warp[w];
+        rows += s_warp[w];
+    }
+    s_end[tid] = end;
+    __syncthreads();
+    for (int at_row = blockIdx.x * 8 + warp; at_row < rows; at_row += gridDim.x * 8) {
+        int lo = 0, hi = ctas - 1;   // the first CTA whose rows end past this one
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_end[mid] > at_row) hi = mid; else lo = mid + 1;
+        }
+        const PrefillJoin d = joins(a.io.workspace)[lo];
+        const int row = at_row - (lo ? s_end[lo - 1] : 0);
+        const int parts = d.last - lo + 1;
         const int i = row / a.G, g = row % a.G;
         const int at = i < a.tokens ? row : kRows + row - a.tokens * a.G;   // row of the pair of tiles
         float ref = kNoRef, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
         for (int q = 0; q < parts; ++q) {
-            const float* s = slot_at(a.io.workspace, ctas, q == 0 ? d.slot : 2 * ((int)blockIdx.x + q));
+            const float* s = slot_at(a.io.workspace, ctas, q == 0 ? d.slot : 2 * (lo + q));
             const float2 ls = *reinterpret_cast<const float2*>(s + (size_t)2 * kRows * kHeadDim + 2 * at);
             const float4 v = *reinterpret_cast<const float4*>(s + (size_t)at * kHeadDim + 4 * lane);
             if (!(ls.y > 0.f)) continue;   // no key of this part is seen: the weighted sum was not written
@@ -953,7 +975,7 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
                                        a, maps.k_prefill, maps.v_prefill, err_word);
     count_launches(1);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)grid, 16);
+    cfg.gridDim = dim3((unsigned)grid * kJoinCtas);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cudaLaunchAttribute attr[1];
