@@ -39,8 +39,7 @@
 #include "attn_internal.cuh"
 #include "attn_mma.cuh"
 #include "attn_tma.cuh"
-#include "ptx.cuh"
-#include "tc.cuh"
+#include "attn_ptx.cuh"
 
 namespace kda {
 namespace {

@@ -16,7 +16,6 @@ constexpr int kErrPrefillWait = 1 << 1;
 constexpr int kErrTestingWait = 1 << 2;
 constexpr int kErrLowrankWait = 1 << 3;
 constexpr int kErrProjWait = 1 << 4;
-constexpr int kErrAttnWait = 1 << 5;
 
 // Longest a kernel waits on one barrier phase before it reports an error.
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;   // 1 s
@@ -54,19 +53,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* m, uint32_t parity) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(m)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Whether that phase is complete, without waiting for it.
-__device__ __forceinline__ bool mbar_test(uint64_t* m, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
         : "r"(smem_u32(m)), "r"(parity)
@@ -180,17 +166,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0,
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(smem_u32(dst)), "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(m))
-        : "memory");
-}
-
-// Tiled TMA load of a 5-D box (coordinates innermost first) into shared
-// memory, completing its bytes on mbarrier m.
-__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, int c4,
-                                            uint64_t* m) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-        ::"r"(smem_u32(dst)), "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(m))
         : "memory");
 }
 

@@ -37,12 +37,6 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// The same with 8-row atoms `eight` bytes apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t eight) {
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(eight >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
 // The descriptor of the operand `off` bytes (a multiple of 16) past the one
 // `d` describes.  The start-address field holds bits 4..17 of the
 // shared-memory address and every operand lies below 256 KiB, so the sum
@@ -58,38 +52,10 @@ __host__ __device__ constexpr uint32_t idesc_tf32(int M, int N) {
     return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Shared-memory matrix descriptor of an MN-major SW128 operand: rows of 128
-// bytes (64 16-bit elements of MN) for consecutive K, 8-row atoms `eight` bytes
-// apart along K, further blocks of 64 elements of MN `block` bytes on.
-__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t block, uint32_t eight) {
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(eight >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-// Instruction descriptor: kind::f16 with A and B both bf16 or both f16, D =
-// f32, A K-major, B K-major or (b_mn) MN-major.
-__host__ __device__ constexpr uint32_t idesc_f16kind(int M, int N, bool bf16, bool b_mn) {
-    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
-           ((uint32_t)(M >> 4) << 24);
-}
-
 // Instruction descriptor: kind::f16 with bf16 A and B, D = f32, both K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-
-// True in one lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t one;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-    return one != 0;
-}
-
-// Registers of the calling warpgroup's threads (every warp of it calls).
-template <int kRegs>
-__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-template <int kRegs>
-__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
 // Whole-warp TMEM allocation; the base address is written to *dst (shared).
 __device__ __forceinline__ void alloc(uint32_t* dst, uint32_t ncols) {
@@ -123,14 +89,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}\n"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
-}
-
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands (A packed two per 32-bit column)
-__device__ __forceinline__ void mma_ts_f16kind(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
