@@ -152,7 +152,7 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
         if (ctl.pre[mid] <= pair) lo = mid; else hi = mid - 1;
     }
     int at = ctl.pre[lo], b = lo * sc.per, n;
-    while (at + (n = pairs_of(a, b)) <= pair) {
+    while (at + (n = pairs_of(a, b)) <= pair && b + 1 < a.io.B) {
         at += n;
         ++b;
     }
