@@ -312,11 +312,12 @@ kda_status kda_attn_prefill(kda_attn_ctx* ctx, int B, int N, const int32_t* cu_n
     return kda::launched(ctx, kda::kInjectPrefill, "attn_prefill launch", [&] {
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
         const bool many = !kda::attn_few_rows(N, ctx->layer.G);   // else no request can have more rows
+        const bool all = many && kda::attn_all_many(B, N, ctx->layer.G);
         if (many) {
             kda::AttnIO m = io;
             m.workspace = static_cast<uint8_t*>(workspace) + kda::attn_decode_workspace_bytes(ctx->dev);
-            const cudaError_t e = kda::launch_attn_many_rows(ctx->layer, ctx->maps, m, ctx->dev, ctx->err_word, st);
-            if (e != cudaSuccess) return e;
+            const cudaError_t e = kda::launch_attn_many_rows(ctx->layer, ctx->maps, m, ctx->dev, ctx->err_word, st, all);
+            if (e != cudaSuccess || all) return e;
         }
         return kda::launch_attn_few_rows(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word, st, many);
     });

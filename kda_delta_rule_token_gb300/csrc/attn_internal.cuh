@@ -96,7 +96,8 @@ bool attn_decode_maps(const AttnLayer& l, AttnMaps& maps);
 bool attn_prefill_maps(const AttnLayer& l, AttnMaps& maps);
 // attn_decode.cu: every request of one token (cu_new null), or those of
 // attn_few_rows (the others are left alone), and the zero rows of requests
-// without keys.  attn_prefill.cu: the remaining requests of a call.
+// without keys.  attn_prefill.cu: the remaining requests of a call, or (`all`)
+// all of them.
 size_t attn_decode_workspace_bytes(const DeviceInfo& dev);
 size_t attn_prefill_workspace_bytes(const DeviceInfo& dev);
 // `beside`: the few-row kernel may start beside the launches before it, the
@@ -105,7 +106,7 @@ size_t attn_prefill_workspace_bytes(const DeviceInfo& dev);
 cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
                                  int* err_word, cudaStream_t stream, bool beside);
 cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
-                                  int* err_word, cudaStream_t stream);
+                                  int* err_word, cudaStream_t stream, bool all);
 
 // Which of the two takes a request of n new tokens and G query heads per key
 // head: up to 32 rows fit two 16-row warp tiles, whose kernel streams the
@@ -114,6 +115,13 @@ constexpr int kAttnFewRows = 32;
 __host__ __device__ __forceinline__ bool attn_few_rows(int n, int G) {
     return n <= 1 || (long long)n * G <= kAttnFewRows;
 }
+
+// Whether a call of B requests and N tokens is left to the many-row kernel as
+// a whole, which saves the two launches of the few-row one (6 us of a 512-token
+// prompt's 25 us).  The host knows the requests' mean length only: from 512
+// rows on, few-row requests among them are a small part of the work (on their
+// own they run up to 1.5 times longer there in e4m3, the same in bf16).
+inline bool attn_all_many(int B, int N, int G) { return B == 1 || (long long)N * G >= 512LL * B; }
 
 #ifdef __CUDACC__
 __device__ __forceinline__ int attn_kv_len(const AttnIO& io, int b, int page_shift) {

@@ -108,6 +108,7 @@ struct PrefillArgs {
     AttnIO io;
     int Hq, Hkv, G;
     int tokens;              // of a tile: 128 / G
+    int all;                 // few-row requests and those without keys are taken too
     int part_cost;           // key tiles that starting and ending a segment costs beside its own, as measured:
                              // 3.8 us of 1.35 us tiles in bf16, 5.3 us of 1.5 us in e4m3
     int page_shift, num_pages;
@@ -140,7 +141,7 @@ __device__ __forceinline__ float* slot_at(void* ws, int ctas, int slot) {
 __device__ __forceinline__ int pairs_of(const PrefillArgs& a, int b) {
     int tok0, n;
     attn_tokens(a.io, b, tok0, n);
-    if (n == 0 || attn_few_rows(n, a.G) || attn_kv_len(a.io, b, a.page_shift) == 0) return 0;
+    if (n == 0 || (!a.all && (attn_few_rows(n, a.G) || attn_kv_len(a.io, b, a.page_shift) == 0))) return 0;
     return (n + 2 * a.tokens - 1) / (2 * a.tokens);
 }
 
@@ -944,7 +945,7 @@ size_t attn_prefill_workspace_bytes(const DeviceInfo& dev) {
 }
 
 cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
-                                  int* err_word, cudaStream_t stream) {
+                                  int* err_word, cudaStream_t stream, bool all) {
     if (dev.device < 0 || dev.device >= 64 || dev.sm_count > kMaxCtas) return cudaErrorInvalidDevice;
     if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
         cudaError_t e = prepare_kernel<false>();
@@ -958,6 +959,7 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
     a.Hkv = l.Hkv;
     a.G = l.G;
     a.tokens = kRows / l.G;
+    a.all = all;
     a.part_cost = l.e4m3 ? 4 : 3;
     a.page_shift = l.page_shift;
     a.num_pages = l.num_pages;

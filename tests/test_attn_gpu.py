@@ -422,6 +422,10 @@ def test_prefill_long_prompt():
     # one long segment among many short ones: the keys are cut
     ([64, 300, 300], [20000, 300, 400], 8, 4, 32, False),
     ([40] * 12 + [70], [300] * 12 + [17000], 8, 4, 16, True),
+    # a long mean length with single tokens, empty requests and unseen rows among them
+    ([1, 900, 0, 3, 700, 40], [3000, 900, 50, 0, 2000, 20], 8, 2, 16, False),
+    ([1, 900, 0, 3, 700, 40], [3000, 900, 50, 0, 2000, 20], 8, 2, 64, True),
+    ([50], [0], 4, 1, 16, False),
     # more requests than threads look at once, small and large chunks mixed
     ([(7 * i) % 50 for i in range(300)], [(7 * i) % 50 + (13 * i) % 200 for i in range(300)], 4, 1, 16, False),
 ])
