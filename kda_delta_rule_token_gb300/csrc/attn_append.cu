@@ -6,7 +6,12 @@
 //
 // The call moves each value once (reads (Hq + 2 Hkv) * 128 bf16 per token,
 // writes as many in bf16 or e4m3) and computes a few operations per byte: it
-// is bound by HBM at prompt sizes and by the launch at single tokens.
+// is bound by HBM at prompt sizes and by the launch at single tokens.  Measured:
+// 16381 tokens of 32 + 8 + 8 heads in bf16, 403 MB: 78 us, 5.2 TB/s, 0.77 of the
+// measured copy rate; one token 4 us.  What is left at prompt sizes is the
+// latency of each half warp's chain position -> angles -> rows (the SMs issue
+// 43 % of the time): fewer rows loaded ahead (two: 88 us), more CTAs per SM
+// (four: 79 us) or more half warps per token (two: 89 us) were not faster.
 //
 // Sixteen lanes (a half warp) take one token, or a share of its heads, and go
 // through them a row at a time, eight consecutive channels per lane (16-byte

@@ -3,8 +3,11 @@
 //   S = scale * Q K^T,  P = exp(S - ref),  O = P V / sum(P),   keys in tiles of 128
 //
 // A prompt token's head takes part in 4 * 128 operations per key: the call is
-// bound by the tensor pipe and, on a par with it, by the exponentials (a 128 x
-// 128 tile of each takes the SM 512 cycles).
+// bound by the tensor pipe (a 128 x 128 tile of S and of O take it 512 cycles
+// each, its exponentials take the SM 512 as well).  Measured: 8192 tokens of 64
+// heads in bf16 617 us, 1783 TFLOP/s of the tokens' own operations, 0.91 of the
+// measured dense rate (e4m3: 700 us, 1572); one key tile of two row tiles takes
+// 2300 cycles of which the tensor pipe works 2048.
 //
 // The rows of one key head are (token, query head) pairs: floor(128 / G) tokens
 // with their G heads fill one 128-row tile, so that all heads that share a key
@@ -16,7 +19,8 @@
 //    into two slots each;
 //  * one thread issues the MMAs: S_X(j) = Q_X K_j^T into TMEM, and
 //    O_X += P_X(j) V_j with P_X read from TMEM.  While the softmax of one
-//    tile runs, the MMAs of the other one do;
+//    tile runs, the MMAs of the other one do.  What that thread executes
+//    between two MMAs was what limited the kernel for long (see there);
 //  * four warps per tile do the softmax, one thread per row: the row's 128
 //    logits from TMEM, its maximum against a running reference, the
 //    exponentials, and their bf16 roundings back into TMEM over S_X.  A row
@@ -27,12 +31,16 @@
 //
 // TMEM: S_0, S_1 (128 columns each, P_X in the first 64), O_0, O_1.
 //
+// P is rounded to bf16 (half a step, 2^-8 of each weight, or f16's 2^-11 for
+// e4m3) as the MMA's operand; the sum it is divided by is of the fp32 weights.
+//
 // CTAs are persistent.  Segments are numbered with the longest of a request
 // first and dealt to the CTAs back and forth, which evens out the causal
-// triangle.  When there are fewer segments than CTAs and the longest is well
-// above the average share, the keys are cut instead: each CTA takes an equal
-// range of (segment, key tile) units and leaves partial results, joined in a
-// fixed order by a dependent launch.
+// triangle.  Where the busiest CTA would then be well above the average share
+// (few segments, or long and short ones together), the keys are cut instead:
+// each CTA takes an equal range of (segment, key tile) units and leaves partial
+// results, joined in a fixed order by a dependent launch (128 tokens behind
+// 32640 cached ones, 16 segments: 70 us).
 #include <atomic>
 #include <type_traits>
 
@@ -100,8 +108,10 @@ struct Ctl {
     int load[kMaxCtas];      // of each CTA, were the segments dealt whole
 };
 
+// Behind the operands: e4m3, a K and a V tile as copied; bf16, 16 KiB for
+// either tile's results on their way out (e4m3: in Q_x).
 template <bool kE4m3>
-constexpr uint32_t smem_bytes() { return kOffStage + (kE4m3 ? 2 * kBlock : 0) + (uint32_t)sizeof(Ctl); }
+constexpr uint32_t smem_bytes() { return kOffStage + 2 * kBlock + (uint32_t)sizeof(Ctl); }
 static_assert(kOffStage + 2 * kBlock + sizeof(Ctl) <= 232448, "shared memory");
 
 struct PrefillArgs {
@@ -109,8 +119,8 @@ struct PrefillArgs {
     int Hq, Hkv, G;
     int tokens;              // of a tile: 128 / G
     int all;                 // few-row requests and those without keys are taken too
-    int part_cost;           // key tiles that starting and ending a segment costs beside its own, as measured:
-                             // 3.8 us of 1.35 us tiles in bf16, 5.3 us of 1.5 us in e4m3
+    int part_cost;           // key tiles that starting and ending a segment costs beside its own: what deals
+                             // ragged chunks best (bf16: 130 us at 3, 137 at 2; e4m3: 5.3 us of 1.5 us tiles)
     int page_shift, num_pages;
     float scale;             // softmax scale * log2(e)
     const float* k_scale;
@@ -296,7 +306,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     constexpr float kOffset = kE4m3 ? 10.f : 0.f;
     constexpr float kLimit = kE4m3 ? 15.f : 8.f;
     extern __shared__ __align__(1024) uint8_t sm[];
-    Ctl& ctl = *reinterpret_cast<Ctl*>(sm + kOffStage + (kE4m3 ? 2 * kBlock : 0));
+    Ctl& ctl = *reinterpret_cast<Ctl*>(sm + kOffStage + 2 * kBlock);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int* dead = &ctl.dead;
 
@@ -477,6 +487,9 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         //  * each barrier is tested before the batch of MMAs that precedes its
         //    use, and waited for only if it was not complete by then;
         //  * giving up leaves the loop from the waits, the MMAs carry no condition.
+        // (With runtime operands and conditions at each MMA the same kernel
+        // ran 8191 tokens of 32 heads in 568 us, with conditions alone in 442,
+        // like this in 333; without any exponentials it then took 349.)
         tc::reg_dec<kRegsOther>();
         Part p;
         int np = 0;
@@ -635,63 +648,87 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         const uint32_t ts = tc::taddr(tm, warp, kColS + 128 * x), to = tc::taddr(tm, warp, kColO + 128 * x);
         uint32_t spar = 0u, opar = 0u;
         bool ok = true;
-        const int chunk = lane & 15;                       // 16 bytes of a row, as rows are copied two at a time
-        uint8_t* rows_x = sm + kOffQ + x * kOperand + (warp & 3) * 32 * 128;   // the warp's rows: two blocks of 128 bytes each
-        auto place = [&](int row, int c) { return rows_x + (c >> 3) * kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
-        while (ok && take_part(ctl, np, p, dead, err)) {
-            const int tokens = p.s.tokens_of(x, a.tokens);
-            const int tok = p.s.tok + x * a.tokens + i_row;
-            const bool live = i_row < tokens;
-            const size_t head = (size_t)tok * a.Hq + p.s.h * a.G + g_row;
-            // The head of the row that this lane copies in round i, and whether it has a token.
-            auto head_of = [&](int i) { return (size_t)__shfl_sync(0xffffffffu, (unsigned long long)head, 2 * i + (lane >> 4)); };
-            const uint32_t lives = __ballot_sync(0xffffffffu, live);
+        // The warp's 32 rows of Q_x, and of the results on their way out (rows
+        // of kOut bytes), both swizzled as TMA would.
+        constexpr int kOut = kE4m3 ? 256 : 128, kOutLanes = kOut / 16, kOutRows = 32 / kOutLanes;
+        uint8_t* rows_q = sm + kOffQ + x * kOperand + (warp & 3) * 32 * 128;
+        uint8_t* rows_o = sm + kOffStage + warp * 32 * 128;
+        auto place_q = [&](int row, int c) { return rows_q + (c >> 3) * kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
+        auto place_o = [&](int row, int c) { return kE4m3 ? place_q(row, c) : rows_o + row * 128 + ((c ^ (row & 7)) << 4); };
+        // A part as this thread's row and the warp's rows see it.
+        struct Rows {
+            bool live;           // the row has a token
+            uint32_t lives;      // the warp's rows that have
+            size_t head;         // of the output, and of q
+            float fac;           // logit -> power of two
+        };
+        auto head_of = [&](const Rows& w, int row) { return (size_t)__shfl_sync(0xffffffffu, (unsigned long long)w.head, row); };
+        // Q rows into shared memory: the copies, two rows a round, and what
+        // follows them.  The loops that run once per part stay rolled: their
+        // instructions come from L2 each time.
+        auto start_rows = [&](const Part& part) {
+            Rows w;
+            w.live = i_row < part.s.tokens_of(x, a.tokens);
+            w.lives = __ballot_sync(0xffffffffu, w.live);
+            w.head = ((size_t)part.s.tok + x * a.tokens + i_row) * a.Hq + part.s.h * a.G + g_row;
+            w.fac = a.scale;
+            if (part.cnt[x] > 0) {
+#pragma unroll 2
+                for (int i = 0; i < 16; ++i) {
+                    const int row = 2 * i + (lane >> 4), c = lane & 15;
+                    const size_t h = head_of(w, row);
+                    ptx::cp_async16(place_q(row, c), a.io.q + h * kHeadDim + 8 * c, w.lives >> row & 1u);
+                }
+                ptx::cp_async_commit();
+            }
+            return w;
+        };
+        auto finish_rows = [&](const Part& part, Rows& w) {
+            if (part.cnt[x] <= 0) return;
+            ptx::cp_async_wait_all();
+            __syncwarp();
+            if (kE4m3) {
+                // To f16, each lane its row: q * 2^(14 - e) with 2^e <= the row's
+                // largest < 2^(e+1), exact down to 2^-28 of it.
+                float top = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(place_q(lane, c));
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        top = mma::max3(top, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
+                }
+                const int ex = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
+                const float up = exp2f((float)(14 - ex));
+                w.fac = a.scale * a.k_scale[part.s.h] * exp2f((float)(ex - 14));
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    uint4* at = reinterpret_cast<uint4*>(place_q(lane, c));
+                    const uint4 v = *at;
+                    uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        u[e] = mma::pack_f16(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
+                    *at = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            tc::fence_before();
+            ptx::mbar_arrive(&ctl.qfull[x]);
+        };
+        Rows w{};
+        bool more = take_part(ctl, np, p, dead, err);
+        if (more) {
+            w = start_rows(p);
+            finish_rows(p, w);
+        }
+        while (more) {
+            const bool live = w.live;
+            const float fac = w.fac;
             float ref = kNoRef, sum = 0.f;
             const int cnt = p.cnt[x];
             if (cnt > 0) {
-                // Q rows into shared memory (swizzled as TMA would), two per
-                // round.  The loops that run once per part stay rolled: their
-                // instructions come from L2 each time.
-                float fac = a.scale;
-#pragma unroll 2
-                for (int i = 0; i < 16; ++i) {
-                    const int row = 2 * i + (lane >> 4);
-                    const size_t h = head_of(i);
-                    ptx::cp_async16(place(row, chunk), a.io.q + h * kHeadDim + 8 * chunk, lives >> row & 1u);
-                }
-                ptx::cp_async_commit();
-                ptx::cp_async_wait_all();
-                __syncwarp();
-                if (kE4m3) {
-                    // To f16, each lane its row: q * 2^(14 - e) with 2^e <= the row's
-                    // largest < 2^(e+1), exact down to 2^-28 of it.
-                    float top = 0.f;
-#pragma unroll 4
-                    for (int c = 0; c < 16; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(place(lane, c));
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            top = mma::max3(top, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
-                    }
-                    const int ex = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
-                    const float up = exp2f((float)(14 - ex));
-                    fac = a.scale * a.k_scale[p.s.h] * exp2f((float)(ex - 14));
-#pragma unroll 4
-                    for (int c = 0; c < 16; ++c) {
-                        uint4* at = reinterpret_cast<uint4*>(place(lane, c));
-                        const uint4 v = *at;
-                        uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            u[e] = mma::pack_f16(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
-                        *at = make_uint4(u[0], u[1], u[2], u[3]);
-                    }
-                }
-                ptx::fence_proxy_async_smem();
-                tc::fence_before();
-                ptx::mbar_arrive(&ctl.qfull[x]);
-
                 // Keys that the row sees; rows without a token see all (their q is zero, nothing is stored).
                 const int sees = live ? p.s.first + x * a.tokens + i_row : 0x7fffffff;
                 for (int j = p.j0; j < p.j0 + cnt; ++j) {
@@ -764,77 +801,99 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                     sum += u + v;
                 }
                 if (!ok) break;
+            }
+            // bf16: the next part's Q rows come in under the last MMAs, and its
+            // first logits are computed while these results go out (S_x and
+            // Q_x are free once O_x is complete).
+            Part pn;
+            Rows wn{};
+            bool more_n = false;
+            if (!kE4m3) {
+                more_n = take_part(ctl, np, pn, dead, err);
+                if (more_n) wn = start_rows(pn);
+            }
+            if (cnt > 0) {
                 ok = pwait(&ctl.ofull[x], opar, dead, err);
                 opar ^= 1u;
                 tc::fence_after();
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             }
+            if (!kE4m3 && more_n) finish_rows(pn, wn);
             // The rows' results, or this part's share of them, through shared
-            // memory (Q_x is not read any more) so that whole rows are
-            // stored together: 64 channels at a time.
+            // memory so that whole stretches of rows are stored together: in
+            // bf16 where that is all there is to write, else in fp32.
             const bool whole = p.slot < 0;
             float* part = whole ? nullptr : slot_at(a.io.workspace, gridDim.x, p.slot);
             if (cnt > 0) {
                 const float n = !whole ? 1.f : sum > 0.f ? (kE4m3 ? a.v_scale[p.s.h] : 1.f) / sum : 0.f;
-                const bool plain = whole && !a.io.gate && !a.io.o_f32;   // bf16, all channels at once
-                if (plain) {
+                const bool plain = whole && !a.io.gate && !a.io.o_f32;
+                const int step = plain ? kOut / 2 : kOut / 4;   // channels at a time
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                for (int c0 = 0; c0 < kHeadDim; c0 += step) {
+#pragma unroll 1
+                    for (int c1 = 0; c1 < step; c1 += 32) {
                         uint32_t o[32];
-                        tc::ld32(to + 32 * c, o);
+                        tc::ld32(to + c0 + c1, o);
                         tc::wait_ld();
+                        if (plain) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(place(lane, 4 * c + (e >> 3))) = make_uint4(
-                                mma::pack_bf16(__uint_as_float(o[e]) * n, __uint_as_float(o[e + 1]) * n),
-                                mma::pack_bf16(__uint_as_float(o[e + 2]) * n, __uint_as_float(o[e + 3]) * n),
-                                mma::pack_bf16(__uint_as_float(o[e + 4]) * n, __uint_as_float(o[e + 5]) * n),
-                                mma::pack_bf16(__uint_as_float(o[e + 6]) * n, __uint_as_float(o[e + 7]) * n));
+                            for (int e = 0; e < 32; e += 8)
+                                *reinterpret_cast<uint4*>(place_o(lane, (c1 + e) >> 3)) = make_uint4(
+                                    mma::pack_bf16(__uint_as_float(o[e]) * n, __uint_as_float(o[e + 1]) * n),
+                                    mma::pack_bf16(__uint_as_float(o[e + 2]) * n, __uint_as_float(o[e + 3]) * n),
+                                    mma::pack_bf16(__uint_as_float(o[e + 4]) * n, __uint_as_float(o[e + 5]) * n),
+                                    mma::pack_bf16(__uint_as_float(o[e + 6]) * n, __uint_as_float(o[e + 7]) * n));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4*>(place_o(lane, (c1 + e) >> 2)) =
+                                    make_float4(__uint_as_float(o[e]) * n, __uint_as_float(o[e + 1]) * n,
+                                                __uint_as_float(o[e + 2]) * n, __uint_as_float(o[e + 3]) * n);
+                        }
                     }
                     __syncwarp();
+                    const int c = lane % kOutLanes, row0 = lane / kOutLanes;
+                    if (plain) {
 #pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        const int row = 2 * i + (lane >> 4);
-                        const size_t h = head_of(i);
-                        const uint4 v = *reinterpret_cast<const uint4*>(place(row, chunk));
-                        if (lives >> row & 1u) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.io.o) + h * kHeadDim + 8 * chunk) = v;
-                    }
-                    __syncwarp();
-                }
-#pragma unroll 1
-                for (int half = plain ? 2 : 0; half < 2; ++half) {
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t o[32];
-                        tc::ld32(to + 64 * half + 32 * c, o);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(place(lane, 8 * c + (e >> 2))) =
-                                make_float4(__uint_as_float(o[e]) * n, __uint_as_float(o[e + 1]) * n,
-                                            __uint_as_float(o[e + 2]) * n, __uint_as_float(o[e + 3]) * n);
-                    }
-                    __syncwarp();
-#pragma unroll 2
-                    for (int i = 0; i < 16; ++i) {
-                        const int row = 2 * i + (lane >> 4);
-                        const size_t h = head_of(i);
-                        const float4 v = *reinterpret_cast<const float4*>(place(row, chunk));
-                        if (lives >> row & 1u) {
-                            if (whole) mma::store4(a.io, h * kHeadDim + 64 * half + 4 * chunk, v);
-                            else *reinterpret_cast<float4*>(part + (size_t)((warp & 7) * 32 + row) * kHeadDim + 64 * half + 4 * chunk) = v;
+                        for (int row = row0; row < 32; row += kOutRows) {
+                            const size_t h = head_of(w, row);
+                            const uint4 v = *reinterpret_cast<const uint4*>(place_o(row, c));
+                            if (w.lives >> row & 1u)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.io.o) + h * kHeadDim + c0 + 8 * c) = v;
+                        }
+                    } else {
+#pragma unroll 4
+                        for (int row = row0; row < 32; row += kOutRows) {
+                            const size_t h = head_of(w, row);
+                            const float4 v = *reinterpret_cast<const float4*>(place_o(row, c));
+                            if (w.lives >> row & 1u) {
+                                if (whole) mma::store4(a.io, h * kHeadDim + c0 + 4 * c, v);
+                                else *reinterpret_cast<float4*>(part + (size_t)(warp * 32 + row) * kHeadDim + c0 + 4 * c) = v;
+                            }
                         }
                     }
                     __syncwarp();
                 }
                 tc::fence_before();
             }
+            const size_t head = w.head;
             if (live && whole && a.io.lse) a.io.lse[head] = sum > 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
             if (live && !whole)
                 *reinterpret_cast<float2*>(part + (size_t)2 * kRows * kHeadDim + 2 * (x * kRows + r)) = make_float2(ref, sum);
             if (tid == 0 && p.last >= 0)
                 joins(a.io.workspace)[blockIdx.x] = PrefillJoin{p.s.tok, p.s.m, p.s.h, p.last, p.slot, {0, 0, 0}};
+            if (kE4m3) {
+                more_n = take_part(ctl, np, pn, dead, err);
+                if (more_n) {
+                    wn = start_rows(pn);
+                    finish_rows(pn, wn);
+                }
+            }
+            p = pn;
+            w = wn;
+            more = more_n;
         }
+        ptx::cp_async_wait_all();   // of a part that was given up
     } else {
         tc::reg_dec<kRegsOther>();
     }
