@@ -10,7 +10,7 @@
 // 176 us, 0.98 of the measured copy rate; one request of 262139 keys 91 us,
 // 0.88; 256 requests in e4m3, 1.16 GB, 190 us, 0.91.  From 17 rows on the
 // products of a tile take as long as its copy: 32 requests of 5 tokens and 4
-// heads, 295 MB, 76 us, 0.58.  The kernel is built around keeping enough bytes
+// heads, 295 MB, 74.5 us, 0.59; 128 of 4096 keys, 2.1 GB, 394 us, 0.81.  The kernel is built around keeping enough bytes
 // in flight on every SM:
 //
 //  * Work is cut into units of one tile (16 keys in bf16, 32 in e4m3) per warp
@@ -31,7 +31,9 @@
 //    part in at most 64 operations there, which the warp-wide instruction
 //    covers without a wait between warps.  From 17 rows on two warps share a
 //    tile's copy, each with its 16 rows (one warp with both halves: twice the
-//    time); beyond 32 query heads of one token there are several passes.  The
+//    time); a request of fewer rows in the same call lets the two take tiles by
+//    turns (128 requests of 4 tokens, 2.1 GB in bf16, 355 us; with the second
+//    warp on empty rows 412; in e4m3 255 and 331); beyond 32 query heads of one token there are several passes.  The
 //    softmax keeps a reference (not the exact maximum) per row and rescales
 //    only when a logit passes it by more than kLimit powers of two: the result
 //    is the same, the rescaling almost never runs.
@@ -343,9 +345,10 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     uint32_t raw[2][16];
     auto load_rows = [&](const Walk& w) {
         const Rows x = rows_of(w);
+        const int first = kRowTiles > 1 && x.n > 16 ? row_tile * 16 : 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int r = row_tile * 16 + half * 8 + g;
+            const int r = first + half * 8 + g;
             const uint16_t* q = a.io.q + head_of(w, x, r) * kHeadDim;
             if (!kE4m3) {
 #pragma unroll
@@ -371,6 +374,10 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         if (kRowTiles > 1) load_rows(cur);
         const Rows rw = rows_of(cur);
         const int h = rw.h, nrows = rw.n;
+        // The warps of a group share its tiles, each with rows of its own, or,
+        // where one row tile holds them all, take them by turns.
+        const bool turns = kRowTiles > 1 && nrows <= 16;
+        const int first_row = turns ? 0 : row_tile * 16;
         const int u0 = cur.u, u1 = (int)min((long long)cur.units, u0 + cur.left);
 
         uint32_t qf[8][4];   // A fragments
@@ -379,7 +386,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         const float base = a.scale * (kE4m3 ? a.k_scale[h] : 1.f);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int r = row_tile * 16 + half * 8 + g;
+            const int r = first_row + half * 8 + g;
             const uint32_t (&w)[16] = raw[half];
             fac[half] = base;
             sees[half] = cur.n > 1 && r < nrows ? cur.len - cur.n + 1 + r / a.G : cur.len;
@@ -425,159 +432,161 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
                 break;
             }
             ++used;
-            uint8_t* stage = ring + s * kStageBytes;
-            const uint32_t ks = ptx::smem_u32(stage), vs = ks + kTileBytes;
-            const int valid = cur.len - key0;   // keys of the tile, if below kTile
-            if (valid < kTile) {
-                // Values past the request's end may be anything, NaN too: their
-                // weight is 0, make them 0 (every warp of the group writes the same).
-                for (int i = lane; i < (int)kTileBytes / 16; i += 32) {
-                    const int row = kE4m3 ? i >> 3 : (i >> 3) & 15;
-                    if (row >= valid) *reinterpret_cast<uint4*>(stage + kTileBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-            }
-
-            // Logits: rows = query heads, columns = keys.
-            float sc[kNT][4];
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
-            if (!kE4m3) {
-                const int key = (lane & 7) + ((lane >> 4) << 3), odd = (lane >> 3) & 1;
-#pragma unroll
-                for (int st = 0; st < 8; ++st) {
-                    const int ch = 2 * st + odd;   // 16-byte chunk of the key's row
-                    uint32_t b[4];
-                    mma::ldmatrix4(b, ks + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
-                    mma::m16n8k16<false>(sc[0], qf[st], b[0], b[1]);
-                    mma::m16n8k16<false>(sc[1], qf[st], b[2], b[3]);
-                }
-            } else {
-                // Column n of a tile is key 4 (n % 2) + n / 2 of its eight, so
-                // that the two rows that a quarter warp reads lie in different banks.
-                const int kr = ((g & 1) << 2) | (g >> 1);
-#pragma unroll
-                for (int n = 0; n < kNT; ++n) {
-                    const uint32_t rowp = ks + (n * 8 + kr) * 128;
-                    const uint4 lo = mma::lds128(rowp + ((c ^ kr) << 4)), hi = mma::lds128(rowp + (((c + 4) ^ kr) << 4));
-                    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                    for (int st = 0; st < 8; ++st) {
-                        const uint32_t x0 = mma::e4m3x2_f16x2(w[st]), x1 = mma::e4m3x2_f16x2(w[st] >> 16);
-                        mma::m16n8k16<true>(sc[n], qf[st], x0, x1);
+            if (!turns || (u - u0) % kRowTiles == row_tile) {
+                uint8_t* stage = ring + s * kStageBytes;
+                const uint32_t ks = ptx::smem_u32(stage), vs = ks + kTileBytes;
+                const int valid = cur.len - key0;   // keys of the tile, if below kTile
+                if (valid < kTile) {
+                    // Values past the request's end may be anything, NaN too: their
+                    // weight is 0, make them 0 (every warp that reads them writes the same).
+                    for (int i = lane; i < (int)kTileBytes / 16; i += 32) {
+                        const int row = kE4m3 ? i >> 3 : (i >> 3) & 15;
+                        if (row >= valid) *reinterpret_cast<uint4*>(stage + kTileBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
                 }
-            }
-            if (valid - (cur.n - 1) < kTile) {
-#pragma unroll
+
+                // Logits: rows = query heads, columns = keys.
+                float sc[kNT][4];
+    #pragma unroll
                 for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int k = key0 + n * 8 + (kE4m3 ? c + 4 * e : 2 * c + e);
-                        if (k >= sees[0]) sc[n][e] = -INFINITY;
-                        if (k >= sees[1]) sc[n][e + 2] = -INFINITY;
+    #pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+                if (!kE4m3) {
+                    const int key = (lane & 7) + ((lane >> 4) << 3), odd = (lane >> 3) & 1;
+    #pragma unroll
+                    for (int st = 0; st < 8; ++st) {
+                        const int ch = 2 * st + odd;   // 16-byte chunk of the key's row
+                        uint32_t b[4];
+                        mma::ldmatrix4(b, ks + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+                        mma::m16n8k16<false>(sc[0], qf[st], b[0], b[1]);
+                        mma::m16n8k16<false>(sc[1], qf[st], b[2], b[3]);
                     }
-            }
-
-            // Softmax weights against the row's reference.
-            uint32_t hi[kNT][2], lo[kNT][2];   // A fragments of the weights, rows g and g + 8
-            // A row is looked at as a whole only when one of its logits passes the reference.
-            float top[2];
-            bool raise = false;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float m = fmaxf(sc[0][2 * half], sc[0][2 * half + 1]);
-#pragma unroll
-                for (int n = 1; n < kNT; ++n) m = mma::max3(m, sc[n][2 * half], sc[n][2 * half + 1]);
-                top[half] = m * fac[half];
-                raise |= top[half] > ref[half] + kLimit;
-            }
-            if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float m = top[half];
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    if (m > ref[half] + kLimit) {
-                        const float to_ref = m - kOffset;
-                        const float f = mma::exp2_approx(ref[half] - to_ref);
-                        ref[half] = to_ref;
-                        sum[half] *= f;
-#pragma unroll
-                        for (int n = 0; n < 16; ++n) {
-                            acc[n][2 * half] *= f;
-                            acc[n][2 * half + 1] *= f;
+                } else {
+                    // Column n of a tile is key 4 (n % 2) + n / 2 of its eight, so
+                    // that the two rows that a quarter warp reads lie in different banks.
+                    const int kr = ((g & 1) << 2) | (g >> 1);
+    #pragma unroll
+                    for (int n = 0; n < kNT; ++n) {
+                        const uint32_t rowp = ks + (n * 8 + kr) * 128;
+                        const uint4 lo = mma::lds128(rowp + ((c ^ kr) << 4)), hi = mma::lds128(rowp + (((c + 4) ^ kr) << 4));
+                        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    #pragma unroll
+                        for (int st = 0; st < 8; ++st) {
+                            const uint32_t x0 = mma::e4m3x2_f16x2(w[st]), x1 = mma::e4m3x2_f16x2(w[st] >> 16);
+                            mma::m16n8k16<true>(sc[n], qf[st], x0, x1);
                         }
                     }
                 }
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int n = 0; n < kNT; ++n) {
-                    const float p0 = mma::exp2_approx(fmaf(sc[n][2 * half], fac[half], -ref[half]));
-                    const float p1 = mma::exp2_approx(fmaf(sc[n][2 * half + 1], fac[half], -ref[half]));
-                    sum[half] += p0 + p1;
-                    if (kE4m3) {
-                        hi[n][half] = mma::pack_f16(p0, p1);
-                    } else {
-                        const uint32_t p = mma::pack_bf16(p0, p1);
-                        hi[n][half] = p;
-                        lo[n][half] = mma::pack_bf16(p0 - __uint_as_float(p << 16), p1 - __uint_as_float(p & 0xffff0000u));
-                    }
+                if (valid - (cur.n - 1) < kTile) {
+    #pragma unroll
+                    for (int n = 0; n < kNT; ++n)
+    #pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int k = key0 + n * 8 + (kE4m3 ? c + 4 * e : 2 * c + e);
+                            if (k >= sees[0]) sc[n][e] = -INFINITY;
+                            if (k >= sees[1]) sc[n][e + 2] = -INFINITY;
+                        }
                 }
 
-            // Weighted values.
-            if (!kE4m3) {
-                const int key = (lane & 7) + (((lane >> 3) & 1) << 3), odd = lane >> 4;
-                uint32_t ah[4], al[4];
-                ah[0] = hi[0][0]; ah[1] = hi[0][1]; ah[2] = hi[1][0]; ah[3] = hi[1][1];
-                al[0] = lo[0][0]; al[1] = lo[0][1]; al[2] = lo[1][0]; al[3] = lo[1][1];
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    uint32_t b[4][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int ch = 2 * (j + i) + odd;
-                        mma::ldmatrix4_trans(b[i], vs + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mma::m16n8k16<false>(acc[2 * (j + i)], ah, b[i][0], b[i][1]);
-                        mma::m16n8k16<false>(acc[2 * (j + i) + 1], ah, b[i][2], b[i][3]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mma::m16n8k16<false>(acc[2 * (j + i)], al, b[i][0], b[i][1]);
-                        mma::m16n8k16<false>(acc[2 * (j + i) + 1], al, b[i][2], b[i][3]);
+                // Softmax weights against the row's reference.
+                uint32_t hi[kNT][2], lo[kNT][2];   // A fragments of the weights, rows g and g + 8
+                // A row is looked at as a whole only when one of its logits passes the reference.
+                float top[2];
+                bool raise = false;
+    #pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float m = fmaxf(sc[0][2 * half], sc[0][2 * half + 1]);
+    #pragma unroll
+                    for (int n = 1; n < kNT; ++n) m = mma::max3(m, sc[n][2 * half], sc[n][2 * half + 1]);
+                    top[half] = m * fac[half];
+                    raise |= top[half] > ref[half] + kLimit;
+                }
+                if (__any_sync(0xffffffffu, raise)) {
+    #pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float m = top[half];
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                        if (m > ref[half] + kLimit) {
+                            const float to_ref = m - kOffset;
+                            const float f = mma::exp2_approx(ref[half] - to_ref);
+                            ref[half] = to_ref;
+                            sum[half] *= f;
+    #pragma unroll
+                            for (int n = 0; n < 16; ++n) {
+                                acc[n][2 * half] *= f;
+                                acc[n][2 * half + 1] *= f;
+                            }
+                        }
                     }
                 }
-            } else {
-                // Rows of the transposed 8 x 8 loads in the weights' key order; a
-                // 16-bit column holds channels 2 n and 2 n + 1 of its chunk, which
-                // are split into two column tiles.
-                const int i = lane & 7, kr = ((i & 1) << 2) | (i >> 1);
-                const int key8 = ((lane >> 3) & 1) << 3, odd = lane >> 4;
-#pragma unroll
-                for (int k2 = 0; k2 < kTile / 16; ++k2) {
-                    uint32_t ap[4];
-                    ap[0] = hi[2 * k2][0]; ap[1] = hi[2 * k2][1];
-                    ap[2] = hi[2 * k2 + 1][0]; ap[3] = hi[2 * k2 + 1][1];
-                    const uint32_t rowp = vs + (k2 * 16 + key8 + kr) * 128;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t b[4];
-                        mma::ldmatrix4_trans(b, rowp + (((2 * j + odd) ^ kr) << 4));
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {   // chunk 2 j + x
-                            const uint32_t y0 = __byte_perm(b[2 * x], 0, 0x3120), y1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
-                            const uint32_t e0 = mma::e4m3x2_f16x2(y0), e1 = mma::e4m3x2_f16x2(y1);
-                            const uint32_t o0 = mma::e4m3x2_f16x2(y0 >> 16), o1 = mma::e4m3x2_f16x2(y1 >> 16);
-                            mma::m16n8k16<true>(acc[4 * j + 2 * x], ap, e0, e1);
-                            mma::m16n8k16<true>(acc[4 * j + 2 * x + 1], ap, o0, o1);
+    #pragma unroll
+                for (int half = 0; half < 2; ++half)
+    #pragma unroll
+                    for (int n = 0; n < kNT; ++n) {
+                        const float p0 = mma::exp2_approx(fmaf(sc[n][2 * half], fac[half], -ref[half]));
+                        const float p1 = mma::exp2_approx(fmaf(sc[n][2 * half + 1], fac[half], -ref[half]));
+                        sum[half] += p0 + p1;
+                        if (kE4m3) {
+                            hi[n][half] = mma::pack_f16(p0, p1);
+                        } else {
+                            const uint32_t p = mma::pack_bf16(p0, p1);
+                            hi[n][half] = p;
+                            lo[n][half] = mma::pack_bf16(p0 - __uint_as_float(p << 16), p1 - __uint_as_float(p & 0xffff0000u));
+                        }
+                    }
+
+                // Weighted values.
+                if (!kE4m3) {
+                    const int key = (lane & 7) + (((lane >> 3) & 1) << 3), odd = lane >> 4;
+                    uint32_t ah[4], al[4];
+                    ah[0] = hi[0][0]; ah[1] = hi[0][1]; ah[2] = hi[1][0]; ah[3] = hi[1][1];
+                    al[0] = lo[0][0]; al[1] = lo[0][1]; al[2] = lo[1][0]; al[3] = lo[1][1];
+    #pragma unroll
+                    for (int j = 0; j < 8; j += 4) {
+                        uint32_t b[4][4];
+    #pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int ch = 2 * (j + i) + odd;
+                            mma::ldmatrix4_trans(b[i], vs + (ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+                        }
+    #pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            mma::m16n8k16<false>(acc[2 * (j + i)], ah, b[i][0], b[i][1]);
+                            mma::m16n8k16<false>(acc[2 * (j + i) + 1], ah, b[i][2], b[i][3]);
+                        }
+    #pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            mma::m16n8k16<false>(acc[2 * (j + i)], al, b[i][0], b[i][1]);
+                            mma::m16n8k16<false>(acc[2 * (j + i) + 1], al, b[i][2], b[i][3]);
+                        }
+                    }
+                } else {
+                    // Rows of the transposed 8 x 8 loads in the weights' key order; a
+                    // 16-bit column holds channels 2 n and 2 n + 1 of its chunk, which
+                    // are split into two column tiles.
+                    const int i = lane & 7, kr = ((i & 1) << 2) | (i >> 1);
+                    const int key8 = ((lane >> 3) & 1) << 3, odd = lane >> 4;
+    #pragma unroll
+                    for (int k2 = 0; k2 < kTile / 16; ++k2) {
+                        uint32_t ap[4];
+                        ap[0] = hi[2 * k2][0]; ap[1] = hi[2 * k2][1];
+                        ap[2] = hi[2 * k2 + 1][0]; ap[3] = hi[2 * k2 + 1][1];
+                        const uint32_t rowp = vs + (k2 * 16 + key8 + kr) * 128;
+    #pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t b[4];
+                            mma::ldmatrix4_trans(b, rowp + (((2 * j + odd) ^ kr) << 4));
+    #pragma unroll
+                            for (int x = 0; x < 2; ++x) {   // chunk 2 j + x
+                                const uint32_t y0 = __byte_perm(b[2 * x], 0, 0x3120), y1 = __byte_perm(b[2 * x + 1], 0, 0x3120);
+                                const uint32_t e0 = mma::e4m3x2_f16x2(y0), e1 = mma::e4m3x2_f16x2(y1);
+                                const uint32_t o0 = mma::e4m3x2_f16x2(y0 >> 16), o1 = mma::e4m3x2_f16x2(y1 >> 16);
+                                mma::m16n8k16<true>(acc[4 * j + 2 * x], ap, e0, e1);
+                                mma::m16n8k16<true>(acc[4 * j + 2 * x + 1], ap, o0, o1);
+                            }
                         }
                     }
                 }
@@ -611,15 +620,16 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
             ok = false;
             break;
         }
-        constexpr int kRowsAll = 16 * kRowTiles;   // rows of a group
+        const int parts = turns ? kWarps : kGroups, rows = turns ? 16 : 16 * kRowTiles;   // partial results, rows of each
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int r = row_tile * 16 + half * 8 + g;
-            float top = s_ref[r];
+            const int r = first_row + half * 8 + g;
+            float top = kNoRef;
 #pragma unroll
-            for (int w = 1; w < kGroups; ++w) top = fmaxf(top, s_ref[w * kRowsAll + r]);
+            for (int w = 0; w < kWarps; ++w)
+                if (w < parts) top = fmaxf(top, s_ref[w * rows + r]);
             const float f = mma::exp2_approx(ref[half] - top);
-            float* m = sm.merge + (group * kRowsAll + r) * kHeadDim;
+            float* m = sm.merge + (warp * 16 + half * 8 + g) * kHeadDim;
             const int flip = (r & 3) << 3;
 #pragma unroll
             for (int n = 0; n < 16; n += kE4m3 ? 2 : 1) {
@@ -642,13 +652,15 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             float top = kNoRef, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < kGroups; ++w) {
-                const float4 x = *reinterpret_cast<const float4*>(sm.merge + (w * kRowsAll + row) * kHeadDim + (col ^ ((row & 3) << 3)));
-                v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-                top = fmaxf(top, s_ref[w * kRowsAll + row]);
-            }
+            for (int w = 0; w < kWarps; ++w)
+                if (w < parts) {
+                    const float4 x = *reinterpret_cast<const float4*>(sm.merge + (w * rows + row) * kHeadDim + (col ^ ((row & 3) << 3)));
+                    v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+                    top = fmaxf(top, s_ref[w * rows + row]);
+                }
 #pragma unroll
-            for (int w = 0; w < kGroups; ++w) l += s_sum[w * kRowsAll + row] * mma::exp2_approx(s_ref[w * kRowsAll + row] - top);
+            for (int w = 0; w < kWarps; ++w)
+                if (w < parts) l += s_sum[w * rows + row] * mma::exp2_approx(s_ref[w * rows + row] - top);
             if (whole) {
                 const float n = l > 0.f ? vscale / l : 0.f;   // 0: the row sees no key
                 const size_t at = head_of(cur, rw, row);

@@ -439,6 +439,21 @@ def test_prefill_schedules(new, kv, hq, hkv, page, e4m3):
     layer.done()
 
 
+@pytest.mark.parametrize("e4m3,page", [(False, 16), (False, 64), (True, 16), (True, 128)])
+@pytest.mark.parametrize("scale", [1, 40])
+def test_prefill_one_and_two_row_tiles(e4m3, page, scale):
+    """Requests of up to 16 rows and of 17 to 32 side by side, in one part and in many."""
+    new = [4, 5, 1, 8, 0, 2, 6, 4, 4, 7, 3, 8]
+    kv = [scale * x + n for x, n in zip([31, 33, 1, 70, 9, 16, 63, 64, 0, 100, 15, 129], new)]
+    layer = Layer(8, 2, page, e4m3, seed=scale)
+    layer.fill(kv)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    verify(layer, queries(layer, cu[-1]), kv, cu)
+    layer.done()
+
+
 def test_prefill_more_segments_than_are_weighed():
     """64 query heads to a key head: four tokens to a segment, 5000 segments."""
     new = [500] * 40
