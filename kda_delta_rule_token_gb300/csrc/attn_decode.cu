@@ -68,7 +68,9 @@ constexpr int kMostCtasPerSm = 3;
 constexpr uint32_t kTileBytes = 4096;            // keys (or values) of one warp tile
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kMergeBytes = kWarps * 16 * kHeadDim * 4;
-constexpr int kJoinRows = 4;                     // CTAs of the join per part, over rows
+constexpr int kJoinRows = 4;                     // CTAs of the join per request and head, over rows, at least
+constexpr int kFewParts = 8;                     // parts of a row that one warp of the join takes
+constexpr int kJoinCtas = 1024;                  // up to which CTAs per row are added
 constexpr int kMaxRows = kAttnFewRows;           // rows of one pass
 
 template <int kRowTiles>
@@ -694,18 +696,34 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
 }
 
 // Joins the parts of a request and head that lie in several CTAs: blockIdx.x
-// the CTA that holds the first part, blockIdx.y over query rows, four channels
-// per lane.  Few parts: a warp per row.  Many: the eight warps share a row's.
-__global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, int ctas) {
+// the CTA that holds the first part (search: the blockIdx.x-th of those that
+// hold one), blockIdx.y over query rows, four channels per lane.  Few parts: a
+// warp per row.  Many: the eight warps share a row's.
+__global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, int ctas, bool search) {
     __shared__ float4 s_acc[8][32];
     __shared__ float s_ref[8], s_sum[8];
+    __shared__ uint32_t s_used[kJoinCtas / 32];
     ptx::griddep_wait();
-    const JoinDesc d = descs(a.io.workspace)[blockIdx.x];
+    int first = (int)blockIdx.x;
+    if (search) {
+        for (int i = (int)threadIdx.x; i < kJoinCtas; i += 256) {
+            const uint32_t used = __ballot_sync(0xffffffffu, i < ctas && descs(a.io.workspace)[i].b >= 0);
+            if ((threadIdx.x & 31) == 0) s_used[i >> 5] = used;
+        }
+        __syncthreads();
+        int before = first, word = 0;
+        while (word < kJoinCtas / 32 && before >= __popc(s_used[word])) before -= __popc(s_used[word++]);
+        if (word == kJoinCtas / 32) return;
+        uint32_t used = s_used[word];
+        while (before-- > 0) used &= used - 1;
+        first = word * 32 + __ffs((int)used) - 1;
+    }
+    const JoinDesc d = descs(a.io.workspace)[first];
     if (d.b < 0) return;
     const int h = d.vh / a.passes, row0 = d.vh % a.passes * a.rows;
     const int rows = d.n > 1 ? d.n * a.G : min(a.rows, a.G - row0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int parts = d.last - (int)blockIdx.x + 1;
+    const int parts = d.last - first + 1;
 
     float ref, sum;
     float4 acc;
@@ -719,13 +737,13 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
         acc.z = acc.z * f + v.z * e;
         acc.w = acc.w * f + v.w * e;
     };
-    auto add_parts = [&](int row, int first, int step) {
+    auto add_parts = [&](int row, int from, int step) {
         ref = kNoRef;
         sum = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int i = first; i < parts; i += step) {
-            const float* p = slot_at(a.io.workspace, ctas, i == 0 ? d.slot : 2 * ((int)blockIdx.x + i));
+        for (int i = from; i < parts; i += step) {
+            const float* p = slot_at(a.io.workspace, ctas, i == 0 ? d.slot : 2 * (first + i));
             const float2 rl = *reinterpret_cast<const float2*>(p + kMaxRows * kHeadDim + 2 * row);
             add(rl.x, rl.y, *reinterpret_cast<const float4*>(p + row * kHeadDim + 4 * lane));
         }
@@ -736,7 +754,7 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
         mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
         if (a.io.lse && lane == 0) a.io.lse[head] = sum > 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
     };
-    if (parts <= 8) {
+    if (parts <= kFewParts) {
         for (int row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
             add_parts(row, 0, 1);
             finish(row);
@@ -828,11 +846,20 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, maps.k_decode, maps.v_decode, err_word);
     count_launches(1);
     if (e != cudaSuccess || grid == 1) return e;   // one CTA leaves no parts
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(most_rows < kJoinRows ? most_rows : kJoinRows));
+    // More than eight parts to a request and head, whose rows a CTA joins one
+    // after another: CTAs for those that hold a first part only, and more of them
+    // over the rows (one request of 30000 keys and 32 / 8 heads, 8 tokens: 65 -> 45 us,
+    // 1 token: 40 both; eight requests, with up to eight parts each: 118 -> 120).
+    const long long pairs = (long long)io.B * l.Hkv * a.passes;
+    const bool search = pairs * kFewParts < grid && grid <= kJoinCtas;
+    const int firsts = search ? (int)pairs : grid;
+    int over_rows = search ? kJoinCtas / firsts : kJoinRows;
+    if (over_rows > most_rows) over_rows = most_rows;
+    cfg.gridDim = dim3((unsigned)firsts, (unsigned)over_rows);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kda_attn_join_kernel, a, grid);
+    e = cudaLaunchKernelEx(&cfg, kda_attn_join_kernel, a, grid, search);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
