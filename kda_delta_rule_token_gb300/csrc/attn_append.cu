@@ -72,8 +72,7 @@ __device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float 
     return lo | (hi << 16);
 }
 
-__device__ __forceinline__ void store_e4m3(uint8_t* to, const f32x2 (&x)[4], float scale) {
-    const float inv = 1.0f / scale;
+__device__ __forceinline__ void store_e4m3(uint8_t* to, const f32x2 (&x)[4], float inv) {
     float y[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) mma::upk(mma::mul2(x[e], mma::pk(inv, inv)), y[2 * e], y[2 * e + 1]);
@@ -256,7 +255,12 @@ kda_attn_append_kernel(const AttnLayer l, const __grid_constant__ RopeTurns turn
         void* dst = is_q ? static_cast<void*>(io.q_out) : is_v ? l.v_cache : l.k_cache;
         uint16_t* dst16 = static_cast<uint16_t*>(dst) + off;
         uint8_t* dst8 = static_cast<uint8_t*>(dst) + off;
-        const float* scale = is_v ? l.v_scale : l.k_scale;
+        float inv[kBatch];
+        if (kE4m3 && to_cache) {
+            const float* scale = (is_v ? l.v_scale : l.k_scale) + h0;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) inv[i] = i < heads ? 1.0f / scale[i] : 0.f;
+        }
         const bool norm = (is_q ? l.q_gamma : l.k_gamma) != nullptr;
 
         // kRows rows from row i0 of the unit on.
@@ -271,7 +275,7 @@ kda_attn_append_kernel(const AttnLayer l, const __grid_constant__ RopeTurns turn
                     if (kE4m3) {
                         f32x2 x[4];
                         unpack8(raw[i], x);
-                        if (writes) store_e4m3(dst8 + (i0 + i) * pitch, x, scale[h0 + i0 + i]);
+                        if (writes) store_e4m3(dst8 + (i0 + i) * pitch, x, kRows > 1 ? inv[i] : inv[0]);
                     } else if (writes) {
                         *reinterpret_cast<uint4*>(dst16 + (i0 + i) * pitch) = raw[i];
                     }
@@ -321,7 +325,7 @@ kda_attn_append_kernel(const AttnLayer l, const __grid_constant__ RopeTurns turn
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = mma::mul2(mma::fma2(y[e], S[e], mma::mul2(x[e], C[e])), rn2);
                 if (kE4m3 && to_cache) {
-                    if (writes) store_e4m3(dst8 + (i0 + i) * pitch, x, scale[h0 + i0 + i]);
+                    if (writes) store_e4m3(dst8 + (i0 + i) * pitch, x, kRows > 1 ? inv[i] : inv[0]);
                 } else if (writes) {
                     *reinterpret_cast<uint4*>(dst16 + (i0 + i) * pitch) = pack8(x);
                 }
@@ -332,7 +336,13 @@ kda_attn_append_kernel(const AttnLayer l, const __grid_constant__ RopeTurns turn
             rows(std::integral_constant<int, kBatch>(), 0);
         } else {
 #pragma unroll 1
-            for (int i = 0; i < heads; ++i) rows(std::integral_constant<int, 1>(), i);
+            for (int i = 0; i < heads; ++i) {
+                rows(std::integral_constant<int, 1>(), i);
+                if (kE4m3) {
+                    inv[0] = inv[1];
+                    inv[1] = inv[2];
+                }
+            }
         }
         copy(stage);
         if (++stage == kDepth) stage = 0;
