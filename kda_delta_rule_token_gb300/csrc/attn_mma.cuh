@@ -62,6 +62,19 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
     return r;
 }
 
+// Two f16 values to e4m3 (nearest, finite), in the low 16 bits.
+__device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t two) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(two));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -5,8 +5,8 @@
 // A prompt token's head takes part in 4 * 128 operations per key: the call is
 // bound by the tensor pipe (a 128 x 128 tile of S and of O take it 512 cycles
 // each, its exponentials take the SM 512 as well).  Measured: 8192 tokens of 64
-// heads in bf16 617 us, 1783 TFLOP/s of the tokens' own operations, 0.91 of the
-// measured dense rate (e4m3: 700 us, 1572); one key tile of two row tiles takes
+// heads in bf16 615 us, 1788 TFLOP/s of the tokens' own operations, 0.91 of the
+// measured dense rate (e4m3: 671 us, 1638); one key tile of two row tiles takes
 // 2300 cycles of which the tensor pipe works 2048.
 //
 // The rows of one key head are (token, query head) pairs: floor(128 / G) tokens
@@ -26,13 +26,28 @@
 //    exponentials, and their bf16 roundings back into TMEM over S_X.  A row
 //    rescales (its O in TMEM as well) only when a logit passes the reference
 //    by more than kLimit powers of two, which after the first tile is rare.
-//  * e4m3: four further warps convert each copied tile to f16, Q is scaled
-//    by a power of two per row, P is f16 within 2^15.
+//  * e4m3: S is made of the keys as they are, with Q (scaled by a power of two
+//    per row) as the sum of two e4m3 parts, which hold bf16's eight bits: two
+//    8-bit products take as long as one 16-bit one, and the keys need no
+//    conversion.  Two further warps convert the values to f16, P is f16 within
+//    2^15.  (Keys converted to f16 too, by a warpgroup of its own: 703 us where
+//    this takes 671, and 741 of ragged chunks where this takes 701.)
+//
+// The loops of all these warps have to fit the SM's instruction cache together:
+// where they do not (a converting loop written out for all of a thread's 16
+// chunks is enough), the misses of all SMs fill the cache behind it, and every
+// warp of an SM slows down two- and threefold for tens of microseconds at a
+// time (ragged e4m3 chunks: hit rate 92 %, 83 % of that cache's peak).  So the
+// converting loop is eight chunks long, and a key tile's MMAs are written once.
 //
 // TMEM: S_0, S_1 (128 columns each, P_X in the first 64), O_0, O_1.
 //
 // P is rounded to bf16 (half a step, 2^-8 of each weight, or f16's 2^-11 for
 // e4m3) as the MMA's operand; the sum it is divided by is of the fp32 weights.
+// e4m3: Q's two parts are exact for channels down to 2^-9 of the row's largest,
+// below that off by up to 2^-17 of it, which is what a logit may be off by per
+// unit of the keys' absolute sum; the products accumulate in fp32 (lse of 3000
+// keys at logits of standard deviation 2: within 1e-5 of 64 bits).
 //
 // CTAs are persistent.  Segments are numbered with the longest of a request
 // first and dealt to the CTAs back and forth, which evens out the causal
@@ -59,6 +74,11 @@ constexpr uint32_t kBlock = 16384;             // Q: one 64-channel block of it;
 // K and V tiles: each eight keys are two swizzled 1024-byte atoms, channels 0-63 and 64-127.
 constexpr uint32_t kAtom = 1024, kEight = 2 * kAtom;
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kOperand, kOffV = 4 * kOperand, kOffStage = 6 * kOperand;
+// e4m3: K tiles as copied, half as large, and behind them the results on their way out; V tiles as copied.
+template <bool kE4m3>
+constexpr uint32_t kSlotK = kE4m3 ? kBlock : kOperand;
+template <bool kE4m3>
+constexpr uint32_t kOffOut = kE4m3 ? kOffK + 2 * kBlock : kOffStage;
 constexpr int kScan = 128;                     // threads of the prefix sums
 constexpr int kMaxCtas = 256;
 constexpr int kJoinCost = 8;                   // key tiles that writing and joining partial results takes (11 us)
@@ -94,7 +114,7 @@ struct Part {
 struct Ctl {
     uint64_t kfull[2], kempty[2], vfull[2], vempty[2], vraw;
     uint64_t qfull[2], sfull[2], pfull[2][2], ofull[2];   // pfull: by tile and half of its keys
-    uint64_t ckfull, ckempty, cvfull, cvempty;            // e4m3 staging
+    uint64_t cvfull[2], cvempty[2];                       // e4m3: values as copied
     uint64_t partfull[2], partempty[2];
     uint64_t drain;
     Part part[2];            // from the copying warp to the others
@@ -108,8 +128,8 @@ struct Ctl {
     int load[kMaxCtas];      // of each CTA, were the segments dealt whole
 };
 
-// Behind the operands: e4m3, a K and a V tile as copied; bf16, 16 KiB for
-// either tile's results on their way out (e4m3: in Q_x).
+// Behind the operands: e4m3, two V tiles as copied; bf16, 16 KiB for either
+// tile's results on their way out.
 template <bool kE4m3>
 constexpr uint32_t smem_bytes() { return kOffStage + 2 * kBlock + (uint32_t)sizeof(Ctl); }
 static_assert(kOffStage + 2 * kBlock + sizeof(Ctl) <= 232448, "shared memory");
@@ -285,22 +305,16 @@ __device__ __forceinline__ int scan_inclusive(int v, int* s_warp, int* total) {
     return v;
 }
 
-constexpr int kWarpMma = 8, kWarpTma = 9, kWarpConvert = 12;
-template <bool kE4m3>
-constexpr int threads_of() { return kE4m3 ? 512 : 384; }
+constexpr int kWarpMma = 8, kWarpTma = 9, kWarpConvert = 10, kConvert = 64;   // e4m3: threads that convert
+constexpr int kThreads = 384;
 // Registers: the launch's share of each thread, and what the softmax
-// warpgroups (0, 1) and the other ones change to; the sum stays within the
+// warpgroups (0, 1) and the other one change to; the sum stays within the
 // launch's (checked against the compiled kernel before its first launch).
-template <bool kE4m3>
-constexpr int regs_launch() { return kE4m3 ? 128 : 168; }
-template <bool kE4m3>
-constexpr int regs_softmax() { return kE4m3 ? 176 : 208; }
-constexpr int kRegsOther = 80;
-static_assert(256 * regs_softmax<false>() + 128 * kRegsOther <= 384 * regs_launch<false>(), "registers");
-static_assert(256 * regs_softmax<true>() + 256 * kRegsOther <= 512 * regs_launch<true>(), "registers");
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 80;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "registers");
 
 template <bool kE4m3>
-__global__ void __launch_bounds__(threads_of<kE4m3>(), 1)
+__global__ void __launch_bounds__(kThreads, 1)
 kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, int* err) {
     constexpr float kOffset = kE4m3 ? 10.f : 0.f;
@@ -313,8 +327,8 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     ptx::griddep_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&ctl.kfull[i], kE4m3 ? 128 : 1);
-            ptx::mbar_init(&ctl.vfull[i], kE4m3 ? 128 : 1);
+            ptx::mbar_init(&ctl.kfull[i], 1);
+            ptx::mbar_init(&ctl.vfull[i], kE4m3 ? kConvert : 1);
             ptx::mbar_init(&ctl.kempty[i], 1);
             ptx::mbar_init(&ctl.vempty[i], 1);
             ptx::mbar_init(&ctl.qfull[i], kRows);
@@ -322,14 +336,12 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             ptx::mbar_init(&ctl.pfull[i][0], kRows);
             ptx::mbar_init(&ctl.pfull[i][1], kRows);
             ptx::mbar_init(&ctl.ofull[i], 1);
+            ptx::mbar_init(&ctl.cvfull[i], 1);
+            ptx::mbar_init(&ctl.cvempty[i], kConvert);
             ptx::mbar_init(&ctl.partfull[i], 1);
-            ptx::mbar_init(&ctl.partempty[i], kE4m3 ? 13 : 9);   // warps that take parts
+            ptx::mbar_init(&ctl.partempty[i], kE4m3 ? 11 : 9);   // warps that take parts
         }
         ptx::mbar_init(&ctl.vraw, 1);
-        ptx::mbar_init(&ctl.ckfull, 1);
-        ptx::mbar_init(&ctl.cvfull, 1);
-        ptx::mbar_init(&ctl.ckempty, 128);
-        ptx::mbar_init(&ctl.cvempty, 128);
         ptx::mbar_init(&ctl.drain, 1);
         ptx::fence_mbar_init();
         ctl.dead = 0;
@@ -428,18 +440,18 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 const bool drop = a.io.drop && it == 0;
                 bool ok = true;
                 if (kE4m3) {
-                    // Staging: one buffer each, emptied by the converting warps.
-                    if (it > 0) ok = pwait(&ctl.ckempty, (uint32_t)(it - 1) & 1u, dead, err);
-                    if (ok && lane == 0 && !drop) ptx::mbar_arrive_expect_tx(&ctl.ckfull, (uint32_t)(pages * rows * 128));
+                    // Keys straight to the operand, values to a buffer that the converting warps empty.
+                    if (it >= 2) ok = pwait(&ctl.kempty[s], par, dead, err);
+                    if (ok && lane == 0 && !drop) ptx::mbar_arrive_expect_tx(&ctl.kfull[s], (uint32_t)(pages * rows * 128));
                     __syncwarp();
                     if (ok && mine_box && !is_v && !drop)
-                        ptx::tma_load_4d(sm + kOffStage + pg * rows * 128, &kmap, 0, 0, 0, ph, &ctl.ckfull);
+                        ptx::tma_load_4d(sm + kOffK + s * kBlock + pg * rows * 128, &kmap, 0, 0, 0, ph, &ctl.kfull[s]);
                     if (ok) ctl.kissued = it + 1;
-                    if (ok && it > 0) ok = pwait(&ctl.cvempty, (uint32_t)(it - 1) & 1u, dead, err);
-                    if (ok && lane == 0) ptx::mbar_arrive_expect_tx(&ctl.cvfull, (uint32_t)(pages * rows * 128));
+                    if (ok && it >= 2) ok = pwait(&ctl.cvempty[s], par, dead, err);
+                    if (ok && lane == 0) ptx::mbar_arrive_expect_tx(&ctl.cvfull[s], (uint32_t)(pages * rows * 128));
                     __syncwarp();
                     if (ok && mine_box && is_v)
-                        ptx::tma_load_4d(sm + kOffStage + kBlock + pg * rows * 128, &vmap, 0, 0, 0, ph, &ctl.cvfull);
+                        ptx::tma_load_4d(sm + kOffStage + s * kBlock + pg * rows * 128, &vmap, 0, 0, 0, ph, &ctl.cvfull[s]);
                     if (ok) ctl.vissued = it + 1;
                 } else {
                     uint8_t* kd = sm + kOffK + s * kOperand + pg * rows * 256;
@@ -482,62 +494,68 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         // ---- MMAs, issued by one thread.  It shares its scheduler with two
         // softmax warps, and the pipe holds only about two MMAs beyond the
         // one it works on, so every instruction between two MMAs counts:
-        //  * the step of a key tile that both tiles go on from is written out
-        //    for either slot, all operands constants but the shared-memory base;
+        //  * the step of a key tile that both tiles go on from has all operands
+        //    constants but the bases of its slots;
         //  * each barrier is tested before the batch of MMAs that precedes its
         //    use, and waited for only if it was not complete by then;
         //  * giving up leaves the loop from the waits, the MMAs carry no condition.
-        // (With runtime operands and conditions at each MMA the same kernel
-        // ran 8191 tokens of 32 heads in 568 us, with conditions alone in 442,
-        // like this in 333; without any exponentials it then took 349.)
+        // (With all operands worked out and conditions at each MMA the same
+        // kernel ran 8191 tokens of 32 heads in 568 us, with conditions alone in
+        // 442, like this in 333.)
         tc::reg_dec<kRegsOther>();
         Part p;
         int np = 0;
         constexpr uint32_t id_s = tc::idesc_f16kind(kRows, kKeys, !kE4m3, false);
         constexpr uint32_t id_o = tc::idesc_f16kind(kRows, kHeadDim, !kE4m3, true);
         const uint32_t base = ptx::smem_u32(sm);
-        const uint64_t dq = tc::desc_sw128(base + kOffQ), dk = tc::desc_sw128(base + kOffK, kEight);
+        const uint64_t dq = tc::desc_sw128(base + kOffQ), dk = tc::desc_sw128(base + kOffK, kE4m3 ? kAtom : kEight);
         const uint64_t dv = tc::desc_sw128_mn(base + kOffV, kAtom, kEight);
         uint32_t qpar[2] = {0u, 0u}, ppar[2] = {0u, 0u};
         int it = 0;
-        // S_x = Q_x K^T and four of the eight MMAs of O_x += P_x V; slots by byte offset.
-        auto mma_s = [&](int x, uint32_t slot) {
+        // S_x = Q_x K^T and four of the eight MMAs of O_x += P_x V.  e4m3: 32
+        // channels of K with the two parts of those of Q, one after the other.
+        auto mma_s = [&](int x, int slot) {
+            const uint64_t k = tc::desc_add(dk, slot * kSlotK<kE4m3>);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                tc::mma_ss_bf16(kColS + 128 * x, tc::desc_add(dq, x * kOperand + (i >> 2) * kBlock + (i & 3) * 32),
-                                tc::desc_add(dk, slot + (i >> 2) * kAtom + (i & 3) * 32), id_s, i > 0);
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t q = tc::desc_add(dq, x * kOperand + (i >> 2) * kBlock + (i & 3) * 32);
+                if (kE4m3)
+                    tc::mma_ss_e4m3(kColS + 128 * x, q, tc::desc_add(k, (i >> 1) * 32), id_s, i > 0);
+                else
+                    tc::mma_ss_bf16(kColS + 128 * x, q, tc::desc_add(k, (i >> 2) * kAtom + (i & 3) * 32), id_s, i > 0);
+            }
             tc::commit(&ctl.sfull[x]);
         };
-        auto mma_pv = [&](int x, uint32_t slot, int half, uint32_t add) {
+        auto mma_pv = [&](int x, int slot, int half, uint32_t add) {
+            const uint64_t v = tc::desc_add(dv, slot * kOperand);
 #pragma unroll
             for (int i = 4 * half; i < 4 * half + 4; ++i)
-                tc::mma_ts_f16kind(kColO + 128 * x, kColS + 128 * x + 8 * i, tc::desc_add(dv, slot + i * 2 * kEight), id_o,
+                tc::mma_ts_f16kind(kColO + 128 * x, kColS + 128 * x + 8 * i, tc::desc_add(v, i * 2 * kEight), id_o,
                                    i > 0 ? 1u : add);
         };
         // The rest of a wait whose barrier was tested before.
         auto need = [&](bool done, uint64_t* bar, uint32_t par) { return done || pwait(bar, par, dead, err); };
         // One key tile of both tiles, with another one after it for both.
         // `ready`: the test of P_0's first half, on return that of the next one's.
-        auto full_step = [&](auto slot_index, bool& ready, uint32_t add) -> bool {
-            constexpr int sl = decltype(slot_index)::value;
-            constexpr uint32_t here = sl * kOperand, there = (1 - sl) * kOperand;
+        auto full_step = [&](bool& ready, uint32_t add) -> bool {
+            const int sl = it & 1;
             const uint32_t npar = (uint32_t)((it + 1) >> 1) & 1u;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 if (!need(ready, &ctl.pfull[x][0], ppar[x])) return false;
                 tc::fence_after();
                 bool t = ptx::mbar_test(&ctl.pfull[x][1], ppar[x]);
-                mma_pv(x, here, 0, add);
+                mma_pv(x, sl, 0, add);
                 if (!need(t, &ctl.pfull[x][1], ppar[x])) return false;
                 tc::fence_after();
                 uint64_t* kv = x ? &ctl.vfull[1 - sl] : &ctl.kfull[1 - sl];
                 t = ptx::mbar_test(kv, npar);
-                mma_pv(x, here, 1, 1u);
+                mma_pv(x, sl, 1, 1u);
                 ppar[x] ^= 1u;
                 if (x) tc::commit(&ctl.vempty[sl]);
                 if (!need(t, kv, npar)) return false;
                 ready = ptx::mbar_test(&ctl.pfull[1 - x][0], ppar[1 - x]);
-                mma_s(x, there);
+                mma_s(x, 1 - sl);
             }
             tc::commit(&ctl.kempty[1 - sl]);
             return true;
@@ -545,19 +563,19 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         // The same for any state of the two tiles.
         auto any_step = [&](int j) -> bool {
             const int sl = it & 1;
-            const uint32_t here = sl * kOperand, there = (1 - sl) * kOperand, npar = (uint32_t)((it + 1) >> 1) & 1u;
+            const uint32_t npar = (uint32_t)((it + 1) >> 1) & 1u;
             for (int x = 0; x < 2; ++x) {
                 if (j >= p.cnt[x]) continue;
                 for (int half = 0; half < 2; ++half) {
                     if (!pwait(&ctl.pfull[x][half], ppar[x], dead, err)) return false;
                     tc::fence_after();
-                    mma_pv(x, here, half, half || j > 0);
+                    mma_pv(x, sl, half, half || j > 0);
                 }
                 ppar[x] ^= 1u;
                 if (x || j >= p.cnt[1]) tc::commit(&ctl.vempty[sl]);
                 if (j + 1 < p.cnt[x]) {
                     if (!pwait(&ctl.kfull[1 - sl], npar, dead, err)) return false;
-                    mma_s(x, there);
+                    mma_s(x, 1 - sl);
                 } else {
                     tc::commit(&ctl.ofull[x]);
                 }
@@ -575,18 +593,17 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 if (!pwait(&ctl.qfull[x], qpar[x], dead, err)) return false;
                 qpar[x] ^= 1u;
                 tc::fence_after();
-                mma_s(x, (it & 1) * kOperand);
+                mma_s(x, it & 1);
             }
             tc::commit(&ctl.kempty[it & 1]);
             if (!pwait(&ctl.vfull[it & 1], (uint32_t)(it >> 1) & 1u, dead, err)) return false;
             int j = 0;
             const int both = min(p.cnt[0], p.cnt[1]) - 1;   // steps that both tiles go on from
             bool ready = false;
-            for (; j < both; ++j, ++it) {
-                const bool ok = (it & 1) ? full_step(std::integral_constant<int, 1>(), ready, j > 0)
-                                         : full_step(std::integral_constant<int, 0>(), ready, j > 0);
-                if (!ok) return false;
-            }
+#pragma unroll 1
+            for (; j < both; ++j, ++it)
+                if (!full_step(ready, j > 0)) return false;
+#pragma unroll 1
             for (; j < p.n; ++j, ++it)
                 if (!any_step(j)) return false;
             return true;
@@ -599,26 +616,25 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         }
         if (issuer) tc::commit(&ctl.drain);   // completes once every MMA that it issued has
     } else if (kE4m3 && warp >= kWarpConvert) {
-        // ---- e4m3 -> f16, one key per thread
+        // ---- e4m3 -> f16 of the values, two keys per thread
         tc::reg_dec<kRegsOther>();
         Part p;
         int np = 0;
-        const int row = tid - 32 * kWarpConvert;
+        const int row0 = tid - 32 * kWarpConvert;
         int it = 0;
         bool ok = true;
         while (ok && take_part(ctl, np, p, dead, err))
-            for (int j = p.j0; j < p.j0 + p.n && ok; ++j, ++it) {
+            for (int j = p.j0; j < p.j0 + p.n; ++j, ++it) {
                 const int s = it & 1;
-                const uint32_t par = (uint32_t)((it >> 1) - 1) & 1u;
-                const bool live = j * kKeys + row < p.s.len;
+                ok = pwait(&ctl.cvfull[s], (uint32_t)(it >> 1) & 1u, dead, err);
+                if (ok && it >= 2) ok = pwait(&ctl.vempty[s], (uint32_t)((it >> 1) - 1) & 1u, dead, err);
+                if (!ok) break;
 #pragma unroll 1
-                for (int v = 0; v < 2 && ok; ++v) {
-                    ok = pwait(v ? &ctl.cvfull : &ctl.ckfull, (uint32_t)it & 1u, dead, err);
-                    if (ok && it >= 2) ok = pwait(v ? &ctl.vempty[s] : &ctl.kempty[s], par, dead, err);
-                    if (!ok) break;
-                    const uint8_t* src = sm + kOffStage + v * kBlock + row * 128;
-                    uint8_t* dst = sm + (v ? kOffV : kOffK) + s * kOperand + (row >> 3) * kEight + (row & 7) * 128;
-#pragma unroll
+                for (int row = row0; row < kKeys; row += kConvert) {
+                    const bool live = j * kKeys + row < p.s.len;
+                    const uint8_t* src = sm + kOffStage + s * kBlock + row * 128;
+                    uint8_t* dst = sm + kOffV + s * kOperand + (row >> 3) * kEight + (row & 7) * 128;
+#pragma unroll 8
                     for (int c = 0; c < 8; ++c) {
                         uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
                         if (!live) w = make_uint4(0u, 0u, 0u, 0u);
@@ -633,14 +649,14 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                         *reinterpret_cast<uint4*>(d + ((((2 * c) & 7) ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
                         *reinterpret_cast<uint4*>(d + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
                     }
-                    ptx::fence_proxy_async_smem();
-                    ptx::mbar_arrive(v ? &ctl.vfull[s] : &ctl.kfull[s]);
-                    ptx::mbar_arrive(v ? &ctl.cvempty : &ctl.ckempty);
                 }
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive(&ctl.vfull[s]);
+                ptx::mbar_arrive(&ctl.cvempty[s]);
             }
     } else if (warp < 8) {
         // ---- softmax, one thread per row of tile x
-        tc::reg_inc<regs_softmax<kE4m3>()>();
+        tc::reg_inc<kRegsSoftmax>();
         Part p;
         int np = 0;
         const int x = warp >> 2, r = tid & (kRows - 1);
@@ -650,11 +666,11 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         bool ok = true;
         // The warp's 32 rows of Q_x, and of the results on their way out (rows
         // of kOut bytes), both swizzled as TMA would.
-        constexpr int kOut = kE4m3 ? 256 : 128, kOutLanes = kOut / 16, kOutRows = 32 / kOutLanes;
+        constexpr int kOut = 128, kOutLanes = kOut / 16, kOutRows = 32 / kOutLanes;
         uint8_t* rows_q = sm + kOffQ + x * kOperand + (warp & 3) * 32 * 128;
-        uint8_t* rows_o = sm + kOffStage + warp * 32 * 128;
+        uint8_t* rows_o = sm + kOffOut<kE4m3> + warp * 32 * 128;
         auto place_q = [&](int row, int c) { return rows_q + (c >> 3) * kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
-        auto place_o = [&](int row, int c) { return kE4m3 ? place_q(row, c) : rows_o + row * 128 + ((c ^ (row & 7)) << 4); };
+        auto place_o = [&](int row, int c) { return rows_o + row * 128 + ((c ^ (row & 7)) << 4); };
         // A part as this thread's row and the warp's rows see it.
         struct Rows {
             bool live;           // the row has a token
@@ -688,8 +704,11 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             ptx::cp_async_wait_all();
             __syncwarp();
             if (kE4m3) {
-                // To f16, each lane its row: q * 2^(14 - e) with 2^e <= the row's
-                // largest < 2^(e+1), exact down to 2^-28 of it.
+                // To two e4m3 parts, each lane its row: q * 2^(7 - e) with 2^e <= the
+                // row's largest < 2^(e+1), rounded, and what that leaves of its eight
+                // bits: exact for values down to 2^-9 of the row's largest, below
+                // that off by up to 2^-17 of it.  Each 64 bytes of a row hold 32
+                // channels' first parts, then their second.
                 float top = 0.f;
 #pragma unroll 4
                 for (int c = 0; c < 16; ++c) {
@@ -700,28 +719,44 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                         top = mma::max3(top, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
                 }
                 const int ex = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
-                const float up = exp2f((float)(14 - ex));
-                w.fac = a.scale * a.k_scale[part.s.h] * exp2f((float)(ex - 14));
-#pragma unroll 4
-                for (int c = 0; c < 16; ++c) {
-                    uint4* at = reinterpret_cast<uint4*>(place_q(lane, c));
-                    const uint4 v = *at;
-                    uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                const float up = exp2f((float)(7 - ex));
+                w.fac = a.scale * a.k_scale[part.s.h] * exp2f((float)(ex - 7));
+                if (top == INFINITY) w.fac = __int_as_float(0x7fc00000);   // which e4m3 does not hold
+#pragma unroll 1
+                for (int c = 0; c < 16; c += 4) {
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        u[e] = mma::pack_f16(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
-                    *at = make_uint4(u[0], u[1], u[2], u[3]);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(place_q(lane, c + k));
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t f0 = mma::pack_f16(__uint_as_float(u[2 * e] << 16) * up, __uint_as_float(u[2 * e] & 0xffff0000u) * up);
+                            const uint32_t f1 = mma::pack_f16(__uint_as_float(u[2 * e + 1] << 16) * up, __uint_as_float(u[2 * e + 1] & 0xffff0000u) * up);
+                            const uint32_t h0 = mma::f16x2_e4m3x2(f0), h1 = mma::f16x2_e4m3x2(f1);
+                            hi[2 * k + e] = h0 | h1 << 16;
+                            lo[2 * k + e] = mma::f16x2_e4m3x2(mma::sub_f16x2(f0, mma::e4m3x2_f16x2(h0))) |
+                                            mma::f16x2_e4m3x2(mma::sub_f16x2(f1, mma::e4m3x2_f16x2(h1))) << 16;
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(place_q(lane, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(place_q(lane, c + 1)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                    *reinterpret_cast<uint4*>(place_q(lane, c + 2)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4*>(place_q(lane, c + 3)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
                 }
             }
             ptx::fence_proxy_async_smem();
+        };
+        auto hand_over = [&](const Part& part) {   // Q_x, and S_x to be written
             tc::fence_before();
-            ptx::mbar_arrive(&ctl.qfull[x]);
+            if (part.cnt[x] > 0) ptx::mbar_arrive(&ctl.qfull[x]);
         };
         Rows w{};
         bool more = take_part(ctl, np, p, dead, err);
         if (more) {
             w = start_rows(p);
             finish_rows(p, w);
+            hand_over(p);
         }
         while (more) {
             const bool live = w.live;
@@ -802,15 +837,15 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 }
                 if (!ok) break;
             }
-            // bf16: the next part's Q rows come in under the last MMAs, and its
-            // first logits are computed while these results go out (S_x and
-            // Q_x are free once O_x is complete).
+            // The next part's Q rows come in under the last MMAs (Q_x is free
+            // since the last logits), and its first logits are computed while
+            // these results go out (S_x is free once O_x is complete).
             Part pn;
             Rows wn{};
-            bool more_n = false;
-            if (!kE4m3) {
-                more_n = take_part(ctl, np, pn, dead, err);
-                if (more_n) wn = start_rows(pn);
+            const bool more_n = take_part(ctl, np, pn, dead, err);
+            if (more_n) {
+                wn = start_rows(pn);
+                finish_rows(pn, wn);
             }
             if (cnt > 0) {
                 ok = pwait(&ctl.ofull[x], opar, dead, err);
@@ -818,7 +853,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 tc::fence_after();
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             }
-            if (!kE4m3 && more_n) finish_rows(pn, wn);
+            if (more_n) hand_over(pn);
             // The rows' results, or this part's share of them, through shared
             // memory so that whole stretches of rows are stored together: in
             // bf16 where that is all there is to write, else in fp32.
@@ -882,13 +917,6 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 *reinterpret_cast<float2*>(part + (size_t)2 * kRows * kHeadDim + 2 * (x * kRows + r)) = make_float2(ref, sum);
             if (tid == 0 && p.last >= 0)
                 joins(a.io.workspace)[blockIdx.x] = PrefillJoin{p.s.tok, p.s.m, p.s.h, p.last, p.slot, {0, 0, 0}};
-            if (kE4m3) {
-                more_n = take_part(ctl, np, pn, dead, err);
-                if (more_n) {
-                    wn = start_rows(pn);
-                    finish_rows(pn, wn);
-                }
-            }
             p = pn;
             w = wn;
             more = more_n;
@@ -904,16 +932,11 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         // (bounded waits) before its TMEM and shared memory are released.
         if (tid == 32 * kWarpMma) ptx::mbar_wait_timed(&ctl.drain, 0);
         if (tid == 32 * kWarpTma) {
-            if (kE4m3) {
-                if (ctl.kissued) ptx::mbar_wait_timed(&ctl.ckfull, (uint32_t)(ctl.kissued - 1) & 1u);
-                if (ctl.vissued) ptx::mbar_wait_timed(&ctl.cvfull, (uint32_t)(ctl.vissued - 1) & 1u);
-            } else {
-                for (int i = max(0, ctl.kissued - 2); i < ctl.kissued; ++i)
-                    ptx::mbar_wait_timed(&ctl.kfull[i & 1], (uint32_t)(i >> 1) & 1u);
-                for (int i = max(0, ctl.vissued - 2); i < ctl.vissued; ++i)
-                    ptx::mbar_wait_timed(&ctl.vfull[i & 1], (uint32_t)(i >> 1) & 1u);
-                if (ctl.raws) ptx::mbar_wait_timed(&ctl.vraw, (uint32_t)(ctl.raws - 1) & 1u);
-            }
+            for (int i = max(0, ctl.kissued - 2); i < ctl.kissued; ++i)
+                ptx::mbar_wait_timed(&ctl.kfull[i & 1], (uint32_t)(i >> 1) & 1u);
+            for (int i = max(0, ctl.vissued - 2); i < ctl.vissued; ++i)
+                ptx::mbar_wait_timed(kE4m3 ? &ctl.cvfull[i & 1] : &ctl.vfull[i & 1], (uint32_t)(i >> 1) & 1u);
+            if (ctl.raws) ptx::mbar_wait_timed(&ctl.vraw, (uint32_t)(ctl.raws - 1) & 1u);
         }
     }
     __syncthreads();
@@ -985,7 +1008,7 @@ cudaError_t prepare_kernel() {
     cudaFuncAttributes f{};
     cudaError_t e = cudaFuncGetAttributes(&f, kda_attn_prefill_kernel<kE4m3>);
     if (e != cudaSuccess) return e;
-    if (f.numRegs < regs_launch<kE4m3>()) return cudaErrorLaunchOutOfResources;   // the splits would never be met
+    if (f.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;   // the splits would never be met
     return cudaFuncSetAttribute(kda_attn_prefill_kernel<kE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem_bytes<kE4m3>());
 }
@@ -1028,7 +1051,7 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
     cudaLaunchConfig_t cfg{};
     const int grid = dev.sm_count;
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(l.e4m3 ? threads_of<true>() : threads_of<false>());
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = l.e4m3 ? smem_bytes<true>() : smem_bytes<false>();
     cfg.stream = stream;
     cudaError_t e = cudaLaunchKernelEx(&cfg, l.e4m3 ? kda_attn_prefill_kernel<true> : kda_attn_prefill_kernel<false>,

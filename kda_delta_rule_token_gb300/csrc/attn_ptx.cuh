@@ -72,6 +72,15 @@ __device__ __forceinline__ void mma_ts_f16kind(uint32_t d, uint32_t a, uint64_t 
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem], both e4m3, K = 32 per instruction (the
+// instruction descriptor is idesc_f16kind's for f16, whose type fields are 0).
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
