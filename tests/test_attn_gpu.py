@@ -262,6 +262,31 @@ def test_append_in_place_and_slots_outside():
     layer.done()
 
 
+@pytest.mark.parametrize("N,hq,hkv,e4m3,inter", [
+    (701, 8, 2, False, False), (4999, 6, 3, True, False), (6001, 5, 1, False, True), (9002, 4, 4, True, True)])
+def test_append_does_not_depend_on_the_call(N, hq, hkv, e4m3, inter):
+    """A token's values are the same in a long call, whose warps' ranges cut tokens, and in short ones."""
+    page = 32
+    g = torch.Generator(device=DEV).manual_seed(N)
+    gam = 1 + 0.3 * torch.randn(D, generator=g, device=DEV)
+    layer = Layer(hq, hkv, page, e4m3, pages=-(-N // page), rot=64, rope_interleaved=inter, q_gamma=gam, k_gamma=gam)
+    q, k, v = (torch.randn(N, h, D, generator=g, device=DEV).to(BF) for h in (hq, hkv, hkv))
+    pos = torch.randint(0, 2 ** 31 - 1, (N,), generator=g, device=DEV).to(torch.int32)
+    slots = torch.randperm(N, generator=g, device=DEV)
+    out = torch.empty_like(q)
+    kda.kda_attn_append(layer.attn, N, q, k, v, pos, slots, out)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    caches = [c.view(torch.uint8).clone() for c in (layer.k, layer.v)]
+    again = torch.empty_like(q)
+    for t in list(range(0, N, 509)) + [N - 3]:
+        n = min(7, N - t)
+        kda.kda_attn_append(layer.attn, n, q[t:], k[t:], v[t:], pos[t:], slots[t:], again[t:])
+        assert torch.equal(again[t:t + n].view(torch.int16), out[t:t + n].view(torch.int16))
+    for c, old in zip((layer.k, layer.v), caches):
+        assert torch.equal(c.view(torch.uint8), old)
+    layer.done()
+
+
 # ------------------------------------------------------- decode, prefill
 
 def run_attend(layer, q, kv_lens, cu=None, gate=None, f32=False, want_lse=True, stream=None):
@@ -451,6 +476,38 @@ def test_prefill_one_and_two_row_tiles(e4m3, page, scale):
     for n in new:
         cu.append(cu[-1] + n)
     verify(layer, queries(layer, cu[-1]), kv, cu)
+    layer.done()
+
+
+def test_prefill_e4m3_wide_queries():
+    """Channels far below their row's largest, whose low bits the e4m3 parts of a
+    query do not hold: a channel is off by at most 2^-17 of that largest, so a
+    logit by that times the keys' absolute sum, lse by as much and a weight by the
+    factor exp(twice that).  Rows with an infinity come out as NaN, alone."""
+    n, kv, hq, hkv, page = 150, 700, 4, 2, 16
+    layer = Layer(hq, hkv, page, True)
+    layer.fill([kv])
+    q = queries(layer, n).float()
+    q = (q * torch.exp2(torch.randint(-14, 1, q.shape, generator=layer.g, device=DEV).float())).to(BF)
+    bad = q.clone()
+    bad[5, 1, 7] = math.inf
+    bad[80, 2, 100] = -math.inf
+    args = (layer.k, layer.v, layer.table_list, [kv], [0, n], page, D ** -0.5, layer.ks, layer.vs, None)
+    want, wl, bound, lb = ref.attend(q, *args)
+    pages = torch.tensor(layer.table_list[0], device=DEV)[: -(-kv // page)]
+    rows = lambda c, s: (c[pages].double().transpose(0, 1).reshape(hkv, -1, D)[:, :kv] * s.double().view(hkv, 1, 1)).abs()
+    keys = rows(layer.k, layer.ks).sum(-1).amax(-1).repeat_interleave(hq // hkv)       # [Hq]
+    top = rows(layer.v, layer.vs).amax((1, 2)).repeat_interleave(hq // hkv)
+    off = D ** -0.5 * 2.0 ** -17 * q.double().abs().amax(-1) * keys
+    bound, lb = bound + (torch.expm1(2 * off) * top)[..., None], lb + off
+    o, lse = run_attend(layer, q, [kv], [0, n], None, True)
+    check(o.t, want, bound, "o")
+    check(lse.t, wl, lb, "lse")
+    o, _ = run_attend(layer, bad, [kv], [0, n], None, True)
+    hit = torch.zeros(n, hq, dtype=torch.bool, device=DEV)
+    hit[5, 1] = hit[80, 2] = True
+    assert bool(o.t[hit].isnan().all())
+    check(o.t[~hit], want[~hit], bound[~hit], "o beside NaN rows")
     layer.done()
 
 
