@@ -984,7 +984,8 @@ __global__ void __launch_bounds__(256) kda_attn_prefill_join_kernel(const Prefil
             const float* s = slot_at(a.io.workspace, ctas, q == 0 ? d.slot : 2 * (lo + q));
             const float2 ls = *reinterpret_cast<const float2*>(s + (size_t)2 * kRows * kHeadDim + 2 * at);
             const float4 v = *reinterpret_cast<const float4*>(s + (size_t)at * kHeadDim + 4 * lane);
-            if (!(ls.y > 0.f)) continue;   // no key of this part is seen: the weighted sum was not written
+            // No key of this part is seen: the weighted sum was not written.  (A NaN sum goes in, and makes the row NaN.)
+            if (ls.y == 0.f) continue;
             const float to = fmaxf(ref, ls.x);
             const float f = mma::exp2_approx(ref - to), e = mma::exp2_approx(ls.x - to);
             ref = to;
@@ -994,7 +995,7 @@ __global__ void __launch_bounds__(256) kda_attn_prefill_join_kernel(const Prefil
             acc.z = acc.z * f + v.z * e;
             acc.w = acc.w * f + v.w * e;
         }
-        const float n = sum > 0.f ? (a.v_scale ? a.v_scale[d.h] : 1.f) / sum : 0.f;
+        const float n = sum != 0.f ? (a.v_scale ? a.v_scale[d.h] : 1.f) / sum : 0.f;
         const size_t head = ((size_t)d.tok + i) * a.Hq + d.h * a.G + g;
         mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
         if (a.io.lse && lane == 0) a.io.lse[head] = sum > 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;

@@ -1,0 +1,121 @@
+"""Attention over caches, queries and gates that hold NaN or infinities: what a
+row sees shows in its outputs, what it does not see has no effect, and neither
+depends on how a call is cut between CTAs."""
+import math
+
+import pytest
+import torch
+
+import attn_ref as ref
+import kda_delta_rule_token_gb300 as kda
+from test_attn_gpu import BF, D, DEV, F8, Layer, _lib, check, queries, run_attend  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_of(kv, cu):
+    """Request, and keys seen, of every packed row."""
+    req, sees = [], []
+    for b, n in enumerate(kv):
+        new = 1 if cu is None else cu[b + 1] - cu[b]
+        req += [b] * new
+        sees += [n - new + 1 + i for i in range(new)]
+    return torch.tensor(req, device=DEV), torch.tensor(sees, device=DEV)
+
+
+def poison(layer, cache, b, key, head, channel, value=math.nan):
+    at = (layer.table_list[b][key // layer.page], head, key % layer.page, channel)
+    if layer.e4m3:
+        cache.view(torch.uint8)[at] = 0x7F
+    else:
+        cache[at] = value
+
+
+def finite(cache):
+    """The cache with 0 for NaN and infinities (and for whatever no request's keys hold)."""
+    x = cache.float()
+    return torch.where(x.isfinite(), x, 0).to(cache.dtype)
+
+
+def expect(layer, q, kv, cu, gate=None):
+    """Values and bounds, were everything finite.  Over an e4m3 cache with the
+    bound of queries held as two e4m3 parts (off by up to 2^-17 of the row's
+    largest channel)."""
+    args = (layer.table_list, kv, cu, layer.page, D ** -0.5, layer.ks, layer.vs, gate)
+    q = torch.where(q.float().isfinite(), q.float(), 0).to(BF)
+    k, v = finite(layer.k), finite(layer.v)
+    want, wl, bound, lb = ref.attend(q, k, v, *args)
+    if layer.e4m3 and cu is not None:
+        G = layer.hq // layer.hkv
+        mag = lambda c, s: (c.float() * s.view(1, -1, 1, 1)).abs()
+        keys = mag(k, layer.ks).sum(-1).amax((0, 2)).repeat_interleave(G)
+        top = mag(v, layer.vs).amax((0, 2, 3)).repeat_interleave(G).double()
+        off = D ** -0.5 * 2.0 ** -17 * q.double().abs().amax(-1) * keys.double()
+        bound, lb = bound + (torch.expm1(2 * off) * top)[..., None], lb + off
+    return want, wl, bound, lb
+
+
+# (new tokens, keys, query heads, key heads, page): decode where new is None
+CALLS = {
+    "decode": (None, [300, 77, 1000], 8, 2, 64),
+    "decode_cut": (None, [30000, 5], 8, 2, 16),
+    "few": ([5, 3, 7], [300, 40, 77], 8, 2, 16),
+    "few_cut": ([8, 2], [20001, 9], 8, 2, 32),
+    "prompt": ([150], [700], 4, 2, 16),
+    "prompt_cut": ([128], [32768], 8, 2, 64),
+}
+
+
+def make(call, e4m3):
+    new, kv, hq, hkv, page = CALLS[call]
+    layer = Layer(hq, hkv, page, e4m3, seed=len(call))
+    layer.fill(kv)
+    cu = None
+    if new is not None:
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+    return layer, kv, cu, queries(layer, len(kv) if cu is None else cu[-1])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("call", CALLS)
+def test_nan_keys_and_queries(call, e4m3):
+    """A NaN in a key makes every row that sees it NaN, and no other; a NaN
+    in a query row that row alone."""
+    layer, kv, cu, q = make(call, e4m3)
+    req, sees = rows_of(kv, cu)
+    G = layer.hq // layer.hkv
+    want, wl, bound, lb = expect(layer, q, kv, cu)
+    last = kv[0] - 1
+    # An early key of head 0 that every row of request 0 sees, or (second turn) one that only its last row does.
+    for key in (last // 3, last):
+        keep = layer.k.clone()
+        poison(layer, layer.k, 0, key, 0, 70)
+        bad_q = q.clone()
+        row = 1 if cu is None else cu[1] - 2
+        bad_q[row, G, 5] = math.nan                       # first query head of key head 1
+        hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+        hit[:, :G] = ((req == 0) & (sees > key))[:, None]
+        hit[row, G] = True
+        o, lse = run_attend(layer, bad_q, kv, cu, None, True)
+        assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+        assert bool(o.t[hit].isnan().all()), "a row that sees NaN is not NaN"
+        check(o.t[~hit], want[~hit], bound[~hit], "o")
+        layer.k.copy_(keep)
+    layer.done()
+
+
+@pytest.mark.parametrize("call", ["prompt", "prompt_cut"])
+def test_infinite_queries_over_e4m3(call):
+    """A query row with an infinity comes out as NaN, alone, however the call is cut."""
+    layer, kv, cu, q = make(call, True)
+    want, wl, bound, lb = expect(layer, q, kv, cu)
+    q[5, 1, 7], q[80, 2, 100] = math.inf, -math.inf
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    hit[5, 1] = hit[80, 2] = True
+    o, lse = run_attend(layer, q, kv, cu, None, True)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    assert bool(o.t[hit].isnan().all())
+    check(o.t[~hit], want[~hit], bound[~hit], "o beside NaN rows")
+    layer.done()
