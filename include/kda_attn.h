@@ -159,7 +159,8 @@ KDA_API size_t kda_attn_workspace_bytes(const kda_attn_ctx *ctx);
  *               request's o is zero and its lse -infinity
  *   gate_logit  [B][Hq][d] fp32, or NULL
  *   o           [B][Hq][d], bf16, or fp32 if o_f32 is nonzero (the input of kda_project_o)
- *   lse         [B][Hq] fp32 or NULL: ln of the sum of exp(softmax_scale * q.k)
+ *   lse         [B][Hq] fp32 or NULL: ln of the sum of exp(softmax_scale * q.k);
+ *               NaN where one of the row's logits is
  *   workspace   kda_attn_workspace_bytes bytes, 16-byte aligned
  * q, o and gate_logit 16-byte aligned, the others 4-byte.  What lies in the
  * cache past a request's length, NaN and infinities among it, has no effect.

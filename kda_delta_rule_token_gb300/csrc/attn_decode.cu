@@ -664,10 +664,10 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
             for (int w = 0; w < kWarps; ++w)
                 if (w < parts) l += s_sum[w * rows + row] * mma::exp2_approx(s_ref[w * rows + row] - top);
             if (whole) {
-                const float n = l > 0.f ? vscale / l : 0.f;   // 0: the row sees no key
+                const float n = l != 0.f ? vscale / l : 0.f;   // 0: the row sees no key (NaN is not 0: a NaN logit shows)
                 const size_t at = head_of(cur, rw, row);
                 mma::store4(a.io, at * kHeadDim + col, make_float4(v.x * n, v.y * n, v.z * n, v.w * n));
-                if (a.io.lse && col == 0) a.io.lse[at] = (top + log2f(l)) / kLog2e;
+                if (a.io.lse && col == 0) a.io.lse[at] = l != 0.f ? (top + log2f(l)) / kLog2e : -INFINITY;
             } else {
                 *reinterpret_cast<float4*>(part + row * kHeadDim + col) = v;
                 if (col == 0) {
@@ -749,10 +749,10 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
         }
     };
     auto finish = [&](int row) {
-        const float n = sum > 0.f ? (a.v_scale ? a.v_scale[h] : 1.f) / sum : 0.f;
+        const float n = sum != 0.f ? (a.v_scale ? a.v_scale[h] : 1.f) / sum : 0.f;
         const size_t head = ((size_t)d.tok0 + (d.n > 1 ? row / a.G : 0)) * a.Hq + h * a.G + (d.n > 1 ? row % a.G : row0 + row);
         mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
-        if (a.io.lse && lane == 0) a.io.lse[head] = sum > 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
+        if (a.io.lse && lane == 0) a.io.lse[head] = sum != 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
     };
     if (parts <= kFewParts) {
         for (int row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {

@@ -860,7 +860,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             const bool whole = p.slot < 0;
             float* part = whole ? nullptr : slot_at(a.io.workspace, gridDim.x, p.slot);
             if (cnt > 0) {
-                const float n = !whole ? 1.f : sum > 0.f ? (kE4m3 ? a.v_scale[p.s.h] : 1.f) / sum : 0.f;
+                const float n = !whole ? 1.f : sum != 0.f ? (kE4m3 ? a.v_scale[p.s.h] : 1.f) / sum : 0.f;
                 const bool plain = whole && !a.io.gate && !a.io.o_f32;
                 const int step = plain ? kOut / 2 : kOut / 4;   // channels at a time
 #pragma unroll 1
@@ -912,7 +912,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 tc::fence_before();
             }
             const size_t head = w.head;
-            if (live && whole && a.io.lse) a.io.lse[head] = sum > 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
+            if (live && whole && a.io.lse) a.io.lse[head] = sum != 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
             if (live && !whole)
                 *reinterpret_cast<float2*>(part + (size_t)2 * kRows * kHeadDim + 2 * (x * kRows + r)) = make_float2(ref, sum);
             if (tid == 0 && p.last >= 0)
@@ -998,7 +998,7 @@ __global__ void __launch_bounds__(256) kda_attn_prefill_join_kernel(const Prefil
         const float n = sum != 0.f ? (a.v_scale ? a.v_scale[d.h] : 1.f) / sum : 0.f;
         const size_t head = ((size_t)d.tok + i) * a.Hq + d.h * a.G + g;
         mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
-        if (a.io.lse && lane == 0) a.io.lse[head] = sum > 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
+        if (a.io.lse && lane == 0) a.io.lse[head] = sum != 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
     }
 }
 

@@ -119,3 +119,25 @@ def test_infinite_queries_over_e4m3(call):
     assert bool(o.t[hit].isnan().all())
     check(o.t[~hit], want[~hit], bound[~hit], "o beside NaN rows")
     layer.done()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("call", CALLS)
+def test_lse_of_nan_rows(call, e4m3):
+    """lse is NaN where the logits are: -infinity says that a row sees no key."""
+    layer, kv, cu, q = make(call, e4m3)
+    req, sees = rows_of(kv, cu)
+    G = layer.hq // layer.hkv
+    want, wl, bound, lb = expect(layer, q, kv, cu)
+    key = kv[0] // 2
+    poison(layer, layer.k, 0, key, 1, 3)
+    row = 1 if cu is None else cu[1] - 2
+    q[row, 0, 100] = math.nan
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    hit[:, G:] = ((req == 0) & (sees > key))[:, None]
+    hit[row, 0] = True
+    o, lse = run_attend(layer, q, kv, cu)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    assert bool(lse.t[hit].isnan().all())
+    check(lse.t[~hit], wl[~hit], lb[~hit], "lse")
+    layer.done()
