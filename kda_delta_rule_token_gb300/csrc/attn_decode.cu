@@ -385,12 +385,11 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         uint32_t qf[8][4];   // A fragments
         float fac[2];        // logit -> power of two
         int sees[2];         // keys that the row sees (all of them where there is one token)
-        const float base = a.scale * (kE4m3 ? a.k_scale[h] : 1.f);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = first_row + half * 8 + g;
             const uint32_t (&w)[16] = raw[half];
-            fac[half] = base;
+            fac[half] = a.scale;
             sees[half] = cur.n > 1 && r < nrows ? cur.len - cur.n + 1 + r / a.G : cur.len;
             float up = 1.f;
             if (kE4m3) {
@@ -401,9 +400,9 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // q * 2^(14 - e) with 2^e <= top < 2^(e+1): exact in f16 down to 2^-28 of the row's largest.
-                const int e = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
+                const int e = mma::query_exponent(top);
                 up = exp2f((float)(14 - e));
-                fac[half] = base * exp2f((float)(e - 14));
+                fac[half] = mma::query_factor(a.scale, e - 14, a.k_scale[h]);
             }
 #pragma unroll
             for (int s = 0; s < 8; ++s)

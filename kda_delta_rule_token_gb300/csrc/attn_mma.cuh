@@ -123,6 +123,18 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Over an e4m3 cache a query row is held as q * 2^(to - e), with e this exponent
+// of its largest value (2^e <= top < 2^(e+1)).  bf16 reaches 2^127; below 2^-100
+// the row keeps less of its bits, which no logit in the range of fp32 shows.
+__device__ __forceinline__ int query_exponent(float top) { return top > 0.f ? max(-100, min(127, ilogbf(top))) : 0; }
+
+// What takes such a row's products with the keys as stored to powers of two:
+// scale * 2^(e - to) * k_scale.  Kept finite and above 0, so that a product of 0
+// and a masked one of -infinity stay what they are.
+__device__ __forceinline__ float query_factor(float scale, int e_to, float k_scale) {
+    return fmaxf(1e-37f, fminf(3e38f, scale * exp2f((float)e_to) * k_scale));
+}
+
 // Four consecutive channels of one head's output row.
 __device__ __forceinline__ void store4(const AttnIO& io, size_t at, float4 v) {
     if (io.gate) {

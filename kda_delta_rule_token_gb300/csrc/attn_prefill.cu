@@ -718,9 +718,9 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                     for (int e = 0; e < 4; ++e)
                         top = mma::max3(top, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
                 }
-                const int ex = top > 0.f ? max(-100, min(100, ilogbf(top))) : 0;
+                const int ex = mma::query_exponent(top);
                 const float up = exp2f((float)(7 - ex));
-                w.fac = a.scale * a.k_scale[part.s.h] * exp2f((float)(ex - 7));
+                w.fac = mma::query_factor(a.scale, ex - 7, a.k_scale[part.s.h]);
                 if (top == INFINITY) w.fac = __int_as_float(0x7fc00000);   // which e4m3 does not hold
 #pragma unroll 1
                 for (int c = 0; c < 16; c += 4) {

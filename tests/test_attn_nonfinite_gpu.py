@@ -141,3 +141,34 @@ def test_lse_of_nan_rows(call, e4m3):
     assert bool(lse.t[hit].isnan().all())
     check(lse.t[~hit], wl[~hit], lb[~hit], "lse")
     layer.done()
+
+
+class LargeQueries(Layer):
+    """Keys and values of different sizes."""
+
+    def values(self, n, scale, sigma):
+        return super().values(n, scale, sigma if scale is self.ks else 1.0)
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("up", [102, 110, 124])
+def test_large_queries_over_e4m3(call, up):
+    """Queries near 2^up (the largest bf16 are near 2^128) on keys near 2^-up: logits of ordinary size."""
+    new, kv, hq, hkv, page = CALLS[call]
+    layer = LargeQueries(hq, hkv, page, True, seed=up)
+    layer.ks.fill_(2.0 ** (4 - up))
+    layer.fill(kv, sigma=2.0 ** -up)
+    cu = None
+    if new is not None:
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+    q = (queries(layer, len(kv) if cu is None else cu[-1]).float() * 2.0 ** up).to(BF)
+    q[::3] = (q[::3].float() * 2.0 ** -up).to(BF)      # rows of ordinary size beside them
+    assert bool(q.float().isfinite().all())
+    want, wl, bound, lb = expect(layer, q, kv, cu)
+    o, lse = run_attend(layer, q, kv, cu, None, True)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    check(o.t, want, bound, "o")
+    check(lse.t, wl, lb, "lse")
+    layer.done()
