@@ -110,6 +110,8 @@ KDA_API kda_status kda_attn_bind_cache(kda_attn_ctx *ctx, int num_pages, void *k
  *   kv_lens     [B] int32 (out): c + n, or 0 for a request not admitted
  *   positions   [N] int32 (out): c + i for the i-th new token
  *   slots       [N] int64 (out): the token's cache slot, -1 for a request not admitted
+ *               (a page id below 0, in the table or the free list, gives -2, which
+ *               kda_attn_append reports)
  *   info        [4] int32 (out): new tokens of all requests (saturated at
  *               2^31 - 1), pages taken, pages left, requests not admitted
  * Rows past the last request's get position 0 and slot -1.  The first

@@ -143,7 +143,9 @@ __global__ void __launch_bounds__(kThreads) kda_attn_plan_kernel(const AttnPlanI
             } else {
                 page = *entry;
             }
-            slot = ((long long)page << shift) + row;
+            // An id below 0 must not come out as -1, which leaves a token unstored
+            // without a word: a slot that the append reports.
+            slot = page < 0 ? -2 : ((long long)page << shift) + row;
         }
         io.slots[t] = slot;
     }
