@@ -82,6 +82,7 @@ struct Smem {
     uint64_t full[kWarps * stages_per_warp<kRowTiles>()];
     uint64_t empty[kWarps * stages_per_warp<kRowTiles>()];
     long long scan[kWarps];
+    uint32_t zeros[kWarps];
     long long total, first_unit;
     int first_b;
     int dead;
@@ -115,19 +116,28 @@ __device__ __forceinline__ float* slot_at(void* ws, int ctas, int slot) {
     return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + desc_bytes(ctas)) + (size_t)slot * kSlotFloats;
 }
 
-// Request b as this file sees it: its new tokens, and its cached keys (0 where
-// it has no rows here).
+// Request b as this file sees it: its new tokens, its cached keys, and those
+// that it is worked on with (0 where it has no rows here).
 struct Request {
-    int tok0, n, len;
+    int tok0, n, keys, len;
 };
 
 __device__ __forceinline__ Request request(const DecodeArgs& a, int b) {
-    Request r{b, 1, attn_kv_len(a.io, b, a.page_shift)};
+    const int keys = attn_kv_len(a.io, b, a.page_shift);
+    Request r{b, 1, keys, keys};
     if (a.io.cu_new) {
         attn_tokens(a.io, b, r.tok0, r.n);
         if (r.n == 0 || !attn_few_rows(r.n, a.G)) r.len = 0;
     }
     return r;
+}
+
+// Rows of a request without keys that one CTA writes; of longer ones (a prompt
+// chunk that the plan refused) every CTA writes a share.  4096 tokens of 64 heads
+// among 300 requests of 2: 172 us, 1186 with a CTA for each request.
+constexpr int kOwnZeroRows = 256;
+__device__ __forceinline__ bool all_zero_it(const DecodeArgs& a, const Request& r) {
+    return r.keys == 0 && (long long)r.n * a.Hq > kOwnZeroRows;
 }
 
 // A position in the CTA's range.  The range also counts kPartCost units for
@@ -205,7 +215,12 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     const int per = (a.io.B + kThreads - 1) / kThreads;
     const int b0 = min(a.io.B, tid * per), b1 = min(a.io.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += cost_of<kUnit>(request(a, b).len, kPartCost);
+    bool shares = false;   // there is a request whose zero rows all CTAs write
+    for (int b = b0; b < b1; ++b) {
+        const Request r = request(a, b);
+        mine += cost_of<kUnit>(r.len, kPartCost);
+        shares |= all_zero_it(a, r);
+    }
     mine *= heads;
     long long upto = mine;
 #pragma unroll
@@ -214,7 +229,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         if (lane >= d) upto += y;
     }
     if (lane == 31) sm.scan[warp] = upto;
-    __syncthreads();
+    shares = __syncthreads_or(shares);
     long long total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -237,14 +252,28 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
         }
     }
     // Requests without keys: zero rows.
+    auto zero_rows = [&](const Request& r, long long from, long long step) {
+        const long long rows = (long long)r.n * a.Hq;
+        for (long long i = from; i < rows * (kHeadDim / 4); i += step)
+            mma::store4(a.io, (size_t)r.tok0 * a.Hq * kHeadDim + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+        if (a.io.lse)
+            for (long long i = from; i < rows; i += step) a.io.lse[(size_t)r.tok0 * a.Hq + i] = -INFINITY;
+    };
     for (int b = blockIdx.x; b < a.io.B; b += gridDim.x)
         if (attn_kv_len(a.io, b, a.page_shift) == 0) {
             const Request r = request(a, b);
-            const long long rows = (long long)r.n * a.Hq;
-            for (long long i = tid; i < rows * (kHeadDim / 4); i += kThreads)
-                mma::store4(a.io, (size_t)r.tok0 * a.Hq * kHeadDim + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
-            if (a.io.lse)
-                for (long long i = tid; i < rows; i += kThreads) a.io.lse[(size_t)r.tok0 * a.Hq + i] = -INFINITY;
+            if (!all_zero_it(a, r)) zero_rows(r, tid, kThreads);
+        }
+    if (shares)
+        for (int base = 0; base < a.io.B; base += kThreads) {
+            const uint32_t found = __ballot_sync(0xffffffffu, base + tid < a.io.B && all_zero_it(a, request(a, base + tid)));
+            if (lane == 0) sm.zeros[warp] = found;
+            __syncthreads();
+            for (int w = 0; w < kWarps; ++w)
+                for (uint32_t m = sm.zeros[w]; m; m &= m - 1)
+                    zero_rows(request(a, base + 32 * w + __ffs((int)m) - 1), (long long)blockIdx.x * kThreads + tid,
+                              (long long)gridDim.x * kThreads);
+            __syncthreads();
         }
     __syncthreads();
     if (!works) {

@@ -1,10 +1,14 @@
 """The paged softmax-attention operators at their edges: pages and offsets that
 are not valid, requests refused by the plan."""
+import math
+import statistics
+
 import pytest
 import torch
 
+import attn_ref as ref
 import kda_delta_rule_token_gb300 as kda
-from test_attn_gpu import BF, D, DEV, Layer, _lib, i32  # noqa: F401
+from test_attn_gpu import BF, D, DEV, Layer, _lib, check, i32, queries, run_attend  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -29,4 +33,64 @@ def test_held_pages_below_zero_are_reported(page, held):
         kda.kda_attn_append(layer.attn, 1, q, k, k, pos, slots, q)
         assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_ERR_INVALID_ARG
         assert torch.equal(layer.k.view(torch.int16), before)
+    layer.done()
+
+
+def _timed(call, n=15):
+    call()
+    times = []
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b) * 1000)
+    return statistics.median(times)
+
+
+def test_a_refused_chunk_is_written_by_all():
+    """A long chunk that the plan refused (its length is 0, its rows still stand in
+    the step) beside requests of few rows: 67 MB of zeros, which the whole device
+    writes in some 20 us beside the call's other 150, and one of its SMs not within 1000."""
+    new, kv, hq, hkv = [2] * 300 + [4096], [100] * 300 + [0], 64, 32
+    layer = Layer(hq, hkv, 16)
+    layer.fill(kv)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    q = queries(layer, cu[-1])
+    o, lse = run_attend(layer, q, kv, cu)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    assert bool((o.t[600:] == 0).all()) and bool((lse.t[600:] == -math.inf).all())
+    assert o.intact() and lse.intact()
+    cu_t, kv_t = i32(cu), i32(kv)
+    us = _timed(lambda: kda.kda_attn_prefill(layer.attn, 301, cu[-1], cu_t, q, layer.table, kv_t, o.t, layer.ws.t, lse=lse.t))
+    print(f"\n  {us:.0f} us")
+    assert us < 400
+    layer.done()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("lse", [False, True])
+def test_several_refused_requests(f32, lse):
+    """Short and long requests without keys among others, more of them than a CTA has threads."""
+    new = [(5 * i) % 9 for i in range(300)] + [200, 0, 130, 3]
+    kv = [0 if i % 3 else 20 + i for i in range(300)] + [0, 0, 0, 50]
+    layer = Layer(4, 2, 16)
+    layer.fill(kv)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    q = queries(layer, cu[-1] + 3)
+    o, l = run_attend(layer, q, kv, cu, None, f32, lse)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    N = cu[-1]
+    want, wl, bound, lb = ref.attend(q[:N], layer.k, layer.v, layer.table_list, kv, cu, 16, D ** -0.5)
+    check(o.t[:N], want, bound if f32 else bound * (1 + ref.UBF) + ref.UBF * want.abs(), "o")
+    if lse:
+        none = wl == -math.inf
+        assert torch.equal(l.t[:N] == -math.inf, none)
+    assert bool((o.t[N:].view(torch.uint8) == 0x5A).all())
+    assert o.intact()
     layer.done()
