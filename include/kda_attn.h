@@ -158,7 +158,7 @@ KDA_API size_t kda_attn_workspace_bytes(const kda_attn_ctx *ctx);
  *   block_table [B][max_pages] int32; entries past a request's length are not read.
  *               A page id outside the cache reads as zeros and is an error.
  *   kv_lens     [B] int32 (clamped to 0 .. max_pages * page_size); 0: the
- *               request's o is zero and its lse -infinity
+ *               request's o is zero, whatever its gate holds, and its lse -infinity
  *   gate_logit  [B][Hq][d] fp32, or NULL
  *   o           [B][Hq][d], bf16, or fp32 if o_f32 is nonzero (the input of kda_project_o)
  *   lse         [B][Hq] fp32 or NULL: ln of the sum of exp(softmax_scale * q.k);
@@ -178,7 +178,7 @@ KDA_API kda_status kda_attn_decode(kda_attn_ctx *ctx, int B, const uint16_t *q, 
  * Causal attention of the N packed new tokens of B requests, whose keys and
  * values are in the cache already (kda_attn_append): of request b's n =
  * cu_new[b + 1] - cu_new[b] tokens, the i-th sees keys 0 .. kv_lens[b] - n + i.
- * A row that sees no key gives o = 0 and lse = -infinity.
+ * A row that sees no key gives o = 0, whatever its gate holds, and lse = -infinity.
  *   cu_new      [B + 1] int32, ascending; rows past cu_new[B] are not written
  *   q           [N][Hq][d] bf16;  gate_logit, o, lse: [N][Hq]... as for kda_attn_decode
  * Otherwise as kda_attn_decode.  B == 0 or N == 0 is a no-op.

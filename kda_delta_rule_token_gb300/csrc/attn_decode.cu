@@ -255,7 +255,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
     auto zero_rows = [&](const Request& r, long long from, long long step) {
         const long long rows = (long long)r.n * a.Hq;
         for (long long i = from; i < rows * (kHeadDim / 4); i += step)
-            mma::store4(a.io, (size_t)r.tok0 * a.Hq * kHeadDim + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+            mma::store4(a.io, (size_t)r.tok0 * a.Hq * kHeadDim + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f), false);
         if (a.io.lse)
             for (long long i = from; i < rows; i += step) a.io.lse[(size_t)r.tok0 * a.Hq + i] = -INFINITY;
     };
@@ -694,7 +694,7 @@ kda_attn_decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap k
             if (whole) {
                 const float n = l != 0.f ? vscale / l : 0.f;   // 0: the row sees no key (NaN is not 0: a NaN logit shows)
                 const size_t at = head_of(cur, rw, row);
-                mma::store4(a.io, at * kHeadDim + col, make_float4(v.x * n, v.y * n, v.z * n, v.w * n));
+                mma::store4(a.io, at * kHeadDim + col, make_float4(v.x * n, v.y * n, v.z * n, v.w * n), l != 0.f);
                 if (a.io.lse && col == 0) a.io.lse[at] = l != 0.f ? (top + log2f(l)) / kLog2e : -INFINITY;
             } else {
                 *reinterpret_cast<float4*>(part + row * kHeadDim + col) = v;
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
     auto finish = [&](int row) {
         const float n = sum != 0.f ? (a.v_scale ? a.v_scale[h] : 1.f) / sum : 0.f;
         const size_t head = ((size_t)d.tok0 + (d.n > 1 ? row / a.G : 0)) * a.Hq + h * a.G + (d.n > 1 ? row % a.G : row0 + row);
-        mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
+        mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n), sum != 0.f);
         if (a.io.lse && lane == 0) a.io.lse[head] = sum != 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
     };
     if (parts <= kFewParts) {

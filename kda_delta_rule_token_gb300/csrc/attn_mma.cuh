@@ -135,9 +135,10 @@ __device__ __forceinline__ float query_factor(float scale, int e_to, float k_sca
     return fmaxf(1e-37f, fminf(3e38f, scale * exp2f((float)e_to) * k_scale));
 }
 
-// Four consecutive channels of one head's output row.
-__device__ __forceinline__ void store4(const AttnIO& io, size_t at, float4 v) {
-    if (io.gate) {
+// Four consecutive channels of one head's output row; a row that sees no key is
+// zero whatever its gate holds.
+__device__ __forceinline__ void store4(const AttnIO& io, size_t at, float4 v, bool sees) {
+    if (io.gate && sees) {
         const float4 g = *reinterpret_cast<const float4*>(io.gate + at);
         v.x /= 1.f + exp2_approx(-g.x * kLog2e);
         v.y /= 1.f + exp2_approx(-g.y * kLog2e);

@@ -862,6 +862,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             if (cnt > 0) {
                 const float n = !whole ? 1.f : sum != 0.f ? (kE4m3 ? a.v_scale[p.s.h] : 1.f) / sum : 0.f;
                 const bool plain = whole && !a.io.gate && !a.io.o_f32;
+                const uint32_t seeing = __ballot_sync(0xffffffffu, sum != 0.f);   // rows that see a key
                 const int step = plain ? kOut / 2 : kOut / 4;   // channels at a time
 #pragma unroll 1
                 for (int c0 = 0; c0 < kHeadDim; c0 += step) {
@@ -902,7 +903,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                             const size_t h = head_of(w, row);
                             const float4 v = *reinterpret_cast<const float4*>(place_o(row, c));
                             if (w.lives >> row & 1u) {
-                                if (whole) mma::store4(a.io, h * kHeadDim + c0 + 4 * c, v);
+                                if (whole) mma::store4(a.io, h * kHeadDim + c0 + 4 * c, v, seeing >> row & 1u);
                                 else *reinterpret_cast<float4*>(part + (size_t)(warp * 32 + row) * kHeadDim + c0 + 4 * c) = v;
                             }
                         }
@@ -997,7 +998,7 @@ __global__ void __launch_bounds__(256) kda_attn_prefill_join_kernel(const Prefil
         }
         const float n = sum != 0.f ? (a.v_scale ? a.v_scale[d.h] : 1.f) / sum : 0.f;
         const size_t head = ((size_t)d.tok + i) * a.Hq + d.h * a.G + g;
-        mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n));
+        mma::store4(a.io, head * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n), sum != 0.f);
         if (a.io.lse && lane == 0) a.io.lse[head] = sum != 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
     }
 }

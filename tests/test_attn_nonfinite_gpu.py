@@ -172,3 +172,40 @@ def test_large_queries_over_e4m3(call, up):
     check(o.t, want, bound, "o")
     check(lse.t, wl, lb, "lse")
     layer.done()
+
+
+GATED = {
+    "decode": (None, [300, 0, 77], 8, 2),
+    "few": ([5, 3, 0, 7], [2, 300, 0, 0], 8, 2),            # rows that see no key, a request without keys
+    "prompt": ([90, 40], [20, 300], 8, 2),
+    "prompt_cut": ([128, 64], [60, 30000], 8, 2),
+    "refused": ([3, 300, 2, 4], [50, 0, 3, 1], 8, 2),
+    "refused_all": ([600, 300], [700, 0], 8, 2),
+}
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("call", GATED)
+def test_rows_without_keys_do_not_read_their_gate(call, f32, e4m3):
+    """o is zero there whatever the gate holds: unused rows are often not written at all."""
+    new, kv, hq, hkv = GATED[call]
+    layer = Layer(hq, hkv, 16, e4m3)
+    layer.fill(kv)
+    cu = None
+    if new is not None:
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+    req, sees = rows_of(kv, cu)
+    q = queries(layer, len(req))
+    gate = torch.randn(len(req), hq, D, generator=layer.g, device=DEV)
+    want, wl, bound, lb = expect(layer, q, kv, cu, gate)
+    gate[sees <= 0] = math.nan
+    o, lse = run_attend(layer, q, kv, cu, gate, f32)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    assert bool((o.t[sees <= 0] == 0).all()) and bool((lse.t[sees <= 0] == -math.inf).all())
+    if not f32:
+        bound = bound * (1 + ref.UBF) + ref.UBF * want.abs()
+    check(o.t[sees > 0], want[sees > 0], bound[sees > 0], "o")
+    layer.done()
