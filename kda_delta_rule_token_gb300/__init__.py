@@ -339,8 +339,24 @@ def kda_attn_bind_cache(attn, num_pages, k_cache, v_cache) -> None:
 
 
 def _pitch(table, given):
-    """Row length of a block table: given, or the tensor's."""
-    return int(given) if given is not None else table.stride(0)
+    """Row length of a block table [B, max_pages]: given, or the tensor's."""
+    if given is not None:
+        return int(given)
+    if table.dim() == 2:
+        (rows, width), (pitch, step) = table.shape, table.stride()
+        if step == 1 or width == 1:
+            if pitch >= width:
+                return pitch
+            if rows == 1:
+                return width
+    raise ValueError(f"block_table must be [B, max_pages] with dense rows: shape {tuple(table.shape)}, strides {table.stride()}")
+
+
+def _dense(t, name):
+    """The address of a tensor that the library takes as dense."""
+    if t is not None and not isinstance(t, int) and not t.is_contiguous():
+        raise ValueError(f"{name} must be dense: shape {tuple(t.shape)}, strides {t.stride()}")
+    return _p(t)
 
 
 def kda_attn_plan(attn, B, N, cache_lens, new_lens, free_pages, free_count, block_table, cu_new, kv_lens,
@@ -357,16 +373,17 @@ def _token_stride(t, given):
     if given is not None:
         return int(given)
     st = t.stride()
-    if st[-1] != 1 or st[-2] != HEAD_DIM:
+    heads = t.shape[-2]
+    if st[-1] != 1 or (st[-2] != HEAD_DIM and heads != 1):
         raise ValueError(f"heads must be dense rows of {HEAD_DIM} elements: strides {tuple(st)}")
-    return st[0]
+    return st[0] if t.shape[0] != 1 else heads * HEAD_DIM   # of one token any stride will do
 
 
 def kda_attn_append(attn, N, q, k, v, positions, slots, q_out, *, q_stride=None, k_stride=None,
                     v_stride=None, stream=None) -> None:
     _check(load().kda_attn_append(attn, N, _p(q), _token_stride(q, q_stride), _p(k), _token_stride(k, k_stride),
-                                  _p(v), _token_stride(v, v_stride), _p(positions), _p(slots), _p(q_out),
-                                  _stream(stream)), "kda_attn_append")
+                                  _p(v), _token_stride(v, v_stride), _p(positions), _p(slots),
+                                  _dense(q_out, "q_out"), _stream(stream)), "kda_attn_append")
 
 
 def kda_attn_workspace_bytes(attn) -> int:
@@ -379,16 +396,17 @@ def _is_f32(o, given):
 
 def kda_attn_decode(attn, B, q, block_table, kv_lens, o, workspace, *, max_pages=None, gate_logit=None,
                     o_f32=None, lse=None, workspace_bytes=0, stream=None) -> None:
-    _check(load().kda_attn_decode(attn, B, _p(q), _p(block_table), _pitch(block_table, max_pages), _p(kv_lens),
-                                  _p(gate_logit), _p(o), _is_f32(o, o_f32), _p(lse), _p(workspace),
+    _check(load().kda_attn_decode(attn, B, _dense(q, "q"), _p(block_table), _pitch(block_table, max_pages),
+                                  _p(kv_lens), _dense(gate_logit, "gate_logit"), _dense(o, "o"),
+                                  _is_f32(o, o_f32), _dense(lse, "lse"), _p(workspace),
                                   _nbytes(workspace, workspace_bytes), _stream(stream)), "kda_attn_decode")
 
 
 def kda_attn_prefill(attn, B, N, cu_new, q, block_table, kv_lens, o, workspace, *, max_pages=None,
                      gate_logit=None, o_f32=None, lse=None, workspace_bytes=0, stream=None) -> None:
-    _check(load().kda_attn_prefill(attn, B, N, _p(cu_new), _p(q), _p(block_table),
-                                   _pitch(block_table, max_pages), _p(kv_lens), _p(gate_logit), _p(o),
-                                   _is_f32(o, o_f32), _p(lse), _p(workspace),
+    _check(load().kda_attn_prefill(attn, B, N, _p(cu_new), _dense(q, "q"), _p(block_table),
+                                   _pitch(block_table, max_pages), _p(kv_lens), _dense(gate_logit, "gate_logit"),
+                                   _dense(o, "o"), _is_f32(o, o_f32), _dense(lse, "lse"), _p(workspace),
                                    _nbytes(workspace, workspace_bytes), _stream(stream)), "kda_attn_prefill")
 
 
