@@ -179,7 +179,9 @@ KDA_API kda_status kda_attn_decode(kda_attn_ctx *ctx, int B, const uint16_t *q, 
  * values are in the cache already (kda_attn_append): of request b's n =
  * cu_new[b + 1] - cu_new[b] tokens, the i-th sees keys 0 .. kv_lens[b] - n + i.
  * A row that sees no key gives o = 0, whatever its gate holds, and lse = -infinity.
- *   cu_new      [B + 1] int32, ascending; rows past cu_new[B] are not written
+ *   cu_new      [B + 1] int32, ascending; rows past cu_new[B] are not written.
+ *               Offsets that claim rows more than once write some of them in no
+ *               set order, or are an error and write none.
  *   q           [N][Hq][d] bf16;  gate_logit, o, lse: [N][Hq]... as for kda_attn_decode
  * Otherwise as kda_attn_decode.  B == 0 or N == 0 is a no-op.
  */
@@ -189,7 +191,8 @@ KDA_API kda_status kda_attn_prefill(kda_attn_ctx *ctx, int B, int N, const int32
                                     size_t workspace_bytes, void *stream);
 
 /* As kda_sync_status: KDA_ERR_TIMEOUT if a bounded wait gave up,
- * KDA_ERR_INVALID_ARG if a kernel met a page id or slot outside the cache. */
+ * KDA_ERR_INVALID_ARG if a kernel met a page id or slot outside the cache, or
+ * row offsets that are not ascending. */
 KDA_API kda_status kda_attn_sync_status(kda_attn_ctx *ctx, void *stream);
 
 #ifdef __cplusplus

@@ -12,7 +12,8 @@
 namespace kda {
 
 // Error-word bits of the attention context beside the bounded-wait ones of
-// ptx.cuh: a page id or slot outside the cache was met (and not accessed).
+// ptx.cuh: a page id or slot outside the cache was met (and not accessed), or
+// row offsets that claim rows more than once (and nothing was done).
 constexpr int kErrAttnIndex = 1 << 16;
 
 // One layer as its kernels see it.

@@ -123,6 +123,7 @@ struct Ctl {
     int busiest;
     int kissued, vissued, raws;   // copies issued (raws: of values whose request ends in the tile)
     int warp_sum[kScan / 32];
+    long long warp_pairs[kScan / 32];
     int pre[kScan];          // pairs of token tiles before the requests of scan thread t
     int units[kScan];        // key tiles and costs before the segments of scan thread t
     int load[kMaxCtas];      // of each CTA, were the segments dealt whole
@@ -285,16 +286,17 @@ __device__ __forceinline__ bool take_part(Ctl& ctl, int& np, Part& p, int* dead,
 }
 
 // Inclusive prefix of v over the first kScan threads; all threads of the CTA call it.
-__device__ __forceinline__ int scan_inclusive(int v, int* s_warp, int* total) {
+template <typename T>
+__device__ __forceinline__ T scan_inclusive(T v, T* s_warp, T* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, d);
+        const T y = __shfl_up_sync(0xffffffffu, v, d);
         if (lane >= d) v += y;
     }
     if (lane == 31 && warp < kScan / 32) s_warp[warp] = v;
     __syncthreads();
-    int all = 0;
+    T all = 0;
 #pragma unroll
     for (int w = 0; w < kScan / 32; ++w) {
         if (w < warp) v += s_warp[w];
@@ -352,13 +354,20 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     // Segments of all requests.
     Sched sc;
     sc.per = (a.io.B + kScan - 1) / kScan;
-    int mine = 0;
+    long long mine = 0, pairs;
     if (tid < kScan)
         for (int b = min(a.io.B, tid * sc.per), end = min(a.io.B, b + sc.per); b < end; ++b) mine += pairs_of(a, b);
-    const int upto = scan_inclusive(mine, ctl.warp_sum, &sc.total);
-    if (sc.total == 0) return;   // every request has few rows
+    const long long upto = scan_inclusive(mine, ctl.warp_pairs, &pairs);
+    if (pairs == 0) return;   // every request has few rows
+    if (pairs > a.io.N) {
+        // More pairs than tokens: the offsets claim rows more than once, and
+        // sums of so many segments need not fit what follows.
+        if (tid == 0 && blockIdx.x == 0) atomicOr(err, kErrAttnIndex);
+        return;
+    }
+    sc.total = (int)pairs;
     if (warp == kWarpMma) tc::alloc(&ctl.tmem, 512);
-    if (tid < kScan) ctl.pre[tid] = upto - mine;
+    if (tid < kScan) ctl.pre[tid] = (int)(upto - mine);
     __syncthreads();
     sc.segments = sc.total * a.Hkv;
     sc.split = false;

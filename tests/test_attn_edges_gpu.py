@@ -8,7 +8,7 @@ import torch
 
 import attn_ref as ref
 import kda_delta_rule_token_gb300 as kda
-from test_attn_gpu import BF, D, DEV, Layer, _lib, check, i32, queries, run_attend  # noqa: F401
+from test_attn_gpu import BF, D, DEV, Layer, _lib, check, i32, queries, run_attend, verify  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -93,4 +93,17 @@ def test_several_refused_requests(f32, lse):
         assert torch.equal(l.t[:N] == -math.inf, none)
     assert bool((o.t[N:].view(torch.uint8) == 0x5A).all())
     assert o.intact()
+    layer.done()
+
+
+def test_offsets_that_claim_rows_twice():
+    """Row offsets that are not ascending and claim more token tiles than there are rows: reported, nothing written."""
+    layer = Layer(128, 1, 16)
+    layer.fill([100] * 5)
+    q = queries(layer, 100)
+    o, lse = run_attend(layer, q, [100] * 5, [0, 100, 0, 100, 0, 100])
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_ERR_INVALID_ARG
+    assert bool((o.t.view(torch.uint8) == 0x5A).all()) and o.intact() and lse.intact()
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    verify(layer, q, [100] * 5, [0, 30, 30, 77, 90, 100])
     layer.done()
