@@ -209,3 +209,47 @@ def test_rows_without_keys_do_not_read_their_gate(call, f32, e4m3):
         bound = bound * (1 + ref.UBF) + ref.UBF * want.abs()
     check(o.t[sees > 0], want[sees > 0], bound[sees > 0], "o")
     layer.done()
+
+
+VALUES = {
+    "few_two_tiles": ([5, 3, 8], [300, 40, 77], 8, 2),          # two warps to a tile, each with rows of its own
+    "few_turns": ([4, 2, 8], [300, 40, 65], 8, 2),              # or by turns, beside one that needs both
+    "few_one": ([7, 9], [129, 9], 4, 4),
+    "few_cut": ([8, 2], [20001, 9], 8, 2),
+}
+
+
+@pytest.mark.parametrize("e4m3,page", [(False, 16), (False, 128), (True, 32), (True, 64)])
+@pytest.mark.parametrize("form", ["plain", "gate", "f32"])
+@pytest.mark.parametrize("call", VALUES)
+def test_values_that_a_row_does_not_see(call, form, e4m3, page):
+    """NaN and infinities in the values of later tokens of the same chunk leave
+    the rows before them as they are; the rows that see one have it in that channel only."""
+    new, kv, hq, hkv = VALUES[call]
+    layer = Layer(hq, hkv, page, e4m3, seed=len(call))
+    layer.fill(kv)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    G = hq // hkv
+    req, sees = rows_of(kv, cu)
+    q = queries(layer, cu[-1])
+    gate = torch.randn(cu[-1], hq, D, generator=layer.g, device=DEV) if form == "gate" else None
+    want, wl, bound, lb = expect(layer, q, kv, cu, gate)
+    hit = torch.zeros(want.shape, dtype=torch.bool, device=DEV)
+    for b, n in enumerate(kv):
+        t = new[b]
+        spots = [(n - 1, 0, 0, math.nan), (n - 1, hkv - 1, 127, -math.inf), (n - 1 - t // 2, 0, 65, math.inf),
+                 (n - t, hkv - 1, 30, math.nan)]
+        for key, head, channel, value in spots[: 4 if b == 0 else 2]:
+            poison(layer, layer.v, b, key, head, channel, value)
+            hit[:, head * G:(head + 1) * G, channel] |= ((req == b) & (sees > key))[:, None]
+    o, lse = run_attend(layer, q, kv, cu, gate, form == "f32")
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    if form != "f32":
+        bound = bound * (1 + ref.UBF) + ref.UBF * want.abs()
+    assert not o.t[hit].isfinite().any()
+    check(o.t[~hit], want[~hit], bound[~hit], "o")
+    check(lse.t, wl, lb, "lse")
+    assert o.intact()
+    layer.done()
