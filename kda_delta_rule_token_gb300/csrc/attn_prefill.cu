@@ -123,7 +123,6 @@ struct Ctl {
     int busiest;
     int kissued, vissued, raws;   // copies issued (raws: of values whose request ends in the tile)
     int warp_sum[kScan / 32];
-    long long warp_pairs[kScan / 32];
     int pre[kScan];          // pairs of token tiles before the requests of scan thread t
     int units[kScan];        // key tiles and costs before the segments of scan thread t
     int load[kMaxCtas];      // of each CTA, were the segments dealt whole
@@ -286,17 +285,16 @@ __device__ __forceinline__ bool take_part(Ctl& ctl, int& np, Part& p, int* dead,
 }
 
 // Inclusive prefix of v over the first kScan threads; all threads of the CTA call it.
-template <typename T>
-__device__ __forceinline__ T scan_inclusive(T v, T* s_warp, T* total) {
+__device__ __forceinline__ int scan_inclusive(int v, int* s_warp, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, v, d);
+        const int y = __shfl_up_sync(0xffffffffu, v, d);
         if (lane >= d) v += y;
     }
     if (lane == 31 && warp < kScan / 32) s_warp[warp] = v;
     __syncthreads();
-    T all = 0;
+    int all = 0;
 #pragma unroll
     for (int w = 0; w < kScan / 32; ++w) {
         if (w < warp) v += s_warp[w];
@@ -354,20 +352,21 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     // Segments of all requests.
     Sched sc;
     sc.per = (a.io.B + kScan - 1) / kScan;
-    long long mine = 0, pairs;
+    long long sum_pairs = 0;
     if (tid < kScan)
-        for (int b = min(a.io.B, tid * sc.per), end = min(a.io.B, b + sc.per); b < end; ++b) mine += pairs_of(a, b);
-    const long long upto = scan_inclusive(mine, ctl.warp_pairs, &pairs);
-    if (pairs == 0) return;   // every request has few rows
-    if (pairs > a.io.N) {
-        // More pairs than tokens: the offsets claim rows more than once, and
-        // sums of so many segments need not fit what follows.
+        for (int b = min(a.io.B, tid * sc.per), end = min(a.io.B, b + sc.per); b < end; ++b) sum_pairs += pairs_of(a, b);
+    const int mine = (int)min(sum_pairs, (long long)(0x7fffffff / kScan));
+    const int upto = scan_inclusive(mine, ctl.warp_sum, &sc.total);
+    if (sc.total == 0) return;   // every request has few rows
+    if (sc.total > a.io.N) {
+        // More pairs than tokens (or a share of them cut short, which memory has
+        // no room for): the offsets claim rows more than once, and sums of so many
+        // segments need not fit what follows.
         if (tid == 0 && blockIdx.x == 0) atomicOr(err, kErrAttnIndex);
         return;
     }
-    sc.total = (int)pairs;
     if (warp == kWarpMma) tc::alloc(&ctl.tmem, 512);
-    if (tid < kScan) ctl.pre[tid] = (int)(upto - mine);
+    if (tid < kScan) ctl.pre[tid] = upto - mine;
     __syncthreads();
     sc.segments = sc.total * a.Hkv;
     sc.split = false;
