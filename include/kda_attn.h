@@ -165,7 +165,9 @@ KDA_API size_t kda_attn_workspace_bytes(const kda_attn_ctx *ctx);
  *               NaN where one of the row's logits is
  *   workspace   kda_attn_workspace_bytes bytes, 16-byte aligned
  * q, o and gate_logit 16-byte aligned, the others 4-byte.  What lies in the
- * cache past a request's length, NaN and infinities among it, has no effect.
+ * cache past a request's length, or at keys that a row does not see, has no
+ * effect on it, NaN and infinities among that.  A row that sees a NaN key is NaN;
+ * one that sees a NaN or infinite value is NaN or infinite in that channel.
  * The result does not depend on the order in which parts of the work end.
  * B == 0 is a no-op.
  */

@@ -47,6 +47,7 @@
 
 #include <atomic>
 
+#include "attn_again.cuh"
 #include "attn_internal.cuh"
 #include "attn_mma.cuh"
 #include "attn_tma.cuh"
@@ -180,22 +181,6 @@ __device__ __forceinline__ void step(const DecodeArgs& a, Walk& w) {
     } while (w.units == 0);
 }
 
-// Four channels of a cached row as fp32, zeros for a page outside the cache.
-template <bool kE4m3>
-__device__ __forceinline__ float4 cached4(const DecodeArgs& a, const void* cache, int b, int h, int key, int col) {
-    const int page = a.io.block_table[(size_t)b * a.io.max_pages + (key >> a.page_shift)];
-    if (page < 0 || page >= a.num_pages) return make_float4(0.f, 0.f, 0.f, 0.f);
-    const size_t at = ((((size_t)page * a.Hkv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * kHeadDim + col;
-    if (kE4m3) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(cache) + at);
-        const uint32_t lo = mma::e4m3x2_f16x2(w), hi = mma::e4m3x2_f16x2(w >> 16);
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo)), y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        return make_float4(x.x, x.y, y.x, y.y);
-    }
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(cache) + at);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-}
-
 // The walk over a CTA's range of `left` units, from unit `first` of request b's heads on.
 template <int kUnit, int kPartCost>
 __device__ __forceinline__ Walk begin_walk(const DecodeArgs& a, long long left, int b, long long first) {
@@ -216,59 +201,29 @@ __device__ __forceinline__ Walk begin_walk(const DecodeArgs& a, long long left, 
     return w;
 }
 
-// Rows of several tokens once more, where a key that a row does not see holds NaN
-// or an infinity in a value.  The products take in whole tiles, and a weight of 0
-// does not silence those: the row's channels that have one are added again, from
-// the keys that it sees, and put in place of what the loop over tiles wrote.  A
-// warp per row, four channels per lane.  Only CTAs that wrote such a value look for
-// rows of this kind, after their work (32 x 5 tokens without any 74.7 -> 75.8 us;
-// looked for in the loop over tiles, by tile or by part: 77 to 84).
+// Puts right rows of several tokens (attn_again.cuh), a warp per request and head.
+// Only CTAs that wrote NaN or an infinity for such a row come here, after their
+// work (32 x 5 tokens without any 74.0 -> 74.6 us; looked for in the loop over tiles,
+// by tile or by part: 77 to 84).
 template <bool kE4m3, int kUnit, int kPartCost>
 __device__ __noinline__ void mend_rows(const DecodeArgs& a, long long left, int first_b, long long first_unit) {
-    const int warp = threadIdx.x >> 5, col = (threadIdx.x & 31) * 4;
+    const int warp = threadIdx.x >> 5, row = threadIdx.x & 31;
     Walk w = begin_walk<kUnit, kPartCost>(a, left, first_b, first_unit);
-    for (bool at_start = true; w.left > 0; at_start = false) {
+    for (int nth = 0; w.left > 0; ++nth) {
         const int u0 = w.u, u1 = (int)min((long long)w.units, u0 + w.left), h = w.vh;   // n > 1: one pass
-        const int from = u0 * kUnit, to = (int)min((long long)w.len, (long long)u1 * kUnit);
-        for (int row = warp; w.n > 1 && row < w.n * a.G; row += kWarps) {
-            const int sees = w.len - w.n + 1 + row / a.G;
-            bool unseen = false;
-            for (int key = max(from, sees); key < to; ++key) {
-                const float4 x = cached4<kE4m3>(a, a.v_cache, w.b, h, key, col);
-                unseen |= !(fabsf(x.x + x.y + x.z + x.w) < INFINITY);
-            }
-            if (!__any_sync(0xffffffffu, unseen)) continue;
+        if (w.n > 1 && nth % kWarps == warp) {
             const size_t head = ((size_t)w.tok0 + row / a.G) * a.Hq + h * a.G + row % a.G;
-            const uint2 qw = *reinterpret_cast<const uint2*>(a.io.q + head * kHeadDim + col);
-            const float factor = a.scale * (kE4m3 ? a.k_scale[h] : 1.f);
-            const float q0 = __uint_as_float(qw.x << 16) * factor, q1 = __uint_as_float(qw.x & 0xffff0000u) * factor;
-            const float q2 = __uint_as_float(qw.y << 16) * factor, q3 = __uint_as_float(qw.y & 0xffff0000u) * factor;
-            float ref = kNoRef, sum = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int key = from; key < min(to, sees); ++key) {
-                const float4 k = cached4<kE4m3>(a, a.k_cache, w.b, h, key, col);
-                const float4 x = cached4<kE4m3>(a, a.v_cache, w.b, h, key, col);
-                float z = q0 * k.x + q1 * k.y + q2 * k.z + q3 * k.w;
-#pragma unroll
-                for (int m = 16; m; m >>= 1) z += __shfl_xor_sync(0xffffffffu, z, m);
-                const float now = fmaxf(ref, z), f = mma::exp2_approx(ref - now), p = mma::exp2_approx(z - now);
-                ref = now;
-                sum = fmaf(sum, f, p);
-                v.x = fmaf(p, x.x, v.x * f);
-                v.y = fmaf(p, x.y, v.y * f);
-                v.z = fmaf(p, x.z, v.z * f);
-                v.w = fmaf(p, x.w, v.w * f);
-            }
-            if (!unseen) continue;
-            if (u0 == 0 && u1 == w.units) {
-                const float n = sum != 0.f ? (kE4m3 ? a.v_scale[h] : 1.f) / sum : 0.f;
-                mma::store4(a.io, head * kHeadDim + col, make_float4(v.x * n, v.y * n, v.z * n, v.w * n), sum != 0.f);
-            } else {
-                float* part = slot_at(a.io.workspace, gridDim.x, 2 * blockIdx.x + (at_start ? 0 : 1));
-                const float f = sum != 0.f ? mma::exp2_approx(ref - part[kMaxRows * kHeadDim + 2 * row]) : 0.f;
-                *reinterpret_cast<float4*>(part + row * kHeadDim + col) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-            }
+            float* part = slot_at(a.io.workspace, gridDim.x, 2 * blockIdx.x + (nth == 0 ? 0 : 1));
+            rows_again<kE4m3>(a, w.b, h, row < w.n * a.G, head, u0 * kUnit, (int)min((long long)w.len, (long long)u1 * kUnit),
+                              w.len - w.n + 1 + row / a.G, [&](int channel, float4 v, float ref, float sum) {
+                if (u0 == 0 && u1 == w.units) {
+                    const float n = sum != 0.f ? (kE4m3 ? a.v_scale[h] : 1.f) / sum : 0.f;
+                    mma::store4(a.io, head * kHeadDim + channel, make_float4(v.x * n, v.y * n, v.z * n, v.w * n), sum != 0.f);
+                } else {
+                    const float f = sum != 0.f ? mma::exp2_approx(ref - part[kMaxRows * kHeadDim + 2 * row]) : 0.f;
+                    *reinterpret_cast<float4*>(part + row * kHeadDim + channel) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                }
+            });
         }
         w.left -= u1 - u0 - 1;
         w.u = u1 - 1;

@@ -113,6 +113,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// The same, NaN if one of them is.
+__device__ __forceinline__ float max3n(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);

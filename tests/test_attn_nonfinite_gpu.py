@@ -216,6 +216,12 @@ VALUES = {
     "few_turns": ([4, 2, 8], [300, 40, 65], 8, 2),              # or by turns, beside one that needs both
     "few_one": ([7, 9], [129, 9], 4, 4),
     "few_cut": ([8, 2], [20001, 9], 8, 2),
+    "prompt": ([150, 40], [700, 41], 4, 2),
+    "prompt_wide": ([300], [300], 2, 2),                        # 128 tokens to a row tile
+    "prompt_deep": ([20], [520], 64, 1),                        # two tokens to a row tile
+    "prompt_rounds": ([700, 650], [900, 650], 16, 8),
+    "prompt_cut": ([128], [32768], 8, 2),
+    "prompt_short": ([64, 33, 50], [64, 33, 90], 8, 2),         # the request ends in the tile
 }
 
 
@@ -252,4 +258,32 @@ def test_values_that_a_row_does_not_see(call, form, e4m3, page):
     check(o.t[~hit], want[~hit], bound[~hit], "o")
     check(lse.t, wl, lb, "lse")
     assert o.intact()
+    layer.done()
+
+
+def test_values_behind_a_prompt_of_clean_ones():
+    """A call after one with NaN values, and requests beside the one that has them, are as ever."""
+    layer = Layer(8, 2, 16)
+    kv, cu = [400, 500], [0, 200, 500]
+    layer.fill(kv)
+    q = queries(layer, 500)
+    clean, _ = run_attend(layer, q, kv, cu)
+    torch.cuda.synchronize()
+    keep = layer.v.clone()
+    poison(layer, layer.v, 0, 399, 0, 9)
+    o, _ = run_attend(layer, q, kv, cu)
+    torch.cuda.synchronize()
+    assert bool(o.t[199, :4, 9].isnan().all())
+    # Bit for bit, but for the channels that are added again (four to a lane, those of key head 0 before the last row).
+    same = torch.ones(500, 8, D, dtype=torch.bool, device=DEV)
+    same[:200, :4, 8:12] = False
+    assert torch.equal(o.t[same].view(torch.int16), clean.t[same].view(torch.int16))
+    want, wl, bound, lb = expect(layer, q, kv, cu)
+    again = ~same
+    again[199, :4, 9] = False
+    check(o.t[again], want[again], (bound * (1 + ref.UBF) + ref.UBF * want.abs())[again], "added again")
+    layer.v.copy_(keep)
+    o, _ = run_attend(layer, q, kv, cu)
+    torch.cuda.synchronize()
+    assert torch.equal(o.t.view(torch.int16), clean.t.view(torch.int16))
     layer.done()
