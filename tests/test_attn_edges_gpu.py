@@ -1,5 +1,6 @@
 """The paged softmax-attention operators at their edges: pages and offsets that
-are not valid, requests refused by the plan."""
+are not valid, requests refused by the plan, requests without tokens, and the
+accuracy that each path's weights are held to."""
 import math
 import statistics
 
@@ -106,4 +107,56 @@ def test_offsets_that_claim_rows_twice():
     assert bool((o.t.view(torch.uint8) == 0x5A).all()) and o.intact() and lse.intact()
     assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
     verify(layer, q, [100] * 5, [0, 30, 30, 77, 90, 100])
+    layer.done()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("tail", [1, 200])
+def test_cut_calls_with_empty_requests_at_the_end(tail, e4m3):
+    """The walk over requests ends with the last one that has tokens."""
+    new = [64, 0, 300, 300] + [0] * tail
+    kv = [20000, 7, 300, 400] + [0, 9] * tail
+    kv = kv[: len(new)]
+    layer = Layer(8, 4, 32, e4m3)
+    layer.fill(kv)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    verify(layer, queries(layer, cu[-1]), kv, cu)
+    layer.done()
+
+
+# (query heads, key heads, new tokens, keys, e4m3): paths whose weights are two bf16 parts or f16
+FINE = [
+    (8, 2, None, [9, 17, 31, 64], False), (24, 1, None, [9, 17, 40], False), (40, 1, None, [8, 33], False),
+    (8, 2, [3, 5, 8], [9, 17, 40], False), (2, 2, [4, 1], [9, 5], False),
+    (8, 2, None, [9, 17, 31, 64], True), (24, 1, None, [9, 17, 40], True), (8, 2, [3, 5, 8], [9, 17, 40], True),
+    (8, 2, [40], [60], True), (128, 1, [9, 3], [33, 12], True),
+]
+
+
+@pytest.mark.parametrize("hq,hkv,new,kv,e4m3", FINE)
+def test_weights_as_fine_as_stated(hq, hkv, new, kv, e4m3, monkeypatch):
+    """fp32 outputs within the weights' own rounding: 2^-16 (two bf16 parts: what
+    the second leaves, 2^-8 of 2^-8), or 2^-11 (f16).  Few keys and small logits,
+    so that the other terms of the bound stay below it."""
+    layer = Layer(hq, hkv, 16, e4m3)
+    layer.fill(kv)
+    cu = None
+    if new is not None:
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+    q = queries(layer, len(kv) if cu is None else cu[-1], 0.05)
+    o, lse = run_attend(layer, q, kv, cu, None, True)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    monkeypatch.setattr(ref, "UBF", 2.0 ** -11 if e4m3 else 2.0 ** -16)
+    want, wl, bound, lb = ref.attend(q, layer.k, layer.v, layer.table_list, kv, cu, 16, D ** -0.5, layer.ks, layer.vs)
+    if e4m3 and cu is not None and max(new) * hq // hkv > 32:
+        # Queries as two e4m3 parts: a logit off by 2^-17 of the row's largest channel per unit of the keys' sum.
+        keys = (layer.k.float().nan_to_num(0.0) * layer.ks.view(1, -1, 1, 1)).abs().sum(-1).amax()
+        off = D ** -0.5 * 2.0 ** -17 * q.double().abs().amax(-1) * keys
+        top = (layer.v.float().nan_to_num(0.0) * layer.vs.view(1, -1, 1, 1)).abs().amax()
+        bound = bound + (torch.expm1(2 * off) * top)[..., None]
+    check(o.t, want, bound, "o")
     layer.done()
