@@ -731,7 +731,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
                 if (w < parts) l += s_sum[w * rows + row] * mma::exp2_approx(s_ref[w * rows + row] - top);
-            if (cur.n > 1 && !(fabsf(v.x + v.y + v.z + v.w) < INFINITY)) sm.spoiled = 1;
+            if (kRowTiles > 1 && cur.n > 1 && !(fabsf(v.x + v.y + v.z + v.w) < INFINITY)) sm.spoiled = 1;
             if (whole) {
                 const float n = l != 0.f ? vscale / l : 0.f;   // 0: the row sees no key (NaN is not 0: a NaN logit shows)
                 const size_t at = head_of(cur, rw, row);
@@ -760,7 +760,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
         // Give-up path: the copies this warp issued complete (bounded waits) before its shared memory is released.
         for (int i = used; i < issued; ++i) ptx::mbar_wait_timed(&full[i % kDepth], (uint32_t)(i / kDepth) & 1u);
         __syncthreads();
-    } else if (a.io.cu_new) {
+    } else if (kRowTiles > 1) {   // (calls with more than a token to a request)
         __syncthreads();
         if (sm.spoiled) mend_rows<kE4m3, kUnit, kPartCost>(a, sm.left, sm.first_b, sm.first_unit);
     }
