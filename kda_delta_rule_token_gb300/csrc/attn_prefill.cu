@@ -5,9 +5,10 @@
 // A prompt token's head takes part in 4 * 128 operations per key: the call is
 // bound by the tensor pipe (a 128 x 128 tile of S and of O take it 512 cycles
 // each, its exponentials take the SM 512 as well).  Measured: 8192 tokens of 64
-// heads in bf16 615 us, 1788 TFLOP/s of the tokens' own operations, 0.91 of the
-// measured dense rate (e4m3: 671 us, 1638); one key tile of two row tiles takes
-// 2300 cycles of which the tensor pipe works 2048.
+// heads in bf16, after a rest, 622 us, 1767 TFLOP/s of the tokens' own operations,
+// 0.90 of the measured dense rate, and back to back 683 us, 1609 TFLOP/s, 0.92 of
+// what a library product sustains (e4m3: 678 and 715 us); one key tile of two row
+// tiles takes 2300 cycles of which the tensor pipe works 2048.
 //
 // The rows of one key head are (token, query head) pairs: floor(128 / G) tokens
 // with their G heads fill one 128-row tile, so that all heads that share a key
@@ -30,8 +31,8 @@
 //    per row) as the sum of two e4m3 parts, which hold bf16's eight bits: two
 //    8-bit products take as long as one 16-bit one, and the keys need no
 //    conversion.  Two further warps convert the values to f16, P is f16 within
-//    2^15.  (Keys converted to f16 too, by a warpgroup of its own: 703 us where
-//    this takes 671, and 741 of ragged chunks where this takes 701.)
+//    2^15.  (Keys converted to f16 too, by a warpgroup of its own: 5 % longer, and
+//    6 % on ragged chunks.)
 //
 // The loops of all these warps have to fit the SM's instruction cache together:
 // where they do not (a converting loop written out for all of a thread's 16
