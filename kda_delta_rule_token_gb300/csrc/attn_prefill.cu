@@ -940,7 +940,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             more = more_n;
         }
         ptx::cp_async_wait_all();   // of a part that was given up
-        if (__any_sync(0xffffffffu, !(spoiled < INFINITY)) && *(volatile int*)dead == 0) {
+        if (__any_sync(0xffffffffu, !(spoiled < INFINITY)) && __all_sync(0xffffffffu, *(volatile int*)dead == 0)) {
             // Values that they do not see may have got into this warp's rows (attn_again.cuh): its parts again.
             // (Looking at all results costs calls without such values 0.6 % of an 8191-token prompt's time, 0.8 % of the
             // ragged e4m3 chunks'; in the join kernel instead, what the join then carries cost calls with cut keys 3 %.)
