@@ -46,7 +46,8 @@
  *    the same suspicion.
  *  - Fault injection for tests: the environment variable KDA_FAULT_INJECT,
  *    read by kda_create, names entry points ("decode", "prefill",
- *    "prefill_varlen", "lowrank", "project", "all"; comma-separated; the
+ *    "prefill_varlen", "lowrank", "project", "all" and those of kda_beam.h;
+ *    comma-separated; the
  *    low-rank decode step counts as "decode" and "lowrank") whose launches
  *    that context replaces by cudaErrorLaunchFailure: nothing is launched,
  *    no buffer changes, and the call returns KDA_ERR_CUDA.  The name
@@ -389,8 +390,9 @@ KDA_API kda_status kda_project_o(kda_ctx *ctx, int N, const float *o, float *y, 
 /*
  * Synchronise `stream` and report whether any kernel launched with this
  * context since the last call gave up on a bounded wait (KDA_ERR_TIMEOUT) or
- * raised a CUDA error (KDA_ERR_CUDA).  Clears the error word, so the next
- * call reports only what happened after this one.
+ * raised a CUDA error (KDA_ERR_CUDA), or met rows that kda_beam_reorder
+ * (kda_beam.h) leaves alone as errors (KDA_ERR_INVALID_ARG).  Clears the error
+ * word, so the next call reports only what happened after this one.
  */
 KDA_API kda_status kda_sync_status(kda_ctx *ctx, void *stream);
 

@@ -21,7 +21,7 @@ __all__ = [
     "LOWRANK_NOALLOC_SCRATCH_BYTES", "kda_bind_projections", "kda_project_qkvg", "kda_project_o",
     "kda_project_o_workspace_bytes", "kda_attn_create", "kda_attn_destroy", "kda_attn_bind_cache",
     "kda_attn_plan", "kda_attn_append", "kda_attn_workspace_bytes", "kda_attn_decode", "kda_attn_prefill",
-    "kda_attn_sync_status", "KDA_CACHE_BF16", "KDA_CACHE_E4M3", "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_ALIGNMENT",
+    "kda_attn_sync_status", "kda_beam_select", "kda_beam_select_workspace_bytes", "kda_beam_reorder", "KDA_CACHE_BF16", "KDA_CACHE_E4M3", "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_ALIGNMENT",
     "KDA_ERR_UNSUPPORTED", "KDA_ERR_CUDA", "KDA_ERR_TIMEOUT", "HEAD_DIM", "CHUNK",
 ]
 
@@ -137,6 +137,12 @@ def load(path: str | None = None):
     lib.kda_attn_prefill.restype = i32
     lib.kda_attn_sync_status.argtypes = [vp, vp]
     lib.kda_attn_sync_status.restype = i32
+    lib.kda_beam_select_workspace_bytes.argtypes = [vp] + [i32] * 4
+    lib.kda_beam_select_workspace_bytes.restype = sz
+    lib.kda_beam_select.argtypes = [vp, i32, i32, i32, vp, i32, i64, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    lib.kda_beam_select.restype = i32
+    lib.kda_beam_reorder.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, vp]
+    lib.kda_beam_reorder.restype = i32
     lib.kda_testing_bounded_wait.argtypes = [vp, ctypes.c_uint, vp]
     lib.kda_testing_bounded_wait.restype = i32
     _lib = lib
@@ -413,6 +419,44 @@ def kda_attn_prefill(attn, B, N, cu_new, q, block_table, kv_lens, o, workspace, 
 def kda_attn_sync_status(attn, stream=None) -> int:
     """Synchronise and return the status code (does not raise)."""
     return int(load().kda_attn_sync_status(attn, _stream(stream)))
+
+
+def _words(t, name, count, size=4):
+    """The address of a dense tensor of at least `count` elements of `size` bytes."""
+    if t is not None and not isinstance(t, int) and (t.element_size() != size or t.numel() < count):
+        raise ValueError(f"{name} must have {count} elements of {size} bytes: shape {tuple(t.shape)}, {t.dtype}")
+    return _dense(t, name)
+
+
+def kda_beam_select_workspace_bytes(ctx, groups, beams, vocab, num) -> int:
+    return int(load().kda_beam_select_workspace_bytes(ctx, int(groups), int(beams), int(vocab), int(num)))
+
+
+def kda_beam_select(ctx, groups, beams, logits, scores, num, out_scores, out_tokens, out_rows, workspace, *,
+                    done=None, end_token=0, keep_places=False, workspace_bytes=0, stream=None) -> None:
+    """The num best continuations of every group (kda_beam.h).  logits [groups * beams, vocab]: fp32 or bf16
+    (or its raw view), rows at any stride; done: bytes or truth values."""
+    if logits.dim() != 2 or logits.shape[0] < groups * beams or (logits.stride(1) != 1 and logits.shape[1] != 1):
+        raise ValueError(f"logits must be [{groups * beams}, vocab] with dense rows: shape {tuple(logits.shape)}, "
+                         f"strides {logits.stride()}")
+    vocab = logits.shape[1]
+    stride = logits.stride(0) if logits.shape[0] > 1 else vocab   # of one row any stride will do
+    _check(load().kda_beam_select(ctx, int(groups), int(beams), vocab, _p(logits), int(logits.element_size() == 2), stride,
+                                  _words(scores, "scores", groups * beams), _words(done, "done", groups * beams, 1),
+                                  int(end_token), int(num), 1 if keep_places else 0,
+                                  _words(out_scores, "out_scores", groups * num), _words(out_tokens, "out_tokens", groups * num),
+                                  _words(out_rows, "out_rows", groups * num), _p(workspace),
+                                  _nbytes(workspace, workspace_bytes), _stream(stream)), "kda_beam_select")
+
+
+def kda_beam_reorder(ctx, B, rows, S, conv_state, *, S_out=None, conv_out=None, stream=None) -> None:
+    """S[b], conv_state[b] <- S[rows[b]], conv_state[rows[b]] in place, or into S_out and conv_out (kda_beam.h)."""
+    S_out, conv_out = S if S_out is None else S_out, conv_state if conv_out is None else conv_out
+    if S_out.element_size() != S.element_size():
+        raise ValueError(f"S is {S.dtype}, S_out {S_out.dtype}")
+    _check(load().kda_beam_reorder(ctx, int(B), _words(rows, "rows", B), _dense(S, "S"), _dense(conv_state, "conv_state"),
+                                   _dense(S_out, "S_out"), _dense(conv_out, "conv_out"), int(S.element_size() == 2),
+                                   _stream(stream)), "kda_beam_reorder")
 
 
 def kda_testing_bounded_wait(ctx, limit_us, stream=None) -> None:

@@ -4,7 +4,7 @@
 //
 // Fault injection for tests: KDA_FAULT_INJECT, read once by kda_create, is a
 // comma-separated list of entry points ("decode", "prefill",
-// "prefill_varlen", "lowrank", "project", or "all") whose launches that
+// "prefill_varlen", "lowrank", "project", "beam_select", "beam_reorder", or "all") whose launches that
 // context replaces by the error cudaErrorLaunchFailure: nothing is launched,
 // no buffer is touched and the call returns KDA_ERR_CUDA
 // (kda_last_error_detail names the error and says it was injected).  The
@@ -23,6 +23,7 @@
 #include <cstring>
 #include <new>
 
+#include "beam_internal.cuh"
 #include "kda_internal.cuh"
 #include "kda_testing.h"
 
@@ -69,7 +70,8 @@ kda_status check_device(const kda_ctx* ctx) {
 
 constexpr unsigned kInjectDecode = 1u, kInjectPrefill = 2u, kInjectVarlen = 4u, kInjectLowrank = 8u,
                    kInjectProject = 16u, kInjectRelayDrop = 32u,
-                   kInjectSplitDrop = 64u, kInjectSplitNofit = 128u;
+                   kInjectSplitDrop = 64u, kInjectSplitNofit = 128u, kInjectSelect = 256u,
+                   kInjectReorder = 512u;
 
 // Parse KDA_FAULT_INJECT (see the top of this file).
 unsigned parse_inject(const char* v) {
@@ -86,10 +88,13 @@ unsigned parse_inject(const char* v) {
         else if (is("prefill_varlen")) m |= kInjectVarlen;
         else if (is("lowrank")) m |= kInjectLowrank;
         else if (is("project")) m |= kInjectProject;
+        else if (is("beam_select")) m |= kInjectSelect;
+        else if (is("beam_reorder")) m |= kInjectReorder;
         else if (is("relay_drop")) m |= kInjectRelayDrop;
         else if (is("split_drop")) m |= kInjectSplitDrop;
         else if (is("split_nofit")) m |= kInjectSplitNofit;
-        else if (is("all")) m |= kInjectDecode | kInjectPrefill | kInjectVarlen | kInjectLowrank | kInjectProject;
+        else if (is("all")) m |= kInjectDecode | kInjectPrefill | kInjectVarlen | kInjectLowrank | kInjectProject |
+                                 kInjectSelect | kInjectReorder;
         p = *e ? e + 1 : e;
     }
     return m;
@@ -109,6 +114,21 @@ void set_launch_detail(const kda_ctx* ctx, unsigned what, const char* name, cuda
     } else {
         set_detail(name, e);
     }
+}
+
+// Sizes of kda_beam_select.
+kda_status check_beams(int groups, int beams, int vocab, int num) {
+    if (groups < 0 || beams < 1 || vocab < 1 || num < 1 || (long long)beams * vocab > 0x7fffffffLL ||
+        (long long)groups * beams > 0x7fffffffLL || num > (long long)beams * vocab) {
+        set_error_text("%d groups of %d beams, %d logits each, %d continuations", groups, beams, vocab, num);
+        return KDA_ERR_INVALID_ARG;
+    }
+    if (beams > KDA_BEAM_MAX_BEAMS || num > KDA_BEAM_MAX_NUM) {
+        set_error_text("%d beams (at most %d), %d continuations (at most %d)", beams, KDA_BEAM_MAX_BEAMS, num,
+                       KDA_BEAM_MAX_NUM);
+        return KDA_ERR_UNSUPPORTED;
+    }
+    return KDA_OK;
 }
 
 }  // namespace
@@ -321,14 +341,84 @@ kda_status kda_sync_status(kda_ctx* ctx, void* stream) {
         return KDA_ERR_CUDA;
     }
     if (word != 0) {
+        const bool rows = (word & ~kda::kErrRows) == 0;
         std::snprintf(kda::g_detail, sizeof(kda::g_detail),
-                      "kernel error word 0x%x (bounded wait gave up)", word);
+                      rows ? "kernel error word 0x%x (rows that there are not, or that move away themselves)"
+                           : "kernel error word 0x%x (bounded wait gave up)", word);
         if ((e = cudaMemset(ctx->err_word, 0, sizeof(int))) != cudaSuccess) {
             kda::set_detail("cudaMemset(error word)", e);
             return KDA_ERR_CUDA;
         }
-        return KDA_ERR_TIMEOUT;
+        return rows ? KDA_ERR_INVALID_ARG : KDA_ERR_TIMEOUT;
     }
+    return KDA_OK;
+}
+
+size_t kda_beam_select_workspace_bytes(const kda_ctx* ctx, int groups, int beams, int vocab, int num) {
+    if (!ctx || groups < 1 || kda::check_beams(groups, beams, vocab, num) != KDA_OK) return 0;
+    return kda::beam_select_workspace_bytes(groups, beams, vocab, num, ctx->dev);
+}
+
+kda_status kda_beam_select(kda_ctx* ctx, int groups, int beams, int vocab, const void* logits, int logits_bf16,
+                           long long row_stride, const float* scores, const uint8_t* done, int end_token, int num,
+                           int keep_places, float* out_scores, int32_t* out_tokens, int32_t* out_rows,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    if (!ctx || groups < 0) return KDA_ERR_INVALID_ARG;
+    if (groups == 0) return KDA_OK;
+    if (const kda_status s = kda::check_beams(groups, beams, vocab, num); s != KDA_OK) return s;
+    if (!logits || !scores || !out_scores || !out_tokens || !out_rows || !workspace) return KDA_ERR_INVALID_ARG;
+    if (row_stride < vocab || (done && (end_token < 0 || end_token >= vocab)) || (keep_places && num != beams)) {
+        kda::set_error_text("row stride %lld of %d logits, end token %d, %d continuations of %d beams%s", row_stride,
+                            vocab, end_token, num, beams, keep_places ? " that keep their places" : "");
+        return KDA_ERR_INVALID_ARG;
+    }
+    if ((reinterpret_cast<uintptr_t>(logits) & (logits_bf16 ? 1u : 3u)) || !aligned4(scores) || !aligned4(out_scores) ||
+        !aligned4(out_tokens) || !aligned4(out_rows) || !aligned16(workspace))
+        return KDA_ERR_ALIGNMENT;
+    const size_t need = kda::beam_select_workspace_bytes(groups, beams, vocab, num, ctx->dev);
+    if (workspace_bytes < need) {
+        kda::set_error_text("workspace of %zu bytes, %zu needed", workspace_bytes, need);
+        return KDA_ERR_INVALID_ARG;
+    }
+    if (const kda_status d = check_device(ctx); d != KDA_OK) return d;
+    const kda::BeamSelectIO io{groups, beams, vocab, logits, logits_bf16 != 0, row_stride, scores, done, end_token,
+                               num, keep_places != 0, out_scores, out_tokens, out_rows, workspace};
+    const cudaError_t e = kda::launch_or_inject(ctx, kda::kInjectSelect, [&] {
+        return kda::launch_beam_select(io, ctx->dev, static_cast<cudaStream_t>(stream));
+    });
+    if (e != cudaSuccess) { kda::set_launch_detail(ctx, kda::kInjectSelect, "beam_select launch", e); return KDA_ERR_CUDA; }
+    return KDA_OK;
+}
+
+kda_status kda_beam_reorder(kda_ctx* ctx, int B, const int32_t* rows, const void* S, const float* conv_state,
+                            void* S_out, float* conv_out, int s_bf16, void* stream) {
+    if (!ctx || B < 0) return KDA_ERR_INVALID_ARG;
+    if (B == 0) return KDA_OK;
+    if (!rows || !S || !conv_state || !S_out || !conv_out) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {S, conv_state, S_out, conv_out};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return KDA_ERR_ALIGNMENT;
+    if (!aligned4(rows)) return KDA_ERR_ALIGNMENT;
+    const long long H = ctx->params.H;
+    if (B * H > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
+    kda::BeamReorderIO io{B, rows, {static_cast<const uint8_t*>(S), reinterpret_cast<const uint8_t*>(conv_state)},
+                          {static_cast<uint8_t*>(S_out), reinterpret_cast<uint8_t*>(conv_out)},
+                          {H * kda::kHeadDim * kda::kHeadDim * (s_bf16 ? 2 : 4), 9 * H * kda::kHeadDim * 4},
+                          S == S_out && conv_state == conv_out};
+    if (!io.in_place)
+        for (const uint8_t* const in : io.src)
+            for (const uint8_t* const out : io.dst) {
+                const long long n = B * io.bytes[in == io.src[0] ? 0 : 1], m = B * io.bytes[out == io.dst[0] ? 0 : 1];
+                if (in < out + m && out < in + n) {
+                    kda::set_error_text("an output overlaps an input, and not both are in place");
+                    return KDA_ERR_INVALID_ARG;
+                }
+            }
+    if (const kda_status d = check_device(ctx); d != KDA_OK) return d;
+    const cudaError_t e = kda::launch_or_inject(ctx, kda::kInjectReorder, [&] {
+        return kda::launch_beam_reorder(io, ctx->dev, ctx->err_word, static_cast<cudaStream_t>(stream));
+    });
+    if (e != cudaSuccess) { kda::set_launch_detail(ctx, kda::kInjectReorder, "beam_reorder launch", e); return KDA_ERR_CUDA; }
     return KDA_OK;
 }
 

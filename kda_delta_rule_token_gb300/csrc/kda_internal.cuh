@@ -13,6 +13,10 @@ namespace kda {
 constexpr int kHeadDim = 128;   // d_k = d_v
 constexpr int kChunk = 64;      // prefill chunk length
 
+// Error-word bit beside the bounded-wait ones of ptx.cuh: a sequence that is to go
+// on from one that there is not, or that moves away itself (and was left as it is).
+constexpr int kErrRows = 1 << 16;
+
 // Everything a kernel needs about one layer: borrowed parameter pointers and
 // the normalisation epsilons.  Passed by value as a kernel argument.
 struct LayerParams {
