@@ -7,22 +7,24 @@
 // measured against (lse).  Every logit is read once; what is left is small:
 // the call is bound by HBM, or by its two launches.
 //
-//  * kda_beam_rows_kernel: a CTA takes a segment of one row in tiles of 256
-//    threads x 16 logits, the next tile's loads under way.  A logit that passes
-//    the threshold T (the num-th largest that the CTA is sure of) joins the
-//    list of candidates in shared memory, any other adds exp(x - ref) to its
-//    thread's sum.  T rises when the list is full, and where one tile has more
-//    candidates than the list holds: of the threads' largest logits the num-th
-//    largest is a bound that at least num logits of the tile reach and at most
-//    num threads pass.  After the first tile few logits pass.
+//  * kda_beam_rows_kernel: the tiles of all rows, 256 threads x 16 logits each, are
+//    dealt in equal ranges to as many CTAs as run at once; what a CTA has of a row
+//    is a segment.  The next tile's loads are under way.  A thread keeps the
+//    largest of its logits and the sum of exp(x - ref), nothing else.  Every four
+//    tiles the CTA finds a bound that num of them reach and few others pass: 64 groups
+//    of threads each have a largest logit, and the num-th of these is it.
+//    The few threads whose largest logit reaches the bound are looked at again,
+//    each by its warp: logits that reach it join the list of candidates, the others
+//    the sums anew.  The list's num best stay; later logits have to
+//    pass the last of them (T).
 //  * kda_beam_join_kernel, a CTA per group: lse of every beam from its segments'
-//    sums, then the num best of the segments' lists, by the same bound over
-//    the threads' best.
+//    sums and lists, then the num best of the lists, by the same bound.
 //
 // Which of two beams' close candidates is the better one hangs on the last bits
 // of their lse.  The largest terms decide these, and they are the candidates:
-// they stay out of the fp32 sums, and their exponentials are taken and added in
-// 64 bits.  Scores are formed and compared in 64 bits and rounded once.
+// they stay out of the fp32 sums (which carry what their additions lose along),
+// and the join adds their exponentials to 2^-31 as whole numbers, in 64 bits, so
+// in any order.  Scores are formed and compared in 64 bits and rounded once.
 #include <math.h>
 
 #include "beam_internal.cuh"
@@ -34,60 +36,171 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 16;               // logits of a thread per tile
 constexpr int kTile = kThreads * kPer;
-constexpr int kList = 1536;            // candidates that a CTA holds
-constexpr int kSoft = 512;             // above which they are thinned out after a tile
+constexpr int kSub = 4;                // tiles between two looks at the largest logits
+static_assert(kSub * kPer == 64, "two logits of a thread for each lane of its warp");
+constexpr int kList = 768;             // candidates that a CTA holds
 constexpr int kMostNum = KDA_BEAM_MAX_NUM;
-static_assert(kSoft + kPer * kMostNum <= kList, "a raised threshold leaves at most kPer * num candidates of a tile");
-constexpr int kJoinEntries = 8192 - KDA_BEAM_MAX_BEAMS;   // candidates of a group's segments that the join takes
-constexpr int kJoinList = 2048;
-static_assert((kJoinEntries + KDA_BEAM_MAX_BEAMS + kThreads - 1) / kThreads * kMostNum <= kJoinList, "candidates that the join's bound leaves");
-constexpr int kJoinParts = 512;        // segments of a group's beams
-constexpr float kRefMargin = 20.f;     // how far above the reference a logit of the sums may be
+constexpr int kJoinPer = 16;           // candidates of a group's segments that a thread of the join takes
+constexpr int kJoinEntries = kJoinPer * kThreads;
+constexpr int kJoinList = 1280;
+static_assert((kJoinPer + 1) * kMostNum <= kJoinList, "candidates that the join's bound leaves");
+static_assert(KDA_BEAM_MAX_BEAMS * kMostNum <= kJoinEntries && KDA_BEAM_MAX_BEAMS <= kThreads, "a segment per beam");
+constexpr float kRefMargin = 16.f;     // how far the largest logit may be from the reference of the sums
 
-// What a segment leaves: the sum of exp(x - most) over it, and its candidates' number.
+// What a segment leaves beside its candidates: the sum of exp(x - ref) over its other logits.
 struct Part {
-    double sum;
-    float most;
-    int count;
+    float sum, more;   // and what the sum's additions lost
+    float ref;         // -infinity: the sum is 0, or NaN
+    float pad;
 };
 
 // A candidate: the logit in the order of unsigned numbers above, the complement of
 // its token below, so that the larger of two is the better one.
-__device__ __forceinline__ uint64_t candidate(float x, int token) {
+__device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);   // -0 is 0
-    return (uint64_t)(u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u)) << 32 | (uint32_t)~token;
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
-__device__ __forceinline__ float logit_of(uint64_t c) {
-    const uint32_t u = (uint32_t)(c >> 32);
-    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+__device__ __forceinline__ float float_of(uint32_t order) {
+    return __uint_as_float(order ^ ((order >> 31) ? 0x80000000u : 0xffffffffu));
 }
+__device__ __forceinline__ uint64_t candidate(float x, int token) {
+    return (uint64_t)order_of(x) << 32 | (uint32_t)~token;
+}
+__device__ __forceinline__ float logit_of(uint64_t c) { return float_of((uint32_t)(c >> 32)); }
 __device__ __forceinline__ int token_of(uint64_t c) { return (int)~(uint32_t)c; }
 
-// exp(d), d <= kRefMargin: the product with log2 e to 2^-24 of itself.
+// exp(d): the product with log2 e to 2^-24 of itself.
 __device__ __forceinline__ float exp_of(float d) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(d, 1.44269502f, d * 1.92596299e-8f)));
     return y;
 }
 
+// 2^f, f in units of 2^-32, in units of 2^-31: the exponential's series in ln 2, whose
+// eleventh term is below 2^-31, each product cut at 2^-32.
+__device__ __forceinline__ uint32_t pow2_fixed(uint32_t f) {
+    constexpr double c[11] = {0.69314718055994531, 0.24022650695910072, 0.055504108664821580, 0.0096181291076284772,
+                              0.0013333558146428443, 1.5403530393381610e-4, 1.5252733804059841e-5, 1.3215486790144309e-6,
+                              1.0178086009239700e-7, 7.0549116208011233e-9, 4.4455382718708116e-10};
+    uint32_t p = 0;
+#pragma unroll
+    for (int k = 10; k >= 0; --k) p = (uint32_t)(c[k] * 4294967296.0) + __umulhi(p, f);
+    return 0x80000000u + (__umulhi(p, f) >> 1);
+}
+
+// exp(x - top), x <= top, as m * 2^(i - 31); i < -40 stands for nothing.
+struct Power {
+    uint32_t m;
+    int i;
+};
+__device__ __forceinline__ Power power_of(float x, float top) {
+    // x - top exactly, and its product with log2 e to 2^-45 of it.
+    constexpr float l1 = 1.44269502f, l2 = 1.92596299e-8f;
+    const float d = x - top, back = d - x;
+    const float low = (x - (d - back)) - (top + back);
+    if (!(d > -40.f)) return Power{0, -64};
+    const float t = d * l1;
+    const float u = fmaf(d, l1, -t) + fmaf(d, l2, low * l1);
+    const int i = __float2int_rd(t);
+    const long long fixed = ((long long)i << 32) + __float2uint_rn((t - (float)i) * 4294967296.f) + __float2int_rn(u * 4294967296.f);
+    return Power{pow2_fixed((uint32_t)fixed), (int)(fixed >> 32)};
+}
+
+// v * exp(x - top) in units of 2^-31, v finite.
+__device__ __forceinline__ long long scaled(float v, const Power& p) {
+    const uint32_t u = __float_as_uint(v);
+    const int e = (int)(u >> 23 & 0xff);
+    if (e == 0 || p.m == 0) return 0;
+    const unsigned long long x = (unsigned long long)((u & 0x7fffff) | 0x800000) * p.m;   // below 2^56
+    const int shift = e - 127 - 23 + p.i;
+    const long long y = shift >= 0 ? (long long)(x << min(shift, 7)) : shift > -64 ? (long long)(x >> -shift) : 0;
+    return u >> 31 ? -y : y;
+}
+
+// ln of x units of 2^-31, x > 0: log2 of the leading 32 bits in fp32, put right by what
+// two to its power is off by, in units of 2^-40, times ln 2.
+__device__ __forceinline__ double ln_fixed(unsigned long long x) {
+    const int lead = __clzll((long long)x);
+    const uint32_t m = (uint32_t)((x << lead) >> 32);
+    const float y = fminf(fmaxf(log2f((float)m * 0x1p-31f), 0.f), 0x1.fffffep-1f);
+    const uint32_t f = (uint32_t)(y * 4294967296.f), p = pow2_fixed(f);
+    const float off = __fdividef((float)(int)(m - p), (float)p) * 1.44269504f;
+    const long long log2 = ((long long)(63 - lead - 31) << 40) + ((long long)f << 8) + __float2int_rn(off * 0x1p40f);
+    constexpr long long ln2 = 0x58b90bfbe8e7bcd6;   // units of 2^-63
+    return (double)__mul64hi(log2 << 14, ln2) * 0x1p-53;
+}
+
+// Floating numbers in 64 bits without the unit of 64-bit arithmetic: x exactly (below 2^-126: 0).
+__device__ __forceinline__ double widened(float x) {
+    const uint32_t u = __float_as_uint(x), e = u >> 23 & 0xff;
+    const uint32_t hi = (u & 0x80000000u) | (e == 0 ? 0 : e == 0xff ? 0x7ff00000u | (u & 0x7fffffu) >> 3 : ((u & 0x7fffffffu) >> 3) + 0x38000000u);
+    return __hiloint2double((int)hi, e == 0 ? 0 : (int)(u << 29));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// A bound that num of the CTA's values reach, num from 1 to 64, and few others pass: of 64
+// groups of four threads, the num-th largest of their largest values, its lower 32 -
+// kBits bits cleared (0: fewer than num groups have one that is not 0).  *top: the
+// largest of all.  s_group: 64 values.  All threads call it; a barrier follows before
+// the next use.
+constexpr int kGroups = 64, kGroup = kThreads / kGroups;
+static_assert(kMostNum <= kGroups && kGroup == 4, "groups of the bound");
+template <int kBits>
+__device__ __forceinline__ uint32_t group_bound(uint32_t best, int num, uint32_t* s_group, uint32_t* top) {
+    const int lane = threadIdx.x & 31;
+    best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
+    best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
+    if (lane % kGroup == 0) s_group[threadIdx.x / kGroup] = best;
+    __syncthreads();
+    const uint32_t v = s_group[lane], w = s_group[lane + 32];
+    *top = __reduce_max_sync(0xffffffffu, max(v, w));
+    uint32_t bound = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 32 - kBits; --bit) {
+        const uint32_t with = bound | 1u << bit;
+        const int reach = __popc(__ballot_sync(0xffffffffu, v >= with)) + __popc(__ballot_sync(0xffffffffu, w >= with));
+        if (reach >= num) bound = with;
+    }
+    return bound;
+}
+
+// How the tiles are dealt: row r's are units [r * per_row, (r + 1) * per_row), CTA c
+// has units [units * c / ctas, units * (c + 1) / ctas).  Segments are numbered
+// r + c, which no two share.
+struct Deal {
+    int per_row, ctas;
+    long long units;
+    __host__ __device__ __forceinline__ long long first(long long cta) const { return units * cta / ctas; }
+    __host__ __device__ __forceinline__ int cta_of(long long unit) const { return (int)(((unit + 1) * ctas - 1) / units); }
+};
+
 struct RowsArgs {
     BeamSelectIO io;
-    int segments;
-    Part* parts;         // [rows][segments]
-    uint64_t* lists;     // [rows][segments][num]
+    Deal deal;
+    Part* parts;         // [segments]
+    uint64_t* lists;     // [segments][num]
 };
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) kda_beam_rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsArgs a) {
     constexpr int kVec = kBf16 ? 8 : 4, kLoads = kPer / kVec, kBytes = kBf16 ? 2 : 4;
-    __shared__ uint64_t s_list[kList], s_best[kThreads];
-    __shared__ uint64_t s_bound;
-    __shared__ double s_sum[kThreads / 32];
-    __shared__ int s_want[3], s_held;
+    __shared__ uint64_t s_list[kList];
+    __shared__ uint32_t s_group[kGroups];
+    __shared__ float2 s_sum[kThreads / 32];
+    __shared__ int s_held, s_count[32], s_warp[kThreads / 32];
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.io.num;
-    const int row = blockIdx.x / a.segments, segment = blockIdx.x % a.segments;
-    if (a.io.done && a.io.done[row]) return;
+    const long long last = a.deal.first(blockIdx.x + 1LL);
+    for (long long unit = a.deal.first(blockIdx.x), next; unit < last; unit = next) {
+    const int row = (int)(unit / a.deal.per_row);
+    const long long row0 = (long long)row * a.deal.per_row;
+    next = min(row0 + a.deal.per_row, last);
+    if (a.io.done && a.io.done[row]) continue;
     const bool alike = a.io.scores[row] == INFINITY;   // at which all finite logits give the same score
 
     // The row: logits before the first 16-byte boundary, whole vectors, logits behind them.
@@ -95,50 +208,71 @@ __global__ void __launch_bounds__(kThreads) kda_beam_rows_kernel(const RowsArgs 
     const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / kBytes, a.io.vocab);
     const int vecs = (a.io.vocab - head) / kVec, tail = a.io.vocab - head - vecs * kVec;
     const int tiles = (vecs + kThreads * kLoads - 1) / (kThreads * kLoads);
-    int t = (int)((long long)tiles * segment / a.segments);
-    int end = (int)((long long)tiles * (segment + 1) / a.segments);
-    if (segment == 0 && head) t = -1;                      // tile -1: the head
-    if (segment == a.segments - 1 && tail) end = tiles + 1;   // tile `tiles`: the tail
+    int begin = (int)(unit - row0), end = min((int)(next - row0), tiles);
+    if (begin == 0 && head) begin = -1;                               // tile -1: the head, a logit per thread
+    if (next - row0 == a.deal.per_row) end = tiles + (tail ? 1 : 0);  // tile `tiles`: the tail
+    begin = min(begin, end);
     const uint4* body = reinterpret_cast<const uint4*>(base + (long long)head * kBytes);
-
-    if (tid == 0) {
-        s_held = 0;
-        s_want[0] = s_want[1] = s_want[2] = 0;
-    }
+    auto single = [&](int t) { return t < 0 || t >= tiles; };
+    // Logit i of a tile, of thread `of`: its token, and whether there is one.
+    auto token = [&](int t, int i, int of) {
+        if (single(t)) return (t < 0 ? 0 : head + vecs * kVec) + of;
+        return head + ((t * kLoads + i / kVec) * kThreads + of) * kVec + i % kVec;
+    };
+    auto there = [&](int t, int i, int of) {
+        if (single(t)) return i == 0 && of < (t < 0 ? head : tail);
+        return (t * kLoads + i / kVec) * kThreads + of < vecs;
+    };
+    auto put_right = [&](float x) { return alike && fabsf(x) < INFINITY ? 0.f : x; };
+    auto logit_at = [&](int at) {
+        return put_right(kBf16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(base)[at] << 16)
+                               : reinterpret_cast<const float*>(base)[at]);
+    };
+    if (tid == 0) s_held = 0;
     __syncthreads();
 
     uint4 raw[kLoads];
-    auto load = [&](int tile) {
-        if (tile < 0 || tile >= tiles) {   // a single logit in the lowest bits of raw[0]
-            const int i = tile < 0 ? tid : head + vecs * kVec + tid;
-            if (tid < (tile < 0 ? head : tail))
-                raw[0].x = kBf16 ? reinterpret_cast<const uint16_t*>(base)[i] : reinterpret_cast<const uint32_t*>(base)[i];
+    auto load = [&](int t) {
+        if (single(t)) {   // in the lowest bits of raw[0]
+            if (there(t, 0, tid))
+                raw[0].x = kBf16 ? reinterpret_cast<const uint16_t*>(base)[token(t, 0, tid)]
+                                 : reinterpret_cast<const uint32_t*>(base)[token(t, 0, tid)];
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            if (there(t, j * kVec, tid)) raw[j] = __ldg(body + (t * kLoads + j) * kThreads + tid);
+    };
+    float x[kPer];
+    auto unpack = [&](int t) {
+        if (single(t)) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) x[i] = -INFINITY;
+            if (there(t, 0, tid)) x[0] = put_right(__uint_as_float(kBf16 ? raw[0].x << 16 : raw[0].x));
             return;
         }
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const int v = (tile * kLoads + j) * kThreads + tid;
-            if (v < vecs) raw[j] = __ldcs(body + v);
+            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                x[j * kVec + i] = __uint_as_float(!kBf16 ? w[i & 3] : i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
         }
+        if ((t + 1) * kLoads * kThreads > vecs)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (!there(t, i, tid)) x[i] = -INFINITY;
+        if (alike)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) x[i] = put_right(x[i]);
     };
 
+    // The reference is a logit of the segment; -infinity: there has been none above that, and the sum is 0 or NaN.
     float T = -INFINITY, ref = -INFINITY, sum = 0.f, low = 0.f;   // the sum and what its additions lost
-    auto add = [&](float x) {
-        const float y = x - low, s = sum + y;
+    auto add = [&](float v) {
+        const float y = v - low, s = sum + y;
         low = (s - sum) - y;
         sum = s;
-    };
-    // A higher threshold; the sums stay within kRefMargin of their reference.
-    auto raise = [&](float to) {
-        T = fmaxf(T, to);
-        if (ref == -INFINITY) {
-            ref = T;
-        } else if (T > ref + kRefMargin) {
-            const float f = expf(ref - T);
-            sum *= f;
-            low *= f;
-            ref = T;
-        }
     };
     // The list's best n, in order; what leaves it joins the sums, in its order, so that they do not
     // depend on the one in which it was written.  All threads call it.
@@ -152,6 +286,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_rows_kernel(const RowsArgs 
             if (i * kThreads + tid < held) {
                 own[i] = s_list[i * kThreads + tid];
                 rank[i] = 0;
+#pragma unroll 8
                 for (int j = 0; j < held; ++j) rank[i] += s_list[j] > own[i];
             }
         }
@@ -161,219 +296,348 @@ __global__ void __launch_bounds__(kThreads) kda_beam_rows_kernel(const RowsArgs 
             if (rank[i] >= 0) s_list[rank[i]] = own[i];
         if (tid == 0) s_held = min(held, n);
         __syncthreads();
-        if (held >= n) raise(logit_of(s_list[n - 1]));
+        if (held >= n) T = logit_of(s_list[n - 1]);
         for (int i = n + tid; i < held; i += kThreads) add(exp_of(logit_of(s_list[i]) - ref));
     };
 
-    if (t < end) load(t);
-    for (int turn = 0; t < end; ++t, turn = turn == 2 ? 0 : turn + 1) {
-        float x[kPer];
-        const bool single = t < 0 || t >= tiles;
-        const int first = t < 0 ? 0 : t >= tiles ? head + vecs * kVec : head + t * kTile;
-        const int at = first + tid * (single ? 1 : kVec);   // token of x[0]; of x[i]: at + i / kVec * kThreads * kVec + i % kVec
-        if (single) {
-            const bool in = tid < (t < 0 ? head : tail);
+    if (begin < end) load(begin);
+    for (int t0 = begin, t1; t0 < end; t0 = t1) {
+        t1 = min(t0 + kSub, end);
+        const float sum0 = sum, low0 = low;
+        float scale0 = 1.f, most;
+        uint32_t bound, top;
+        for (;;) {
+            sum = sum0 * scale0;
+            low = low0 * scale0;
+            most = -INFINITY;
+            for (int t = t0; t < t1; ++t) {
+                unpack(t);
+                if (t + 1 < end) load(t + 1);
+                float m = max3(max3(x[0], x[1], x[2]), x[3], x[4]);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = -INFINITY;
-            if (in) x[0] = kBf16 ? __uint_as_float(raw[0].x << 16) : __uint_as_float(raw[0].x);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const bool in = (t * kLoads + j) * kThreads + tid < vecs;
-                const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const float f = kBf16 ? __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) : __uint_as_float(w[i & 3]);
-                    x[j * kVec + i] = in ? f : -INFINITY;
+                for (int i = 5; i < kPer - 1; i += 2) m = max3(m, x[i], x[i + 1]);
+                m = fmaxf(m, x[kPer - 1]);
+                m = fmaxf(m, -INFINITY);   // not NaN
+                if (t == begin && ref == -INFINITY) {
+                    const uint32_t w = __reduce_max_sync(0xffffffffu, order_of(m));
+                    if (lane == 0) s_group[warp] = w;
+                    __syncthreads();
+                    const float first = float_of(__reduce_max_sync(0xffffffffu, s_group[lane & (kThreads / 32 - 1)]));
+                    if (fabsf(first) < INFINITY) ref = first;
+                    __syncthreads();
                 }
+                most = fmaxf(most, m);
+                const float to = ref == -INFINITY ? 0.f : ref;
+                float part = 0.f;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) part += exp_of(x[i] - to);
+                add(part);
             }
+            bound = group_bound<16>(order_of(most), n, s_group, &top);
+            const float now = float_of(top);
+            if (fabsf(now) == INFINITY || (ref != -INFINITY && now - ref <= kRefMargin)) break;
+            // The first logits above -infinity, or ones far above the reference: these tiles once more.
+            if (ref != -INFINITY) scale0 *= expf(ref - now);
+            ref = now;
+            __syncthreads();
+            load(t0);
         }
-        if (t + 1 < end) load(t + 1);
-        if (alike) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (fabsf(x[i]) < INFINITY) x[i] = 0.f;
-        }
-
-        int want = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) want += x[i] > T;
-        if (want) atomicAdd(&s_want[turn], want);
+        // Threads whose largest logit is a candidate, one after another: two of its logits for each lane.
+        const float s0 = sum0 * scale0, l0 = low0 * scale0;
+        const int held = s_held;
         __syncthreads();
-        const int all = s_want[turn];
-        if (tid == 0) s_want[turn ? turn - 1 : 2] = 0;   // the one after the next, which all have read
-        if (all) {
-            auto token = [&](int i) { return at + i / kVec * (kThreads * kVec) + i % kVec; };
-            uint64_t bound = 0;
-            if (s_held + all > kList) {
-                // The num-th largest of the threads' best: at least num logits of the tile reach it.
-                uint64_t best = 0;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (x[i] > T) best = max(best, candidate(x[i], token(i)));
-                s_best[tid] = best;
-                if (tid == 0) s_bound = 0;
-                __syncthreads();
-                int above = 0;
-#pragma unroll 8
-                for (int j = 0; j < kThreads; ++j) above += s_best[j] > best;
-                if (best && above == n - 1) s_bound = best;
-                __syncthreads();
-                bound = s_bound;
-            }
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (x[i] > T) {
-                    const uint64_t c = candidate(x[i], token(i));
-                    if (c >= bound) {
-                        s_list[atomicAdd(&s_held, 1)] = c;
-                        x[i] = -INFINITY;
-                    }
+        uint32_t again = __ballot_sync(0xffffffffu, most > T && order_of(most) >= bound);
+        if (again >> lane & 1) {
+            sum = s0;
+            low = l0;
+        }
+        const int t_mine = t0 + 2 * lane / kPer, i_mine = 2 * lane % kPer;
+        const uint8_t* mine_at = base + (long long)token(t_mine, i_mine, 0) * kBytes;
+        for (; again; again &= again - 1) {
+            const int of = warp * 32 + __ffs((int)again) - 1;
+            float v[2] = {-INFINITY, -INFINITY};
+            if (t_mine < t1 && there(t_mine, i_mine, of)) {
+                if (single(t_mine)) {
+                    v[0] = logit_at(token(t_mine, 0, of));
+                } else {
+                    const uint2 w = kBf16 ? make_uint2(*reinterpret_cast<const uint32_t*>(mine_at + of * 16), 0u)
+                                          : *reinterpret_cast<const uint2*>(mine_at + of * 16);
+                    v[0] = put_right(__uint_as_float(kBf16 ? w.x << 16 : w.x));
+                    v[1] = put_right(__uint_as_float(kBf16 ? w.x & 0xffff0000u : w.y));
                 }
-            // Tokens behind this tile have to be above it to be better.
-            if (bound) raise(logit_of(bound));
-        }
-        // Logits below the threshold: where there is none yet, they are all -infinity or NaN.
-        const float to = ref == -INFINITY ? 0.f : ref;
-        float part = 0.f;
+            }
+            float rest = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) part += exp_of(x[i] - to);
-        add(part);
-        if (all) {
+            for (int i = 0; i < 2; ++i)
+                if (v[i] > T && order_of(v[i]) >= bound) {
+                    const int to = atomicAdd(&s_held, 1);
+                    if (to < kList) s_list[to] = candidate(v[i], token(t_mine, i_mine + i, of));
+                } else {
+                    rest += exp_of(v[i] - ref);
+                }
+            add(rest);
+        }
+        __syncthreads();
+        if (s_held > kList) {
+            // Many logits are equal, or many of one thread pass all others.  The num-th largest above T by
+            // its bits, and those that are equal to it in the order of their tokens.
+            if (tid < 32) s_count[tid] = 0;
             __syncthreads();
-            if (s_held > kSoft) thin(s_held);
+            if (tid == 0) s_held = held;
+            uint32_t nth = 0;
+            for (int bit = 31; bit >= 0; --bit) {
+                const uint32_t with = nth | 1u << bit;
+                int count = 0;
+                for (int t = t0; t < t1; ++t)
+                    for (int i = 0; i < kPer; ++i)
+                        if (there(t, i, tid)) {
+                            const float v = logit_at(token(t, i, tid));
+                            count += v > T && order_of(v) >= with;
+                        }
+                count = __reduce_add_sync(0xffffffffu, count);
+                if (lane == 0) atomicAdd(&s_count[bit], count);
+                __syncthreads();
+                if (s_count[bit] >= n) nth = with;
+            }
+            __syncthreads();
+            int above = 0;
+            for (int t = t0; t < t1; ++t)
+                for (int i = 0; i < kPer; ++i)
+                    if (there(t, i, tid)) above += logit_at(token(t, i, tid)) > float_of(nth);
+            above = __reduce_add_sync(0xffffffffu, above);
+            if (lane == 0) s_warp[warp] = above;
+            __syncthreads();
+            int need = n;
+            for (int w = 0; w < kThreads / 32; ++w) need -= s_warp[w];
+            sum = s0;
+            low = l0;
+            for (int t = t0; t < t1; ++t)
+                for (int j = 0; j < kPer; j += kVec) {
+                    int equal = 0;
+                    for (int i = j; i < j + kVec; ++i)
+                        if (there(t, i, tid)) equal += logit_at(token(t, i, tid)) == float_of(nth);
+                    int upto = equal;
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, upto, d);
+                        if (lane >= d) upto += y;
+                    }
+                    __syncthreads();
+                    if (lane == 31) s_warp[warp] = upto;
+                    __syncthreads();
+                    int all = 0;
+                    for (int w = 0; w < kThreads / 32; ++w) {
+                        if (w == warp) upto += all;
+                        all += s_warp[w];
+                    }
+                    int left = need - (upto - equal);   // of this thread's equal ones, the first that are wanted
+                    float rest = 0.f;
+                    for (int i = j; i < j + kVec; ++i) {
+                        if (!there(t, i, tid)) continue;
+                        const int at = token(t, i, tid);
+                        const float v = logit_at(at);
+                        if (v > float_of(nth) || (v == float_of(nth) && left-- > 0)) s_list[atomicAdd(&s_held, 1)] = candidate(v, at);
+                        else rest += exp_of(v - ref);
+                    }
+                    add(rest);
+                    need -= all;
+                }
             __syncthreads();
         }
+        if (s_held != held) thin(s_held);
+        __syncthreads();
     }
-    __syncthreads();
-    thin(s_held);
     const int kept = s_held;
+    const size_t segment = (size_t)row + blockIdx.x;
 
-    // The segment's sum, measured from its largest candidate.
-    double total = (double)sum - (double)low;
+    // The threads' sums, with what the additions lose.
+    float more = -low;
+    auto join = [&](float s, float m) {
+        const float t = sum + s, back = t - sum;
+        more += m + ((sum - (t - back)) + (s - back));
+        sum = t;
+    };
 #pragma unroll
-    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-    if (lane == 0) s_sum[warp] = total;
-    __syncthreads();
-    if (warp == 0) {
-        const float most = kept ? logit_of(s_list[0]) : -INFINITY;
-        total = lane < kThreads / 32 ? s_sum[lane] : 0.0;
-        // Without a candidate above -infinity there is nothing to measure from: the sum is 0, or NaN.
-        if (kept && ref != -INFINITY) total *= exp((double)ref - (double)most);
-        for (int i = lane; i < kept; i += 32) total += exp((double)logit_of(s_list[i]) - (double)most);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        if (lane == 0) a.parts[blockIdx.x] = Part{total, most, kept};
+    for (int d = 16; d; d >>= 1) {
+        const float s = __shfl_xor_sync(0xffffffffu, sum, d), m = __shfl_xor_sync(0xffffffffu, more, d);
+        join(s, m);
     }
-    for (int i = tid; i < kept; i += kThreads) a.lists[(size_t)blockIdx.x * n + i] = s_list[i];
+    if (lane == 0) s_sum[warp] = make_float2(sum, more);
+    __syncthreads();
+    if (tid == 0) {
+        sum = more = 0.f;
+        for (int w = 0; w < kThreads / 32; ++w) join(s_sum[w].x, s_sum[w].y);
+        a.parts[segment] = Part{sum, more, ref, 0.f};
+    }
+    for (int i = tid; i < n; i += kThreads) a.lists[segment * n + i] = i < kept ? s_list[i] : 0;
+    __syncthreads();
+    }
 }
 
-// A continuation: its score and beam * vocab + token.
-struct Choice {
-    double score;
+// A continuation: its score in the order of unsigned numbers (64-bit comparisons of
+// floating numbers run at a sixty-fourth of the rate), and beam * vocab + token.
+struct __align__(16) Choice {
+    uint64_t key;
     uint32_t at;
 };
+constexpr uint64_t kLowestKey = 0x000fffffffffffffull;   // -infinity's
+__device__ __forceinline__ uint64_t key_of(double score) {
+    uint64_t u = (uint64_t)__double_as_longlong(score);
+    if (u == 1ull << 63) u = 0;   // -0 is 0
+    return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double score_of(uint64_t key) {
+    return __longlong_as_double((long long)(key ^ ((key >> 63) ? 1ull << 63 : ~0ull)));
+}
 __device__ __forceinline__ bool better(const Choice& a, const Choice& b) {
-    return a.score > b.score || (a.score == b.score && a.at < b.at);
+    return (a.key > b.key) | ((a.key == b.key) & (a.at < b.at));   // no branch: loops over it are bound by its latency
 }
 
 struct JoinArgs {
     BeamSelectIO io;
-    int segments;
+    Deal deal;
+    int most;            // segments of a row
+    int rounds;          // candidates of a thread
+    uint32_t per_segments, per_most;   // 2^31 over K * most and over most, rounded up: quotients of numbers below 2^12
     const Part* parts;
     const uint64_t* lists;
 };
 
 __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs a) {
-    __shared__ double s_most[KDA_BEAM_MAX_BEAMS], s_ln[KDA_BEAM_MAX_BEAMS], s_score[KDA_BEAM_MAX_BEAMS];
-    __shared__ uint8_t s_done[KDA_BEAM_MAX_BEAMS];
-    __shared__ Choice s_best[kThreads];
+    __shared__ double s_from[KDA_BEAM_MAX_BEAMS];   // a score is (logit - most) + from
+    __shared__ double s_most[KDA_BEAM_MAX_BEAMS];
+    __shared__ int s_first[KDA_BEAM_MAX_BEAMS], s_segments[KDA_BEAM_MAX_BEAMS];   // (none of a beam at its end)
+    __shared__ uint32_t s_group[kGroups];
+    __shared__ Choice s_best[kThreads], s_bound;
     __shared__ Choice s_list[kJoinList];
     __shared__ Choice s_sorted[kMostNum];
-    __shared__ Choice s_bound;
     __shared__ int s_held, s_beam[kMostNum];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = blockIdx.x, K = a.io.beams, n = a.io.num, S = a.segments;
+    const int g = blockIdx.x, K = a.io.beams, n = a.io.num, S = a.most;
+    const uint8_t* done = a.io.done ? a.io.done + (size_t)g * K : nullptr;
+    const float* scores = a.io.scores + (size_t)g * K;
+    if (tid == 0) s_held = 0;
     for (int k = tid; k < K; k += kThreads) {
-        s_score[k] = a.io.scores[(size_t)g * K + k];
-        s_done[k] = a.io.done ? a.io.done[(size_t)g * K + k] : 0;
+        const long long row = (long long)g * K + k;
+        const int from = a.deal.cta_of(row * a.deal.per_row), to = a.deal.cta_of((row + 1) * a.deal.per_row - 1);
+        s_first[k] = (int)row + from;
+        s_segments[k] = done && done[k] ? 0 : to - from + 1;
     }
-    if (tid == 0) {
-        s_held = 0;
-        s_bound = Choice{-INFINITY, 0xffffffffu};
-    }
-    ptx::griddep_wait();
     __syncthreads();
+    ptx::griddep_wait();
 
-    // The beams' sums: ln of the sum of exp(x - most).
-    for (int k = warp; k < K; k += kThreads / 32) {
-        if (s_done[k]) continue;
-        const Part* p = a.parts + ((size_t)g * K + k) * S;
-        float most = -INFINITY;
-        for (int s = lane; s < S; s += 32) most = fmaxf(most, p[s].most);
+    // This thread's share of the segments' lists, taken as all first candidates, then all second ones,
+    // ..., in turns by the groups of threads of the bound below: each group has some of every beam.
+    const int segments = K * S;
+    uint64_t own[kJoinPer];
+    int beam_of[kJoinPer];
+    {
+        const int turn = tid % kGroup * kGroups + tid / kGroup;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-        double sum = 0.0;
-        for (int s = lane; s < S; s += 32) {
-            const Part x = p[s];
-            // A segment of -infinities adds nothing (one with a NaN: NaN).
-            sum += x.most == -INFINITY ? x.sum : x.sum * exp((double)x.most - (double)most);
+        for (int j = 0; j < kJoinPer; ++j) {
+            if (j >= a.rounds) break;
+            const uint32_t i = j * kThreads + turn, nth = __umulhi(2 * i, a.per_segments), at = i - nth * segments;
+            const int k = (int)__umulhi(2 * at, a.per_most), s = (int)at - k * S;
+            beam_of[j] = k;
+            own[j] = nth < (uint32_t)n && s < s_segments[k] ? a.lists[(size_t)(s_first[k] + s) * n + nth] : 0;
         }
+    }
+
+    // The beams' sums of exp(x - most).  Where one is NaN, the beam has nothing to offer.
+    for (int k = warp; k < K; k += kThreads / 32) {
+        const int here = s_segments[k];
+        if (here == 0) continue;
+        const Part* p = a.parts + s_first[k];
+        const uint64_t* l = a.lists + (size_t)s_first[k] * n;
+        // Up to 32 parts and 64 candidates at once: one latency for all of them.
+        const Part none{0.f, 0.f, -INFINITY, 0.f}, x0 = lane < here ? p[lane] : none;
+        uint64_t head = lane < here ? l[lane * n] : 0;
+        const uint64_t c0 = lane < here * n ? l[lane] : 0, c1 = lane + 32 < here * n ? l[lane + 32] : 0;
+        for (int s = lane + 32; s < here; s += 32) head = max(head, l[s * n]);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, (uint32_t)(head >> 32));
+        const float most = top ? float_of(top) : -INFINITY;
+        long long sum = 0;
+        bool bad = !(most < INFINITY);
+        auto add_candidate = [&](uint64_t c) {
+            const Power e = power_of(c ? logit_of(c) : -INFINITY, most);
+            sum += e.i > -32 ? e.m >> -e.i : 0u;
+        };
+        auto add_part = [&](const Part& x) {
+            bad |= !(x.sum < INFINITY);
+            if (x.ref != -INFINITY) {   // which is at most the segment's first candidate
+                const Power e = power_of(x.ref, most);
+                sum += scaled(x.sum, e) + scaled(x.more, e);
+            }
+        };
+        add_candidate(c0);
+        if (here * n > 32) add_candidate(c1);
+        for (int i = lane + 64; i < here * n; i += 32) add_candidate(l[i]);
+        add_part(x0);
+        for (int s = lane + 32; s < here; s += 32) add_part(p[s]);
 #pragma unroll
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        bad = __any_sync(0xffffffffu, bad);
         if (lane == 0) {
             s_most[k] = most;
-            s_ln[k] = log(sum);
+            s_from[k] = bad || sum <= 0 ? -INFINITY : (double)scores[k] - ln_fixed((unsigned long long)sum);
         }
     }
     __syncthreads();
 
-    // The choice at place i of beam k's segments' lists, or a beam's end; false if there is none above -infinity.
-    const int per_beam = S * n, entries = K * per_beam;
-    auto entry = [&](int i, Choice& c) {
-        if (i >= entries) {
-            const int k = i - entries;
-            c = Choice{s_score[k], (uint32_t)k * (uint32_t)a.io.vocab + (uint32_t)a.io.end_token};
-            return s_done[k] && c.score > -INFINITY;
+    // The continuations above -infinity; the last is that of a beam at its end.
+    Choice mine[kJoinPer + 1];
+    Choice best{0, 0xffffffffu};
+#pragma unroll
+    for (int j = 0; j <= kJoinPer; ++j) {
+        if (j >= a.rounds && j < kJoinPer) continue;
+        if (j < kJoinPer) {
+            const int k = beam_of[j];
+            const double score = (widened(logit_of(own[j])) - s_most[k]) + s_from[k];
+            // Of NaN the key tells nothing.
+            const bool number = ((uint64_t)__double_as_longlong(score) << 1) <= 0xffe0000000000000ull;
+            const uint64_t key = key_of(score);
+            mine[j] = Choice{own[j] && number && key > kLowestKey ? key : 0,
+                             (uint32_t)k * (uint32_t)a.io.vocab + (uint32_t)token_of(own[j])};
+        } else {
+            mine[j] = Choice{0, 0};
+            if (done && tid < K && done[tid] && scores[tid] > -INFINITY)
+                mine[j] = Choice{key_of(scores[tid]), (uint32_t)tid * (uint32_t)a.io.vocab + (uint32_t)a.io.end_token};
         }
-        const int k = i / per_beam;
-        if (s_done[k]) return false;
-        const size_t part = ((size_t)g * K + k) * S + (i - k * per_beam) / n;
-        if ((i - k * per_beam) % n >= a.parts[part].count) return false;
-        const uint64_t x = a.lists[part * n + (i - k * per_beam) % n];
-        // x - most is exact or rounded once; NaN is no choice.
-        c = Choice{((double)logit_of(x) - s_most[k]) - s_ln[k] + s_score[k],
-                   (uint32_t)k * (uint32_t)a.io.vocab + (uint32_t)token_of(x)};
-        return c.score > -INFINITY;
-    };
-
-    // Of the threads' best, the num-th: no chosen one is below it.
-    Choice best{-INFINITY, 0xffffffffu};
-    bool any = false;
-    for (int i = tid; i < entries + K; i += kThreads) {
-        Choice c;
-        if (entry(i, c) && (!any || better(c, best))) {
-            best = c;
-            any = true;
-        }
+        if (better(mine[j], best)) best = mine[j];
     }
-    s_best[tid] = best;
-    __syncthreads();
-    int above = 0;
-    for (int j = 0; j < kThreads; ++j) above += better(s_best[j], best);
-    if (any && above == n - 1) s_bound = best;
-    __syncthreads();
-    const Choice bound = s_bound;
-    if (any && !better(bound, best))   // else none of this thread's reach it
-        for (int i = tid; i < entries + K; i += kThreads) {
-            Choice c;
-            if (entry(i, c) && !better(bound, c)) s_list[atomicAdd(&s_held, 1)] = c;
+    // A bound that num of them reach, as in the rows' kernel; of equal scores all pass.
+    uint32_t top;
+    Choice bound{max((uint64_t)group_bound<24>((uint32_t)(best.key >> 32), n, s_group, &top) << 32, (uint64_t)1), 0xffffffffu};
+    for (;;) {
+        int count = 0;
+#pragma unroll
+        for (int j = 0; j <= kJoinPer; ++j)
+            if (j < a.rounds || j == kJoinPer) count += !better(bound, mine[j]);
+        int to = count ? atomicAdd(&s_held, count) : 0;
+        const bool fits = to + count <= kJoinList;
+        if (count && fits)
+#pragma unroll
+            for (int j = 0; j <= kJoinPer; ++j)
+                if ((j < a.rounds || j == kJoinPer) && !better(bound, mine[j])) s_list[to++] = mine[j];
+        if (!__syncthreads_or(!fits)) break;
+        // Too many: the num-th best of the threads' best, which num threads at most reach.
+        s_best[tid] = best;
+        if (tid == 0) {
+            s_held = 0;
+            s_bound = Choice{1, 0xffffffffu};
         }
-    __syncthreads();
+        __syncthreads();
+        int above = 0;
+#pragma unroll 8
+        for (int j = 0; j < kThreads; ++j) above += better(s_best[j], best);
+        if (best.key && above == n - 1) s_bound = best;
+        __syncthreads();
+        bound = s_bound;
+    }
     const int held = s_held, chosen = min(held, n);
     for (int i = tid; i < held; i += kThreads) {
         const Choice c = s_list[i];
         int rank = 0;
+#pragma unroll 8
         for (int j = 0; j < held; ++j) rank += better(s_list[j], c);
         if (rank < n) s_sorted[rank] = c;
     }
@@ -385,7 +649,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
             bool used = false;
             for (int i = lane; i < chosen; i += 32) used |= s_sorted[i].at == at;
             if (__any_sync(0xffffffffu, used)) continue;
-            if (lane == 0) s_sorted[m] = Choice{-INFINITY, at};
+            if (lane == 0) s_sorted[m] = Choice{kLowestKey, at};
             ++m;
         }
     }
@@ -421,45 +685,58 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
             }
         }
         const size_t out = (size_t)g * n + place;
-        a.io.out_scores[out] = (float)s_sorted[tid].score;
+        a.io.out_scores[out] = (float)score_of(s_sorted[tid].key);
         a.io.out_tokens[out] = (int)(s_sorted[tid].at % (uint32_t)a.io.vocab);
         a.io.out_rows[out] = g * K + beam;
     }
 }
 
-// Segments per row: about four CTAs for every SM, none smaller than a tile, and no
-// more lists than the join takes.
-int segments_of(int groups, int beams, int vocab, int num, const DeviceInfo& dev) {
+// The deal, and the most segments of a row.  No CTA has less than a tile, and the
+// join takes K * num candidates for each of a row's segments.
+constexpr int kCtasPerSm = 4;
+Deal deal_of(int groups, int beams, int vocab, int num, const DeviceInfo& dev, int& most) {
     const long long rows = (long long)groups * beams;
-    long long s = (8LL * dev.sm_count + rows - 1) / rows;
-    const long long tiles = (vocab + kTile - 1) / kTile;
-    if (s > tiles) s = tiles;
-    if (s > kJoinEntries / (beams * num)) s = kJoinEntries / (beams * num);
-    if (s > kJoinParts / beams) s = kJoinParts / beams;
-    return s < 1 ? 1 : (int)s;
+    Deal d;
+    d.per_row = (vocab + kTile - 1) / kTile;
+    d.units = rows * d.per_row;
+    long long ctas = (long long)kCtasPerSm * dev.sm_count;
+    if (ctas > d.units) ctas = d.units;
+    for (;; ctas = ctas > 2 * rows ? ctas - rows : rows) {
+        // Ranges of `least` units or one more: a row's units lie in so many of them at most.
+        const long long least = d.units / ctas;
+        most = ctas == rows ? 1 : (int)((d.per_row - 1 + least - 1) / least) + 1;
+        if (most == 1 || (long long)beams * num * most <= kJoinEntries) break;
+    }
+    d.ctas = (int)ctas;
+    return d;
 }
 
 size_t parts_bytes(size_t parts) { return (parts * sizeof(Part) + 255) & ~size_t(255); }
+size_t parts_of(const BeamSelectIO& io, const Deal& d) { return (size_t)io.groups * io.beams + d.ctas; }
 
 }  // namespace
 
 size_t beam_select_workspace_bytes(int groups, int beams, int vocab, int num, const DeviceInfo& dev) {
-    const size_t parts = (size_t)groups * beams * segments_of(groups, beams, vocab, num, dev);
+    int most;
+    const Deal d = deal_of(groups, beams, vocab, num, dev, most);
+    const size_t parts = (size_t)groups * beams + d.ctas;
     return parts_bytes(parts) + parts * num * sizeof(uint64_t);
 }
 
 cudaError_t launch_beam_select(const BeamSelectIO& io, const DeviceInfo& dev, cudaStream_t stream) {
-    const int S = segments_of(io.groups, io.beams, io.vocab, io.num, dev);
-    const size_t parts = (size_t)io.groups * io.beams * S;
+    int most;
+    const Deal d = deal_of(io.groups, io.beams, io.vocab, io.num, dev, most);
     Part* p = static_cast<Part*>(io.workspace);
-    uint64_t* lists = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(io.workspace) + parts_bytes(parts));
-    const RowsArgs r{io, S, p, lists};
-    if (io.bf16) kda_beam_rows_kernel<true><<<(unsigned)parts, kThreads, 0, stream>>>(r);
-    else kda_beam_rows_kernel<false><<<(unsigned)parts, kThreads, 0, stream>>>(r);
+    uint64_t* lists = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(io.workspace) + parts_bytes(parts_of(io, d)));
+    const RowsArgs r{io, d, p, lists};
+    if (io.bf16) kda_beam_rows_kernel<true><<<(unsigned)d.ctas, kThreads, 0, stream>>>(r);
+    else kda_beam_rows_kernel<false><<<(unsigned)d.ctas, kThreads, 0, stream>>>(r);
     count_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const JoinArgs j{io, S, p, lists};
+    const uint64_t segments = (uint64_t)io.beams * most;
+    const JoinArgs j{io, d, most, (int)((segments * io.num + kThreads - 1) / kThreads),
+                     (uint32_t)(((1ull << 31) + segments - 1) / segments), (uint32_t)(((1ull << 31) + most - 1) / most), p, lists};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
