@@ -12,6 +12,9 @@
  *                     into their cache slots
  *   kda_attn_decode   attention of one new token per request
  *   kda_attn_prefill  causal attention of a chunk of new tokens per request
+ *   kda_attn_fork     pages shared, released and copied as requests take over
+ *                     one another (beam search, samples of one prompt)
+ *   kda_attn_copy_pages  those copies, in one layer's cache
  *
  * Heads are 128 wide (d).  Hq query heads share Hkv key/value heads, query
  * head h using key/value head h / (Hq / Hkv).
@@ -26,7 +29,8 @@
  * on the caller's stream, no allocation and no synchronisation per call,
  * arguments checked on the host before any launch, one host thread per context
  * at a time, bounded waits, KDA_FAULT_INJECT (names "attn_plan",
- * "attn_append", "attn_decode", "attn_prefill"; "all" includes them; the name
+ * "attn_append", "attn_decode", "attn_prefill", "attn_fork", "attn_copy_pages";
+ * "all" includes them; the name
  * "attn_drop", not part of "all", makes every CTA of the attention kernels leave
  * out its first copy of keys: the bounded waits on it run out and
  * kda_attn_sync_status reports KDA_ERR_TIMEOUT).
@@ -50,7 +54,7 @@ typedef struct kda_attn_ctx kda_attn_ctx;
 /* Formats of the cached keys and values. */
 enum { KDA_CACHE_BF16 = 0, KDA_CACHE_E4M3 = 1 };
 
-/* Most requests of one kda_attn_plan call. */
+/* Most requests of one kda_attn_plan or kda_attn_fork call. */
 #define KDA_ATTN_MAX_PLAN_REQUESTS 16384
 
 typedef struct kda_attn_config {
@@ -146,6 +150,70 @@ KDA_API kda_status kda_attn_append(kda_attn_ctx *ctx, int N, const uint16_t *q, 
                                    long long v_stride, const int32_t *positions, const int64_t *slots,
                                    uint16_t *q_out, void *stream);
 
+/* Bytes of device workspace of kda_attn_fork. */
+KDA_API size_t kda_attn_fork_workspace_bytes(const kda_attn_ctx *ctx, int B, int max_pages);
+
+/*
+ * Requests take over one another: request b goes on from the tokens of request
+ * rows[b] (its own, or another's), for b = 0 .. B - 1; once per step, for all
+ * layers.  With P = page_size and L = kv_lens[rows[b]]:
+ *
+ *   - new_table[b] gets the ceil(L / P) pages of rows[b]'s row and new_lens[b]
+ *     gets L.  Full pages are shared by all requests that go on from rows[b].
+ *   - A partly full last page stays with the first (lowest b) of these requests;
+ *     every other one gets a page of its own, into which the rows that hold tokens
+ *     are to be copied: copy_src[b], copy_dst[b], copy_rows[b] say from where,
+ *     to where and how many, and kda_attn_copy_pages does it in every layer.
+ *     copy_src[b] is -1 where nothing is to be copied.
+ *   - A request that none goes on from lets go of its pages.  A page that nobody
+ *     holds any more goes onto the free list's END: pages in the order of their
+ *     place in the rows, pages of one place in the order of the requests (of the
+ *     last one, where several let go of it).
+ *   - The copies' pages come from the list's END, freed ones among them, in the
+ *     order of the requests.  A request that finds none left is refused: new_lens[b]
+ *     is 0 and it holds nothing.
+ *
+ *   rows        [B] int32 (in): 0 .. B - 1, or -1: request b is empty afterwards.  Any
+ *               other value is an error and counts as -1.
+ *   kv_lens     [B] int32 (in): tokens in the cache (clamped to 0 .. max_pages * P)
+ *   block_table [B][max_pages] int32 (in); entries past a request's pages are not read
+ *   page_refs   [num_pages of the bound cache] int32 (in, out): how many hold a page
+ *               beside the first.  0 for a page that one request holds, and for a free
+ *               one: all zero before the first fork, and kda_attn_plan has nothing to do
+ *               with it.  Who holds a page outside of the block table (a prompt kept for
+ *               later) adds 1.  A page is held at one and the same place of all rows that
+ *               hold it, and a partly full one by one request.
+ *   free_pages  [free_capacity] int32 (in, out), free_count [1] int32 (in): the stack, as
+ *               for kda_attn_plan; entries from free_count on may be written
+ *   new_table   [B][max_pages] int32 (out), new_lens [B] int32 (out): not the old ones.
+ *               Entries past a request's pages are not written.
+ *   copy_src, copy_dst, copy_rows  [B] int32 (out)
+ *   info        [4] int32 (out): pages freed, pages taken, pages left on the stack (carry
+ *               on with free_count = info[2]), requests refused
+ *   workspace   kda_attn_fork_workspace_bytes bytes, 16-byte aligned
+ * int32 arrays are 4-byte aligned; no output may alias an input but those marked
+ * (in, out).  A page id outside the cache is copied as it is and counted nowhere; it,
+ * a page that more requests let go of than hold it, and a free list without room for
+ * the freed pages (which are lost) are errors.  B == 0 is a no-op.  B above
+ * KDA_ATTN_MAX_PLAN_REQUESTS: KDA_ERR_UNSUPPORTED.
+ */
+KDA_API kda_status kda_attn_fork(kda_attn_ctx *ctx, int B, const int32_t *rows, const int32_t *kv_lens,
+                                 const int32_t *block_table, int max_pages, int32_t *page_refs,
+                                 int32_t *free_pages, int free_capacity, const int32_t *free_count,
+                                 int32_t *new_table, int32_t *new_lens, int32_t *copy_src, int32_t *copy_dst,
+                                 int32_t *copy_rows, int32_t *info, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/*
+ * Copies the first rows[i] (clamped to 0 .. page_size) keys and values of page src[i],
+ * all heads, to page dst[i], for i = 0 .. n - 1, in the bound cache.  src[i] == -1: nothing.
+ * Any other page outside the cache is an error, and nothing is copied for that i.  No
+ * destination may be a source, or a destination twice.  [n] int32 each, 4-byte
+ * aligned.  n == 0 is a no-op.
+ */
+KDA_API kda_status kda_attn_copy_pages(kda_attn_ctx *ctx, int n, const int32_t *src, const int32_t *dst,
+                                       const int32_t *rows, void *stream);
+
 /* Bytes of device workspace that kda_attn_decode and kda_attn_prefill need,
  * whatever their sizes.  One workspace serves one call at a time. */
 KDA_API size_t kda_attn_workspace_bytes(const kda_attn_ctx *ctx);
@@ -193,8 +261,8 @@ KDA_API kda_status kda_attn_prefill(kda_attn_ctx *ctx, int B, int N, const int32
                                     size_t workspace_bytes, void *stream);
 
 /* As kda_sync_status: KDA_ERR_TIMEOUT if a bounded wait gave up,
- * KDA_ERR_INVALID_ARG if a kernel met a page id or slot outside the cache, or
- * row offsets that are not ascending. */
+ * KDA_ERR_INVALID_ARG if a kernel met a page id or slot outside the cache, row
+ * offsets that are not ascending, or one of kda_attn_fork's errors. */
 KDA_API kda_status kda_attn_sync_status(kda_attn_ctx *ctx, void *stream);
 
 #ifdef __cplusplus

@@ -21,6 +21,7 @@ __all__ = [
     "LOWRANK_NOALLOC_SCRATCH_BYTES", "kda_bind_projections", "kda_project_qkvg", "kda_project_o",
     "kda_project_o_workspace_bytes", "kda_attn_create", "kda_attn_destroy", "kda_attn_bind_cache",
     "kda_attn_plan", "kda_attn_append", "kda_attn_workspace_bytes", "kda_attn_decode", "kda_attn_prefill",
+    "kda_attn_fork", "kda_attn_fork_workspace_bytes", "kda_attn_copy_pages",
     "kda_attn_sync_status", "kda_beam_select", "kda_beam_select_workspace_bytes", "kda_beam_reorder", "KDA_CACHE_BF16", "KDA_CACHE_E4M3", "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_ALIGNMENT",
     "KDA_ERR_UNSUPPORTED", "KDA_ERR_CUDA", "KDA_ERR_TIMEOUT", "HEAD_DIM", "CHUNK",
 ]
@@ -135,6 +136,12 @@ def load(path: str | None = None):
     lib.kda_attn_decode.restype = i32
     lib.kda_attn_prefill.argtypes = [vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, sz, vp]
     lib.kda_attn_prefill.restype = i32
+    lib.kda_attn_fork_workspace_bytes.argtypes = [vp, i32, i32]
+    lib.kda_attn_fork_workspace_bytes.restype = sz
+    lib.kda_attn_fork.argtypes = [vp, i32, vp, vp, vp, i32, vp, vp, i32] + [vp] * 8 + [sz, vp]
+    lib.kda_attn_fork.restype = i32
+    lib.kda_attn_copy_pages.argtypes = [vp, i32, vp, vp, vp, vp]
+    lib.kda_attn_copy_pages.restype = i32
     lib.kda_attn_sync_status.argtypes = [vp, vp]
     lib.kda_attn_sync_status.restype = i32
     lib.kda_beam_select_workspace_bytes.argtypes = [vp] + [i32] * 4
@@ -414,6 +421,31 @@ def kda_attn_prefill(attn, B, N, cu_new, q, block_table, kv_lens, o, workspace, 
                                    _pitch(block_table, max_pages), _p(kv_lens), _dense(gate_logit, "gate_logit"),
                                    _dense(o, "o"), _is_f32(o, o_f32), _dense(lse, "lse"), _p(workspace),
                                    _nbytes(workspace, workspace_bytes), _stream(stream)), "kda_attn_prefill")
+
+
+def kda_attn_fork_workspace_bytes(attn, B, max_pages) -> int:
+    return int(load().kda_attn_fork_workspace_bytes(attn, int(B), int(max_pages)))
+
+
+def kda_attn_fork(attn, B, rows, kv_lens, block_table, page_refs, free_pages, free_count, new_table, new_lens,
+                  copy_src, copy_dst, copy_rows, info, workspace, *, free_capacity=None, max_pages=None,
+                  workspace_bytes=0, stream=None) -> None:
+    """Requests take over one another's pages (kda_attn.h).  Both tables have rows of the same pitch."""
+    cap = free_pages.numel() if free_capacity is None else int(free_capacity)
+    pitch = _pitch(block_table, max_pages)
+    if max_pages is None and _pitch(new_table, None) != pitch:
+        raise ValueError(f"rows of block_table are {pitch} apart, those of new_table {_pitch(new_table, None)}")
+    _check(load().kda_attn_fork(attn, B, _words(rows, "rows", B), _words(kv_lens, "kv_lens", B), _p(block_table), pitch,
+                                _words(page_refs, "page_refs", 0), _words(free_pages, "free_pages", cap), cap,
+                                _p(free_count), _p(new_table), _words(new_lens, "new_lens", B),
+                                _words(copy_src, "copy_src", B), _words(copy_dst, "copy_dst", B),
+                                _words(copy_rows, "copy_rows", B), _words(info, "info", 4), _p(workspace),
+                                _nbytes(workspace, workspace_bytes), _stream(stream)), "kda_attn_fork")
+
+
+def kda_attn_copy_pages(attn, n, src, dst, rows, *, stream=None) -> None:
+    _check(load().kda_attn_copy_pages(attn, n, _words(src, "src", n), _words(dst, "dst", n), _words(rows, "rows", n),
+                                      _stream(stream)), "kda_attn_copy_pages")
 
 
 def kda_attn_sync_status(attn, stream=None) -> int:

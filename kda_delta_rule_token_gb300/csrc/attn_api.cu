@@ -5,7 +5,7 @@
 //
 // KDA_FAULT_INJECT, read once by kda_attn_create, replaces the launches of
 // the entry points it names ("attn_plan", "attn_append", "attn_decode",
-// "attn_prefill", or "all") by the error cudaErrorLaunchFailure.  The name
+// "attn_prefill", "attn_fork", "attn_copy_pages", or "all") by the error cudaErrorLaunchFailure.  The name
 // "attn_drop" (not part of "all") instead makes every CTA of the attention
 // kernels leave out its first copy of keys, so that a bounded wait inside the
 // kernel runs out.
@@ -29,7 +29,8 @@ struct kda_attn_ctx {
 namespace kda {
 namespace {
 
-constexpr unsigned kInjectPlan = 1u, kInjectAppend = 2u, kInjectDecode = 4u, kInjectPrefill = 8u, kInjectDrop = 16u;
+constexpr unsigned kInjectPlan = 1u, kInjectAppend = 2u, kInjectDecode = 4u, kInjectPrefill = 8u, kInjectDrop = 16u,
+                   kInjectFork = 32u, kInjectCopy = 64u;
 
 unsigned parse_inject(const char* v) {
     unsigned m = 0u;
@@ -42,8 +43,10 @@ unsigned parse_inject(const char* v) {
         else if (is("attn_append")) m |= kInjectAppend;
         else if (is("attn_decode")) m |= kInjectDecode;
         else if (is("attn_prefill")) m |= kInjectPrefill;
+        else if (is("attn_fork")) m |= kInjectFork;
+        else if (is("attn_copy_pages")) m |= kInjectCopy;
         else if (is("attn_drop")) m |= kInjectDrop;
-        else if (is("all")) m |= kInjectPlan | kInjectAppend | kInjectDecode | kInjectPrefill;
+        else if (is("all")) m |= kInjectPlan | kInjectAppend | kInjectDecode | kInjectPrefill | kInjectFork | kInjectCopy;
         p = *e ? e + 1 : e;
     }
     return m;
@@ -281,6 +284,61 @@ kda_status kda_attn_append(kda_attn_ctx* ctx, int N, const uint16_t* q, long lon
     });
 }
 
+size_t kda_attn_fork_workspace_bytes(const kda_attn_ctx* ctx, int B, int max_pages) {
+    return ctx && B > 0 && max_pages > 0 ? kda::attn_fork_workspace_bytes(B, max_pages) : 0;
+}
+
+kda_status kda_attn_fork(kda_attn_ctx* ctx, int B, const int32_t* rows, const int32_t* kv_lens,
+                         const int32_t* block_table, int max_pages, int32_t* page_refs, int32_t* free_pages,
+                         int free_capacity, const int32_t* free_count, int32_t* new_table, int32_t* new_lens,
+                         int32_t* copy_src, int32_t* copy_dst, int32_t* copy_rows, int32_t* info, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    if (!ctx || B < 0) return KDA_ERR_INVALID_ARG;
+    if (B == 0) return KDA_OK;
+    if (!rows || !kv_lens || !block_table || max_pages < 1 || !page_refs || free_capacity < 0 ||
+        (free_capacity && !free_pages) || !free_count || !new_table || !new_lens || !copy_src || !copy_dst ||
+        !copy_rows || !info || !workspace)
+        return KDA_ERR_INVALID_ARG;
+    const void* words[] = {rows, kv_lens, block_table, page_refs, free_pages, free_count, new_table,
+                           new_lens, copy_src, copy_dst, copy_rows, info};
+    for (const void* p : words)
+        if (!aligned(p, 4)) return KDA_ERR_ALIGNMENT;
+    if (!aligned(workspace, 16)) return KDA_ERR_ALIGNMENT;
+    if ((long long)max_pages * ctx->layer.page_size > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
+    if (block_table == new_table || kv_lens == new_lens) {
+        kda::set_error_text("the new table and lengths may not be the old ones");
+        return KDA_ERR_INVALID_ARG;
+    }
+    if (B > KDA_ATTN_MAX_PLAN_REQUESTS) {
+        kda::set_error_text("%d requests in one fork, at most %d", B, KDA_ATTN_MAX_PLAN_REQUESTS);
+        return KDA_ERR_UNSUPPORTED;
+    }
+    const size_t need = kda::attn_fork_workspace_bytes(B, max_pages);
+    if (workspace_bytes < need) {
+        kda::set_error_text("workspace of %zu bytes, %zu needed", workspace_bytes, need);
+        return KDA_ERR_INVALID_ARG;
+    }
+    if (const kda_status s = kda::need_cache(ctx); s != KDA_OK) return s;
+    const kda::AttnForkIO io{B, rows, kv_lens, block_table, max_pages, page_refs, free_pages, free_capacity, free_count,
+                             new_table, new_lens, copy_src, copy_dst, copy_rows, info, workspace};
+    return kda::launched(ctx, kda::kInjectFork, "attn_fork launch", [&] {
+        return kda::launch_attn_fork(ctx->layer, io, ctx->dev, ctx->err_word, static_cast<cudaStream_t>(stream));
+    });
+}
+
+kda_status kda_attn_copy_pages(kda_attn_ctx* ctx, int n, const int32_t* src, const int32_t* dst, const int32_t* rows,
+                               void* stream) {
+    if (!ctx || n < 0) return KDA_ERR_INVALID_ARG;
+    if (n == 0) return KDA_OK;
+    if (!src || !dst || !rows) return KDA_ERR_INVALID_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(rows, 4)) return KDA_ERR_ALIGNMENT;
+    if (const kda_status s = kda::need_cache(ctx); s != KDA_OK) return s;
+    const kda::AttnCopyIO io{n, src, dst, rows};
+    return kda::launched(ctx, kda::kInjectCopy, "attn_copy_pages launch", [&] {
+        return kda::launch_attn_copy_pages(ctx->layer, io, ctx->err_word, static_cast<cudaStream_t>(stream));
+    });
+}
+
 size_t kda_attn_workspace_bytes(const kda_attn_ctx* ctx) {
     return ctx ? kda::workspace_bytes_of(ctx) : 0;
 }
@@ -332,7 +390,7 @@ kda_status kda_attn_sync_status(kda_attn_ctx* ctx, void* stream) {
         return kda::cuda_failed("cudaMemcpy(error word)", e);
     if (word == 0) return KDA_OK;
     const bool index = (word & ~kda::kErrAttnIndex) == 0;
-    kda::set_error_text(index ? "kernel error word 0x%x (a page id or slot outside the cache, or row offsets that are not ascending)"
+    kda::set_error_text(index ? "kernel error word 0x%x (a page id, slot or request that there is not, row offsets that are not ascending, or holders miscounted)"
                               : "kernel error word 0x%x (bounded wait gave up)", word);
     if ((e = cudaMemset(ctx->err_word, 0, sizeof(int))) != cudaSuccess)
         return kda::cuda_failed("cudaMemset(error word)", e);

@@ -12,8 +12,9 @@
 namespace kda {
 
 // Error-word bits of the attention context beside the bounded-wait ones of
-// ptx.cuh: a page id or slot outside the cache was met (and not accessed), or
-// row offsets that claim rows more than once (and nothing was done).
+// ptx.cuh: a page id or slot outside the cache was met (and not accessed), row
+// offsets that claim rows more than once (and nothing was done), or a page that
+// more requests let go of than held it.
 constexpr int kErrAttnIndex = 1 << 16;
 
 // One layer as its kernels see it.
@@ -72,6 +73,32 @@ struct AttnAppendIO {
     uint16_t* q_out;
 };
 
+struct AttnForkIO {
+    int B;
+    const int* rows;
+    const int* kv_lens;
+    const int* block_table;
+    int max_pages;
+    int* page_refs;
+    int* free_pages;
+    int free_capacity;
+    const int* free_count;
+    int* new_table;
+    int* new_lens;
+    int* copy_src;
+    int* copy_dst;
+    int* copy_rows;
+    int* info;
+    void* workspace;
+};
+
+struct AttnCopyIO {
+    int n;
+    const int* src;
+    const int* dst;
+    const int* rows;
+};
+
 struct AttnIO {
     int B, N;                // decode: N = B
     const int* cu_new;       // prefill; null for decode (one token each)
@@ -92,6 +119,10 @@ struct AttnIO {
 cudaError_t launch_attn_plan(const AttnLayer& l, const AttnPlanIO& io, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_attn_append(const AttnLayer& l, const RopeTurns& turns, const AttnAppendIO& io,
                                const DeviceInfo& dev, int* err_word, cudaStream_t stream);
+size_t attn_fork_workspace_bytes(int B, int max_pages);
+cudaError_t launch_attn_fork(const AttnLayer& l, const AttnForkIO& io, const DeviceInfo& dev, int* err_word,
+                             cudaStream_t stream);
+cudaError_t launch_attn_copy_pages(const AttnLayer& l, const AttnCopyIO& io, int* err_word, cudaStream_t stream);
 // The bound cache's tensor maps; false if they cannot be encoded.
 bool attn_decode_maps(const AttnLayer& l, AttnMaps& maps);
 bool attn_prefill_maps(const AttnLayer& l, AttnMaps& maps);
