@@ -11,6 +11,8 @@
  *   kda_attn_append   RMS norm of every q and k head, rotary position, k and v
  *                     into their cache slots
  *   kda_attn_decode   attention of one new token per request
+ *   kda_attn_decode_shared  the same where groups of requests share a prefix,
+ *                     whose keys are read once for all of them
  *   kda_attn_prefill  causal attention of a chunk of new tokens per request
  *   kda_attn_fork     pages shared, released and copied as requests take over
  *                     one another (beam search, samples of one prompt)
@@ -29,8 +31,8 @@
  * on the caller's stream, no allocation and no synchronisation per call,
  * arguments checked on the host before any launch, one host thread per context
  * at a time, bounded waits, KDA_FAULT_INJECT (names "attn_plan",
- * "attn_append", "attn_decode", "attn_prefill", "attn_fork", "attn_copy_pages";
- * "all" includes them; the name
+ * "attn_append", "attn_decode", "attn_prefill", "attn_fork", "attn_copy_pages",
+ * "attn_decode_shared"; "all" includes them; the name
  * "attn_drop", not part of "all", makes every CTA of the attention kernels leave
  * out its first copy of keys: the bounded waits on it run out and
  * kda_attn_sync_status reports KDA_ERR_TIMEOUT).
@@ -243,6 +245,32 @@ KDA_API kda_status kda_attn_decode(kda_attn_ctx *ctx, int B, const uint16_t *q, 
                                    int max_pages, const int32_t *kv_lens, const float *gate_logit, void *o,
                                    int o_f32, float *lse, void *workspace, size_t workspace_bytes,
                                    void *stream);
+
+/* Bytes of device workspace of kda_attn_decode_shared for up to B requests. */
+KDA_API size_t kda_attn_shared_workspace_bytes(const kda_attn_ctx *ctx, int B);
+
+/*
+ * kda_attn_decode where groups of requests have their first tokens in common
+ * (beams, samples of one prompt: the block tables that kda_attn_fork makes).  Every
+ * request's table row names all of its pages, as ever, and the results are
+ * those of kda_attn_decode up to rounding; the groups say what need not be read more
+ * than once.
+ *   groups      0 to B
+ *   cu_groups   [groups + 1] int32, ascending from 0 or more to B or less: group g is
+ *               requests cu_groups[g] to cu_groups[g + 1] - 1; requests of no group share
+ *               nothing.  Other offsets are an error, and nothing is shared.
+ *   prefix_lens [groups] int32: the first so many keys of the group's requests are the
+ *               same keys.  The pages that they fill are read through the table row of any
+ *               one request that has so many; a page that they fill in part counts as
+ *               the request's own, and so do all keys of a request of fewer.
+ *   workspace   kda_attn_shared_workspace_bytes bytes, 16-byte aligned
+ * Otherwise as kda_attn_decode.  cu_groups and prefix_lens may be NULL if groups is 0.
+ */
+KDA_API kda_status kda_attn_decode_shared(kda_attn_ctx *ctx, int B, const uint16_t *q, const int32_t *block_table,
+                                          int max_pages, const int32_t *kv_lens, int groups,
+                                          const int32_t *cu_groups, const int32_t *prefix_lens,
+                                          const float *gate_logit, void *o, int o_f32, float *lse,
+                                          void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Causal attention of the N packed new tokens of B requests, whose keys and

@@ -21,7 +21,7 @@ __all__ = [
     "LOWRANK_NOALLOC_SCRATCH_BYTES", "kda_bind_projections", "kda_project_qkvg", "kda_project_o",
     "kda_project_o_workspace_bytes", "kda_attn_create", "kda_attn_destroy", "kda_attn_bind_cache",
     "kda_attn_plan", "kda_attn_append", "kda_attn_workspace_bytes", "kda_attn_decode", "kda_attn_prefill",
-    "kda_attn_fork", "kda_attn_fork_workspace_bytes", "kda_attn_copy_pages",
+    "kda_attn_decode_shared", "kda_attn_shared_workspace_bytes", "kda_attn_fork", "kda_attn_fork_workspace_bytes", "kda_attn_copy_pages",
     "kda_attn_sync_status", "kda_beam_select", "kda_beam_select_workspace_bytes", "kda_beam_reorder", "KDA_CACHE_BF16", "KDA_CACHE_E4M3", "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_ALIGNMENT",
     "KDA_ERR_UNSUPPORTED", "KDA_ERR_CUDA", "KDA_ERR_TIMEOUT", "HEAD_DIM", "CHUNK",
 ]
@@ -136,6 +136,10 @@ def load(path: str | None = None):
     lib.kda_attn_decode.restype = i32
     lib.kda_attn_prefill.argtypes = [vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, sz, vp]
     lib.kda_attn_prefill.restype = i32
+    lib.kda_attn_shared_workspace_bytes.argtypes = [vp, i32]
+    lib.kda_attn_shared_workspace_bytes.restype = sz
+    lib.kda_attn_decode_shared.argtypes = [vp, i32, vp, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.kda_attn_decode_shared.restype = i32
     lib.kda_attn_fork_workspace_bytes.argtypes = [vp, i32, i32]
     lib.kda_attn_fork_workspace_bytes.restype = sz
     lib.kda_attn_fork.argtypes = [vp, i32, vp, vp, vp, i32, vp, vp, i32] + [vp] * 8 + [sz, vp]
@@ -413,6 +417,20 @@ def kda_attn_decode(attn, B, q, block_table, kv_lens, o, workspace, *, max_pages
                                   _p(kv_lens), _dense(gate_logit, "gate_logit"), _dense(o, "o"),
                                   _is_f32(o, o_f32), _dense(lse, "lse"), _p(workspace),
                                   _nbytes(workspace, workspace_bytes), _stream(stream)), "kda_attn_decode")
+
+
+def kda_attn_shared_workspace_bytes(attn, B) -> int:
+    return int(load().kda_attn_shared_workspace_bytes(attn, int(B)))
+
+
+def kda_attn_decode_shared(attn, B, q, block_table, kv_lens, groups, cu_groups, prefix_lens, o, workspace, *, max_pages=None,
+                           gate_logit=None, o_f32=None, lse=None, workspace_bytes=0, stream=None) -> None:
+    """kda_attn_decode where group g's requests, cu_groups[g] to cu_groups[g + 1] - 1, share their first prefix_lens[g] keys."""
+    _check(load().kda_attn_decode_shared(attn, B, _dense(q, "q"), _p(block_table), _pitch(block_table, max_pages), _p(kv_lens),
+                                         int(groups), _dense(cu_groups, "cu_groups"), _dense(prefix_lens, "prefix_lens"),
+                                         _dense(gate_logit, "gate_logit"), _dense(o, "o"), _is_f32(o, o_f32), _dense(lse, "lse"),
+                                         _p(workspace), _nbytes(workspace, workspace_bytes), _stream(stream)),
+           "kda_attn_decode_shared")
 
 
 def kda_attn_prefill(attn, B, N, cu_new, q, block_table, kv_lens, o, workspace, *, max_pages=None,

@@ -5,7 +5,8 @@
 //
 // KDA_FAULT_INJECT, read once by kda_attn_create, replaces the launches of
 // the entry points it names ("attn_plan", "attn_append", "attn_decode",
-// "attn_prefill", "attn_fork", "attn_copy_pages", or "all") by the error cudaErrorLaunchFailure.  The name
+// "attn_prefill", "attn_fork", "attn_copy_pages", "attn_decode_shared", or
+// "all") by the error cudaErrorLaunchFailure.  The name
 // "attn_drop" (not part of "all") instead makes every CTA of the attention
 // kernels leave out its first copy of keys, so that a bounded wait inside the
 // kernel runs out.
@@ -30,7 +31,7 @@ namespace kda {
 namespace {
 
 constexpr unsigned kInjectPlan = 1u, kInjectAppend = 2u, kInjectDecode = 4u, kInjectPrefill = 8u, kInjectDrop = 16u,
-                   kInjectFork = 32u, kInjectCopy = 64u;
+                   kInjectFork = 32u, kInjectCopy = 64u, kInjectShared = 128u;
 
 unsigned parse_inject(const char* v) {
     unsigned m = 0u;
@@ -45,8 +46,10 @@ unsigned parse_inject(const char* v) {
         else if (is("attn_prefill")) m |= kInjectPrefill;
         else if (is("attn_fork")) m |= kInjectFork;
         else if (is("attn_copy_pages")) m |= kInjectCopy;
+        else if (is("attn_decode_shared")) m |= kInjectShared;
         else if (is("attn_drop")) m |= kInjectDrop;
-        else if (is("all")) m |= kInjectPlan | kInjectAppend | kInjectDecode | kInjectPrefill | kInjectFork | kInjectCopy;
+        else if (is("all")) m |= kInjectPlan | kInjectAppend | kInjectDecode | kInjectPrefill | kInjectFork | kInjectCopy |
+                                 kInjectShared;
         p = *e ? e + 1 : e;
     }
     return m;
@@ -94,8 +97,8 @@ size_t workspace_bytes_of(const kda_attn_ctx* ctx) {
     return attn_decode_workspace_bytes(ctx->dev) + attn_prefill_workspace_bytes(ctx->dev);
 }
 
-// What kda_attn_decode and kda_attn_prefill check alike.
-kda_status check_attend(const kda_attn_ctx* ctx, const AttnIO& io, size_t workspace_bytes) {
+// What the attention calls check alike.
+kda_status check_attend(const kda_attn_ctx* ctx, const AttnIO& io, size_t workspace_bytes, size_t need) {
     if (!io.q || !io.block_table || io.max_pages < 1 || !io.kv_lens || !io.o || !io.workspace)
         return KDA_ERR_INVALID_ARG;
     if (!aligned(io.q, 16) || !aligned(io.o, 16) || !aligned(io.gate, 16) || !aligned(io.workspace, 16) ||
@@ -105,9 +108,8 @@ kda_status check_attend(const kda_attn_ctx* ctx, const AttnIO& io, size_t worksp
         set_error_text("max_pages (%d) pages of %d tokens exceed 2^31 - 2^16 keys", io.max_pages, ctx->layer.page_size);
         return KDA_ERR_INVALID_ARG;
     }
-    if (workspace_bytes < workspace_bytes_of(ctx)) {
-        set_error_text("workspace of %zu bytes, %zu needed", workspace_bytes,
-                       workspace_bytes_of(ctx));
+    if (workspace_bytes < need) {
+        set_error_text("workspace of %zu bytes, %zu needed", workspace_bytes, need);
         return KDA_ERR_INVALID_ARG;
     }
     return need_cache(ctx);
@@ -349,11 +351,45 @@ kda_status kda_attn_decode(kda_attn_ctx* ctx, int B, const uint16_t* q, const in
     if (!ctx || B < 0) return KDA_ERR_INVALID_ARG;
     if (B == 0) return KDA_OK;
     const kda::AttnIO io{B, B, nullptr, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace,
-                         (ctx->inject & kda::kInjectDrop) ? 1 : 0};
-    if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes); s != KDA_OK) return s;
+                         (ctx->inject & kda::kInjectDrop) ? 1 : 0, 0, 0, nullptr, nullptr, nullptr};
+    if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes, kda::workspace_bytes_of(ctx)); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectDecode, "attn_decode launch", [&] {
         return kda::launch_attn_few_rows(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word,
                                          static_cast<cudaStream_t>(stream), false);
+    });
+}
+
+size_t kda_attn_shared_workspace_bytes(const kda_attn_ctx* ctx, int B) {
+    return ctx && B > 0 ? kda::attn_shared_workspace_bytes(ctx->layer, B, ctx->dev) : 0;
+}
+
+kda_status kda_attn_decode_shared(kda_attn_ctx* ctx, int B, const uint16_t* q, const int32_t* block_table, int max_pages,
+                                  const int32_t* kv_lens, int groups, const int32_t* cu_groups,
+                                  const int32_t* prefix_lens, const float* gate_logit, void* o, int o_f32, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    if (!ctx || B < 0 || groups < 0) return KDA_ERR_INVALID_ARG;
+    if (B == 0) return KDA_OK;
+    if (groups > B || (groups && (!cu_groups || !prefix_lens))) {
+        kda::set_error_text("%d groups of %d requests, or no offsets and lengths of theirs", groups, B);
+        return KDA_ERR_INVALID_ARG;
+    }
+    if (!aligned(prefix_lens, 4)) return KDA_ERR_ALIGNMENT;
+    kda::AttnIO io{};
+    io.cu_new = cu_groups;
+    io.q = q;
+    io.block_table = block_table;
+    io.max_pages = max_pages;
+    io.kv_lens = kv_lens;
+    io.gate = gate_logit;
+    io.o = o;
+    io.lse = lse;
+    io.workspace = workspace;
+    if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes, kda_attn_shared_workspace_bytes(ctx, B)); s != KDA_OK)
+        return s;
+    const kda::AttnSharedIO sh{B, groups, cu_groups, prefix_lens, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0,
+                               lse, workspace, (ctx->inject & kda::kInjectDrop) ? 1 : 0};
+    return kda::launched(ctx, kda::kInjectShared, "attn_decode_shared launch", [&] {
+        return kda::launch_attn_shared(ctx->layer, ctx->maps, sh, ctx->dev, ctx->err_word, static_cast<cudaStream_t>(stream));
     });
 }
 
@@ -365,8 +401,8 @@ kda_status kda_attn_prefill(kda_attn_ctx* ctx, int B, int N, const int32_t* cu_n
     if (B == 0 || N == 0) return KDA_OK;
     if (!cu_new) return KDA_ERR_INVALID_ARG;
     const kda::AttnIO io{B, N, cu_new, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace,
-                         (ctx->inject & kda::kInjectDrop) ? 1 : 0};
-    if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes); s != KDA_OK) return s;
+                         (ctx->inject & kda::kInjectDrop) ? 1 : 0, 0, 0, nullptr, nullptr, nullptr};
+    if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes, kda::workspace_bytes_of(ctx)); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectPrefill, "attn_prefill launch", [&] {
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
         const bool many = !kda::attn_few_rows(N, ctx->layer.G);   // else no request can have more rows

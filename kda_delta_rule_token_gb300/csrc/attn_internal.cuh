@@ -114,6 +114,31 @@ struct AttnIO {
     // Test injection (KDA_FAULT_INJECT "attn_drop"): every CTA leaves out
     // its first copy of keys, so that a bounded wait runs out.
     int drop;
+    // Requests that share a prefix (attn_shared.cu): the few-row kernel takes
+    // `groups` prefixes first, as requests of their members' tokens, then what each of
+    // `singles` requests has beyond its own; B is the number of both, cu_new has the
+    // groups' members, and o and lse hold 2 * singles tokens: over the prefixes, then
+    // beyond them.  The many-row kernel takes prefixes alone, B = groups.
+    int groups, singles;
+    const int* prefix;       // [singles] shared keys of a request, whole pages and decode tiles
+    const int* group_len;    // [groups] keys of the group's prefix, 0 if it is not shared
+    const int* group_row;    // [groups] the block table's row that has its pages
+};
+
+struct AttnSharedIO {
+    int B, groups;
+    const int* cu_groups;
+    const int* prefix_lens;
+    const uint16_t* q;
+    const int* block_table;
+    int max_pages;
+    const int* kv_lens;
+    const float* gate;       // may be null
+    void* o;
+    int o_f32;
+    float* lse;              // may be null
+    void* workspace;
+    int drop;
 };
 
 cudaError_t launch_attn_plan(const AttnLayer& l, const AttnPlanIO& io, const DeviceInfo& dev, cudaStream_t stream);
@@ -139,6 +164,15 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
                                  int* err_word, cudaStream_t stream, bool beside);
 cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
                                   int* err_word, cudaStream_t stream, bool all);
+
+// The same for requests that share a prefix (AttnIO), and all of kda_attn_decode_shared (attn_shared.cu).
+cudaError_t launch_attn_few_rows_shared(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io,
+                                        const DeviceInfo& dev, int* err_word, cudaStream_t stream, bool beside);
+cudaError_t launch_attn_many_rows_shared(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io,
+                                         const DeviceInfo& dev, int* err_word, cudaStream_t stream);
+size_t attn_shared_workspace_bytes(const AttnLayer& l, int B, const DeviceInfo& dev);
+cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const AttnSharedIO& io, const DeviceInfo& dev,
+                               int* err_word, cudaStream_t stream);
 
 // Which of the two takes a request of n new tokens and G query heads per key
 // head: up to 32 rows fit two 16-row warp tiles, whose kernel streams the

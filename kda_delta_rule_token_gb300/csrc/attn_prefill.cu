@@ -97,12 +97,15 @@ struct Segment {
     int len;                 // keys of the request
     __device__ __forceinline__ int tokens_of(int x, int per) const { return x ? max(m - per, 0) : min(m, per); }
     // Key tiles of tile x (one, fully masked, where its rows see no key).
+    template <bool kShared>
     __device__ __forceinline__ int tiles(int x, int per) const {
         const int t = tokens_of(x, per);
         if (t == 0) return 0;
+        if (kShared) return (len + kKeys - 1) / kKeys;
         return max(1, (first + (x ? m : t) - 1 + kKeys - 1) / kKeys);
     }
-    __device__ __forceinline__ int tiles_all(int per) const { return max(tiles(0, per), tiles(1, per)); }
+    template <bool kShared>
+    __device__ __forceinline__ int tiles_all(int per) const { return max(tiles<kShared>(0, per), tiles<kShared>(1, per)); }
 };
 
 // What a CTA does next: key tiles [j0, j0 + n) of a segment, cnt[x] of them for tile x.
@@ -171,14 +174,19 @@ __device__ __forceinline__ float* slot_at(void* ws, int ctas, int slot) {
     return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + join_bytes(ctas)) + (size_t)slot * kSlotFloats;
 }
 
-// Pairs of token tiles of request b that this file works on.
+// Pairs of token tiles of request b that this file works on.  kShared: b is a group of
+// requests, their single tokens see all of its prefix.
+template <bool kShared>
 __device__ __forceinline__ int pairs_of(const PrefillArgs& a, int b) {
     int tok0, n;
     attn_tokens(a.io, b, tok0, n);
+    if (kShared && (a.io.group_len[b] == 0 || attn_few_rows(n, a.G))) return 0;
+    if (kShared) return (n + 2 * a.tokens - 1) / (2 * a.tokens);
     if (n == 0 || (!a.all && (attn_few_rows(n, a.G) || attn_kv_len(a.io, b, a.page_shift) == 0))) return 0;
     return (n + 2 * a.tokens - 1) / (2 * a.tokens);
 }
 
+template <bool kShared>
 __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, int s) {
     const int pair = (int)((unsigned)s / (unsigned)a.Hkv);
     int lo = 0, hi = kScan - 1;   // the last scan thread with pre <= pair
@@ -187,7 +195,7 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
         if (ctl.pre[mid] <= pair) lo = mid; else hi = mid - 1;
     }
     int at = ctl.pre[lo], b = lo * sc.per, n;
-    while (at + (n = pairs_of(a, b)) <= pair && b + 1 < a.io.B) {
+    while (at + (n = pairs_of<kShared>(a, b)) <= pair && b + 1 < a.io.B) {
         at += n;
         ++b;
     }
@@ -197,7 +205,7 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
     int tok0, tokens;
     attn_tokens(a.io, b, tok0, tokens);
     const int i0 = (n - 1 - (pair - at)) * 2 * a.tokens;   // the longest first
-    g.len = attn_kv_len(a.io, b, a.page_shift);
+    g.len = kShared ? a.io.group_len[b] : attn_kv_len(a.io, b, a.page_shift);
     g.tok = tok0 + i0;
     g.m = min(2 * a.tokens, tokens - i0);
     g.first = g.len - tokens + i0 + 1;
@@ -205,9 +213,10 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
 }
 
 // The segment after segment s - 1, which g holds: the next head of its pair, or the next pair.
+template <bool kShared>
 __device__ __forceinline__ void next_segment(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, int s, Segment& g) {
     if (g.h + 1 < a.Hkv) ++g.h;
-    else if (s < sc.segments) g = find_segment(a, ctl, sc, s);
+    else if (s < sc.segments) g = find_segment<kShared>(a, ctl, sc, s);
 }
 
 // Where a CTA is in its work (the copying warp's).
@@ -219,6 +228,7 @@ struct Cursor {
 };
 
 // The next part of this CTA; p.n = 0 past the last.
+template <bool kShared>
 __device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, Cursor& c, Part& p) {
     p.n = 0;
     if (!sc.split) {
@@ -227,14 +237,14 @@ __device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, 
             if (base >= sc.segments) return;
             const int s = (int)(base + ((c.k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
             if (s >= sc.segments) continue;
-            p.s = find_segment(a, ctl, sc, s);
+            p.s = find_segment<kShared>(a, ctl, sc, s);
             break;
         }
         ++c.k;
         p.j0 = 0;
-        p.n = p.s.tiles_all(a.tokens);
-        p.cnt[0] = p.s.tiles(0, a.tokens);
-        p.cnt[1] = p.s.tiles(1, a.tokens);
+        p.n = p.s.template tiles_all<kShared>(a.tokens);
+        p.cnt[0] = p.s.template tiles<kShared>(0, a.tokens);
+        p.cnt[1] = p.s.template tiles<kShared>(1, a.tokens);
         p.slot = p.last = -1;
         return;
     }
@@ -248,20 +258,20 @@ __device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, 
         }
         c.k = lo * sc.chunk;
         c.at = ctl.units[lo];
-        if (c.k < sc.segments) c.s = find_segment(a, ctl, sc, c.k);
+        if (c.k < sc.segments) c.s = find_segment<kShared>(a, ctl, sc, c.k);
     }
     while (c.k < sc.segments && c.at < to) {
         p.s = c.s;
-        const int tiles = p.s.tiles_all(a.tokens), at = c.at;
+        const int tiles = p.s.template tiles_all<kShared>(a.tokens), at = c.at;
         ++c.k;
-        next_segment(a, ctl, sc, c.k, c.s);
+        next_segment<kShared>(a, ctl, sc, c.k, c.s);
         c.at += tiles + a.part_cost;
         // A segment's first part_cost units stand for its cost, the others for its tiles.
         const int j0 = max(from - at - a.part_cost, 0), j1 = min(to - at - a.part_cost, tiles);
         if (j1 <= j0) continue;
         p.j0 = j0;
         p.n = j1 - j0;
-        for (int x = 0; x < 2; ++x) p.cnt[x] = min(max(p.s.tiles(x, a.tokens) - j0, 0), p.n);
+        for (int x = 0; x < 2; ++x) p.cnt[x] = min(max(p.s.template tiles<kShared>(x, a.tokens) - j0, 0), p.n);
         const bool whole = p.n == tiles;
         p.slot = whole ? -1 : 2 * (int)blockIdx.x + (c.begun ? 1 : 0);
         // The CTA whose range [units i / ctas, units (i + 1) / ctas) holds the segment's last unit.
@@ -317,7 +327,7 @@ constexpr int kThreads = 384;
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 80;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "registers");
 
-template <bool kE4m3>
+template <bool kE4m3, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1)
 kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, int* err) {
@@ -358,7 +368,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     sc.per = (a.io.B + kScan - 1) / kScan;
     long long sum_pairs = 0;
     if (tid < kScan)
-        for (int b = min(a.io.B, tid * sc.per), end = min(a.io.B, b + sc.per); b < end; ++b) sum_pairs += pairs_of(a, b);
+        for (int b = min(a.io.B, tid * sc.per), end = min(a.io.B, b + sc.per); b < end; ++b) sum_pairs += pairs_of<kShared>(a, b);
     const int mine = (int)min(sum_pairs, (long long)(0x7fffffff / kScan));
     const int upto = scan_inclusive(mine, ctl.warp_sum, &sc.total);
     if (sc.total == 0) return;   // every request has few rows
@@ -385,17 +395,17 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         long long sum = 0;
         if (tid < kScan && tid * sc.chunk < n) {
             int s = tid * sc.chunk;
-            Segment g = find_segment(a, ctl, sc, s);
+            Segment g = find_segment<kShared>(a, ctl, sc, s);
             int round = s / (int)gridDim.x, r = s - round * (int)gridDim.x;
             for (const int end = min(n, s + sc.chunk); s < end;) {
-                const int u = g.tiles_all(a.tokens) + a.part_cost;
+                const int u = g.template tiles_all<kShared>(a.tokens) + a.part_cost;
                 sum += u;
                 atomicAdd(&ctl.load[(round & 1) ? gridDim.x - 1 - r : r], u);
                 if (++r == (int)gridDim.x) {
                     r = 0;
                     ++round;
                 }
-                next_segment(a, ctl, sc, ++s, g);
+                next_segment<kShared>(a, ctl, sc, ++s, g);
             }
         }
         const int u = (int)min(sum, (long long)(0x7fffffff / kScan));   // beyond that, shares are not worth cutting for
@@ -425,7 +435,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         const int pg = lane & 15;
         int it = 0, raws = 0;
         for (int np = 0;; ++np) {
-            next_part(a, ctl, sc, cur, p);
+            next_part<kShared>(a, ctl, sc, cur, p);
             if (np >= 2 && !__all_sync(0xffffffffu, pwait(&ctl.partempty[np & 1], (uint32_t)((np >> 1) - 1) & 1u, dead, err)))
                 break;
             if (lane == 0) {
@@ -433,7 +443,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 ptx::mbar_arrive(&ctl.partfull[np & 1]);
             }
             if (p.n == 0) break;
-            const int* table = a.io.block_table + (size_t)p.s.b * a.io.max_pages;
+            const int* table = a.io.block_table + (size_t)(kShared ? a.io.group_row[p.s.b] : p.s.b) * a.io.max_pages;
             auto page_of = [&](int j) {
                 const int key = j * kKeys + pg * rows;
                 return pg < boxes && key < p.s.len ? table[key >> a.page_shift] : 0;
@@ -778,7 +788,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             const int cnt = p.cnt[x];
             if (cnt > 0) {
                 // Keys that the row sees; rows without a token see all (their q is zero, nothing is stored).
-                const int sees = live ? p.s.first + x * a.tokens + i_row : 0x7fffffff;
+                const int sees = kShared ? p.s.len : live ? p.s.first + x * a.tokens + i_row : 0x7fffffff;
                 for (int j = p.j0; j < p.j0 + cnt; ++j) {
                     ok = pwait(&ctl.sfull[x], spar, dead, err);
                     spar ^= 1u;
@@ -887,7 +897,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                         float z = 0.f;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) z = mma::max3n(z, fabsf(__uint_as_float(o[e])), fabsf(__uint_as_float(o[e + 1])));
-                        if (live) spoiled = mma::max3n(spoiled, z, z);
+                        if (!kShared && live) spoiled = mma::max3n(spoiled, z, z);
                         if (plain) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 8)
@@ -940,13 +950,13 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             more = more_n;
         }
         ptx::cp_async_wait_all();   // of a part that was given up
-        if (__any_sync(0xffffffffu, !(spoiled < INFINITY)) && __all_sync(0xffffffffu, *(volatile int*)dead == 0)) {
+        if (!kShared && __any_sync(0xffffffffu, !(spoiled < INFINITY)) && __all_sync(0xffffffffu, *(volatile int*)dead == 0)) {
             // Values that they do not see may have got into this warp's rows (attn_again.cuh): its parts again.
             // (Looking at all results costs calls without such values 0.6 % of an 8191-token prompt's time, 0.8 % of the
             // ragged e4m3 chunks'; in the join kernel instead, what the join then carries cost calls with cut keys 3 %.)
             __syncwarp();
             Cursor cur{sc.split ? -1 : 0, 0, false, {}};
-            for (next_part(a, ctl, sc, cur, p); p.n > 0; next_part(a, ctl, sc, cur, p)) {
+            for (next_part<kShared>(a, ctl, sc, cur, p); p.n > 0; next_part<kShared>(a, ctl, sc, cur, p)) {
                 const int i = x * a.tokens + i_row;
                 const size_t head = ((size_t)p.s.tok + i) * a.Hq + p.s.h * a.G + g_row;
                 float* part = slot_at(a.io.workspace, gridDim.x, max(p.slot, 0));
@@ -1048,13 +1058,13 @@ __global__ void __launch_bounds__(256) kda_attn_prefill_join_kernel(const Prefil
 
 std::atomic<bool> g_attr_done[64];
 
-template <bool kE4m3>
+template <bool kE4m3, bool kShared>
 cudaError_t prepare_kernel() {
     cudaFuncAttributes f{};
-    cudaError_t e = cudaFuncGetAttributes(&f, kda_attn_prefill_kernel<kE4m3>);
+    cudaError_t e = cudaFuncGetAttributes(&f, kda_attn_prefill_kernel<kE4m3, kShared>);
     if (e != cudaSuccess) return e;
     if (f.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;   // the splits would never be met
-    return cudaFuncSetAttribute(kda_attn_prefill_kernel<kE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(kda_attn_prefill_kernel<kE4m3, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem_bytes<kE4m3>());
 }
 
@@ -1071,12 +1081,15 @@ size_t attn_prefill_workspace_bytes(const DeviceInfo& dev) {
     return join_bytes(dev.sm_count) + (size_t)dev.sm_count * 2 * kSlotFloats * sizeof(float);
 }
 
-cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
-                                  int* err_word, cudaStream_t stream, bool all) {
+namespace {
+cudaError_t launch(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev, int* err_word,
+                   cudaStream_t stream, bool all, bool shared) {
     if (dev.device < 0 || dev.device >= 64 || dev.sm_count > kMaxCtas) return cudaErrorInvalidDevice;
     if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
-        cudaError_t e = prepare_kernel<false>();
-        if (e == cudaSuccess) e = prepare_kernel<true>();
+        cudaError_t e = prepare_kernel<false, false>();
+        if (e == cudaSuccess) e = prepare_kernel<true, false>();
+        if (e == cudaSuccess) e = prepare_kernel<false, true>();
+        if (e == cudaSuccess) e = prepare_kernel<true, true>();
         if (e != cudaSuccess) return e;
         g_attr_done[dev.device].store(true, std::memory_order_release);
     }
@@ -1101,8 +1114,9 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = l.e4m3 ? smem_bytes<true>() : smem_bytes<false>();
     cfg.stream = stream;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, l.e4m3 ? kda_attn_prefill_kernel<true> : kda_attn_prefill_kernel<false>,
-                                       a, maps.k_prefill, maps.v_prefill, err_word);
+    auto kernel = shared ? (l.e4m3 ? kda_attn_prefill_kernel<true, true> : kda_attn_prefill_kernel<false, true>)
+                         : (l.e4m3 ? kda_attn_prefill_kernel<true, false> : kda_attn_prefill_kernel<false, false>);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, maps.k_prefill, maps.v_prefill, err_word);
     count_launches(1);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)grid * kJoinCtas);
@@ -1116,6 +1130,18 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
     e = cudaLaunchKernelEx(&cfg, kda_attn_prefill_join_kernel, a, grid);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
+                                  int* err_word, cudaStream_t stream, bool all) {
+    return launch(l, maps, io, dev, err_word, stream, all, false);
+}
+
+cudaError_t launch_attn_many_rows_shared(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io,
+                                         const DeviceInfo& dev, int* err_word, cudaStream_t stream) {
+    return launch(l, maps, io, dev, err_word, stream, false, true);
 }
 
 }  // namespace kda
