@@ -426,7 +426,7 @@ kda_status kda_attn_sync_status(kda_attn_ctx* ctx, void* stream) {
         return kda::cuda_failed("cudaMemcpy(error word)", e);
     if (word == 0) return KDA_OK;
     const bool index = (word & ~kda::kErrAttnIndex) == 0;
-    kda::set_error_text(index ? "kernel error word 0x%x (a page id, slot or request that there is not, row offsets that are not ascending, or holders miscounted)"
+    kda::set_error_text(index ? "kernel error word 0x%x (a page id or slot outside the cache, a request that there is not, row offsets that are not ascending, or holders miscounted)"
                               : "kernel error word 0x%x (bounded wait gave up)", word);
     if ((e = cudaMemset(ctx->err_word, 0, sizeof(int))) != cudaSuccess)
         return kda::cuda_failed("cudaMemset(error word)", e);
