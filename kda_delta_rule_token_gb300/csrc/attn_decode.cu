@@ -124,23 +124,11 @@ __device__ __forceinline__ float* slot_at(void* ws, int ctas, int slot) {
 // that it is worked on with (0 where it has no rows here).
 struct Request {
     int tok0, n, keys, len;
-    const int* table;        // requests that share a prefix only
 };
 
-template <bool kShared>
 __device__ __forceinline__ Request request(const DecodeArgs& a, int b) {
-    if (kShared) {
-        const AttnIO& io = a.io;
-        if (b < io.groups) {
-            const int tok0 = io.cu_new[b], n = io.cu_new[b + 1] - tok0, len = io.group_len[b];
-            return Request{tok0, n, 1, len && attn_few_rows(n, a.G) ? len : 0, io.block_table + (size_t)io.group_row[b] * io.max_pages};
-        }
-        b -= io.groups;
-        const int before = io.prefix[b], keys = attn_kv_len(io, b, a.page_shift) - before;
-        return Request{io.singles + b, 1, keys, keys, io.block_table + (size_t)b * io.max_pages + (before >> a.page_shift)};
-    }
     const int keys = attn_kv_len(a.io, b, a.page_shift);
-    Request r{b, 1, keys, keys, nullptr};
+    Request r{b, 1, keys, keys};
     if (a.io.cu_new) {
         attn_tokens(a.io, b, r.tok0, r.n);
         if (r.n == 0 || !attn_few_rows(r.n, a.G)) r.len = 0;
@@ -165,7 +153,6 @@ struct Walk {
     int b, vh, u;     // request, virtual head, unit of it
     int len, units;   // of request b
     int tok0, n;
-    const int* table; // as Request's
 };
 
 // Units of a request and head, and those with its cost.
@@ -176,7 +163,7 @@ template <int kUnit>
 __device__ __forceinline__ long long cost_of(int len, int part_cost) { return len ? units_of<kUnit>(len) + part_cost : 0; }
 
 // To the next unit (of the next request with any, at the end of one).
-template <int kUnit, int kPartCost, bool kShared>
+template <int kUnit, int kPartCost>
 __device__ __forceinline__ void step(const DecodeArgs& a, Walk& w) {
     --w.left;
     if (++w.u < w.units) return;
@@ -186,26 +173,24 @@ __device__ __forceinline__ void step(const DecodeArgs& a, Walk& w) {
     w.vh = 0;
     if (w.left <= 0) return;
     do {
-        const Request r = request<kShared>(a, ++w.b);
+        const Request r = request(a, ++w.b);
         w.len = r.len;
         w.tok0 = r.tok0;
         w.n = r.n;
-        w.table = r.table;
         w.units = units_of<kUnit>(w.len);
     } while (w.units == 0);
 }
 
 // The walk over a CTA's range of `left` units, from unit `first` of request b's heads on.
-template <int kUnit, int kPartCost, bool kShared>
+template <int kUnit, int kPartCost>
 __device__ __forceinline__ Walk begin_walk(const DecodeArgs& a, long long left, int b, long long first) {
     Walk w;
     w.left = left;
     w.b = b;
-    const Request r = request<kShared>(a, b);
+    const Request r = request(a, b);
     w.len = r.len;
     w.tok0 = r.tok0;
     w.n = r.n;
-    w.table = r.table;
     w.units = units_of<kUnit>(w.len);
     w.vh = (int)(first / (w.units + kPartCost));
     w.u = (int)(first % (w.units + kPartCost)) - kPartCost;
@@ -223,7 +208,7 @@ __device__ __forceinline__ Walk begin_walk(const DecodeArgs& a, long long left, 
 template <bool kE4m3, int kUnit, int kPartCost>
 __device__ __noinline__ void mend_rows(const DecodeArgs& a, long long left, int first_b, long long first_unit) {
     const int warp = threadIdx.x >> 5, row = threadIdx.x & 31;
-    Walk w = begin_walk<kUnit, kPartCost, false>(a, left, first_b, first_unit);
+    Walk w = begin_walk<kUnit, kPartCost>(a, left, first_b, first_unit);
     for (int nth = 0; w.left > 0; ++nth) {
         const int u0 = w.u, u1 = (int)min((long long)w.units, u0 + w.left), h = w.vh;   // n > 1: one pass
         if (w.n > 1 && nth % kWarps == warp) {
@@ -242,11 +227,11 @@ __device__ __noinline__ void mend_rows(const DecodeArgs& a, long long left, int 
         }
         w.left -= u1 - u0 - 1;
         w.u = u1 - 1;
-        step<kUnit, kPartCost, false>(a, w);
+        step<kUnit, kPartCost>(a, w);
     }
 }
 
-template <bool kE4m3, int kRowTiles, bool kShared>
+template <bool kE4m3, int kRowTiles>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<kRowTiles>())
 kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, int* err) {
@@ -286,7 +271,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
     long long mine = 0;
     bool shares = false;   // there is a request whose zero rows all CTAs write
     for (int b = b0; b < b1; ++b) {
-        const Request r = request<kShared>(a, b);
+        const Request r = request(a, b);
         mine += cost_of<kUnit>(r.len, kPartCost);
         shares |= all_zero_it(a, r);
     }
@@ -311,7 +296,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
     if (works && upto - mine <= from && from < upto) {
         long long at = upto - mine;
         for (int b = b0;; ++b) {
-            const long long n = cost_of<kUnit>(request<kShared>(a, b).len, kPartCost) * heads;
+            const long long n = cost_of<kUnit>(request(a, b).len, kPartCost) * heads;
             if (from < at + n) {
                 sm.first_b = b;
                 sm.first_unit = from - at;
@@ -330,18 +315,18 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
             for (long long i = from; i < rows; i += step) a.io.lse[(size_t)r.tok0 * a.Hq + i] = -INFINITY;
     };
     for (int b = blockIdx.x; b < a.io.B; b += gridDim.x)
-        if (kShared ? request<kShared>(a, b).keys == 0 : attn_kv_len(a.io, b, a.page_shift) == 0) {
-            const Request r = request<kShared>(a, b);
+        if (attn_kv_len(a.io, b, a.page_shift) == 0) {
+            const Request r = request(a, b);
             if (!all_zero_it(a, r)) zero_rows(r, tid, kThreads);
         }
     if (shares)
         for (int base = 0; base < a.io.B; base += kThreads) {
-            const uint32_t found = __ballot_sync(0xffffffffu, base + tid < a.io.B && all_zero_it(a, request<kShared>(a, base + tid)));
+            const uint32_t found = __ballot_sync(0xffffffffu, base + tid < a.io.B && all_zero_it(a, request(a, base + tid)));
             if (lane == 0) sm.zeros[warp] = found;
             __syncthreads();
             for (int w = 0; w < kWarps; ++w)
                 for (uint32_t m = sm.zeros[w]; m; m &= m - 1)
-                    zero_rows(request<kShared>(a, base + 32 * w + __ffs((int)m) - 1), (long long)blockIdx.x * kThreads + tid,
+                    zero_rows(request(a, base + 32 * w + __ffs((int)m) - 1), (long long)blockIdx.x * kThreads + tid,
                               (long long)gridDim.x * kThreads);
             __syncthreads();
         }
@@ -351,7 +336,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
         return;
     }
 
-    Walk cur = begin_walk<kUnit, kPartCost, kShared>(a, sm.left, sm.first_b, sm.first_unit);
+    Walk cur = begin_walk<kUnit, kPartCost>(a, sm.left, sm.first_b, sm.first_unit);
 
     // Producer: lane 0 issues the warp's tiles; the page ids of the next tile
     // are loaded one issue ahead of their use.
@@ -360,10 +345,10 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
     Walk ahead = cur;
     int ids[kTile / 16];
     auto fetch_ids = [&]() {   // to the warp's next tile, if there is one
-        while (ahead.left > 0 && (ahead.u * kGroups + group) * kTile >= ahead.len) step<kUnit, kPartCost, kShared>(a, ahead);
+        while (ahead.left > 0 && (ahead.u * kGroups + group) * kTile >= ahead.len) step<kUnit, kPartCost>(a, ahead);
         if (ahead.left <= 0) return;
         const int key = (ahead.u * kGroups + group) * kTile;
-        const int* t = (kShared ? ahead.table : a.io.block_table + (size_t)ahead.b * a.io.max_pages) + (key >> a.page_shift);
+        const int* t = a.io.block_table + (size_t)ahead.b * a.io.max_pages + (key >> a.page_shift);
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i)
             if (i < boxes) ids[i] = key + i * box_rows < ahead.len ? t[i] : ids[0];
@@ -399,7 +384,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
             return;
         }
         ++issued;
-        step<kUnit, kPartCost, kShared>(a, ahead);
+        step<kUnit, kPartCost>(a, ahead);
         fetch_ids();
     };
     if (lead) {
@@ -435,8 +420,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = first + half * 8 + g;
-            const size_t at = head_of(w, x, r) - (kShared && w.b >= a.io.groups ? (size_t)a.io.singles * a.Hq : 0);
-            const uint16_t* q = a.io.q + at * kHeadDim;
+            const uint16_t* q = a.io.q + head_of(w, x, r) * kHeadDim;
             if (!kE4m3) {
 #pragma unroll
                 for (int s = 0; s < 16; ++s)
@@ -475,7 +459,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
             const int r = first_row + half * 8 + g;
             const uint32_t (&w)[16] = raw[half];
             fac[half] = a.scale;
-            sees[half] = !kShared && cur.n > 1 && r < nrows ? cur.len - cur.n + 1 + r / a.G : cur.len;
+            sees[half] = cur.n > 1 && r < nrows ? cur.len - cur.n + 1 + r / a.G : cur.len;
             float up = 1.f;
             if (kE4m3) {
                 float top = 0.f;
@@ -565,7 +549,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
                         }
                     }
                 }
-                if (valid - (kShared ? 0 : cur.n - 1) < kTile) {
+                if (valid - (cur.n - 1) < kTile) {
     #pragma unroll
                     for (int n = 0; n < kNT; ++n)
     #pragma unroll
@@ -684,7 +668,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
         Walk next = cur;
         next.left -= u1 - u0 - 1;
         next.u = u1 - 1;
-        step<kUnit, kPartCost, kShared>(a, next);
+        step<kUnit, kPartCost>(a, next);
         if (kRowTiles == 1 && next.left > 0) load_rows(next);
 
         // The warps' partial results meet.  The buffers of references and
@@ -747,7 +731,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
                 if (w < parts) l += s_sum[w * rows + row] * mma::exp2_approx(s_ref[w * rows + row] - top);
-            if (!kShared && kRowTiles > 1 && cur.n > 1 && !(fabsf(v.x + v.y + v.z + v.w) < INFINITY)) sm.spoiled = 1;
+            if (kRowTiles > 1 && cur.n > 1 && !(fabsf(v.x + v.y + v.z + v.w) < INFINITY)) sm.spoiled = 1;
             if (whole) {
                 const float n = l != 0.f ? vscale / l : 0.f;   // 0: the row sees no key (NaN is not 0: a NaN logit shows)
                 const size_t at = head_of(cur, rw, row);
@@ -776,7 +760,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
         // Give-up path: the copies this warp issued complete (bounded waits) before its shared memory is released.
         for (int i = used; i < issued; ++i) ptx::mbar_wait_timed(&full[i % kDepth], (uint32_t)(i / kDepth) & 1u);
         __syncthreads();
-    } else if (!kShared && kRowTiles > 1) {   // (calls with more than a token to a request)
+    } else if (kRowTiles > 1) {   // (calls with more than a token to a request)
         __syncthreads();
         if (sm.spoiled) mend_rows<kE4m3, kUnit, kPartCost>(a, sm.left, sm.first_b, sm.first_unit);
     }
@@ -868,9 +852,9 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
 
 std::atomic<bool> g_attr_done[64];
 
-template <bool kE4m3, int kRowTiles, bool kShared = false>
+template <bool kE4m3, int kRowTiles>
 cudaError_t set_smem() {
-    return cudaFuncSetAttribute(kda_attn_decode_kernel<kE4m3, kRowTiles, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(kda_attn_decode_kernel<kE4m3, kRowTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)sizeof(Smem<kRowTiles>));
 }
 
@@ -888,17 +872,14 @@ size_t attn_decode_workspace_bytes(const DeviceInfo& dev) {
     return desc_bytes(ctas) + (size_t)ctas * 2 * kSlotFloats * sizeof(float);
 }
 
-namespace {
-cudaError_t launch(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev, int* err_word,
-                   cudaStream_t stream, bool beside, bool shared) {
+cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
+                                 int* err_word, cudaStream_t stream, bool beside) {
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
         cudaError_t e = set_smem<false, 1>();
         if (e == cudaSuccess) e = set_smem<false, 2>();
         if (e == cudaSuccess) e = set_smem<true, 1>();
         if (e == cudaSuccess) e = set_smem<true, 2>();
-        if (e == cudaSuccess) e = set_smem<false, 2, true>();
-        if (e == cudaSuccess) e = set_smem<true, 2, true>();
         if (e != cudaSuccess) return e;
         g_attr_done[dev.device].store(true, std::memory_order_release);
     }
@@ -917,17 +898,15 @@ cudaError_t launch(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, c
     a.k_cache = l.k_cache;
     a.v_cache = l.v_cache;
     // A call with a token per request has G rows at most; else any count up to 32 may occur.
-    const int most_rows = (io.cu_new || shared) && l.G < kMaxRows ? kMaxRows : a.rows;
+    const int most_rows = io.cu_new && l.G < kMaxRows ? kMaxRows : a.rows;
     // Never more CTAs than the longest table allows units.
     const int tile = (most_rows <= 16 ? kWarps : kWarps / 2) * (l.e4m3 ? 32 : 16);
     const long long most = (long long)io.B * l.Hkv * a.passes * ((((long long)io.max_pages << l.page_shift) + tile - 1) / tile);
     const bool two = most_rows > 16;
     const int ctas = dev.sm_count * (two ? ctas_per_sm<2>() : ctas_per_sm<1>());
     const int grid = (int)(most < ctas ? most : ctas);
-    // (Shared: most_rows is above 16 whatever G is.)
-    auto kernel = shared   ? (l.e4m3 ? kda_attn_decode_kernel<true, 2, true> : kda_attn_decode_kernel<false, 2, true>)
-                  : l.e4m3 ? (two ? kda_attn_decode_kernel<true, 2, false> : kda_attn_decode_kernel<true, 1, false>)
-                           : (two ? kda_attn_decode_kernel<false, 2, false> : kda_attn_decode_kernel<false, 1, false>);
+    auto kernel = l.e4m3 ? (two ? kda_attn_decode_kernel<true, 2> : kda_attn_decode_kernel<true, 1>)
+                         : (two ? kda_attn_decode_kernel<false, 2> : kda_attn_decode_kernel<false, 1>);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -957,18 +936,6 @@ cudaError_t launch(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, c
     e = cudaLaunchKernelEx(&cfg, kda_attn_join_kernel, a, grid, search);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
-                                 int* err_word, cudaStream_t stream, bool beside) {
-    return launch(l, maps, io, dev, err_word, stream, beside, false);
-}
-
-cudaError_t launch_attn_few_rows_shared(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io,
-                                        const DeviceInfo& dev, int* err_word, cudaStream_t stream, bool beside) {
-    return launch(l, maps, io, dev, err_word, stream, beside, true);
 }
 
 }  // namespace kda

@@ -114,15 +114,11 @@ struct AttnIO {
     // Test injection (KDA_FAULT_INJECT "attn_drop"): every CTA leaves out
     // its first copy of keys, so that a bounded wait runs out.
     int drop;
-    // Requests that share a prefix (attn_shared.cu): the few-row kernel takes
-    // `groups` prefixes first, as requests of their members' tokens, then what each of
-    // `singles` requests has beyond its own; B is the number of both, cu_new has the
-    // groups' members, and o and lse hold 2 * singles tokens: over the prefixes, then
-    // beyond them.  The many-row kernel takes prefixes alone, B = groups.
-    int groups, singles;
-    const int* prefix;       // [singles] shared keys of a request, whole pages and decode tiles
-    const int* group_len;    // [groups] keys of the group's prefix, 0 if it is not shared
-    const int* group_row;    // [groups] the block table's row that has its pages
+    // Groups of requests that share a prefix (attn_shared.cu; the many-row kernel alone):
+    // B groups, whose members cu_new has, and whose single tokens see all of a prefix.
+    const int* group_len;            // [B] keys of the prefix
+    const int* group_row;            // [B] the block table's row that has its pages
+    const long long* group_start;    // [B + 1] units of work before the group's, none for one that is not its own
 };
 
 struct AttnSharedIO {
@@ -165,11 +161,15 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
 cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, const DeviceInfo& dev,
                                   int* err_word, cudaStream_t stream, bool all);
 
-// The same for requests that share a prefix (AttnIO), and all of kda_attn_decode_shared (attn_shared.cu).
-cudaError_t launch_attn_few_rows_shared(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io,
-                                        const DeviceInfo& dev, int* err_word, cudaStream_t stream, bool beside);
+// The prefixes of kda_attn_decode_shared in the many-row kernel: group g's segments of
+// up to 2 * (128 / G) tokens and a key head, each of ceil(len / 128) + attn_many_rows_cost
+// units, dealt in equal ranges to min(SMs, units) CTAs.  A segment that one CTA has
+// whole goes to o and lse, others' parts to the slots, two of 256 rows per CTA.
+int attn_many_rows_cost(const AttnLayer& l);
+float* attn_many_rows_slots(void* workspace, const DeviceInfo& dev);
 cudaError_t launch_attn_many_rows_shared(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io,
                                          const DeviceInfo& dev, int* err_word, cudaStream_t stream);
+// All of kda_attn_decode_shared (attn_shared.cu).
 size_t attn_shared_workspace_bytes(const AttnLayer& l, int B, const DeviceInfo& dev);
 cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const AttnSharedIO& io, const DeviceInfo& dev,
                                int* err_word, cudaStream_t stream);

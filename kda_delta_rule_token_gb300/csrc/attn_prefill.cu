@@ -97,15 +97,12 @@ struct Segment {
     int len;                 // keys of the request
     __device__ __forceinline__ int tokens_of(int x, int per) const { return x ? max(m - per, 0) : min(m, per); }
     // Key tiles of tile x (one, fully masked, where its rows see no key).
-    template <bool kShared>
     __device__ __forceinline__ int tiles(int x, int per) const {
         const int t = tokens_of(x, per);
         if (t == 0) return 0;
-        if (kShared) return (len + kKeys - 1) / kKeys;
         return max(1, (first + (x ? m : t) - 1 + kKeys - 1) / kKeys);
     }
-    template <bool kShared>
-    __device__ __forceinline__ int tiles_all(int per) const { return max(tiles<kShared>(0, per), tiles<kShared>(1, per)); }
+    __device__ __forceinline__ int tiles_all(int per) const { return max(tiles(0, per), tiles(1, per)); }
 };
 
 // What a CTA does next: key tiles [j0, j0 + n) of a segment, cnt[x] of them for tile x.
@@ -161,6 +158,7 @@ struct Sched {
     int chunk;               // segments of a scan thread
     bool split;
     int units, ctas;         // split: key tiles and costs of all segments, CTAs that share them
+    long long all;           // groups: the same
 };
 
 struct PrefillJoin {
@@ -174,19 +172,14 @@ __device__ __forceinline__ float* slot_at(void* ws, int ctas, int slot) {
     return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + join_bytes(ctas)) + (size_t)slot * kSlotFloats;
 }
 
-// Pairs of token tiles of request b that this file works on.  kShared: b is a group of
-// requests, their single tokens see all of its prefix.
-template <bool kShared>
+// Pairs of token tiles of request b that this file works on.
 __device__ __forceinline__ int pairs_of(const PrefillArgs& a, int b) {
     int tok0, n;
     attn_tokens(a.io, b, tok0, n);
-    if (kShared && (a.io.group_len[b] == 0 || attn_few_rows(n, a.G))) return 0;
-    if (kShared) return (n + 2 * a.tokens - 1) / (2 * a.tokens);
     if (n == 0 || (!a.all && (attn_few_rows(n, a.G) || attn_kv_len(a.io, b, a.page_shift) == 0))) return 0;
     return (n + 2 * a.tokens - 1) / (2 * a.tokens);
 }
 
-template <bool kShared>
 __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, int s) {
     const int pair = (int)((unsigned)s / (unsigned)a.Hkv);
     int lo = 0, hi = kScan - 1;   // the last scan thread with pre <= pair
@@ -195,7 +188,7 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
         if (ctl.pre[mid] <= pair) lo = mid; else hi = mid - 1;
     }
     int at = ctl.pre[lo], b = lo * sc.per, n;
-    while (at + (n = pairs_of<kShared>(a, b)) <= pair && b + 1 < a.io.B) {
+    while (at + (n = pairs_of(a, b)) <= pair && b + 1 < a.io.B) {
         at += n;
         ++b;
     }
@@ -205,7 +198,7 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
     int tok0, tokens;
     attn_tokens(a.io, b, tok0, tokens);
     const int i0 = (n - 1 - (pair - at)) * 2 * a.tokens;   // the longest first
-    g.len = kShared ? a.io.group_len[b] : attn_kv_len(a.io, b, a.page_shift);
+    g.len = attn_kv_len(a.io, b, a.page_shift);
     g.tok = tok0 + i0;
     g.m = min(2 * a.tokens, tokens - i0);
     g.first = g.len - tokens + i0 + 1;
@@ -213,10 +206,9 @@ __device__ __forceinline__ Segment find_segment(const PrefillArgs& a, const Ctl&
 }
 
 // The segment after segment s - 1, which g holds: the next head of its pair, or the next pair.
-template <bool kShared>
 __device__ __forceinline__ void next_segment(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, int s, Segment& g) {
     if (g.h + 1 < a.Hkv) ++g.h;
-    else if (s < sc.segments) g = find_segment<kShared>(a, ctl, sc, s);
+    else if (s < sc.segments) g = find_segment(a, ctl, sc, s);
 }
 
 // Where a CTA is in its work (the copying warp's).
@@ -225,26 +217,64 @@ struct Cursor {
     int at;                  // cut: units before segment k
     bool begun;              // cut: a part was found
     Segment s;               // cut: segment k
+    long long unit;          // groups: units passed (k: the group)
 };
 
 // The next part of this CTA; p.n = 0 past the last.
+// kShared: groups of requests that share a prefix (AttnIO), which all of their tokens see.
 template <bool kShared>
 __device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, const Sched& sc, Cursor& c, Part& p) {
     p.n = 0;
+    if (kShared) {
+        if ((int)blockIdx.x >= sc.ctas) return;
+        const long long from = sc.all * blockIdx.x / sc.ctas, to = sc.all * (blockIdx.x + 1) / sc.ctas;
+        if (c.k < 0) {
+            int lo = 0, hi = a.io.B - 1;   // the last group whose segments begin at or before `from`
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (a.io.group_start[mid] <= from) lo = mid; else hi = mid - 1;
+            }
+            c.k = lo;
+            c.unit = from;
+        }
+        while (c.unit < to) {
+            while (a.io.group_start[c.k + 1] <= c.unit) ++c.k;
+            const int g = c.k, len = a.io.group_len[g], tiles = (len + kKeys - 1) / kKeys, per = tiles + a.part_cost;
+            const int segment = (int)((c.unit - a.io.group_start[g]) / per), pair = segment / a.Hkv;
+            const long long at = a.io.group_start[g] + (long long)segment * per, end = min(at + per, to);
+            const int j0 = max((int)(c.unit - at) - a.part_cost, 0), j1 = (int)(end - at) - a.part_cost;
+            c.unit = end;
+            if (j1 <= j0) continue;
+            const int tok0 = a.io.cu_new[g], n = a.io.cu_new[g + 1] - tok0;
+            p.s.b = a.io.group_row[g];
+            p.s.h = segment - pair * a.Hkv;
+            p.s.tok = tok0 + pair * 2 * a.tokens;
+            p.s.m = min(2 * a.tokens, n - pair * 2 * a.tokens);
+            p.s.first = p.s.len = len;
+            p.j0 = j0;
+            p.n = j1 - j0;
+            for (int x = 0; x < 2; ++x) p.cnt[x] = p.s.tokens_of(x, a.tokens) ? p.n : 0;
+            p.slot = j0 == 0 && j1 == tiles ? -1 : 2 * (int)blockIdx.x + (c.begun ? 1 : 0);
+            p.last = -1;
+            c.begun = true;
+            return;
+        }
+        return;
+    }
     if (!sc.split) {
         for (;; ++c.k) {
             const long long base = (long long)c.k * gridDim.x;
             if (base >= sc.segments) return;
             const int s = (int)(base + ((c.k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
             if (s >= sc.segments) continue;
-            p.s = find_segment<kShared>(a, ctl, sc, s);
+            p.s = find_segment(a, ctl, sc, s);
             break;
         }
         ++c.k;
         p.j0 = 0;
-        p.n = p.s.template tiles_all<kShared>(a.tokens);
-        p.cnt[0] = p.s.template tiles<kShared>(0, a.tokens);
-        p.cnt[1] = p.s.template tiles<kShared>(1, a.tokens);
+        p.n = p.s.tiles_all(a.tokens);
+        p.cnt[0] = p.s.tiles(0, a.tokens);
+        p.cnt[1] = p.s.tiles(1, a.tokens);
         p.slot = p.last = -1;
         return;
     }
@@ -258,20 +288,20 @@ __device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, 
         }
         c.k = lo * sc.chunk;
         c.at = ctl.units[lo];
-        if (c.k < sc.segments) c.s = find_segment<kShared>(a, ctl, sc, c.k);
+        if (c.k < sc.segments) c.s = find_segment(a, ctl, sc, c.k);
     }
     while (c.k < sc.segments && c.at < to) {
         p.s = c.s;
-        const int tiles = p.s.template tiles_all<kShared>(a.tokens), at = c.at;
+        const int tiles = p.s.tiles_all(a.tokens), at = c.at;
         ++c.k;
-        next_segment<kShared>(a, ctl, sc, c.k, c.s);
+        next_segment(a, ctl, sc, c.k, c.s);
         c.at += tiles + a.part_cost;
         // A segment's first part_cost units stand for its cost, the others for its tiles.
         const int j0 = max(from - at - a.part_cost, 0), j1 = min(to - at - a.part_cost, tiles);
         if (j1 <= j0) continue;
         p.j0 = j0;
         p.n = j1 - j0;
-        for (int x = 0; x < 2; ++x) p.cnt[x] = min(max(p.s.template tiles<kShared>(x, a.tokens) - j0, 0), p.n);
+        for (int x = 0; x < 2; ++x) p.cnt[x] = min(max(p.s.tiles(x, a.tokens) - j0, 0), p.n);
         const bool whole = p.n == tiles;
         p.slot = whole ? -1 : 2 * (int)blockIdx.x + (c.begun ? 1 : 0);
         // The CTA whose range [units i / ctas, units (i + 1) / ctas) holds the segment's last unit.
@@ -363,58 +393,69 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         ctl.kissued = ctl.vissued = ctl.raws = 0;
         joins(a.io.workspace)[blockIdx.x].m = 0;
     }
-    // Segments of all requests.
     Sched sc;
-    sc.per = (a.io.B + kScan - 1) / kScan;
-    long long sum_pairs = 0;
-    if (tid < kScan)
-        for (int b = min(a.io.B, tid * sc.per), end = min(a.io.B, b + sc.per); b < end; ++b) sum_pairs += pairs_of<kShared>(a, b);
-    const int mine = (int)min(sum_pairs, (long long)(0x7fffffff / kScan));
-    const int upto = scan_inclusive(mine, ctl.warp_sum, &sc.total);
-    if (sc.total == 0) return;   // every request has few rows
-    if (sc.total > a.io.N) {
-        // More pairs than tokens (or a share of them cut short, which memory has
-        // no room for): the offsets claim rows more than once, and sums of so many
-        // segments need not fit what follows.
-        if (tid == 0 && blockIdx.x == 0) atomicOr(err, kErrAttnIndex);
-        return;
-    }
-    if (warp == kWarpMma) tc::alloc(&ctl.tmem, 512);
-    if (tid < kScan) ctl.pre[tid] = upto - mine;
-    __syncthreads();
-    sc.segments = sc.total * a.Hkv;
-    sc.split = false;
-    sc.units = sc.ctas = sc.chunk = 0;
-    if (sc.segments > 0 && sc.segments <= kMostWeighed * (int)gridDim.x) {
-        // The load of every CTA if whole segments are dealt, against equal
-        // shares of key tiles, which cost up to two more parts per CTA and the join.
-        for (int i = tid; i < kMaxCtas; i += blockDim.x) ctl.load[i] = 0;
-        __syncthreads();
-        const int n = sc.segments;
-        sc.chunk = (sc.total + kScan - 1) / kScan * a.Hkv;   // whole pairs, so that the threads find theirs together
-        long long sum = 0;
-        if (tid < kScan && tid * sc.chunk < n) {
-            int s = tid * sc.chunk;
-            Segment g = find_segment<kShared>(a, ctl, sc, s);
-            int round = s / (int)gridDim.x, r = s - round * (int)gridDim.x;
-            for (const int end = min(n, s + sc.chunk); s < end;) {
-                const int u = g.template tiles_all<kShared>(a.tokens) + a.part_cost;
-                sum += u;
-                atomicAdd(&ctl.load[(round & 1) ? gridDim.x - 1 - r : r], u);
-                if (++r == (int)gridDim.x) {
-                    r = 0;
-                    ++round;
-                }
-                next_segment<kShared>(a, ctl, sc, ++s, g);
-            }
+    if (kShared) {
+        // (Beside the few-row kernel, whose start has waited for the plan.)
+        sc.all = a.io.group_start[a.io.B];
+        sc.ctas = (int)min((long long)gridDim.x, sc.all);
+        if ((int)blockIdx.x >= sc.ctas) {
+            ptx::griddep_wait();   // ends after it
+            return;
         }
-        const int u = (int)min(sum, (long long)(0x7fffffff / kScan));   // beyond that, shares are not worth cutting for
-        const int to = scan_inclusive(u, ctl.warp_sum, &sc.units);
-        if (tid < kScan) ctl.units[tid] = to - u;
-        for (int i = tid; i < (int)gridDim.x; i += blockDim.x) atomicMax(&ctl.busiest, ctl.load[i]);
-        const bool fits = !__syncthreads_or(tid < kScan && (long long)u != sum);
-        sc.ctas = min((int)gridDim.x, sc.units);
-        sc.split = fits && ctl.busiest > (sc.units + sc.ctas - 1) / sc.ctas + 2 * a.part_cost + kJoinCost;
+        if (warp == kWarpMma) tc::alloc(&ctl.tmem, 512);
+    } else {
+        // Segments of all requests.
+        sc.per = (a.io.B + kScan - 1) / kScan;
+        long long sum_pairs = 0;
+        if (tid < kScan)
+            for (int b = min(a.io.B, tid * sc.per), end = min(a.io.B, b + sc.per); b < end; ++b) sum_pairs += pairs_of(a, b);
+        const int mine = (int)min(sum_pairs, (long long)(0x7fffffff / kScan));
+        const int upto = scan_inclusive(mine, ctl.warp_sum, &sc.total);
+        if (sc.total == 0) return;   // every request has few rows
+        if (sc.total > a.io.N) {
+            // More pairs than tokens (or a share of them cut short, which memory has
+            // no room for): the offsets claim rows more than once, and sums of so many
+            // segments need not fit what follows.
+            if (tid == 0 && blockIdx.x == 0) atomicOr(err, kErrAttnIndex);
+            return;
+        }
+        if (warp == kWarpMma) tc::alloc(&ctl.tmem, 512);
+        if (tid < kScan) ctl.pre[tid] = upto - mine;
+        __syncthreads();
+        sc.segments = sc.total * a.Hkv;
+        sc.split = false;
+        sc.units = sc.ctas = sc.chunk = 0;
+        if (sc.segments > 0 && sc.segments <= kMostWeighed * (int)gridDim.x) {
+            // The load of every CTA if whole segments are dealt, against equal
+            // shares of key tiles, which cost up to two more parts per CTA and the join.
+            for (int i = tid; i < kMaxCtas; i += blockDim.x) ctl.load[i] = 0;
+            __syncthreads();
+            const int n = sc.segments;
+            sc.chunk = (sc.total + kScan - 1) / kScan * a.Hkv;   // whole pairs, so that the threads find theirs together
+            long long sum = 0;
+            if (tid < kScan && tid * sc.chunk < n) {
+                int s = tid * sc.chunk;
+                Segment g = find_segment(a, ctl, sc, s);
+                int round = s / (int)gridDim.x, r = s - round * (int)gridDim.x;
+                for (const int end = min(n, s + sc.chunk); s < end;) {
+                    const int u = g.tiles_all(a.tokens) + a.part_cost;
+                    sum += u;
+                    atomicAdd(&ctl.load[(round & 1) ? gridDim.x - 1 - r : r], u);
+                    if (++r == (int)gridDim.x) {
+                        r = 0;
+                        ++round;
+                    }
+                    next_segment(a, ctl, sc, ++s, g);
+                }
+            }
+            const int u = (int)min(sum, (long long)(0x7fffffff / kScan));   // beyond that, shares are not worth cutting for
+            const int to = scan_inclusive(u, ctl.warp_sum, &sc.units);
+            if (tid < kScan) ctl.units[tid] = to - u;
+            for (int i = tid; i < (int)gridDim.x; i += blockDim.x) atomicMax(&ctl.busiest, ctl.load[i]);
+            const bool fits = !__syncthreads_or(tid < kScan && (long long)u != sum);
+            sc.ctas = min((int)gridDim.x, sc.units);
+            sc.split = fits && ctl.busiest > (sc.units + sc.ctas - 1) / sc.ctas + 2 * a.part_cost + kJoinCost;
+        }
     }
     tc::fence_before();
     __syncthreads();
@@ -429,7 +470,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         // ---- copies
         tc::reg_dec<kRegsOther>();
         Part p;
-        Cursor cur{sc.split ? -1 : 0, 0, false, {}};
+        Cursor cur{kShared || sc.split ? -1 : 0, 0, false, {}, 0};
         const int rows = min(1 << a.page_shift, kKeys), boxes = kKeys / rows;   // rows of a box, pages of a tile
         const int is_v = lane >> 4;
         const int pg = lane & 15;
@@ -443,7 +484,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
                 ptx::mbar_arrive(&ctl.partfull[np & 1]);
             }
             if (p.n == 0) break;
-            const int* table = a.io.block_table + (size_t)(kShared ? a.io.group_row[p.s.b] : p.s.b) * a.io.max_pages;
+            const int* table = a.io.block_table + (size_t)p.s.b * a.io.max_pages;
             auto page_of = [&](int j) {
                 const int key = j * kKeys + pg * rows;
                 return pg < boxes && key < p.s.len ? table[key >> a.page_shift] : 0;
@@ -955,7 +996,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
             // (Looking at all results costs calls without such values 0.6 % of an 8191-token prompt's time, 0.8 % of the
             // ragged e4m3 chunks'; in the join kernel instead, what the join then carries cost calls with cut keys 3 %.)
             __syncwarp();
-            Cursor cur{sc.split ? -1 : 0, 0, false, {}};
+            Cursor cur{kShared || sc.split ? -1 : 0, 0, false, {}, 0};
             for (next_part<kShared>(a, ctl, sc, cur, p); p.n > 0; next_part<kShared>(a, ctl, sc, cur, p)) {
                 const int i = x * a.tokens + i_row;
                 const size_t head = ((size_t)p.s.tok + i) * a.Hq + p.s.h * a.G + g_row;
@@ -995,6 +1036,7 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     }
     __syncthreads();
     if (warp == kWarpMma) tc::dealloc(tm, 512);
+    if (kShared) ptx::griddep_wait();
 }
 
 // Joins the parts of segments cut between CTAs, a warp per row, four channels
@@ -1077,6 +1119,12 @@ bool attn_prefill_maps(const AttnLayer& l, AttnMaps& maps) {
     return make_cache_map_atoms(&maps.k_prefill, l, l.k_cache, rows) && make_cache_map_atoms(&maps.v_prefill, l, l.v_cache, rows);
 }
 
+int attn_many_rows_cost(const AttnLayer& l) { return l.e4m3 ? 4 : 3; }
+
+float* attn_many_rows_slots(void* workspace, const DeviceInfo& dev) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + join_bytes(dev.sm_count));
+}
+
 size_t attn_prefill_workspace_bytes(const DeviceInfo& dev) {
     return join_bytes(dev.sm_count) + (size_t)dev.sm_count * 2 * kSlotFloats * sizeof(float);
 }
@@ -1100,7 +1148,7 @@ cudaError_t launch(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, c
     a.G = l.G;
     a.tokens = kRows / l.G;
     a.all = all;
-    a.part_cost = l.e4m3 ? 4 : 3;
+    a.part_cost = attn_many_rows_cost(l);
     a.page_shift = l.page_shift;
     a.num_pages = l.num_pages;
     a.scale = l.softmax_scale * kLog2e;
@@ -1109,6 +1157,11 @@ cudaError_t launch(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, c
     a.k_cache = l.k_cache;
     a.v_cache = l.v_cache;
     cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = shared ? 1 : 0;
     const int grid = dev.sm_count;
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
@@ -1118,14 +1171,10 @@ cudaError_t launch(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io, c
                          : (l.e4m3 ? kda_attn_prefill_kernel<true, false> : kda_attn_prefill_kernel<false, false>);
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, maps.k_prefill, maps.v_prefill, err_word);
     count_launches(1);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || shared) return e;
     cfg.gridDim = dim3((unsigned)grid * kJoinCtas);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kda_attn_prefill_join_kernel, a, grid);
     count_launches(1);

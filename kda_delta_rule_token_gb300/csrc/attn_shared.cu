@@ -5,70 +5,141 @@
 // with o_p and a = lse of the request's row over the prefix, o_r and b over the
 // keys that are its own.  A prefix's keys are read once for all of its
 // requests, whose rows stand beside each other in the products: n requests of G
-// heads per key head are n * G rows.  Up to 32 of them the cache's bytes are what
-// counts, and the few-row kernel (attn_decode.cu) takes the prefixes together
-// with the requests' own keys, as one list of work; more go to the prompts' tensor
-// core kernel (attn_prefill.cu), without a causal edge.  Both leave fp32 results
-// and their lse in the workspace; what joins them reads 1 KiB per row.
+// heads per key head are n * G rows.  Four launches:
 //
-// What the groups look like is worked out by one CTA before (3 us beside which
-// nothing runs): which requests are long enough to take part (those that are not
-// attend to all of their keys by themselves), whose table has the prefix's
-// pages, and how much of the prefix counts: whole pages, and whole tiles of the few-row
-// kernel, so that no tile has keys of both kinds.
+//  * the plan, one CTA: which requests are long enough to take part (the others
+//    attend to all of their keys by themselves), whose table has the prefix's pages, and
+//    how much of the prefix counts: whole pages, and whole tiles of the next kernel, so
+//    that no tile has keys of both kinds.  From these the work's prefix sums, which the
+//    other kernels find their shares and each other's results by.
+//  * kda_attn_shared_few_kernel: the requests' own keys, and prefixes of up to 16 rows
+//    per key head (of up to 32 in calls that can have no more), 16 rows at a time.
+//    Own keys are often few, so a warp works alone: all warps get equal ranges
+//    of tiles, copied by TMA ahead of their use across the ends of requests, and no warp
+//    waits for another.
+//  * the prompts' tensor core kernel (attn_prefill.cu), without a causal edge: prefixes of
+//    more rows, cut into equal ranges of key tiles for all SMs.  Its CTAs start as
+//    the few-row kernel's end.
+//  * the join: a warp per row.  What one warp (or CTA) had of a row alone came to the
+//    workspace as a finished result, what several had as parts; where they are follows
+//    from the prefix sums.
+#include <atomic>
+
 #include "attn_internal.cuh"
 #include "attn_mma.cuh"
-#include "ptx.cuh"
+#include "attn_ptx.cuh"
+#include "attn_rows.cuh"
+#include "attn_tma.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kWarps = 4, kThreads = kWarps * 32, kCtasPerSm = 2;
+constexpr int kStages = 3;                       // tiles that a warp has under way
+constexpr uint32_t kStageBytes = 2 * kRowTileBytes;
+constexpr int kRows = 16;                        // rows of a tile
+constexpr int kCost = 2;                         // tiles that starting and ending a request and head costs beside its own
+constexpr int kSlotFloats = kRows * (kHeadDim + 2);
 
-struct Space {
-    uint8_t* few;       // the kernels' own
-    uint8_t* many;
-    int* prefix;        // [B]
-    int* group_len;     // [B], of which the groups' are used
-    int* group_row;
-    float* o;           // [2 B][Hq][128]
-    float* lse;         // [2 B][Hq]
-    size_t bytes;
+// A request's own keys, or a group's prefix, as the few-row kernel sees it.
+struct __align__(16) Item {
+    long long table;     // place of its first page in the block table
+    int len;             // keys, 0: nothing to do
+    int q, out, n;       // first token of q and of the results, tokens
+    int tiles;           // row tiles per key head
+    int pad;
 };
 
-Space space_of(void* workspace, const AttnLayer& l, int B, const DeviceInfo& dev) {
-    Space s;
+struct Args {
+    AttnSharedIO io;
+    int Hq, Hkv, G;
+    int few_rows;        // rows of a group, at most, that the few-row kernel takes
+    int tile_shift;      // keys of its tiles
+    int page_shift, num_pages;
+    int tokens;          // of a row tile of the tensor core kernel
+    int many_cost;       // key tiles that a segment costs there
+    float scale;         // softmax scale * log2(e)
+    const float* k_scale;
+    const float* v_scale;
+    Item* items;             // [groups + B]
+    long long* start;        // [groups + B + 1] units (tiles, and costs) before each, in the few-row kernel
+    long long* many_start;   // [groups + 1] the same in the tensor core kernel
+    int* group_of;           // [B] the group that a request shares in, or -1
+    int* group_len;          // [groups]
+    int* group_row;          // [groups]
+    float* slots;            // parts of the few-row kernel, two per warp
+    const float* many_slots; // of the tensor core kernel, two per CTA
+    float* o;                // [2 B][Hq][128] results over the prefix, then of own keys
+    float* lse;              // [2 B][Hq]
+    int warps, many_ctas;
+};
+
+size_t carve(Args& a, AttnIO& many, void* workspace, const AttnLayer& l, int B, const DeviceInfo& dev) {
     uint8_t* at = static_cast<uint8_t*>(workspace);
     auto take = [&](size_t bytes) {
         uint8_t* p = at;
         at += (bytes + 255) & ~size_t(255);
         return p;
     };
-    s.few = take(attn_decode_workspace_bytes(dev));
-    s.many = take(attn_prefill_workspace_bytes(dev));
-    s.prefix = reinterpret_cast<int*>(take((size_t)B * 4));
-    s.group_len = reinterpret_cast<int*>(take((size_t)B * 4));
-    s.group_row = reinterpret_cast<int*>(take((size_t)B * 4));
-    s.o = reinterpret_cast<float*>(take((size_t)2 * B * l.Hq * kHeadDim * 4));
-    s.lse = reinterpret_cast<float*>(take((size_t)2 * B * l.Hq * 4));
-    s.bytes = (size_t)(at - static_cast<uint8_t*>(workspace));
-    return s;
+    const size_t warps = (size_t)dev.sm_count * kCtasPerSm * kWarps, n = (size_t)2 * B;   // groups + B at most
+    a.slots = reinterpret_cast<float*>(take(warps * 2 * kSlotFloats * 4));
+    many.workspace = take(attn_prefill_workspace_bytes(dev));
+    a.many_slots = attn_many_rows_slots(many.workspace, dev);
+    a.items = reinterpret_cast<Item*>(take(n * sizeof(Item)));
+    a.start = reinterpret_cast<long long*>(take((n + 1) * 8));
+    a.many_start = reinterpret_cast<long long*>(take((size_t)(B + 1) * 8));
+    a.group_of = reinterpret_cast<int*>(take((size_t)B * 4));
+    a.group_len = reinterpret_cast<int*>(take((size_t)B * 4));
+    a.group_row = reinterpret_cast<int*>(take((size_t)B * 4));
+    a.o = reinterpret_cast<float*>(take(n * l.Hq * kHeadDim * 4));
+    a.lse = reinterpret_cast<float*>(take(n * l.Hq * 4));
+    return (size_t)(at - static_cast<uint8_t*>(workspace));
+}
+
+__device__ __forceinline__ int own_length(const AttnSharedIO& io, int b, int shift) {
+    return min(max(io.kv_lens[b], 0), io.max_pages << shift);
+}
+
+// Exclusive prefix of v over the CTA's threads; *total gets the sum.
+__device__ __forceinline__ long long block_exclusive(long long v, long long* s_warp, long long* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    long long w = s_warp[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, w, d);
+        if (lane >= d) w += y;
+    }
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const long long before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
+    __syncthreads();   // s_warp may be used again
+    return before + x - v;
 }
 
 // Offsets that are not ascending within the requests are an error, and nothing is
 // shared then; the results are the same.
-__global__ void __launch_bounds__(kPlanThreads)
-kda_attn_shared_plan_kernel(const AttnSharedIO io, int* prefix, int* group_len, int* group_row, int shift, int unit, int* err) {
+__global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(const Args a, int* err) {
+    __shared__ long long s_warp[32];
+    ptx::griddep_launch_dependents();
+    const AttnSharedIO& io = a.io;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int unit = max(1 << a.page_shift, 1 << a.tile_shift), most = io.max_pages << a.page_shift;
     bool bad = false;
     for (int g = tid; g < io.groups; g += kPlanThreads) {
         const int from = io.cu_groups[g], to = io.cu_groups[g + 1];
         bad |= from < 0 || to < from || to > io.B;
     }
-    for (int b = tid; b < io.B; b += kPlanThreads) prefix[b] = 0;
+    for (int b = tid; b < io.B; b += kPlanThreads) a.group_of[b] = -1;
     bad = __syncthreads_or(bad);
     if (bad && tid == 0) atomicOr(err, kErrAttnIndex);
-    const int most = io.max_pages << shift;
     for (int g = warp; g < io.groups; g += kPlanThreads / 32) {
         const int from = bad ? 0 : io.cu_groups[g], to = bad ? 0 : io.cu_groups[g + 1];
         const int len = min(max(io.prefix_lens[g], 0), most) / unit * unit;
@@ -81,95 +152,445 @@ kda_attn_shared_plan_kernel(const AttnSharedIO io, int* prefix, int* group_len, 
             }
         const bool share = members > 1;
         if (lane == 0) {
-            group_len[g] = share ? len : 0;
-            group_row[g] = row;
+            a.group_len[g] = share ? len : 0;
+            a.group_row[g] = row;
         }
         if (share)
             for (int b = from + lane; b < to; b += 32)
-                if (min(io.kv_lens[b], most) >= len) prefix[b] = len;
+                if (min(io.kv_lens[b], most) >= len) a.group_of[b] = g;
+    }
+    __syncthreads();
+
+    const int count = io.groups + io.B;
+    const int per = (count + kPlanThreads - 1) / kPlanThreads, i0 = min(count, tid * per), i1 = min(count, i0 + per);
+    auto item_of = [&](int i, long long& many) {
+        Item x;
+        many = 0;
+        x.pad = 0;
+        if (i < io.groups) {
+            x.len = a.group_len[i];
+            x.q = x.out = x.len ? io.cu_groups[i] : 0;
+            x.n = x.len ? io.cu_groups[i + 1] - x.q : 0;
+            x.table = (long long)a.group_row[i] * io.max_pages;
+            if ((long long)x.n * a.G > a.few_rows) {
+                const int pairs = (x.n + 2 * a.tokens - 1) / (2 * a.tokens);
+                many = (long long)pairs * a.Hkv * ((x.len + 127) / 128 + a.many_cost);
+                x.len = 0;
+            }
+            x.tiles = (x.n * a.G + kRows - 1) / kRows;   // of groups with len: at most two
+            return x;
+        }
+        const int b = i - io.groups, g = a.group_of[b], before = g >= 0 ? a.group_len[g] : 0;
+        x.len = own_length(io, b, a.page_shift) - before;
+        x.q = b;
+        x.out = io.B + b;
+        x.n = 1;
+        x.table = (long long)b * io.max_pages + (before >> a.page_shift);
+        x.tiles = (a.G + kRows - 1) / kRows;
+        return x;
+    };
+    auto units_of = [&](const Item& x) {
+        return x.len ? (long long)((x.len + (1 << a.tile_shift) - 1 >> a.tile_shift) + kCost) * a.Hkv * x.tiles : 0LL;
+    };
+    long long few = 0, many = 0, total, many_total;
+    for (int i = i0; i < i1; ++i) {
+        long long m;
+        const Item x = item_of(i, m);
+        few += units_of(x);
+        many += m;
+    }
+    few = block_exclusive(few, s_warp, &total);
+    many = block_exclusive(many, s_warp, &many_total);
+    for (int i = i0; i < i1; ++i) {
+        long long m;
+        const Item x = item_of(i, m);
+        a.items[i] = x;
+        a.start[i] = few;
+        if (i < io.groups) a.many_start[i] = many;
+        few += units_of(x);
+        many += m;
+    }
+    if (tid == 0) {
+        a.start[count] = total;
+        a.many_start[io.groups] = many_total;
     }
 }
 
-// A warp per row, four channels per lane.
-__global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const AttnIO out, const float* o, const float* lse,
-                                                                   const int* prefix, int Hq, long long rows) {
-    ptx::griddep_wait();
+// Whose units these are: the last i < count with start[i] <= unit, of those with any units.  A warp's lanes look together.
+__device__ __forceinline__ int find_item(const long long* start, int count, long long unit) {
     const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    int lo = 0, n = count;   // start[lo] <= unit < start[lo + n]
+    while (n > 1) {
+        const int step = (n + 31) >> 5;
+        const int at = lo + min(lane * step, n);
+        const uint32_t below = __ballot_sync(0xffffffffu, lane * step < n && start[at] <= unit);
+        const int k = 31 - __clz((int)below);
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return lo;
+}
+
+struct Smem {
+    uint8_t ring[kWarps * kStages * kStageBytes];
+    uint64_t full[kWarps * kStages];
+    int dead;
+};
+
+// A place in a warp's range of units.  The range also counts kCost units before each
+// request's (or group's) and row tile's first.
+struct Walk {
+    long long left;      // units of the range not yet passed, this one included; none if <= 0
+    int i, vh, u;        // item, (key head, row tile) of it, tile of keys
+    int units;           // tiles of keys of item i
+    Item x;
+};
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+kda_attn_shared_few_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap vmap, int* err) {
+    using Tile = RowTile<kE4m3>;
+    constexpr int kKeys = Tile::kKeys;
+    extern __shared__ __align__(1024) uint8_t sm_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(sm_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
+    uint64_t* full = sm.full + warp * kStages;
+    uint8_t* ring = sm.ring + warp * kStages * kStageBytes;
+    if (lane == 0)
+        for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 1);
+    if (tid == 0) sm.dead = 0;
+    ptx::fence_mbar_init();
+    __syncthreads();
+    ptx::griddep_wait();               // the plan; the launch behind this one needs it too
+    ptx::griddep_launch_dependents();
+
+    const int count = a.io.groups + a.io.B;
+    const long long total = a.start[count];
+    const long long warps = min((long long)a.warps, total);
+    const int w = blockIdx.x * kWarps + warp;
+    if (w >= warps) return;
+    const long long from = total * w / warps, to = total * (w + 1) / warps;
+
+    auto enter = [&](Walk& k, int i) {
+        k.i = i;
+        k.x = a.items[i];
+        k.units = (k.x.len + kKeys - 1) / kKeys;
+    };
+    auto step = [&](Walk& k) {
+        --k.left;
+        if (++k.u < k.units) return;
+        k.u = 0;
+        k.left -= kCost;
+        if (++k.vh < a.Hkv * k.x.tiles) return;
+        k.vh = 0;
+        if (k.left <= 0) return;
+        do enter(k, k.i + 1);
+        while (k.units == 0);
+    };
+    Walk cur;
+    {
+        int i = find_item(a.start, count, from);
+        enter(cur, i);
+        const long long in = from - a.start[i];
+        const int per = cur.units + kCost;
+        cur.vh = (int)(in / per);
+        cur.u = (int)(in - (long long)cur.vh * per) - kCost;
+        cur.left = to - from;
+        if (cur.u < 0) {
+            cur.left += cur.u;
+            cur.u = 0;
+        }
+    }
+
+    // Copies: lane 0 issues the warp's tiles; the page ids of the next tile are loaded one issue ahead.
+    const int boxes = max(1, kKeys >> a.page_shift), box_rows = kKeys / boxes;
+    const int page_mask = (1 << a.page_shift) - 1;
+    Walk ahead = cur;
+    int ids[kKeys / 16];
+    auto fetch_ids = [&]() {
+        if (ahead.left <= 0) return;
+        const int key = ahead.u * kKeys;
+        const int* t = a.io.block_table + ahead.x.table + (key >> a.page_shift);
+#pragma unroll
+        for (int i = 0; i < kKeys / 16; ++i)
+            if (i < boxes) ids[i] = key + i * box_rows < ahead.x.len ? t[i] : ids[0];
+    };
+    int issued = 0;
+    auto issue = [&]() {
+        if (ahead.left <= 0) return;
+        const int s = issued % kStages;
+        if (lane == 0 && !(a.io.drop && warp == 0 && issued == 0)) {
+            uint8_t* st = ring + s * kStageBytes;
+            const int row = ahead.u * kKeys & page_mask, h = ahead.vh / ahead.x.tiles;
+            ptx::mbar_arrive_expect_tx(&full[s], kStageBytes);
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i)
+                if (i < boxes) {
+                    const bool in = ids[i] >= 0 && ids[i] < a.num_pages;
+                    if (!in) atomicOr(err, kErrAttnIndex);
+                    // A page outside the cache: a box outside the tensor, which reads as zeros.
+                    const int ph = (in ? ids[i] : a.num_pages) * a.Hkv + (in ? h : 0);
+                    const uint32_t off = i * (kRowTileBytes / boxes);
+                    ptx::tma_load_4d(st + off, &kmap, 0, row, 0, ph, &full[s]);
+                    ptx::tma_load_4d(st + kRowTileBytes + off, &vmap, 0, row, 0, ph, &full[s]);
+                }
+        }
+        __syncwarp();
+        ++issued;
+        step(ahead);
+        fetch_ids();
+    };
+    fetch_ids();
+    for (int s = 0; s < kStages; ++s) issue();
+
+    // Row r of a row tile: query head R % G of token R / G, R = 16 * tile + r.
+    uint32_t raw[2][16];
+    auto load_rows = [&](const Walk& k) {
+        const int h = k.vh / k.x.tiles, row0 = k.vh % k.x.tiles * kRows, rows = k.x.n * a.G;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int R = row0 + half * 8 + g, token = k.x.n > 1 ? R / a.G : 0;
+            Tile::load(a.io.q + (((size_t)k.x.q + token) * a.Hq + h * a.G + R - token * a.G) * kHeadDim, R < rows, raw[half]);
+        }
+    };
+    int used = 0;
+    bool ok = true, first = true;
+    if (cur.left > 0) load_rows(cur);
+    while (cur.left > 0) {
+        const int h = cur.vh / cur.x.tiles, row0 = cur.vh % cur.x.tiles * kRows, rows = cur.x.n * a.G;
+        const int u0 = cur.u, u1 = (int)min((long long)cur.units, u0 + cur.left);
+        Tile t;
+        t.begin(raw, a.scale, kE4m3 ? a.k_scale[h] : 1.f);
+        for (int u = u0; u < u1; ++u) {
+            const int s = used % kStages;
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait_timed(&full[s], (uint32_t)(used / kStages) & 1u, &sm.dead));
+            if (!ok) break;
+            ++used;
+            t.add(ring + s * kStageBytes, cur.x.len - u * kKeys);
+            __syncwarp();   // every lane has read the stage: it may be filled again
+            issue();
+        }
+        if (!ok) {
+            sm.dead = 1;
+            atomicOr(err, ptx::kErrAttnWait);
+            break;
+        }
+        Walk next = cur;
+        next.left -= u1 - u0 - 1;
+        next.u = u1 - 1;
+        step(next);
+        if (next.left > 0) load_rows(next);
+        t.finish();
+        // Alone with the rows: their results.  Else a part of them.
+        const bool whole = u0 == 0 && u1 == cur.units;
+        float* part = a.slots + (size_t)(2 * w + (first ? 0 : 1)) * kSlotFloats;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = half * 8 + g, R = row0 + r, token = cur.x.n > 1 ? R / a.G : 0;
+            if (R >= rows) continue;
+            const float l = t.sum[half];
+            if (whole) {
+                const size_t at = ((size_t)cur.x.out + token) * a.Hq + h * a.G + R - token * a.G;
+                t.store(half, l != 0.f ? (kE4m3 ? a.v_scale[h] : 1.f) / l : 0.f, a.o + at * kHeadDim);
+                if ((lane & 3) == 0) a.lse[at] = l != 0.f ? (t.ref[half] + log2f(l)) / kLog2e : -INFINITY;
+            } else {
+                t.store(half, 1.f, part + r * kHeadDim);
+                if ((lane & 3) == 0) *reinterpret_cast<float2*>(part + kRows * kHeadDim + 2 * r) = make_float2(t.ref[half], l);
+            }
+        }
+        cur = next;
+        first = false;
+    }
+    // Gave up: the copies that this warp issued complete (bounded waits) before its shared memory is released.
+    if (!ok)
+        for (int i = used; i < issued; ++i) ptx::mbar_wait_timed(&full[i % kStages], (uint32_t)(i / kStages) & 1u);
+}
+
+// Where a row's result over some keys is: finished at `whole`, or in `parts` parts.
+struct Source {
+    int parts;               // 0: no keys; 1: finished
+    const float* part0;      // the first part's 128 sums, and its reference and sum
+    const float* ref0;
+    const float* part1;      // the second's, and the distance to the next
+    const float* ref1;
+    size_t pitch;
+};
+
+// Equal ranges of `total` units for n workers: whose unit u is, and whether the worker
+// was at work on something else before unit `from`.
+__device__ __forceinline__ int worker_of(long long u, long long total, long long n) { return (int)(((u + 1) * n - 1) / total); }
+__device__ __forceinline__ Source cut_source(long long start, int cost, int units, long long total, long long n, const float* slots,
+                                             size_t slot_floats, size_t refs, int row) {
+    Source s;
+    const int w0 = worker_of(start + cost, total, n), w1 = worker_of(start + cost + units - 1, total, n);
+    s.parts = w1 - w0 + 1;
+    const int slot = 2 * w0 + (total * w0 / n < start ? 1 : 0);
+    s.part0 = slots + (size_t)slot * slot_floats + (size_t)row * kHeadDim;
+    s.ref0 = slots + (size_t)slot * slot_floats + refs + 2 * row;
+    s.part1 = slots + (size_t)2 * (w0 + 1) * slot_floats + (size_t)row * kHeadDim;
+    s.ref1 = slots + (size_t)2 * (w0 + 1) * slot_floats + refs + 2 * row;
+    s.pitch = 2 * slot_floats;
+    return s;
+}
+
+// A warp per row, four channels per lane.
+__global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_constant__ Args a, const AttnIO out) {
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31, B = a.io.B, groups = a.io.groups;
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5), rows = (long long)B * a.Hq;
     if (row >= rows) return;
-    const bool shares = prefix[row / Hq] > 0;
-    const float a = shares ? lse[row] : -INFINITY, b = lse[rows + row];
-    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 x = shares ? *reinterpret_cast<const float4*>(o + row * kHeadDim + 4 * lane) : none;
-    const float4 y = *reinterpret_cast<const float4*>(o + (rows + row) * kHeadDim + 4 * lane);
-    // NaN where either is; -infinity where no key is seen: weights of 0.
-    const float top = a != a || b != b ? a + b : fmaxf(a, b);
-    const float u = top == -INFINITY ? 0.f : mma::exp2_approx((a - top) * kLog2e);
-    const float v = top == -INFINITY ? 0.f : mma::exp2_approx((b - top) * kLog2e);
-    const float sum = u + v, n = sum != 0.f ? 1.f / sum : 0.f;
-    mma::store4(out, row * kHeadDim + 4 * lane,
-                make_float4((x.x * u + y.x * v) * n, (x.y * u + y.y * v) * n, (x.z * u + y.z * v) * n, (x.w * u + y.w * v) * n),
-                sum != 0.f);
-    if (out.lse && lane == 0) out.lse[row] = sum != 0.f ? top + logf(sum) : -INFINITY;
+    const int b = (int)(row / a.Hq), hq = (int)(row - (long long)b * a.Hq), h = hq / a.G, head = hq - h * a.G;
+    const long long total = a.start[groups + B], warps = min((long long)a.warps, total);
+    // Rows R of item i's in the few-row kernel.
+    auto few = [&](int i, const Item& x, int R) {
+        Source s{};
+        if (x.len == 0) return s;
+        const int units = (x.len + (1 << a.tile_shift) - 1) >> a.tile_shift;
+        return cut_source(a.start[i] + (long long)(h * x.tiles + R / kRows) * (units + kCost), kCost, units, total, warps, a.slots, kSlotFloats,
+                          kRows * kHeadDim, R % kRows);
+    };
+    float ref = kNoRef, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float r, float l, const float4& v, float f) {
+        if (l == 0.f) return;   // sees no key there (NaN is not 0: it goes in)
+        const float to = fmaxf(ref, r), e = mma::exp2_approx(ref - to), d = mma::exp2_approx(r - to);
+        ref = to;
+        sum = sum * e + l * d;
+        const float df = d * f;
+        acc.x = acc.x * e + v.x * df;
+        acc.y = acc.y * e + v.y * df;
+        acc.z = acc.z * e + v.z * df;
+        acc.w = acc.w * e + v.w * df;
+    };
+    const float vs = a.v_scale ? a.v_scale[h] : 1.f;
+    auto add_source = [&](const Source& s, long long at) {
+        if (s.parts == 1) {   // finished: its lse, and a sum of 1
+            const float l = a.lse[at];
+            add(l * kLog2e, l == -INFINITY ? 0.f : l == l ? 1.f : l, *reinterpret_cast<const float4*>(a.o + at * kHeadDim + 4 * lane), 1.f);
+            return;
+        }
+#pragma unroll 8
+        for (int p = 0; p < s.parts; ++p) {
+            const float2 rl = *reinterpret_cast<const float2*>(p ? s.ref1 + (p - 1) * s.pitch : s.ref0);
+            const float4 v = *reinterpret_cast<const float4*>((p ? s.part1 + (p - 1) * s.pitch : s.part0) + 4 * lane);
+            add(rl.x, rl.y, v, vs);
+        }
+    };
+    const Item own = a.items[groups + b];
+    const int g = a.group_of[b];
+    Source prefix{};
+    if (g >= 0) {
+        const Item x = a.items[g];
+        const int i = b - a.io.cu_groups[g];
+        if (x.len) {
+            prefix = few(g, x, i * a.G + head);
+        } else {   // the tensor core kernel's: token tiles in pairs
+            const int pair = i / (2 * a.tokens), in = i - pair * 2 * a.tokens, side = in >= a.tokens;
+            const int units = (a.group_len[g] + 127) / 128;
+            const long long all = a.many_start[groups];
+            prefix = cut_source(a.many_start[g] + (long long)(pair * a.Hkv + h) * (units + a.many_cost), a.many_cost, units, all,
+                                min((long long)a.many_ctas, all), a.many_slots, 2 * 128 * (kHeadDim + 2), 2 * 128 * kHeadDim,
+                                side * 128 + (in - side * a.tokens) * a.G + head);
+        }
+    }
+    add_source(prefix, row);
+    add_source(few(groups + b, own, head), rows + row);
+    const float n = sum != 0.f ? 1.f / sum : 0.f;
+    mma::store4(out, row * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n), sum != 0.f);
+    if (out.lse && lane == 0) out.lse[row] = sum != 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
+}
+
+std::atomic<bool> g_attr_done[64];
+
+// A launch that may start beside the one before it in the stream.
+cudaLaunchConfig_t beside(cudaLaunchAttribute& attr, unsigned grid, int threads, size_t smem, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cfg;
 }
 
 }  // namespace
 
 size_t attn_shared_workspace_bytes(const AttnLayer& l, int B, const DeviceInfo& dev) {
-    return space_of(nullptr, l, B, dev).bytes;
+    Args a{};
+    AttnIO many{};
+    return carve(a, many, nullptr, l, B, dev);
 }
 
 cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const AttnSharedIO& io, const DeviceInfo& dev,
                                int* err_word, cudaStream_t stream) {
-    const Space s = space_of(io.workspace, l, io.B, dev);
-    const int tile = l.e4m3 ? 32 : 16;
-    kda_attn_shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(io, s.prefix, s.group_len, s.group_row, l.page_shift,
-                                                                 l.page_size > tile ? l.page_size : tile, err_word);
-    count_launches(1);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    AttnIO a{};
-    a.N = io.B;
-    a.cu_new = io.cu_groups;
-    a.q = io.q;
-    a.block_table = io.block_table;
-    a.max_pages = io.max_pages;
-    a.kv_lens = io.kv_lens;
-    a.o = s.o;
-    a.o_f32 = 1;
-    a.lse = s.lse;
-    a.drop = io.drop;
-    a.groups = io.groups;
-    a.singles = io.B;
-    a.prefix = s.prefix;
-    a.group_len = s.group_len;
-    a.group_row = s.group_row;
-    const bool many = io.groups && !attn_few_rows(io.B, l.G);   // else no group has more
-    if (many) {
-        a.B = io.groups;
-        a.workspace = s.many;
-        if ((e = launch_attn_many_rows_shared(l, maps, a, dev, err_word, stream)) != cudaSuccess) return e;
+    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+    cudaError_t e;
+    if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kda_attn_shared_few_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kda_attn_shared_few_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+        if (e != cudaSuccess) return e;
+        g_attr_done[dev.device].store(true, std::memory_order_release);
     }
-    a.B = io.groups + io.B;
-    a.workspace = s.few;
-    if ((e = launch_attn_few_rows_shared(l, maps, a, dev, err_word, stream, many)) != cudaSuccess) return e;
+    Args a{};
+    AttnIO many{};
+    carve(a, many, io.workspace, l, io.B, dev);
+    a.io = io;
+    a.Hq = l.Hq;
+    a.Hkv = l.Hkv;
+    a.G = l.G;
+    // Groups of more than 16 rows go to the tensor core kernel.  A call that can have none of more than 32
+    // leaves that kernel out, whose launch and set-up cost small calls more than their keys' second reading.
+    const bool has_many = io.groups && (long long)io.B * l.G > 2 * kRows;
+    a.few_rows = has_many ? kRows : 2 * kRows;
+    a.tile_shift = l.e4m3 ? 5 : 4;
+    a.page_shift = l.page_shift;
+    a.num_pages = l.num_pages;
+    a.tokens = 128 / l.G;
+    a.many_cost = attn_many_rows_cost(l);
+    a.scale = l.softmax_scale * kLog2e;
+    a.k_scale = l.k_scale;
+    a.v_scale = l.v_scale;
+    a.many_ctas = dev.sm_count;
+    const int grid = dev.sm_count * kCtasPerSm;
+    a.warps = grid * kWarps;
+    kda_attn_shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, err_word);
+    count_launches(1);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = beside(attr, (unsigned)grid, kThreads, sizeof(Smem), stream);
+    e = cudaLaunchKernelEx(&cfg, l.e4m3 ? kda_attn_shared_few_kernel<true> : kda_attn_shared_few_kernel<false>, a, maps.k_decode,
+                           maps.v_decode, err_word);
+    count_launches(1);
+    if (e != cudaSuccess) return e;
+    if (has_many) {
+        many.B = io.groups;
+        many.N = io.B;
+        many.cu_new = io.cu_groups;
+        many.q = io.q;
+        many.block_table = io.block_table;
+        many.max_pages = io.max_pages;
+        many.o = a.o;
+        many.o_f32 = 1;
+        many.lse = a.lse;
+        many.drop = io.drop;
+        many.group_len = a.group_len;
+        many.group_row = a.group_row;
+        many.group_start = a.many_start;
+        if ((e = launch_attn_many_rows_shared(l, maps, many, dev, err_word, stream)) != cudaSuccess) return e;
+    }
     AttnIO out{};
     out.o = io.o;
     out.o_f32 = io.o_f32;
     out.lse = io.lse;
     out.gate = io.gate;
     const long long rows = (long long)io.B * l.Hq;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kda_attn_shared_join_kernel, out, (const float*)s.o, (const float*)s.lse, (const int*)s.prefix,
-                           l.Hq, rows);
+    cfg = beside(attr, (unsigned)((rows + 7) / 8), 256, 0, stream);
+    e = cudaLaunchKernelEx(&cfg, kda_attn_shared_join_kernel, a, out);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
