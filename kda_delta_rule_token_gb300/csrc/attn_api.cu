@@ -351,7 +351,7 @@ kda_status kda_attn_decode(kda_attn_ctx* ctx, int B, const uint16_t* q, const in
     if (!ctx || B < 0) return KDA_ERR_INVALID_ARG;
     if (B == 0) return KDA_OK;
     const kda::AttnIO io{B, B, nullptr, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace,
-                         (ctx->inject & kda::kInjectDrop) ? 1 : 0, nullptr, nullptr, nullptr};
+                         (ctx->inject & kda::kInjectDrop) ? 1 : 0, nullptr, nullptr, nullptr, nullptr, nullptr};
     if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes, kda::workspace_bytes_of(ctx)); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectDecode, "attn_decode launch", [&] {
         return kda::launch_attn_few_rows(ctx->layer, ctx->maps, io, ctx->dev, ctx->err_word,
@@ -369,6 +369,7 @@ kda_status kda_attn_decode_shared(kda_attn_ctx* ctx, int B, const uint16_t* q, c
                                   void* workspace, size_t workspace_bytes, void* stream) {
     if (!ctx || B < 0 || groups < 0) return KDA_ERR_INVALID_ARG;
     if (B == 0) return KDA_OK;
+    if ((long long)B * ctx->layer.Hq > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
     if (groups > B || (groups && (!cu_groups || !prefix_lens))) {
         kda::set_error_text("%d groups of %d requests, or no offsets and lengths of theirs", groups, B);
         return KDA_ERR_INVALID_ARG;
@@ -401,7 +402,7 @@ kda_status kda_attn_prefill(kda_attn_ctx* ctx, int B, int N, const int32_t* cu_n
     if (B == 0 || N == 0) return KDA_OK;
     if (!cu_new) return KDA_ERR_INVALID_ARG;
     const kda::AttnIO io{B, N, cu_new, q, block_table, max_pages, kv_lens, gate_logit, o, o_f32 != 0, lse, workspace,
-                         (ctx->inject & kda::kInjectDrop) ? 1 : 0, nullptr, nullptr, nullptr};
+                         (ctx->inject & kda::kInjectDrop) ? 1 : 0, nullptr, nullptr, nullptr, nullptr, nullptr};
     if (const kda_status s = kda::check_attend(ctx, io, workspace_bytes, kda::workspace_bytes_of(ctx)); s != KDA_OK) return s;
     return kda::launched(ctx, kda::kInjectPrefill, "attn_prefill launch", [&] {
         const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -119,6 +119,8 @@ struct AttnIO {
     const int* group_len;            // [B] keys of the prefix
     const int* group_row;            // [B] the block table's row that has its pages
     const long long* group_start;    // [B + 1] units of work before the group's, none for one that is not its own
+    const int* group_pairs;          // [B] pairs of token tiles before the group's
+    int2* parts;                     // [pairs][Hkv] (out) first part's slot, -1 if there is but one, and last part's
 };
 
 struct AttnSharedIO {
@@ -164,7 +166,8 @@ cudaError_t launch_attn_many_rows(const AttnLayer& l, const AttnMaps& maps, cons
 // The prefixes of kda_attn_decode_shared in the many-row kernel: group g's segments of
 // up to 2 * (128 / G) tokens and a key head, each of ceil(len / 128) + attn_many_rows_cost
 // units, dealt in equal ranges to min(SMs, units) CTAs.  A segment that one CTA has
-// whole goes to o and lse, others' parts to the slots, two of 256 rows per CTA.
+// whole goes to o and lse, others' parts to the slots, two of 256 rows per CTA: the
+// first part's, then the first slot of each CTA behind it.
 int attn_many_rows_cost(const AttnLayer& l);
 float* attn_many_rows_slots(void* workspace, const DeviceInfo& dev);
 cudaError_t launch_attn_many_rows_shared(const AttnLayer& l, const AttnMaps& maps, const AttnIO& io,

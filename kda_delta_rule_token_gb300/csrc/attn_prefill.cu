@@ -256,6 +256,12 @@ __device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, 
             for (int x = 0; x < 2; ++x) p.cnt[x] = p.s.tokens_of(x, a.tokens) ? p.n : 0;
             p.slot = j0 == 0 && j1 == tiles ? -1 : 2 * (int)blockIdx.x + (c.begun ? 1 : 0);
             p.last = -1;
+            if ((threadIdx.x & 31) == 0) {   // (the copying warp calls this)
+                int2* note = a.io.parts + (size_t)a.io.group_pairs[g] * a.Hkv + segment;
+                const int slot = 2 * (int)blockIdx.x + (c.begun ? 1 : 0);
+                if (j0 == 0) note->x = p.slot;
+                if (j1 == tiles) note->y = slot;
+            }
             c.begun = true;
             return;
         }

@@ -11,7 +11,7 @@
 //    attend to all of their keys by themselves), whose table has the prefix's pages, and
 //    how much of the prefix counts: whole pages, and whole tiles of the next kernel, so
 //    that no tile has keys of both kinds.  From these the work's prefix sums, which the
-//    other kernels find their shares and each other's results by.
+//    other kernels find their shares by.
 //  * kda_attn_shared_few_kernel: the requests' own keys, and prefixes of up to 16 rows
 //    per key head (of up to 32 in calls that can have no more), 16 rows at a time.
 //    Own keys are often few, so a warp works alone: all warps get equal ranges
@@ -20,9 +20,9 @@
 //  * the prompts' tensor core kernel (attn_prefill.cu), without a causal edge: prefixes of
 //    more rows, cut into equal ranges of key tiles for all SMs.  Its CTAs start as
 //    the few-row kernel's end.
-//  * the join: a warp per row.  What one warp (or CTA) had of a row alone came to the
-//    workspace as a finished result, what several had as parts; where they are follows
-//    from the prefix sums.
+//  * the join: a warp per row, or a CTA where rows are few.  What one warp (or CTA) had
+//    of a row alone came to the workspace as a finished result, what several had as parts;
+//    who had the first and the last one noted it.
 #include <atomic>
 
 #include "attn_internal.cuh"
@@ -34,7 +34,7 @@
 namespace kda {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kNear = 2048;
 constexpr int kWarps = 4, kThreads = kWarps * 32, kCtasPerSm = 2;
 constexpr int kStages = 3;                       // tiles that a warp has under way
 constexpr uint32_t kStageBytes = 2 * kRowTileBytes;
@@ -65,6 +65,9 @@ struct Args {
     Item* items;             // [groups + B]
     long long* start;        // [groups + B + 1] units (tiles, and costs) before each, in the few-row kernel
     long long* many_start;   // [groups + 1] the same in the tensor core kernel
+    int* many_pairs;         // [groups] pairs of its token tiles before each
+    int2* few_parts;         // first part's slot (-1: finished) and last part's, of an item, key head and row tile
+    int2* many_parts;        // [pairs][Hkv] the same of the tensor core kernel
     int* group_of;           // [B] the group that a request shares in, or -1
     int* group_len;          // [groups]
     int* group_row;          // [groups]
@@ -72,7 +75,7 @@ struct Args {
     const float* many_slots; // of the tensor core kernel, two per CTA
     float* o;                // [2 B][Hq][128] results over the prefix, then of own keys
     float* lse;              // [2 B][Hq]
-    int warps, many_ctas;
+    int warps;
 };
 
 size_t carve(Args& a, AttnIO& many, void* workspace, const AttnLayer& l, int B, const DeviceInfo& dev) {
@@ -89,6 +92,9 @@ size_t carve(Args& a, AttnIO& many, void* workspace, const AttnLayer& l, int B, 
     a.items = reinterpret_cast<Item*>(take(n * sizeof(Item)));
     a.start = reinterpret_cast<long long*>(take((n + 1) * 8));
     a.many_start = reinterpret_cast<long long*>(take((size_t)(B + 1) * 8));
+    a.many_pairs = reinterpret_cast<int*>(take((size_t)B * 4));
+    a.few_parts = reinterpret_cast<int2*>(take((size_t)B * l.Hkv * (2 + (l.G + kRows - 1) / kRows) * 8));
+    a.many_parts = reinterpret_cast<int2*>(take((size_t)B * l.Hkv * 8));
     a.group_of = reinterpret_cast<int*>(take((size_t)B * 4));
     a.group_len = reinterpret_cast<int*>(take((size_t)B * 4));
     a.group_row = reinterpret_cast<int*>(take((size_t)B * 4));
@@ -128,92 +134,119 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long* s_w
 // shared then; the results are the same.
 __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(const Args a, int* err) {
     __shared__ long long s_warp[32];
+    __shared__ int s_group[kNear], s_len[kNear];   // group_of and group_len, where they fit
     ptx::griddep_launch_dependents();
     const AttnSharedIO& io = a.io;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int unit = max(1 << a.page_shift, 1 << a.tile_shift), most = io.max_pages << a.page_shift;
+    const int shift = max(a.page_shift, a.tile_shift), most = io.max_pages << a.page_shift;
+    int* group_of = io.B <= kNear ? s_group : a.group_of;
+    int* group_len = io.B <= kNear ? s_len : a.group_len;   // (no more groups than requests)
+    const int count = io.groups + io.B;
+    const int per = (count + kPlanThreads - 1) / kPlanThreads, i0 = min(count, tid * per), i1 = min(count, i0 + per);
     bool bad = false;
     for (int g = tid; g < io.groups; g += kPlanThreads) {
         const int from = io.cu_groups[g], to = io.cu_groups[g + 1];
         bad |= from < 0 || to < from || to > io.B;
     }
-    for (int b = tid; b < io.B; b += kPlanThreads) a.group_of[b] = -1;
+    for (int b = tid; b < io.B; b += kPlanThreads) group_of[b] = -1;
     bad = __syncthreads_or(bad);
     if (bad && tid == 0) atomicOr(err, kErrAttnIndex);
     for (int g = warp; g < io.groups; g += kPlanThreads / 32) {
         const int from = bad ? 0 : io.cu_groups[g], to = bad ? 0 : io.cu_groups[g + 1];
-        const int len = min(max(io.prefix_lens[g], 0), most) / unit * unit;
+        const int len = min(max(io.prefix_lens[g], 0), most) >> shift << shift;
         int members = 0, row = 0;
+        uint32_t first32 = 0;   // who of the first 32 has so many keys
         if (len)
             for (int b = from; b < to; b += 32) {
                 const uint32_t has = __ballot_sync(0xffffffffu, b + lane < to && min(io.kv_lens[b + lane], most) >= len);
                 if (members == 0 && has) row = b + __ffs((int)has) - 1;
+                if (b == from) first32 = has;
                 members += __popc(has);
             }
         const bool share = members > 1;
         if (lane == 0) {
-            a.group_len[g] = share ? len : 0;
+            group_len[g] = a.group_len[g] = share ? len : 0;
             a.group_row[g] = row;
         }
-        if (share)
-            for (int b = from + lane; b < to; b += 32)
-                if (min(io.kv_lens[b], most) >= len) a.group_of[b] = g;
+        if (share) {
+            if (first32 >> lane & 1) group_of[from + lane] = g;
+            for (int b = from + 32 + lane; b < to; b += 32)
+                if (min(io.kv_lens[b], most) >= len) group_of[b] = g;
+        }
     }
     __syncthreads();
 
-    const int count = io.groups + io.B;
-    const int per = (count + kPlanThreads - 1) / kPlanThreads, i0 = min(count, tid * per), i1 = min(count, i0 + per);
-    auto item_of = [&](int i, long long& many) {
+    struct Cost {
+        long long few, many;
+        int pairs;
+    };
+    auto item_of = [&](int i, Cost& cost) {
         Item x;
-        many = 0;
+        cost.many = 0;
+        cost.pairs = 0;
         x.pad = 0;
         if (i < io.groups) {
-            x.len = a.group_len[i];
+            x.len = group_len[i];
             x.q = x.out = x.len ? io.cu_groups[i] : 0;
             x.n = x.len ? io.cu_groups[i + 1] - x.q : 0;
             x.table = (long long)a.group_row[i] * io.max_pages;
             if ((long long)x.n * a.G > a.few_rows) {
-                const int pairs = (x.n + 2 * a.tokens - 1) / (2 * a.tokens);
-                many = (long long)pairs * a.Hkv * ((x.len + 127) / 128 + a.many_cost);
+                cost.pairs = (x.n + 2 * a.tokens - 1) / (2 * a.tokens);
+                cost.many = (long long)cost.pairs * a.Hkv * ((x.len + 127) / 128 + a.many_cost);
                 x.len = 0;
             }
             x.tiles = (x.n * a.G + kRows - 1) / kRows;   // of groups with len: at most two
-            return x;
+        } else {
+            const int b = i - io.groups, g = group_of[b], before = g >= 0 ? group_len[g] : 0;
+            a.group_of[b] = g;
+            x.len = own_length(io, b, a.page_shift) - before;
+            x.q = b;
+            x.out = io.B + b;
+            x.n = 1;
+            x.table = (long long)b * io.max_pages + (before >> a.page_shift);
+            x.tiles = (a.G + kRows - 1) / kRows;
         }
-        const int b = i - io.groups, g = a.group_of[b], before = g >= 0 ? a.group_len[g] : 0;
-        x.len = own_length(io, b, a.page_shift) - before;
-        x.q = b;
-        x.out = io.B + b;
-        x.n = 1;
-        x.table = (long long)b * io.max_pages + (before >> a.page_shift);
-        x.tiles = (a.G + kRows - 1) / kRows;
+        cost.few = x.len ? (long long)(((x.len + (1 << a.tile_shift) - 1) >> a.tile_shift) + kCost) * a.Hkv * x.tiles : 0;
         return x;
     };
-    auto units_of = [&](const Item& x) {
-        return x.len ? (long long)((x.len + (1 << a.tile_shift) - 1 >> a.tile_shift) + kCost) * a.Hkv * x.tiles : 0LL;
-    };
-    long long few = 0, many = 0, total, many_total;
+    Cost mine{0, 0, 0}, c{};
+    Item x{};
     for (int i = i0; i < i1; ++i) {
-        long long m;
-        const Item x = item_of(i, m);
-        few += units_of(x);
-        many += m;
+        x = item_of(i, c);
+        mine.few += c.few;
+        mine.many += c.many;
+        mine.pairs += c.pairs;
     }
-    few = block_exclusive(few, s_warp, &total);
-    many = block_exclusive(many, s_warp, &many_total);
+    long long total, many_total, pairs_total;
+    long long few = block_exclusive(mine.few, s_warp, &total);
+    long long many = 0, pairs = 0;
+    many_total = 0;
+    if (__syncthreads_or(mine.many != 0)) {
+        many = block_exclusive(mine.many, s_warp, &many_total);
+        pairs = block_exclusive(mine.pairs, s_warp, &pairs_total);
+    }
     for (int i = i0; i < i1; ++i) {
-        long long m;
-        const Item x = item_of(i, m);
+        if (per > 1) x = item_of(i, c);
         a.items[i] = x;
         a.start[i] = few;
-        if (i < io.groups) a.many_start[i] = many;
-        few += units_of(x);
-        many += m;
+        if (i < io.groups) {
+            a.many_start[i] = many;
+            a.many_pairs[i] = (int)pairs;
+        }
+        few += c.few;
+        many += c.many;
+        pairs += c.pairs;
     }
     if (tid == 0) {
         a.start[count] = total;
         a.many_start[io.groups] = many_total;
     }
+}
+
+// Where the notes on an item's parts begin.
+__device__ __forceinline__ int2* parts_of(const Args& a, int i) {
+    const size_t own = (size_t)(a.G + kRows - 1) / kRows * a.Hkv;
+    return a.few_parts + (i < a.io.groups ? (size_t)i * 2 * a.Hkv : (size_t)a.io.groups * 2 * a.Hkv + (i - a.io.groups) * own);
 }
 
 // Whose units these are: the last i < count with start[i] <= unit, of those with any units.  A warp's lanes look together.
@@ -384,7 +417,13 @@ kda_attn_shared_few_kernel(const __grid_constant__ Args a, const __grid_constant
         t.finish();
         // Alone with the rows: their results.  Else a part of them.
         const bool whole = u0 == 0 && u1 == cur.units;
-        float* part = a.slots + (size_t)(2 * w + (first ? 0 : 1)) * kSlotFloats;
+        const int slot = 2 * w + (first ? 0 : 1);
+        float* part = a.slots + (size_t)slot * kSlotFloats;
+        if (lane == 0) {
+            int2* note = parts_of(a, cur.i) + cur.vh;
+            if (u0 == 0) note->x = whole ? -1 : slot;
+            if (u1 == cur.units) note->y = slot;
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int r = half * 8 + g, R = row0 + r, token = cur.x.n > 1 ? R / a.G : 0;
@@ -407,49 +446,20 @@ kda_attn_shared_few_kernel(const __grid_constant__ Args a, const __grid_constant
         for (int i = used; i < issued; ++i) ptx::mbar_wait_timed(&full[i % kStages], (uint32_t)(i / kStages) & 1u);
 }
 
-// Where a row's result over some keys is: finished at `whole`, or in `parts` parts.
-struct Source {
-    int parts;               // 0: no keys; 1: finished
-    const float* part0;      // the first part's 128 sums, and its reference and sum
-    const float* ref0;
-    const float* part1;      // the second's, and the distance to the next
-    const float* ref1;
-    size_t pitch;
-};
+// Rows of the join that get a CTA each, whose warps share the parts.
+constexpr int kWideRows = 4096;
 
-// Equal ranges of `total` units for n workers: whose unit u is, and whether the worker
-// was at work on something else before unit `from`.
-__device__ __forceinline__ int worker_of(long long u, long long total, long long n) { return (int)(((u + 1) * n - 1) / total); }
-__device__ __forceinline__ Source cut_source(long long start, int cost, int units, long long total, long long n, const float* slots,
-                                             size_t slot_floats, size_t refs, int row) {
-    Source s;
-    const int w0 = worker_of(start + cost, total, n), w1 = worker_of(start + cost + units - 1, total, n);
-    s.parts = w1 - w0 + 1;
-    const int slot = 2 * w0 + (total * w0 / n < start ? 1 : 0);
-    s.part0 = slots + (size_t)slot * slot_floats + (size_t)row * kHeadDim;
-    s.ref0 = slots + (size_t)slot * slot_floats + refs + 2 * row;
-    s.part1 = slots + (size_t)2 * (w0 + 1) * slot_floats + (size_t)row * kHeadDim;
-    s.ref1 = slots + (size_t)2 * (w0 + 1) * slot_floats + refs + 2 * row;
-    s.pitch = 2 * slot_floats;
-    return s;
-}
-
-// A warp per row, four channels per lane.
+// kWide: a CTA per row, its eight warps taking parts in turn; else a warp per row.  Four
+// channels per lane.
+template <bool kWide>
 __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_constant__ Args a, const AttnIO out) {
+    __shared__ float4 s_acc[8][32];
+    __shared__ float s_ref[8], s_sum[8];
     ptx::griddep_wait();
-    const int lane = threadIdx.x & 31, B = a.io.B, groups = a.io.groups;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5), rows = (long long)B * a.Hq;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = a.io.groups;
+    const uint32_t rows = (uint32_t)a.io.B * a.Hq, row = kWide ? blockIdx.x : blockIdx.x * 8 + warp;
     if (row >= rows) return;
-    const int b = (int)(row / a.Hq), hq = (int)(row - (long long)b * a.Hq), h = hq / a.G, head = hq - h * a.G;
-    const long long total = a.start[groups + B], warps = min((long long)a.warps, total);
-    // Rows R of item i's in the few-row kernel.
-    auto few = [&](int i, const Item& x, int R) {
-        Source s{};
-        if (x.len == 0) return s;
-        const int units = (x.len + (1 << a.tile_shift) - 1) >> a.tile_shift;
-        return cut_source(a.start[i] + (long long)(h * x.tiles + R / kRows) * (units + kCost), kCost, units, total, warps, a.slots, kSlotFloats,
-                          kRows * kHeadDim, R % kRows);
-    };
+    const int b = (int)(row / (uint32_t)a.Hq), hq = (int)(row - (uint32_t)b * a.Hq), h = hq / a.G, head = hq - h * a.G;
     float ref = kNoRef, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float r, float l, const float4& v, float f) {
@@ -464,40 +474,54 @@ __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_
         acc.w = acc.w * e + v.w * df;
     };
     const float vs = a.v_scale ? a.v_scale[h] : 1.f;
-    auto add_source = [&](const Source& s, long long at) {
-        if (s.parts == 1) {   // finished: its lse, and a sum of 1
-            const float l = a.lse[at];
-            add(l * kLog2e, l == -INFINITY ? 0.f : l == l ? 1.f : l, *reinterpret_cast<const float4*>(a.o + at * kHeadDim + 4 * lane), 1.f);
+    int nth = 0;   // parts so far: kWide, part p is warp p % 8's
+    // Parts from the noted slots, two slots to a worker: the first part's, then the first slot of each worker
+    // behind it up to the last one's.
+    auto add_parts = [&](int2 note, const float* slots, size_t slot_floats, size_t refs, int r, uint32_t at) {
+        if (note.x < 0) {   // finished: its lse, and a sum of 1
+            if (!kWide || (nth++ & 7) == warp) {
+                const float l = a.lse[at];
+                add(l * kLog2e, l == -INFINITY ? 0.f : l == l ? 1.f : l, *reinterpret_cast<const float4*>(a.o + (size_t)at * kHeadDim + 4 * lane), 1.f);
+            }
             return;
         }
-#pragma unroll 8
-        for (int p = 0; p < s.parts; ++p) {
-            const float2 rl = *reinterpret_cast<const float2*>(p ? s.ref1 + (p - 1) * s.pitch : s.ref0);
-            const float4 v = *reinterpret_cast<const float4*>((p ? s.part1 + (p - 1) * s.pitch : s.part0) + 4 * lane);
-            add(rl.x, rl.y, v, vs);
+        const int parts = (note.y >> 1) - (note.x >> 1) + 1;
+#pragma unroll 4
+        for (int p = kWide ? (warp - nth) & 7 : 0; p < parts; p += kWide ? 8 : 1) {
+            const float* s = slots + (size_t)(p ? (note.x & ~1) + 2 * p : note.x) * slot_floats;
+            const float2 rl = *reinterpret_cast<const float2*>(s + refs + 2 * r);
+            add(rl.x, rl.y, *reinterpret_cast<const float4*>(s + (size_t)r * kHeadDim + 4 * lane), vs);
         }
+        nth += parts;
     };
-    const Item own = a.items[groups + b];
-    const int g = a.group_of[b];
-    Source prefix{};
+    const int g = a.group_of[b], own = a.items[groups + b].len;
     if (g >= 0) {
-        const Item x = a.items[g];
-        const int i = b - a.io.cu_groups[g];
-        if (x.len) {
-            prefix = few(g, x, i * a.G + head);
+        const int len = a.items[g].len, i = b - a.io.cu_groups[g];
+        if (len) {
+            const int R = i * a.G + head;
+            add_parts(parts_of(a, g)[h * a.items[g].tiles + R / kRows], a.slots, kSlotFloats, kRows * kHeadDim, R % kRows, row);
         } else {   // the tensor core kernel's: token tiles in pairs
             const int pair = i / (2 * a.tokens), in = i - pair * 2 * a.tokens, side = in >= a.tokens;
-            const int units = (a.group_len[g] + 127) / 128;
-            const long long all = a.many_start[groups];
-            prefix = cut_source(a.many_start[g] + (long long)(pair * a.Hkv + h) * (units + a.many_cost), a.many_cost, units, all,
-                                min((long long)a.many_ctas, all), a.many_slots, 2 * 128 * (kHeadDim + 2), 2 * 128 * kHeadDim,
-                                side * 128 + (in - side * a.tokens) * a.G + head);
+            add_parts(a.many_parts[(size_t)(a.many_pairs[g] + pair) * a.Hkv + h], a.many_slots, 2 * 128 * (kHeadDim + 2), 2 * 128 * kHeadDim,
+                      side * 128 + (in - side * a.tokens) * a.G + head, row);
         }
     }
-    add_source(prefix, row);
-    add_source(few(groups + b, own, head), rows + row);
+    if (own)
+        add_parts(parts_of(a, groups + b)[h * ((a.G + kRows - 1) / kRows) + head / kRows], a.slots, kSlotFloats, kRows * kHeadDim, head % kRows,
+                  rows + row);
+    if (kWide) {
+        s_acc[warp][lane] = acc;
+        if (lane == 0) {
+            s_ref[warp] = ref;
+            s_sum[warp] = sum;
+        }
+        __syncthreads();
+        if (warp) return;
+#pragma unroll
+        for (int w = 1; w < 8; ++w) add(s_ref[w], s_sum[w], s_acc[w][lane], 1.f);
+    }
     const float n = sum != 0.f ? 1.f / sum : 0.f;
-    mma::store4(out, row * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n), sum != 0.f);
+    mma::store4(out, (size_t)row * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n), sum != 0.f);
     if (out.lse && lane == 0) out.lse[row] = sum != 0.f ? (ref + log2f(sum)) / kLog2e : -INFINITY;
 }
 
@@ -555,7 +579,6 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     a.scale = l.softmax_scale * kLog2e;
     a.k_scale = l.k_scale;
     a.v_scale = l.v_scale;
-    a.many_ctas = dev.sm_count;
     const int grid = dev.sm_count * kCtasPerSm;
     a.warps = grid * kWarps;
     kda_attn_shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, err_word);
@@ -581,6 +604,8 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
         many.group_len = a.group_len;
         many.group_row = a.group_row;
         many.group_start = a.many_start;
+        many.group_pairs = a.many_pairs;
+        many.parts = a.many_parts;
         if ((e = launch_attn_many_rows_shared(l, maps, many, dev, err_word, stream)) != cudaSuccess) return e;
     }
     AttnIO out{};
@@ -589,8 +614,9 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     out.lse = io.lse;
     out.gate = io.gate;
     const long long rows = (long long)io.B * l.Hq;
-    cfg = beside(attr, (unsigned)((rows + 7) / 8), 256, 0, stream);
-    e = cudaLaunchKernelEx(&cfg, kda_attn_shared_join_kernel, a, out);
+    const bool wide = rows <= kWideRows;
+    cfg = beside(attr, (unsigned)(wide ? rows : (rows + 7) / 8), 256, 0, stream);
+    e = cudaLaunchKernelEx(&cfg, wide ? kda_attn_shared_join_kernel<true> : kda_attn_shared_join_kernel<false>, a, out);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
