@@ -451,7 +451,7 @@ def kda_attn_fork(attn, B, rows, kv_lens, block_table, page_refs, free_pages, fr
     """Requests take over one another's pages (kda_attn.h).  Both tables have rows of the same pitch."""
     cap = free_pages.numel() if free_capacity is None else int(free_capacity)
     pitch = _pitch(block_table, max_pages)
-    if max_pages is None and _pitch(new_table, None) != pitch:
+    if max_pages is None and new_table.stride() != block_table.stride() and _pitch(new_table, None) != pitch:
         raise ValueError(f"rows of block_table are {pitch} apart, those of new_table {_pitch(new_table, None)}")
     _check(load().kda_attn_fork(attn, B, _words(rows, "rows", B), _words(kv_lens, "kv_lens", B), _p(block_table), pitch,
                                 _words(page_refs, "page_refs", 0), _words(free_pages, "free_pages", cap), cap,
@@ -473,9 +473,11 @@ def kda_attn_sync_status(attn, stream=None) -> int:
 
 def _words(t, name, count, size=4):
     """The address of a dense tensor of at least `count` elements of `size` bytes."""
-    if t is not None and not isinstance(t, int) and (t.element_size() != size or t.numel() < count):
-        raise ValueError(f"{name} must have {count} elements of {size} bytes: shape {tuple(t.shape)}, {t.dtype}")
-    return _dense(t, name)
+    if t is None or t.__class__ is int:
+        return t
+    if t.numel() >= count and t.element_size() == size and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must have {count} dense elements of {size} bytes: shape {tuple(t.shape)}, strides {t.stride()}, {t.dtype}")
 
 
 def kda_beam_select_workspace_bytes(ctx, groups, beams, vocab, num) -> int:

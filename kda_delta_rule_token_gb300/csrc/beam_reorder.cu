@@ -11,7 +11,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kLoads = 4;
+constexpr int kLoads = 16;
 constexpr int kCopy = kThreads * kLoads * 16;
 
 __global__ void __launch_bounds__(kThreads) kda_beam_reorder_kernel(const BeamReorderIO io, int chunks0, int* err) {
