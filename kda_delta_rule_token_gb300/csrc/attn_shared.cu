@@ -73,6 +73,7 @@ struct Args {
     int* group_row;          // [groups]
     float* slots;            // parts of the few-row kernel, two per warp
     const float* many_slots; // of the tensor core kernel, two per CTA
+    void* decode;            // of kda_attn_decode's kernels
     float* o;                // [2 B][Hq][128] results over the prefix, then of own keys
     float* lse;              // [2 B][Hq]
     int warps;
@@ -86,6 +87,7 @@ size_t carve(Args& a, AttnIO& many, void* workspace, const AttnLayer& l, int B, 
         return p;
     };
     const size_t warps = (size_t)dev.sm_count * kCtasPerSm * kWarps, n = (size_t)2 * B;   // groups + B at most
+    a.decode = take(attn_decode_workspace_bytes(dev));
     a.slots = reinterpret_cast<float*>(take(warps * 2 * kSlotFloats * 4));
     many.workspace = take(attn_prefill_workspace_bytes(dev));
     a.many_slots = attn_many_rows_slots(many.workspace, dev);
@@ -241,6 +243,17 @@ __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(cons
         a.start[count] = total;
         a.many_start[io.groups] = many_total;
     }
+}
+
+// The check of the offsets alone.
+__global__ void __launch_bounds__(256) kda_attn_shared_check_kernel(const AttnSharedIO io, int* err) {
+    ptx::griddep_launch_dependents();
+    bool bad = false;
+    for (int g = threadIdx.x; g < io.groups; g += 256) {
+        const int from = io.cu_groups[g], to = io.cu_groups[g + 1];
+        bad |= from < 0 || to < from || to > io.B;
+    }
+    if (bad) atomicOr(err, kErrAttnIndex);
 }
 
 // Where the notes on an item's parts begin.
@@ -563,6 +576,30 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     Args a{};
     AttnIO many{};
     carve(a, many, io.workspace, l, io.B, dev);
+    // A block table too narrow for so many bytes of keys and values, were all of its pages full and nothing
+    // shared: kda_attn_decode's kernels, whose two launches take less than four do (four requests of 600
+    // tokens, 32 / 8 heads, 9.7 MB at most: 10.5 us and 13.5; 24 MB are 3.5 us of the copy rate).
+    constexpr long long kSmall = 24LL << 20;
+    if (!io.groups || ((long long)io.B * l.Hkv * io.max_pages << l.page_shift) * kHeadDim * (l.e4m3 ? 2 : 4) <= kSmall) {
+        if (io.groups) {
+            kda_attn_shared_check_kernel<<<1, 256, 0, stream>>>(io, err_word);
+            count_launches(1);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
+        AttnIO d{};
+        d.B = d.N = io.B;
+        d.q = io.q;
+        d.block_table = io.block_table;
+        d.max_pages = io.max_pages;
+        d.kv_lens = io.kv_lens;
+        d.gate = io.gate;
+        d.o = io.o;
+        d.o_f32 = io.o_f32;
+        d.lse = io.lse;
+        d.workspace = a.decode;
+        d.drop = io.drop;
+        return launch_attn_few_rows(l, maps, d, dev, err_word, stream, io.groups > 0);
+    }
     a.io = io;
     a.Hq = l.Hq;
     a.Hkv = l.Hkv;

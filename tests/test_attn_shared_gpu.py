@@ -71,7 +71,12 @@ def verify(layer, q, lens, status=kda.KDA_OK, **more):
     check(lse.masked_fill(none, 0), wl.masked_fill(none, 0), (2 * lb + weights).masked_fill(none, 1), "lse")
 
 
-def build(groups, own, hq, hkv, page, e4m3, seed=0, ragged=True):
+def wide(layer, B):
+    """Columns of a block table that is too wide for the call to pass over its groups."""
+    return (30 << 20) // (B * layer.hkv * layer.page * D * (2 if layer.e4m3 else 4)) + 1
+
+
+def build(groups, own, hq, hkv, page, e4m3, seed=0, ragged=True, narrow=False):
     """groups: (requests, prefix); lens = prefix + own, different from request to request."""
     lens, spans, at = [], [], 0
     for i, (n, prefix) in enumerate(groups):
@@ -79,9 +84,14 @@ def build(groups, own, hq, hkv, page, e4m3, seed=0, ragged=True):
         spans.append((at, at + n, prefix))
         at += n
     layer = Layer(hq, hkv, page, e4m3, seed=seed)
-    layer.fill(lens)
+    fill(layer, lens, narrow=narrow)
     share(layer, spans, lens)
     return layer, lens
+
+
+def fill(layer, lens, narrow=False, **more):
+    least = max(1, -(-max(lens) // layer.page))
+    layer.fill(lens, width=least if narrow else max(least, wide(layer, len(lens))), **more)
 
 
 HEADS = [(1, 1, 16, False), (8, 2, 16, False), (32, 8, 64, False), (5, 1, 32, False), (16, 1, 128, False), (40, 1, 16, False),
@@ -108,6 +118,18 @@ def test_groups(groups, hq, hkv, page, e4m3):
     layer.done()
 
 
+@pytest.mark.parametrize("groups", GROUPS[1:], ids=lambda g: "_".join(f"{n}x{p}" for n, p in g))
+@pytest.mark.parametrize("hq,hkv,page,e4m3", [(8, 2, 16, False), (8, 2, 32, True)])
+def test_narrow_tables(groups, hq, hkv, page, e4m3):
+    """Calls that are small enough to pass over their groups."""
+    layer, lens = build(groups, 1, hq, hkv, page, e4m3, narrow=True)
+    verify(layer, queries(layer, len(lens)), lens)
+    layer.groups = [(0, 2, 5), (1 << 20, 1, 5)]
+    o, _ = attend(layer, queries(layer, len(lens)), lens)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_ERR_INVALID_ARG
+    layer.done()
+
+
 @pytest.mark.parametrize("hq,hkv,page,e4m3", [(8, 2, 16, False), (16, 1, 64, False), (8, 2, 32, True), (64, 4, 16, True)])
 @pytest.mark.parametrize("n,prefix", [(2, 30000), (9, 20011), (40, 9000)])
 def test_long_prefixes(n, prefix, hq, hkv, page, e4m3):
@@ -125,7 +147,7 @@ def test_requests_without_keys_and_short_ones(n, hq, hkv, page, e4m3):
     lens[0], lens[1], lens[2] = 0, prefix - 1, prefix
     lens[n], lens[n + 1], lens[n + 3] = 17, prefix, 1
     layer = Layer(hq, hkv, page, e4m3)
-    layer.fill(lens)
+    fill(layer, lens)
     share(layer, [(0, n, prefix), (n, 2 * n, prefix)], lens)
     verify(layer, queries(layer, 2 * n), lens)
     layer.done()
@@ -137,7 +159,7 @@ def test_groups_of_one_long_request(n):
     prefix = 512
     lens = [prefix - 1] * n + [prefix + 9] + [0] * (n - 1)
     layer = Layer(8, 2, 16)
-    layer.fill(lens)
+    fill(layer, lens)
     share(layer, [(0, n, prefix), (n, 2 * n, prefix)], lens)
     verify(layer, queries(layer, 2 * n), lens)
     verify(layer, queries(layer, 2 * n), [0] * (2 * n))
@@ -192,7 +214,7 @@ def test_gate(n, f32, e4m3):
 def test_value_ranges(n, sigma, qs):
     lens = [640 + 5 * b for b in range(n)]
     layer = Layer(8, 2, 16)
-    layer.fill(lens, sigma=sigma)
+    fill(layer, lens, sigma=sigma)
     share(layer, [(0, n, 600)], lens)
     verify(layer, queries(layer, n, qs), lens)
     layer.done()
@@ -205,7 +227,7 @@ def test_nan_and_infinity(n, e4m3):
     page, prefix = 32, 256
     lens = [prefix + 20 + b for b in range(n)] + [200, 300]
     layer = Layer(8, 2, page, e4m3)
-    layer.fill(lens)
+    fill(layer, lens)
     share(layer, [(0, n + 2, prefix)], lens)
     q = queries(layer, n + 2)
     clean, _ = attend(layer, q, lens)
@@ -261,7 +283,7 @@ def test_large_batches_against_decode(cuts, prefix, hq, hkv, e4m3):
     for a, b, p in spans:
         lens += [p + 5 + 3 * (r % 50) for r in range(a, b)]
     layer = Layer(hq, hkv, 32, e4m3)
-    layer.fill(lens)
+    fill(layer, lens)
     share(layer, spans, lens)
     q = queries(layer, 256)
     o, lse = attend(layer, q, lens, f32=True)
