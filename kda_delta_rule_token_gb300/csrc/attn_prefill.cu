@@ -57,6 +57,10 @@
 // each CTA takes an equal range of (segment, key tile) units and leaves partial
 // results, joined in a fixed order by a dependent launch (128 tokens behind
 // 32640 cached ones, 16 segments: 70 us).
+//
+// kShared: prefixes that groups of requests share (attn_shared.cu), whose single
+// tokens all see all of it.  Segments are always cut into equal ranges then, found from
+// the plan's sums without a schedule of its own, and the join is not this file's.
 #include <atomic>
 #include <type_traits>
 

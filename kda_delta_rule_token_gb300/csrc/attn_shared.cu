@@ -12,8 +12,8 @@
 //    how much of the prefix counts: whole pages, and whole tiles of the next kernel, so
 //    that no tile has keys of both kinds.  From these the work's prefix sums, which the
 //    other kernels find their shares by.
-//  * kda_attn_shared_few_kernel: the requests' own keys, and prefixes of up to 16 rows
-//    per key head (of up to 32 in calls that can have no more), 16 rows at a time.
+//  * kda_attn_shared_few_kernel: the requests' own keys, and prefixes of few rows per
+//    key head (16 in bf16; 32 in e4m3, and in calls that can have no more), 16 at a time.
 //    Own keys are often few, so a warp works alone: all warps get equal ranges
 //    of tiles, copied by TMA ahead of their use across the ends of requests, and no warp
 //    waits for another.
@@ -23,6 +23,16 @@
 //  * the join: a warp per row, or a CTA where rows are few.  What one warp (or CTA) had
 //    of a row alone came to the workspace as a finished result, what several had as parts;
 //    who had the first and the last one noted it.
+//
+// Measured: 32 prompts of up to 4,100 tokens with 1 to 30 requests each, 32 / 8 heads,
+// bf16, 534 MB: 124 us, 0.64 of the copy rate (the two kernels 50 us each, at
+// 5.7 and 5 TB/s; plan and join 4 and 8).  64 requests behind 8,192 tokens, 65 MB: 39 us (4, 9,
+// 14 and 6 us and the launches' gaps; kda_attn_decode: 178 us); of the tensor core kernel's 14 us its
+// 3 or 4 key tiles are 4, the parts' way out 4.  256 requests of 64 heads behind four
+// documents of up to 16,300 tokens in e4m3, 128 GFLOP: 133 us, of which the tensor core
+// kernel 90.  The requests' own keys in the decode's kernel, where four warps share a
+// request's tiles and meet at its end: 36 us of that instead of 21.  Queries and
+// requests brought near ahead of their use: no faster.
 #include <atomic>
 
 #include "attn_internal.cuh"
@@ -40,6 +50,7 @@ constexpr int kStages = 3;                       // tiles that a warp has under 
 constexpr uint32_t kStageBytes = 2 * kRowTileBytes;
 constexpr int kRows = 16;                        // rows of a tile
 constexpr int kCost = 2;                         // tiles that starting and ending a request and head costs beside its own
+                                                 // (1, 4 and 6: within 1 %)
 constexpr int kSlotFloats = kRows * (kHeadDim + 2);
 
 // A request's own keys, or a group's prefix, as the few-row kernel sees it.
@@ -604,10 +615,14 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     a.Hq = l.Hq;
     a.Hkv = l.Hkv;
     a.G = l.G;
-    // Groups of more than 16 rows go to the tensor core kernel.  A call that can have none of more than 32
-    // leaves that kernel out, whose launch and set-up cost small calls more than their keys' second reading.
+    // Groups of more rows than this go to the tensor core kernel.  17 to 32 rows are two row tiles in the few-row
+    // kernel, which reads the keys for each: in e4m3, where the tensor core kernel converts them, still the
+    // faster way (32 prompts of 4000 tokens with 8 requests, 4 heads on one: 105 us and 123; 16 of 8000 with two, 16
+    // on one: 62 and 69), in bf16 not (132 and 143, the other way round; 74 and 103).  A call that can have none
+    // of more than 32 leaves that kernel out, whose launch and set-up are as long as a short
+    // prefix takes (8 requests behind 2000 tokens in bf16 17 us and 23, behind 8192 23 and 27, behind 60000 91 and 60).
     const bool has_many = io.groups && (long long)io.B * l.G > 2 * kRows;
-    a.few_rows = has_many ? kRows : 2 * kRows;
+    a.few_rows = has_many && !l.e4m3 ? kRows : 2 * kRows;
     a.tile_shift = l.e4m3 ? 5 : 4;
     a.page_shift = l.page_shift;
     a.num_pages = l.num_pages;
