@@ -119,7 +119,7 @@ void set_launch_detail(const kda_ctx* ctx, unsigned what, const char* name, cuda
 // Sizes of kda_beam_select.
 kda_status check_beams(int groups, int beams, int vocab, int num) {
     if (groups < 0 || beams < 1 || vocab < 1 || num < 1 || (long long)beams * vocab > 0x7fffffffLL ||
-        (long long)groups * beams > 0x7fffffffLL || num > (long long)beams * vocab) {
+        (long long)groups * beams > 1LL << 30 || num > (long long)beams * vocab) {
         set_error_text("%d groups of %d beams, %d logits each, %d continuations", groups, beams, vocab, num);
         return KDA_ERR_INVALID_ARG;
     }

@@ -166,6 +166,24 @@ def test_large_vocabulary_of_many_rows():
     run(x, scores, 8, keep=True)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_many_small_groups(bf16):
+    """More rows than CTAs by far."""
+    G, K, V, num = 20011, 2, 5, 3
+    x, scores = make(G, K, V, bf16, seed=5)
+    with Ctx() as ctx:
+        got = select(ctx, x, scores, num)
+    y = beam_ref.scores64(x, scores, None, 0)
+    s, k, v = beam_ref.best(y, num)
+    assert bool(((got[0].double() - s).abs() <= SLACK + 2.0 ** -23 * s.abs()).all())
+    # Neighbours of different beams that are further apart than their scores may be off have the formula's place.
+    s4 = beam_ref.best(y, num + 1)[0]
+    apart = torch.cat([torch.ones_like(s4[:, :1], dtype=torch.bool), (s4[:, :-1] - s4[:, 1:]) > 2 * SLACK], 1)
+    sure = apart[:, :-1] & apart[:, 1:]
+    rows = k + torch.arange(G, device=DEV)[:, None] * K
+    assert bool(((got[1] == v) & (got[2] == rows))[sure].all()) and float(sure.float().mean()) > 0.9
+
+
 def test_result_does_not_depend_on_the_run():
     x, scores = make(3, 8, 70001, bf16=True, seed=13)
     with Ctx() as ctx:
@@ -225,6 +243,12 @@ def test_select_refusals():
         refused(unsupported, out(4), 1, 65, x.repeat(9, 1), scores.repeat(9, 1), 4)
         assert kda.kda_beam_select_workspace_bytes(ctx, 2, 65, 100, 4) == 0
         assert kda.kda_beam_select_workspace_bytes(ctx, 0, 4, 100, 4) == 0
+        # Parts of rows are numbered in 32 bits, up to two for each row.
+        for groups, beams in ((2 ** 30 + 1, 1), (2 ** 24 + 1, 64), (2 ** 31 - 1, 1)):
+            assert kda.kda_beam_select_workspace_bytes(ctx, groups, beams, 8, 1) == 0
+            assert kda.load().kda_beam_select(ctx, groups, beams, 8, x.data_ptr(), 0, 8, scores.data_ptr(), None, 0, 1, 0, 16, 16, 16,
+                                              ws.data_ptr(), 1 << 62, None) == bad
+        assert kda.kda_beam_select_workspace_bytes(ctx, 2 ** 30, 1, 8, 1) > 2 ** 34
         kda.kda_beam_select(ctx, 0, 4, x, scores, 4, *out(4), ws)
         for wrong in (dict(scores=scores.double()), dict(done=done.int()), dict(logits=x.t()), dict(scores=scores[:1])):
             args = {"logits": x, "scores": scores, **wrong}
@@ -312,6 +336,24 @@ def test_reorder_errors_into_other_buffers():
         assert kda.kda_sync_status(ctx) == kda.KDA_ERR_INVALID_ARG
     assert torch.equal(other_inner[0][0], inner[0][2]) and torch.equal(other_inner[0][2], inner[0][0])
     assert torch.equal(other_inner[0][1], left)
+
+
+def test_reorder_beyond_4_gib():
+    B, H = 300, 256
+    S = torch.zeros(B, H, D, D, device=DEV)
+    conv = torch.zeros(B, 3, 3 * H * D, device=DEV)
+    for b in (0, 7, 299):
+        S[b], conv[b] = b + 1, -b - 1
+    rows = list(range(B))
+    rows[298], rows[1], rows[150] = 299, 7, 299
+    with Ctx(H) as ctx:
+        kda.kda_beam_reorder(ctx, B, torch.tensor(rows, dtype=torch.int32, device=DEV), S, conv)
+        assert kda.kda_sync_status(ctx) == kda.KDA_OK
+    want = torch.zeros(B, device=DEV)
+    for b in (0, 7, 299):
+        want[b] = b + 1
+    want[298], want[1], want[150] = 300, 8, 300
+    assert bool((S.view(B, -1) == want[:, None]).all()) and bool((conv.view(B, -1) == -want[:, None]).all())
 
 
 def test_reorder_refusals():
