@@ -259,6 +259,48 @@ def test_nan_and_infinity(n, e4m3):
     layer.done()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,prefix", [(4, 217), (40, 217), (40, 16), (40, 400)])
+def test_own_keys_behind_a_prefix_do_not_reach_the_others(n, prefix, e4m3):
+    """The request whose table row names the prefix's pages has NaN in all keys and values behind it."""
+    page = 16
+    lens = [prefix + 30 + b for b in range(n)]
+    layer = Layer(8, 2, page, e4m3)
+    fill(layer, lens)
+    share(layer, [(0, n, prefix)], lens)
+    q = queries(layer, n)
+    clean, cl = attend(layer, q, lens)
+    for c in (layer.k, layer.v):
+        c = c.view(torch.uint8) if e4m3 else c
+        for key in range(prefix, -(-lens[0] // page) * page):
+            c[layer.table_list[0][key // page], :, key % page] = 0x7F if e4m3 else math.nan
+    o, lse = attend(layer, q, lens)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    assert bool(o[0].isnan().all()) and bool(lse[0].isnan().all())
+    assert torch.equal(o[1:].view(torch.int16), clean[1:].view(torch.int16)) and torch.equal(lse[1:], cl[1:])
+    layer.done()
+
+
+def test_two_calls_at_once():
+    """Two contexts, workspaces and streams."""
+    made, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for seed, e4m3 in ((3, False), (4, True)):
+        layer, lens = build([(40, 900), (5, 300)], 9, 16, 2, 16, e4m3, seed=seed)
+        q = queries(layer, 45)
+        want, _ = attend(layer, q, lens)
+        ws = torch.empty(kda.kda_attn_shared_workspace_bytes(layer.attn, 45), dtype=torch.uint8, device=DEV)
+        made.append((layer, q, (i32(lens), 2, i32([0, 40, 45]), i32([900, 300])), want, torch.zeros_like(want), ws))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (layer, q, args, _, o, ws), s in zip(made, streams):
+            kda.kda_attn_decode_shared(layer.attn, 45, q, layer.table, *args, o, ws, stream=s)
+    torch.cuda.synchronize()
+    for layer, _, _, want, o, _ in made:
+        assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+        assert torch.equal(o.view(torch.int16), want.view(torch.int16))
+        layer.done()
+
+
 @pytest.mark.parametrize("n", [4, 40])
 def test_pages_outside_the_cache(n):
     layer, lens = build([(n, 300)], 40, 8, 2, 16, False)
