@@ -24,15 +24,17 @@
 //    of a row alone came to the workspace as a finished result, what several had as parts;
 //    who had the first and the last one noted it.
 //
-// Measured: 32 prompts of up to 4,100 tokens with 1 to 30 requests each, 32 / 8 heads,
-// bf16, 534 MB: 124 us, 0.64 of the copy rate (the two kernels 50 us each, at
-// 5.7 and 5 TB/s; plan and join 4 and 8).  64 requests behind 8,192 tokens, 65 MB: 39 us (4, 9,
-// 14 and 6 us and the launches' gaps; kda_attn_decode: 178 us); of the tensor core kernel's 14 us its
-// 3 or 4 key tiles are 4, the parts' way out 4.  256 requests of 64 heads behind four
-// documents of up to 16,300 tokens in e4m3, 128 GFLOP: 133 us, of which the tensor core
-// kernel 90.  The requests' own keys in the decode's kernel, where four warps share a
-// request's tiles and meet at its end: 36 us of that instead of 21.  Queries and
-// requests brought near ahead of their use: no faster.
+// Measured (a kernel's share: what the call takes longer when it is launched twice): 32 prompts of up
+// to 4,100 tokens with 1 to 30 requests each, 32 / 8 heads, bf16, 534 MB: 123 us, 0.64 of
+// the copy rate (the few-row kernel 53 us and the tensor core kernel about 57, 5 TB/s each; plan
+// 5, join 7).  64 requests behind 8,192 tokens, 65 MB: 38 us (plan 4, few-row kernel 9,
+// tensor core kernel 15, join 9, whose 20 MB of parts come from L2; kda_attn_decode: 178 us); of
+// the tensor core kernel's 15 its 3 or 4 key tiles take 4, the parts' way out 4.  256 requests of 64 heads
+// behind four documents of up to 16,300 tokens in e4m3, 128 GFLOP: 131 us (plan 6, few-row kernel
+// 17, tensor core kernel about 97, join 11).  The requests' own keys in the decode's kernel,
+// where four warps share a request's tiles and meet at its end: 15 us slower.  Queries and
+// requests brought near ahead of their use, more tiles per warp: no faster.  The join with
+// several rows of a request per CTA, their places found once: 1 to 5 us slower.
 #include <atomic>
 
 #include "attn_internal.cuh"
@@ -116,10 +118,6 @@ size_t carve(Args& a, AttnIO& many, void* workspace, const AttnLayer& l, int B, 
     return (size_t)(at - static_cast<uint8_t*>(workspace));
 }
 
-__device__ __forceinline__ int own_length(const AttnSharedIO& io, int b, int shift) {
-    return min(max(io.kv_lens[b], 0), io.max_pages << shift);
-}
-
 // Exclusive prefix of v over the CTA's threads; *total gets the sum.
 __device__ __forceinline__ long long block_exclusive(long long v, long long* s_warp, long long* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -157,6 +155,14 @@ __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(cons
     const int count = io.groups + io.B;
     const int per = (count + kPlanThreads - 1) / kPlanThreads, i0 = min(count, tid * per), i1 = min(count, i0 + per);
     bool bad = false;
+    // What this thread's first item and this warp's first group need, on the way beside the offsets.
+    const int kv0 = i0 < i1 && i0 >= io.groups ? io.kv_lens[i0 - io.groups] : 0;
+    int from0 = 0, to0 = 0, len0 = 0;
+    if (warp < io.groups) {
+        from0 = io.cu_groups[warp];
+        to0 = io.cu_groups[warp + 1];
+        len0 = io.prefix_lens[warp];
+    }
     for (int g = tid; g < io.groups; g += kPlanThreads) {
         const int from = io.cu_groups[g], to = io.cu_groups[g + 1];
         bad |= from < 0 || to < from || to > io.B;
@@ -165,8 +171,9 @@ __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(cons
     bad = __syncthreads_or(bad);
     if (bad && tid == 0) atomicOr(err, kErrAttnIndex);
     for (int g = warp; g < io.groups; g += kPlanThreads / 32) {
-        const int from = bad ? 0 : io.cu_groups[g], to = bad ? 0 : io.cu_groups[g + 1];
-        const int len = min(max(io.prefix_lens[g], 0), most) >> shift << shift;
+        const bool near = g == warp;
+        const int from = bad ? 0 : near ? from0 : io.cu_groups[g], to = bad ? 0 : near ? to0 : io.cu_groups[g + 1];
+        const int len = min(max(near ? len0 : io.prefix_lens[g], 0), most) >> shift << shift;
         int members = 0, row = 0;
         uint32_t first32 = 0;   // who of the first 32 has so many keys
         if (len)
@@ -212,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(cons
         } else {
             const int b = i - io.groups, g = group_of[b], before = g >= 0 ? group_len[g] : 0;
             a.group_of[b] = g;
-            x.len = own_length(io, b, a.page_shift) - before;
+            x.len = min(max(i == i0 ? kv0 : io.kv_lens[b], 0), most) - before;
             x.q = b;
             x.out = io.B + b;
             x.n = 1;
@@ -518,21 +525,27 @@ __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_
         }
         nth += parts;
     };
+    // Where the results are; a load that depends on another is under way before the parts are read.
     const int g = a.group_of[b], own = a.items[groups + b].len;
+    const int2 own_note = parts_of(a, groups + b)[h * ((a.G + kRows - 1) / kRows) + head / kRows];   // (of no keys: not used)
+    const bool many = g >= 0 && a.items[g].len == 0;
+    int row_in = 0;
+    int2 note = make_int2(0, 0);
     if (g >= 0) {
-        const int len = a.items[g].len, i = b - a.io.cu_groups[g];
-        if (len) {
+        const int i = b - a.io.cu_groups[g], tiles = a.items[g].tiles, before = a.many_pairs[g];
+        if (!many) {
             const int R = i * a.G + head;
-            add_parts(parts_of(a, g)[h * a.items[g].tiles + R / kRows], a.slots, kSlotFloats, kRows * kHeadDim, R % kRows, row);
+            note = parts_of(a, g)[h * tiles + R / kRows];
+            row_in = R % kRows;
         } else {   // the tensor core kernel's: token tiles in pairs
             const int pair = i / (2 * a.tokens), in = i - pair * 2 * a.tokens, side = in >= a.tokens;
-            add_parts(a.many_parts[(size_t)(a.many_pairs[g] + pair) * a.Hkv + h], a.many_slots, 2 * 128 * (kHeadDim + 2), 2 * 128 * kHeadDim,
-                      side * 128 + (in - side * a.tokens) * a.G + head, row);
+            note = a.many_parts[(size_t)(before + pair) * a.Hkv + h];
+            row_in = side * 128 + (in - side * a.tokens) * a.G + head;
         }
     }
-    if (own)
-        add_parts(parts_of(a, groups + b)[h * ((a.G + kRows - 1) / kRows) + head / kRows], a.slots, kSlotFloats, kRows * kHeadDim, head % kRows,
-                  rows + row);
+    if (own) add_parts(own_note, a.slots, kSlotFloats, kRows * kHeadDim, head % kRows, rows + row);
+    if (g >= 0)
+        add_parts(note, many ? a.many_slots : a.slots, many ? 2 * 128 * (kHeadDim + 2) : kSlotFloats, (many ? 2 * 128 : kRows) * kHeadDim, row_in, row);
     if (kWide) {
         s_acc[warp][lane] = acc;
         if (lane == 0) {
