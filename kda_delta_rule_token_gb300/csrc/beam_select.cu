@@ -49,6 +49,8 @@ constexpr int kTile = kThreads * kPer;
 constexpr int kSub = 4;                // tiles between two looks at the largest logits
 static_assert(kSub * kPer == 64, "two logits of a thread for each lane of its warp");
 constexpr int kList = 768;             // candidates that a CTA holds
+constexpr int kThin = 256;             // more than these are brought down to num
+static_assert(kThin + KDA_BEAM_MAX_NUM <= kList, "room for num candidates");
 constexpr int kMostNum = KDA_BEAM_MAX_NUM;
 constexpr int kJoinPer = 16;           // candidates of a group's segments that a thread of the join takes
 constexpr int kJoinEntries = kJoinPer * kThreads;
@@ -79,10 +81,10 @@ __device__ __forceinline__ uint64_t candidate(float x, int token) {
 __device__ __forceinline__ float logit_of(uint64_t c) { return float_of((uint32_t)(c >> 32)); }
 __device__ __forceinline__ int token_of(uint64_t c) { return (int)~(uint32_t)c; }
 
-// exp(d): the product with log2 e to 2^-24 of itself.
+// exp(d): the exponent is off by 2^-24 and 2^-26 of itself, the product's rounding and log2 e's.
 __device__ __forceinline__ float exp_of(float d) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(d, 1.44269502f, d * 1.92596299e-8f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * 1.44269502f));
     return y;
 }
 
@@ -154,29 +156,35 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // A bound that num of the CTA's values reach, num from 1 to 64, and few others pass: of 64
-// groups of four threads, the num-th largest of their largest values, its lower 32 -
-// kBits bits cleared (0: fewer than num groups have one that is not 0).  *top: the
-// largest of all.  s_group: 64 values.  All threads call it; a barrier follows before
-// the next use.
+// groups of four threads, the num-th largest of their largest values (0: fewer than num
+// groups have one that is not 0).  *top: the largest of all.  Each group finds the place of its
+// own, a thread against sixteen others.  All threads call it; two barriers are in it.
 constexpr int kGroups = 64, kGroup = kThreads / kGroups;
 static_assert(kMostNum <= kGroups && kGroup == 4, "groups of the bound");
-template <int kBits>
-__device__ __forceinline__ uint32_t group_bound(uint32_t best, int num, uint32_t* s_group, uint32_t* top) {
-    const int lane = threadIdx.x & 31;
+struct __align__(16) Groups {
+    uint32_t best[kGroups];
+    uint32_t bound, top;
+};
+__device__ __forceinline__ uint32_t group_bound(uint32_t best, int num, Groups& sm, uint32_t* top) {
+    const int own = threadIdx.x / kGroup, from = threadIdx.x % kGroup * (kGroups / kGroup);
     best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
     best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
-    if (lane % kGroup == 0) s_group[threadIdx.x / kGroup] = best;
+    if (from == 0) sm.best[own] = best;
     __syncthreads();
-    const uint32_t v = s_group[lane], w = s_group[lane + 32];
-    *top = __reduce_max_sync(0xffffffffu, max(v, w));
-    uint32_t bound = 0;
+    int before = 0;   // of equal ones those of lower groups
 #pragma unroll
-    for (int bit = 31; bit >= 32 - kBits; --bit) {
-        const uint32_t with = bound | 1u << bit;
-        const int reach = __popc(__ballot_sync(0xffffffffu, v >= with)) + __popc(__ballot_sync(0xffffffffu, w >= with));
-        if (reach >= num) bound = with;
+    for (int j = 0; j < kGroups / kGroup; j += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(&sm.best[from + j]);
+        before += (u.x >= best + (from + j >= own)) + (u.y >= best + (from + j + 1 >= own)) + (u.z >= best + (from + j + 2 >= own)) +
+                  (u.w >= best + (from + j + 3 >= own));
     }
-    return bound;
+    before += __shfl_xor_sync(0xffffffffu, before, 1);
+    before += __shfl_xor_sync(0xffffffffu, before, 2);
+    if (from == 0 && before == num - 1) sm.bound = best;
+    if (from == 0 && before == 0) sm.top = best;
+    __syncthreads();
+    *top = sm.top;
+    return sm.bound;
 }
 
 // How the tiles are dealt: row r's are units [r * per_row, (r + 1) * per_row), CTA c
@@ -199,8 +207,8 @@ struct RowsArgs {
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsArgs a) {
     constexpr int kVec = kBf16 ? 8 : 4, kLoads = kPer / kVec, kBytes = kBf16 ? 2 : 4;
-    __shared__ uint64_t s_list[kList];
-    __shared__ uint32_t s_group[kGroups];
+    __shared__ uint64_t s_list[kList], s_ranked[kList];
+    __shared__ Groups s_group;
     __shared__ float2 s_sum[kThreads / 32];
     __shared__ int s_held, s_count[32], s_warp[kThreads / 32];
     ptx::griddep_launch_dependents();
@@ -279,35 +287,32 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
 
     // The reference is a logit of the segment; -infinity: there has been none above that, and the sum is 0 or NaN.
     float T = -INFINITY, ref = -INFINITY, sum = 0.f, low = 0.f;   // the sum and what its additions lost
+    int held = 0;   // s_held, between the tiles of two looks
     auto add = [&](float v) {
         const float y = v - low, s = sum + y;
         low = (s - sum) - y;
         sum = s;
     };
     // The list's best n, in order; what leaves it joins the sums, in its order, so that they do not
-    // depend on the one in which it was written.  All threads call it.
-    auto thin = [&](int held) {
-        uint64_t own[kList / kThreads];
-        int rank[kList / kThreads];
-#pragma unroll
-        for (int i = 0; i < kList / kThreads; ++i) {
-            rank[i] = -1;
-            if (i * kThreads >= held) continue;
-            if (i * kThreads + tid < held) {
-                own[i] = s_list[i * kThreads + tid];
-                rank[i] = 0;
-#pragma unroll 8
-                for (int j = 0; j < held; ++j) rank[i] += s_list[j] > own[i];
-            }
+    // depend on the one in which it was written.  All threads call it, behind a barrier.
+    auto thin = [&]() {
+        for (int i = tid; i < held; i += kThreads) {
+            const uint64_t own = s_list[i];
+            int rank = 0;
+#pragma unroll 4
+            for (int j = 0; j < held; ++j) rank += s_list[j] > own;
+            s_ranked[rank] = own;
         }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kList / kThreads; ++i)
-            if (rank[i] >= 0) s_list[rank[i]] = own[i];
-        if (tid == 0) s_held = min(held, n);
+        for (int i = tid; i < held; i += kThreads) {
+            const uint64_t c = s_ranked[i];
+            if (i < n) s_list[i] = c;
+            else add(exp_of(logit_of(c) - ref));
+        }
+        if (held >= n) T = fmaxf(T, logit_of(s_ranked[n - 1]));
+        held = min(held, n);
+        if (tid == 0) s_held = held;
         __syncthreads();
-        if (held >= n) T = logit_of(s_list[n - 1]);
-        for (int i = n + tid; i < held; i += kThreads) add(exp_of(logit_of(s_list[i]) - ref));
     };
 
     if (begin < end) load(begin);
@@ -330,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
                 m = fmaxf(m, -INFINITY);   // not NaN
                 if (t == begin && ref == -INFINITY) {
                     const uint32_t w = __reduce_max_sync(0xffffffffu, order_of(m));
-                    if (lane == 0) s_group[warp] = w;
+                    if (lane == 0) s_group.best[warp] = w;
                     __syncthreads();
-                    const float first = float_of(__reduce_max_sync(0xffffffffu, s_group[lane & (kThreads / 32 - 1)]));
+                    const float first = float_of(__reduce_max_sync(0xffffffffu, s_group.best[lane & (kThreads / 32 - 1)]));
                     if (fabsf(first) < INFINITY) ref = first;
                     __syncthreads();
                 }
@@ -343,20 +348,18 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
                 for (int i = 0; i < kPer; ++i) part += exp_of(x[i] - to);
                 add(part);
             }
-            bound = group_bound<16>(order_of(most), n, s_group, &top);
+            bound = group_bound(order_of(most), n, s_group, &top);
             const float now = float_of(top);
             if (fabsf(now) == INFINITY || (ref != -INFINITY && now - ref <= kRefMargin)) break;
             // The first logits above -infinity, or ones far above the reference: these tiles once more.
             if (ref != -INFINITY) scale0 *= expf(ref - now);
             ref = now;
-            __syncthreads();
             load(t0);
         }
         // Threads whose largest logit is a candidate, one after another: two of its logits for each lane.
         const float s0 = sum0 * scale0, l0 = low0 * scale0;
-        const int held = s_held;
-        __syncthreads();
-        uint32_t again = __ballot_sync(0xffffffffu, most > T && order_of(most) >= bound);
+        const float least = float_of(max(bound, order_of(T) + 1));   // of a candidate: the bound, or above T
+        uint32_t again = __ballot_sync(0xffffffffu, most >= least);
         if (again >> lane & 1) {
             sum = s0;
             low = l0;
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
             float rest = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (v[i] > T && order_of(v[i]) >= bound) {
+                if (v[i] >= least) {
                     const int to = atomicAdd(&s_held, 1);
                     if (to < kList) s_list[to] = candidate(v[i], token(t_mine, i_mine + i, of));
                 } else {
@@ -453,10 +456,11 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
                 }
             __syncthreads();
         }
-        if (s_held != held) thin(s_held);
-        __syncthreads();
+        held = s_held;   // (the next candidate is behind the next bound's barrier)
+        T = fmaxf(T, float_of(bound));   // which num logits reach, all of them in the list
+        if (held > kThin || t1 == end) thin();
     }
-    const int kept = s_held;
+    const int kept = held;
     const size_t segment = (size_t)row + blockIdx.x;
 
     // The threads' sums, with what the additions lose.
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
     __shared__ double s_from[KDA_BEAM_MAX_BEAMS];   // a score is (logit - most) + from
     __shared__ double s_most[KDA_BEAM_MAX_BEAMS];
     __shared__ int s_first[KDA_BEAM_MAX_BEAMS], s_segments[KDA_BEAM_MAX_BEAMS];   // (none of a beam at its end)
-    __shared__ uint32_t s_group[kGroups];
+    __shared__ Groups s_group;
     __shared__ Choice s_best[kThreads], s_bound;
     __shared__ Choice s_list[kJoinList];
     __shared__ Choice s_sorted[kMostNum];
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
     }
     // A bound that num of them reach, as in the rows' kernel; of equal scores all pass.
     uint32_t top;
-    Choice bound{max((uint64_t)group_bound<24>((uint32_t)(best.key >> 32), n, s_group, &top) << 32, (uint64_t)1), 0xffffffffu};
+    Choice bound{max((uint64_t)group_bound((uint32_t)(best.key >> 32), n, s_group, &top) << 32, (uint64_t)1), 0xffffffffu};
     for (;;) {
         int count = 0;
 #pragma unroll
@@ -702,8 +706,12 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
 }
 
 // The deal, and the most segments of a row.  No CTA has less than a tile, and the
-// join takes K * num candidates for each of a row's segments.
+// join takes K * num candidates for each of a row's segments.  Fewer CTAs, each with
+// a part of one row alone, if what they have more to read than all that fit costs less than
+// the second segment does that these begin (128 rows of 32 tiles, 512 CTAs and 608: 31.1 us and
+// 33.5; 512 rows, as many CTAs and 608: 67.9 and 65.3).
 constexpr int kCtasPerSm = 4;
+constexpr int kSegmentCost = 3;        // tiles
 Deal deal_of(int groups, int beams, int vocab, int num, const DeviceInfo& dev, int& most) {
     const long long rows = (long long)groups * beams;
     Deal d;
@@ -711,6 +719,10 @@ Deal deal_of(int groups, int beams, int vocab, int num, const DeviceInfo& dev, i
     d.units = rows * d.per_row;
     long long ctas = (long long)kCtasPerSm * dev.sm_count;
     if (ctas > d.units) ctas = d.units;
+    if (ctas >= rows) {
+        const long long alone = ctas / rows * rows;
+        if ((d.units + alone - 1) / alone < (d.units + ctas - 1) / ctas + kSegmentCost) ctas = alone;
+    }
     for (;; ctas = ctas > 2 * rows ? ctas - rows : rows) {
         // Ranges of `least` units or one more: a row's units lie in so many of them at most.
         const long long least = d.units / ctas;
