@@ -47,7 +47,7 @@ constexpr int kThreads = 256;
 constexpr int kPer = 16;               // logits of a thread per tile
 constexpr int kTile = kThreads * kPer;
 constexpr int kSub = 4;                // tiles between two looks at the largest logits
-static_assert(kSub * kPer == 64, "two logits of a thread for each lane of its warp");
+static_assert(kSub * kPer == 64, "four logits of a thread for each lane of half a warp");
 constexpr int kList = 768;             // candidates that a CTA holds
 constexpr int kThin = 256;             // more than these are brought down to num
 static_assert(kThin + KDA_BEAM_MAX_NUM <= kList, "room for num candidates");
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
             ref = now;
             load(t0);
         }
-        // Threads whose largest logit is a candidate, one after another: two of its logits for each lane.
+        // Threads whose largest logit is a candidate, two at a time: four of its logits for each lane of half a warp.
         const float s0 = sum0 * scale0, l0 = low0 * scale0;
         const float least = float_of(max(bound, order_of(T) + 1));   // of a candidate: the bound, or above T
         uint32_t again = __ballot_sync(0xffffffffu, most >= least);
@@ -364,31 +364,46 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
             sum = s0;
             low = l0;
         }
-        const int t_mine = t0 + 2 * lane / kPer, i_mine = 2 * lane % kPer;
+        const int t_mine = t0 + 4 * (lane & 15) / kPer, i_mine = 4 * (lane & 15) % kPer;
         const uint8_t* mine_at = base + (long long)token(t_mine, i_mine, 0) * kBytes;
-        for (; again; again &= again - 1) {
-            const int of = warp * 32 + __ffs((int)again) - 1;
-            float v[2] = {-INFINITY, -INFINITY};
-            if (t_mine < t1 && there(t_mine, i_mine, of)) {
+        while (again) {
+            int of = __ffs((int)again) - 1;
+            again &= again - 1;
+            if (lane >= 16) of = again ? __ffs((int)again) - 1 : -1;
+            again &= again - 1;
+            float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const int thread = warp * 32 + of;
+            if (of >= 0 && t_mine < t1 && there(t_mine, i_mine, thread)) {
                 if (single(t_mine)) {
-                    v[0] = logit_at(token(t_mine, 0, of));
+                    v[0] = logit_at(token(t_mine, 0, thread));
                 } else {
-                    const uint2 w = kBf16 ? make_uint2(*reinterpret_cast<const uint32_t*>(mine_at + of * 16), 0u)
-                                          : *reinterpret_cast<const uint2*>(mine_at + of * 16);
-                    v[0] = put_right(__uint_as_float(kBf16 ? w.x << 16 : w.x));
-                    v[1] = put_right(__uint_as_float(kBf16 ? w.x & 0xffff0000u : w.y));
+                    uint4 w;
+                    if (kBf16) {
+                        const uint2 two = *reinterpret_cast<const uint2*>(mine_at + thread * 16);
+                        w = make_uint4(two.x << 16, two.x & 0xffff0000u, two.y << 16, two.y & 0xffff0000u);
+                    } else {
+                        w = *reinterpret_cast<const uint4*>(mine_at + thread * 16);
+                    }
+                    v[0] = put_right(__uint_as_float(w.x));
+                    v[1] = put_right(__uint_as_float(w.y));
+                    v[2] = put_right(__uint_as_float(w.z));
+                    v[3] = put_right(__uint_as_float(w.w));
                 }
             }
             float rest = 0.f;
+            uint32_t in = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (v[i] >= least) {
-                    const int to = atomicAdd(&s_held, 1);
-                    if (to < kList) s_list[to] = candidate(v[i], token(t_mine, i_mine + i, of));
-                } else {
-                    rest += exp_of(v[i] - ref);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const bool is = v[i] >= least;
+                in |= (uint32_t)is << i;
+                rest += is ? 0.f : exp_of(v[i] - ref);
+            }
             add(rest);
+            for (; in; in &= in - 1) {
+                const int i = __ffs((int)in) - 1, to = atomicAdd(&s_held, 1);
+                const float x4 = i < 2 ? (i ? v[1] : v[0]) : (i == 2 ? v[2] : v[3]);
+                if (to < kList) s_list[to] = candidate(x4, token(t_mine, i_mine + i, thread));
+            }
         }
         __syncthreads();
         if (s_held > kList) {
