@@ -211,6 +211,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
     __shared__ Groups s_group;
     __shared__ float2 s_sum[kThreads / 32];
     __shared__ int s_held, s_count[32], s_warp[kThreads / 32];
+    __shared__ uint32_t s_mask[kThreads / 32];
+    __shared__ uint16_t s_again[kThreads];
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.io.num;
     const long long last = a.deal.first(blockIdx.x + 1LL);
@@ -356,24 +358,33 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
             ref = now;
             load(t0);
         }
-        // Threads whose largest logit is a candidate, two at a time: four of its logits for each lane of half a warp.
+        // Threads whose largest logit is a candidate, dealt to the half warps in turn: four of a thread's
+        // logits for each lane.
         const float s0 = sum0 * scale0, l0 = low0 * scale0;
         const float least = float_of(max(bound, order_of(T) + 1));   // of a candidate: the bound, or above T
-        uint32_t again = __ballot_sync(0xffffffffu, most >= least);
-        if (again >> lane & 1) {
+        const bool mine = most >= least;
+        const uint32_t again = __ballot_sync(0xffffffffu, mine);
+        if (lane == 0) s_mask[warp] = again;
+        __syncthreads();
+        int total = 0, at = __popc(again & ((1u << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const int count = __popc(s_mask[w]);
+            if (w < warp) at += count;
+            total += count;
+        }
+        if (mine) {
+            s_again[at] = (uint16_t)tid;
             sum = s0;
             low = l0;
         }
+        __syncthreads();
         const int t_mine = t0 + 4 * (lane & 15) / kPer, i_mine = 4 * (lane & 15) % kPer;
         const uint8_t* mine_at = base + (long long)token(t_mine, i_mine, 0) * kBytes;
-        while (again) {
-            int of = __ffs((int)again) - 1;
-            again &= again - 1;
-            if (lane >= 16) of = again ? __ffs((int)again) - 1 : -1;
-            again &= again - 1;
+        for (int k = tid / 16; k < total; k += kThreads / 16) {
+            const int thread = s_again[k];
             float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            const int thread = warp * 32 + of;
-            if (of >= 0 && t_mine < t1 && there(t_mine, i_mine, thread)) {
+            if (t_mine < t1 && there(t_mine, i_mine, thread)) {
                 if (single(t_mine)) {
                     v[0] = logit_at(token(t_mine, 0, thread));
                 } else {
