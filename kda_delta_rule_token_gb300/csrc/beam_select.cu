@@ -46,8 +46,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 16;               // logits of a thread per tile
 constexpr int kTile = kThreads * kPer;
-constexpr int kSub = 4;                // tiles between two looks at the largest logits
-static_assert(kSub * kPer == 64, "four logits of a thread for each lane of half a warp");
+constexpr int kSub = 8;                // tiles between two looks at the largest logits
+static_assert(kSub * kPer % 64 == 0, "four logits of a thread for each lane of half a warp");
 constexpr int kList = 768;             // candidates that a CTA holds
 constexpr int kThin = 256;             // more than these are brought down to num
 static_assert(kThin + KDA_BEAM_MAX_NUM <= kList, "room for num candidates");
@@ -379,10 +379,11 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
             low = l0;
         }
         __syncthreads();
-        const int t_mine = t0 + 4 * (lane & 15) / kPer, i_mine = 4 * (lane & 15) % kPer;
-        const uint8_t* mine_at = base + (long long)token(t_mine, i_mine, 0) * kBytes;
-        for (int k = tid / 16; k < total; k += kThreads / 16) {
-            const int thread = s_again[k];
+        constexpr int kTurns = kSub * kPer / 64;
+        const int i_mine = 4 * (lane & 15) % kPer;
+        for (int k = tid / 16; k < total * kTurns; k += kThreads / 16) {
+            const int thread = s_again[k / kTurns], t_mine = t0 + (k % kTurns * 64 + 4 * (lane & 15)) / kPer;
+            const uint8_t* mine_at = base + (long long)token(t_mine, i_mine, 0) * kBytes;
             float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (t_mine < t1 && there(t_mine, i_mine, thread)) {
                 if (single(t_mine)) {
