@@ -10,13 +10,13 @@
 //  * kda_beam_rows_kernel: the tiles of all rows, 256 threads x 16 logits each, are
 //    dealt in equal ranges to as many CTAs as run at once; what a CTA has of a row
 //    is a segment.  The next tile's loads are under way.  A thread keeps the
-//    largest of its logits and the sum of exp(x - ref), nothing else.  Every four
+//    largest of its logits and the sum of exp(x - ref), nothing else.  Every eight
 //    tiles the CTA finds a bound that num of them reach and few others pass: 64 groups
 //    of threads each have a largest logit, and the num-th of these is it.
 //    The few threads whose largest logit reaches the bound are looked at again,
-//    each by its warp: logits that reach it join the list of candidates, the others
-//    the sums anew.  The list's num best stay; later logits have to
-//    pass the last of them (T).
+//    each by half a warp: logits that reach it join the list of candidates, the others
+//    the sums anew.  Later logits have to pass the bound (T); the list's num best
+//    stay at the end.
 //  * kda_beam_join_kernel, a CTA per group: lse of every beam from its segments'
 //    sums and lists, then the num best of the lists, by the same bound.
 //
@@ -27,16 +27,19 @@
 // in any order.  Scores are formed and compared in 64 bits and rounded once.
 //
 // Measured (both launches, inputs in HBM but for what L2 kept of them): 512 rows of
-// 131072 logits in fp32, 268 MB, 65 us, of which the rows take 57 (4.7 TB/s, 0.69
-// of the copy rate): a segment's beginning and end, 3 us that other CTAs of the SM
-// cover in part, twice per CTA.  128 rows of 131071 in bf16, 33 MB, 34 us, the same
-// with 54 threads looked at again per segment instead of 22 (num is 16).  Four rows of 32000,
-// 10.3 us: two launches, and in the join a chain of loads and 64-bit arithmetic.
-// Tried on the 512 rows: copies of four tiles ahead by cp.async 62 us, but 12.4 for
+// 131072 logits in fp32, 268 MB, 54 us, of which the rows take 47 (5.7 TB/s, 0.84
+// of the copy rate): looks at the largest logits, 3000 cycles each, which other CTAs of the SM
+// cover in part.  128 rows of 131071 in bf16, 33 MB, 23 us: one or two looks to a CTA's 8 tiles.  Four rows of
+// 32000, 8.7 us: two launches, and in the join a chain of loads, 64-bit arithmetic and instructions
+// that no CTA before has fetched.  What runs once per segment is short for the same reason (the list
+// ranked by loops written out: 2 us more).  A look every four tiles 57 us; before that, the bound found bit
+// by bit 65 instead of 62, threads looked at again by their own warps 59.7 instead of 57.6, by quarters of
+// warps 60.7.  Tried earlier: copies of four tiles ahead by cp.async 62 us and 65, but 12.4 and 10 for
 // the four rows; candidates taken out of every tile at once 69 to 73; two tiles'
 // loads ahead in registers with three CTAs per SM 71.
 #include <math.h>
 
+#include "attn_mma.cuh"
 #include "beam_internal.cuh"
 #include "ptx.cuh"
 
@@ -83,9 +86,13 @@ __device__ __forceinline__ int token_of(uint64_t c) { return (int)~(uint32_t)c; 
 
 // exp(d): the exponent is off by 2^-24 and 2^-26 of itself, the product's rounding and log2 e's.
 __device__ __forceinline__ float exp_of(float d) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * 1.44269502f));
-    return y;
+    return mma::exp2_approx(d * 1.44269502f);
+}
+
+__device__ __forceinline__ mma::f32x2 exp_of(mma::f32x2 d) {
+    float a, b;
+    mma::upk(mma::mul2(d, mma::pk(1.44269502f, 1.44269502f)), a, b);
+    return mma::pk(mma::exp2_approx(a), mma::exp2_approx(b));
 }
 
 // 2^f, f in units of 2^-32, in units of 2^-31: the exponential's series in ln 2, whose
@@ -147,12 +154,6 @@ __device__ __forceinline__ double widened(float x) {
     const uint32_t u = __float_as_uint(x), e = u >> 23 & 0xff;
     const uint32_t hi = (u & 0x80000000u) | (e == 0 ? 0 : e == 0xff ? 0x7ff00000u | (u & 0x7fffffu) >> 3 : ((u & 0x7fffffffu) >> 3) + 0x38000000u);
     return __hiloint2double((int)hi, e == 0 ? 0 : (int)(u << 29));
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 
 // A bound that num of the CTA's values reach, num from 1 to 64, and few others pass: of 64
@@ -330,9 +331,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
             for (int t = t0; t < t1; ++t) {
                 unpack(t);
                 if (t + 1 < end) load(t + 1);
-                float m = max3(max3(x[0], x[1], x[2]), x[3], x[4]);
+                float m = mma::max3(mma::max3(x[0], x[1], x[2]), x[3], x[4]);
 #pragma unroll
-                for (int i = 5; i < kPer - 1; i += 2) m = max3(m, x[i], x[i + 1]);
+                for (int i = 5; i < kPer - 1; i += 2) m = mma::max3(m, x[i], x[i + 1]);
                 m = fmaxf(m, x[kPer - 1]);
                 m = fmaxf(m, -INFINITY);   // not NaN
                 if (t == begin && ref == -INFINITY) {
@@ -345,10 +346,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
                 }
                 most = fmaxf(most, m);
                 const float to = ref == -INFINITY ? 0.f : ref;
-                float part = 0.f;
+                mma::f32x2 part = mma::pk(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) part += exp_of(x[i] - to);
-                add(part);
+                for (int i = 0; i < kPer; i += 2) part = mma::add2(part, exp_of(mma::add2(mma::pk(x[i], x[i + 1]), mma::pk(-to, -to))));
+                float even, odd;
+                mma::upk(part, even, odd);
+                add(even + odd);
             }
             bound = group_bound(order_of(most), n, s_group, &top);
             const float now = float_of(top);
@@ -735,10 +738,10 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
 // The deal, and the most segments of a row.  No CTA has less than a tile, and the
 // join takes K * num candidates for each of a row's segments.  Fewer CTAs, each with
 // a part of one row alone, if what they have more to read than all that fit costs less than
-// the second segment does that these begin (128 rows of 32 tiles, 512 CTAs and 608: 31.1 us and
-// 33.5; 512 rows, as many CTAs and 608: 67.9 and 65.3).
+// the second segment does that these begin (256 rows of 8 tiles in bf16, 512 CTAs and 608: 14.5 us
+// and 18; 400 rows of 13 tiles, as many CTAs and 608: 20.0 and 22.7; 512 rows of 32 tiles: 54.9 and 54.3).
 constexpr int kCtasPerSm = 4;
-constexpr int kSegmentCost = 3;        // tiles
+constexpr int kSegmentCost = 5;        // tiles
 Deal deal_of(int groups, int beams, int vocab, int num, const DeviceInfo& dev, int& most) {
     const long long rows = (long long)groups * beams;
     Deal d;
