@@ -27,12 +27,12 @@
 // in any order.  Scores are formed and compared in 64 bits and rounded once.
 //
 // Measured (both launches, inputs in HBM but for what L2 kept of them): 512 rows of
-// 131072 logits in fp32, 268 MB, 54 us, of which the rows take 47 (5.7 TB/s, 0.84
+// 131072 logits in fp32, 268 MB, 53 us, of which the rows take 47 (5.7 TB/s, 0.84
 // of the copy rate): looks at the largest logits, 3000 cycles each, which other CTAs of the SM
-// cover in part.  128 rows of 131071 in bf16, 33 MB, 23 us: one or two looks to a CTA's 8 tiles.  Four rows of
-// 32000, 8.7 us: two launches, and in the join a chain of loads, 64-bit arithmetic and instructions
-// that no CTA before has fetched.  What runs once per segment is short for the same reason (the list
-// ranked by loops written out: 2 us more).  A look every four tiles 57 us; before that, the bound found bit
+// cover in part.  128 rows of 131071 in bf16, 33 MB, 22 us: one or two looks to a CTA's 8 tiles.  Four rows of
+// 32000, 7.7 us: two launches, and in the join a chain of loads, 64-bit arithmetic and instructions
+// that no CTA before has fetched.  What runs once per segment or CTA is short for the same reason (the list
+// ranked by loops written out 2 us more, the join with 16 candidates to a thread 1 us).  A look every four tiles 57 us; before that, the bound found bit
 // by bit 65 instead of 62, threads looked at again by their own warps 59.7 instead of 57.6, by quarters of
 // warps 60.7.  Tried earlier: copies of four tiles ahead by cp.async 62 us and 65, but 12.4 and 10 for
 // the four rows; candidates taken out of every tile at once 69 to 73; two tiles'
@@ -55,8 +55,9 @@ constexpr int kList = 768;             // candidates that a CTA holds
 constexpr int kThin = 256;             // more than these are brought down to num
 static_assert(kThin + KDA_BEAM_MAX_NUM <= kList, "room for num candidates");
 constexpr int kMostNum = KDA_BEAM_MAX_NUM;
-constexpr int kJoinPer = 16;           // candidates of a group's segments that a thread of the join takes
-constexpr int kJoinEntries = kJoinPer * kThreads;
+constexpr int kJoinThreads = 1024;     // of the join, at most
+constexpr int kJoinPer = 4;            // candidates of a group's segments that a thread of the join takes
+constexpr int kJoinEntries = kJoinPer * kJoinThreads;
 constexpr int kJoinList = 1280;
 static_assert((kJoinPer + 1) * kMostNum <= kJoinList, "candidates that the join's bound leaves");
 static_assert(KDA_BEAM_MAX_BEAMS * kMostNum <= kJoinEntries && KDA_BEAM_MAX_BEAMS <= kThreads, "a segment per beam");
@@ -157,32 +158,31 @@ __device__ __forceinline__ double widened(float x) {
 }
 
 // A bound that num of the CTA's values reach, num from 1 to 64, and few others pass: of 64
-// groups of four threads, the num-th largest of their largest values (0: fewer than num
-// groups have one that is not 0).  *top: the largest of all.  Each group finds the place of its
-// own, a thread against sixteen others.  All threads call it; two barriers are in it.
-constexpr int kGroups = 64, kGroup = kThreads / kGroups;
-static_assert(kMostNum <= kGroups && kGroup == 4, "groups of the bound");
+// groups of `group` (4, 8 or 16) threads, the num-th largest of their largest values (0: fewer
+// than num groups have one that is not 0).  *top: the largest of all.  Each group finds the place
+// of its own, four threads each against sixteen others.  All threads call it; two barriers are in it.
+constexpr int kGroups = 64, kGroup = kThreads / kGroups, kCounters = 4;
+static_assert(kMostNum <= kGroups && kGroup == kCounters && kJoinThreads <= 16 * kGroups, "groups of the bound");
 struct __align__(16) Groups {
     uint32_t best[kGroups];
     uint32_t bound, top;
 };
-__device__ __forceinline__ uint32_t group_bound(uint32_t best, int num, Groups& sm, uint32_t* top) {
-    const int own = threadIdx.x / kGroup, from = threadIdx.x % kGroup * (kGroups / kGroup);
-    best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
-    best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
-    if (from == 0) sm.best[own] = best;
+__device__ __forceinline__ uint32_t group_bound(uint32_t best, int num, Groups& sm, uint32_t* top, int group = kGroup) {
+    const int own = threadIdx.x / group, in = threadIdx.x % group, from = in % kCounters * (kGroups / kCounters);
+    for (int d = 1; d < group; d *= 2) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
+    if (in == 0) sm.best[own] = best;
     __syncthreads();
     int before = 0;   // of equal ones those of lower groups
 #pragma unroll
-    for (int j = 0; j < kGroups / kGroup; j += 4) {
+    for (int j = 0; j < kGroups / kCounters; j += 4) {
         const uint4 u = *reinterpret_cast<const uint4*>(&sm.best[from + j]);
         before += (u.x >= best + (from + j >= own)) + (u.y >= best + (from + j + 1 >= own)) + (u.z >= best + (from + j + 2 >= own)) +
                   (u.w >= best + (from + j + 3 >= own));
     }
     before += __shfl_xor_sync(0xffffffffu, before, 1);
     before += __shfl_xor_sync(0xffffffffu, before, 2);
-    if (from == 0 && before == num - 1) sm.bound = best;
-    if (from == 0 && before == 0) sm.top = best;
+    if (in == 0 && before == num - 1) sm.bound = best;
+    if (in == 0 && before == 0) sm.top = best;
     __syncthreads();
     *top = sm.top;
     return sm.bound;
@@ -203,6 +203,7 @@ struct RowsArgs {
     Deal deal;
     Part* parts;         // [segments]
     uint64_t* lists;     // [segments][num]
+    bool early;
 };
 
 template <bool kBf16>
@@ -214,7 +215,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
     __shared__ int s_held, s_count[32], s_warp[kThreads / 32];
     __shared__ uint32_t s_mask[kThreads / 32];
     __shared__ uint16_t s_again[kThreads];
-    ptx::griddep_launch_dependents();
+    // The join's CTAs may come now where SMs have room for them, else at the last segment's end: beside rows
+    // they cost more than they save (64 rows of 50257 18.2 us instead of 13.0, 4 of 32000 7.7 instead of 8.2).
+    if (a.early) ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.io.num;
     const long long last = a.deal.first(blockIdx.x + 1LL);
     for (long long unit = a.deal.first(blockIdx.x), next; unit < last; unit = next) {
@@ -490,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
         T = fmaxf(T, float_of(bound));   // which num logits reach, all of them in the list
         if (held > kThin || t1 == end) thin();
     }
+    if (next == last) ptx::griddep_launch_dependents();
     const int kept = held;
     const size_t segment = (size_t)row + blockIdx.x;
 
@@ -546,21 +550,24 @@ struct JoinArgs {
     const uint64_t* lists;
 };
 
-__global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs a) {
+// (What runs once per CTA waits for its instructions: little of it is written out.)
+template <int kMost>
+__global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) {
     __shared__ double s_from[KDA_BEAM_MAX_BEAMS];   // a score is (logit - most) + from
     __shared__ double s_most[KDA_BEAM_MAX_BEAMS];
     __shared__ int s_first[KDA_BEAM_MAX_BEAMS], s_segments[KDA_BEAM_MAX_BEAMS];   // (none of a beam at its end)
     __shared__ Groups s_group;
-    __shared__ Choice s_best[kThreads], s_bound;
+    __shared__ Choice s_best[kMost], s_bound;
     __shared__ Choice s_list[kJoinList];
     __shared__ Choice s_sorted[kMostNum];
     __shared__ int s_held, s_beam[kMostNum];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = kMost;
     const int g = blockIdx.x, K = a.io.beams, n = a.io.num, S = a.most;
     const uint8_t* done = a.io.done ? a.io.done + (size_t)g * K : nullptr;
     const float* scores = a.io.scores + (size_t)g * K;
     if (tid == 0) s_held = 0;
-    for (int k = tid; k < K; k += kThreads) {
+    if (tid < K) {
+        const int k = tid;
         const long long row = (long long)g * K + k;
         const int from = a.deal.cta_of(row * a.deal.per_row), to = a.deal.cta_of((row + 1) * a.deal.per_row - 1);
         s_first[k] = (int)row + from;
@@ -575,11 +582,12 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
     uint64_t own[kJoinPer];
     int beam_of[kJoinPer];
     {
-        const int turn = tid % kGroup * kGroups + tid / kGroup;
+        constexpr int group = kMost / kGroups;
+        const int turn = tid % group * kGroups + tid / group;
 #pragma unroll
         for (int j = 0; j < kJoinPer; ++j) {
             if (j >= a.rounds) break;
-            const uint32_t i = j * kThreads + turn, nth = __umulhi(2 * i, a.per_segments), at = i - nth * segments;
+            const uint32_t i = j * threads + turn, nth = __umulhi(2 * i, a.per_segments), at = i - nth * segments;
             const int k = (int)__umulhi(2 * at, a.per_most), s = (int)at - k * S;
             beam_of[j] = k;
             own[j] = nth < (uint32_t)n && s < s_segments[k] ? a.lists[(size_t)(s_first[k] + s) * n + nth] : 0;
@@ -587,7 +595,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
     }
 
     // The beams' sums of exp(x - most).  Where one is NaN, the beam has nothing to offer.
-    for (int k = warp; k < K; k += kThreads / 32) {
+    for (int k = warp; k < K; k += threads / 32) {
         const int here = s_segments[k];
         if (here == 0) continue;
         const Part* p = a.parts + s_first[k];
@@ -650,7 +658,7 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
     }
     // A bound that num of them reach, as in the rows' kernel; of equal scores all pass.
     uint32_t top;
-    Choice bound{max((uint64_t)group_bound((uint32_t)(best.key >> 32), n, s_group, &top) << 32, (uint64_t)1), 0xffffffffu};
+    Choice bound{max((uint64_t)group_bound((uint32_t)(best.key >> 32), n, s_group, &top, kMost / kGroups) << 32, (uint64_t)1), 0xffffffffu};
     for (;;) {
         int count = 0;
 #pragma unroll
@@ -671,17 +679,17 @@ __global__ void __launch_bounds__(kThreads) kda_beam_join_kernel(const JoinArgs 
         }
         __syncthreads();
         int above = 0;
-#pragma unroll 8
-        for (int j = 0; j < kThreads; ++j) above += better(s_best[j], best);
+#pragma unroll 4
+        for (int j = 0; j < threads; ++j) above += better(s_best[j], best);
         if (best.key && above == n - 1) s_bound = best;
         __syncthreads();
         bound = s_bound;
     }
     const int held = s_held, chosen = min(held, n);
-    for (int i = tid; i < held; i += kThreads) {
+    for (int i = tid; i < held; i += threads) {
         const Choice c = s_list[i];
         int rank = 0;
-#pragma unroll 8
+#pragma unroll 4
         for (int j = 0; j < held; ++j) rank += better(s_list[j], c);
         if (rank < n) s_sorted[rank] = c;
     }
@@ -780,25 +788,29 @@ cudaError_t launch_beam_select(const BeamSelectIO& io, const DeviceInfo& dev, cu
     const Deal d = deal_of(io.groups, io.beams, io.vocab, io.num, dev, most);
     Part* p = static_cast<Part*>(io.workspace);
     uint64_t* lists = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(io.workspace) + parts_bytes(parts_of(io, d)));
-    const RowsArgs r{io, d, p, lists};
+    const RowsArgs r{io, d, p, lists, d.ctas <= dev.sm_count};
     if (io.bf16) kda_beam_rows_kernel<true><<<(unsigned)d.ctas, kThreads, 0, stream>>>(r);
     else kda_beam_rows_kernel<false><<<(unsigned)d.ctas, kThreads, 0, stream>>>(r);
     count_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const uint64_t segments = (uint64_t)io.beams * most;
-    const JoinArgs j{io, d, most, (int)((segments * io.num + kThreads - 1) / kThreads),
+    // Threads for all candidates, kJoinPer each at most.
+    int threads = kThreads;
+    while (threads < kJoinThreads && segments * io.num > (uint64_t)kJoinPer * threads) threads *= 2;
+    const JoinArgs j{io, d, most, (int)((segments * io.num + threads - 1) / threads),
                      (uint32_t)(((1ull << 31) + segments - 1) / segments), (uint32_t)(((1ull << 31) + most - 1) / most), p, lists};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)io.groups);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kda_beam_join_kernel, j);
+    auto join = threads == kThreads ? kda_beam_join_kernel<kThreads> : threads == 512 ? kda_beam_join_kernel<512> : kda_beam_join_kernel<kJoinThreads>;
+    e = cudaLaunchKernelEx(&cfg, join, j);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
