@@ -166,6 +166,27 @@ def test_large_vocabulary_of_many_rows():
     run(x, scores, 8, keep=True)
 
 
+@pytest.mark.parametrize("kind", ["random", "ascending", "descending"])
+def test_long_segments(kind):
+    """Rows of which a CTA has 44 tiles, 64 candidates and more from every look: its list is brought down in between."""
+    G, K, V, num = 80, 8, 41 * 4096 + 7, 64
+    x, scores = make(G, K, V, seed=3, scale=2.0)
+    if kind != "random":
+        ramp = torch.arange(V, device=DEV) * 2e-4
+        x.copy_(ramp if kind == "ascending" else ramp.flip(0))
+        x.add_(torch.arange(G * K, device=DEV)[:, None] * 7e-5)
+    with Ctx() as ctx:
+        got = select(ctx, x, scores, num)
+        assert kda.kda_sync_status(ctx) == kda.KDA_OK
+    for g in range(G):
+        y = beam_ref.scores64(x[g * K:(g + 1) * K], scores[g:g + 1], None, 0)
+        s, k, v = (t[0] for t in beam_ref.best(y, num + 1))
+        assert bool(((got[0][g].double() - s[:num]).abs() <= SLACK + 2.0 ** -23 * s[:num].abs()).all()), g
+        apart = torch.cat([torch.ones(1, dtype=torch.bool, device=DEV), s[:-1] - s[1:] > 2 * SLACK])
+        sure = apart[:-1] & apart[1:]
+        assert bool(((got[1][g] == v[:num]) & (got[2][g] == k[:num] + g * K))[sure].all()), g
+
+
 @pytest.mark.parametrize("bf16", [False, True])
 def test_many_small_groups(bf16):
     """More rows than CTAs by far."""
