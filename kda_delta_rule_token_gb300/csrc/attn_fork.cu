@@ -28,6 +28,7 @@
 #include <atomic>
 
 #include "attn_internal.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace kda {
@@ -62,6 +63,7 @@ __global__ void __launch_bounds__(kThreads) kda_attn_fork_kernel(const AttnForkI
     __shared__ int s_tile[kThreads][kCols + 1];
     __shared__ int s_ended[kThreads];
     __shared__ int s_warp[kWarps];
+    ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const Space ws = space_of(io.workspace, io.B, io.max_pages);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(kThreads) kda_attn_fork_pages_kernel(const Att
 
 // rows x 128 values of one head's keys or values, from page src to page dst.
 __global__ void __launch_bounds__(128) kda_attn_copy_pages_kernel(const AttnCopyIO io, const AttnLayer l, int* err) {
+    ptx::griddep_wait();
     const int i = blockIdx.x, src = io.src[i], dst = io.dst[i];
     if (src == -1) return;
     if ((unsigned)src >= (unsigned)l.num_pages || (unsigned)dst >= (unsigned)l.num_pages) {
@@ -323,29 +326,15 @@ cudaError_t launch_attn_fork(const AttnLayer& l, const AttnForkIO& io, const Dev
     int over = (int)((dev.sm_count + cols - 1) / cols);
     const int most = (io.B + kWarps - 1) / kWarps;
     if (over > most) over = most;
-    kda_attn_fork_kernel<<<dim3(cols, (unsigned)over), kThreads, (size_t)io.B * 8, stream>>>(io, l.page_shift, l.num_pages, err_word);
-    count_launches(1);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_behind(kda_attn_fork_kernel, dim3(cols, (unsigned)over), kThreads, (size_t)io.B * 8, stream, io, l.page_shift,
+                                        l.num_pages, err_word);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(cols);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kda_attn_fork_pages_kernel, io, l.page_shift, l.num_pages, err_word);
-    count_launches(1);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_behind(kda_attn_fork_pages_kernel, dim3(cols), kThreads, 0, stream, io, l.page_shift, l.num_pages, err_word);
 }
 
 cudaError_t launch_attn_copy_pages(const AttnLayer& l, const AttnCopyIO& io, int* err_word, cudaStream_t stream) {
     const unsigned parts = l.Hkv < 32768 ? 2u * l.Hkv : 65535u;
-    kda_attn_copy_pages_kernel<<<dim3((unsigned)io.n, parts), 128, 0, stream>>>(io, l, err_word);
-    count_launches(1);
-    return cudaGetLastError();
+    return launch_behind(kda_attn_copy_pages_kernel, dim3((unsigned)io.n, parts), 128, 0, stream, io, l, err_word);
 }
 
 }  // namespace kda

@@ -42,6 +42,7 @@
 #include "attn_ptx.cuh"
 #include "attn_rows.cuh"
 #include "attn_tma.cuh"
+#include "launch.cuh"
 
 namespace kda {
 namespace {
@@ -146,6 +147,7 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long* s_w
 __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(const Args a, int* err) {
     __shared__ long long s_warp[32];
     __shared__ int s_group[kNear], s_len[kNear];   // group_of and group_len, where they fit
+    ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const AttnSharedIO& io = a.io;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -265,7 +267,8 @@ __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(cons
 
 // The check of the offsets alone.
 __global__ void __launch_bounds__(256) kda_attn_shared_check_kernel(const AttnSharedIO io, int* err) {
-    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();   // (now that the inputs are there, which the next kernel does not wait for)
     bool bad = false;
     for (int g = threadIdx.x; g < io.groups; g += 256) {
         const int from = io.cu_groups[g], to = io.cu_groups[g + 1];
@@ -564,20 +567,6 @@ __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_
 
 std::atomic<bool> g_attr_done[64];
 
-// A launch that may start beside the one before it in the stream.
-cudaLaunchConfig_t beside(cudaLaunchAttribute& attr, unsigned grid, int threads, size_t smem, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cfg;
-}
-
 }  // namespace
 
 size_t attn_shared_workspace_bytes(const AttnLayer& l, int B, const DeviceInfo& dev) {
@@ -605,11 +594,7 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     // tokens, 32 / 8 heads, 9.7 MB at most: 10.5 us and 13.5; 24 MB are 3.5 us of the copy rate).
     constexpr long long kSmall = 24LL << 20;
     if (!io.groups || ((long long)io.B * l.Hkv * io.max_pages << l.page_shift) * kHeadDim * (l.e4m3 ? 2 : 4) <= kSmall) {
-        if (io.groups) {
-            kda_attn_shared_check_kernel<<<1, 256, 0, stream>>>(io, err_word);
-            count_launches(1);
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        }
+        if (io.groups && (e = launch_behind(kda_attn_shared_check_kernel, dim3(1), 256, 0, stream, io, err_word)) != cudaSuccess) return e;
         AttnIO d{};
         d.B = d.N = io.B;
         d.q = io.q;
@@ -646,14 +631,9 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     a.v_scale = l.v_scale;
     const int grid = dev.sm_count * kCtasPerSm;
     a.warps = grid * kWarps;
-    kda_attn_shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, err_word);
-    count_launches(1);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = beside(attr, (unsigned)grid, kThreads, sizeof(Smem), stream);
-    e = cudaLaunchKernelEx(&cfg, l.e4m3 ? kda_attn_shared_few_kernel<true> : kda_attn_shared_few_kernel<false>, a, maps.k_decode,
-                           maps.v_decode, err_word);
-    count_launches(1);
+    if ((e = launch_behind(kda_attn_shared_plan_kernel, dim3(1), kPlanThreads, 0, stream, a, err_word)) != cudaSuccess) return e;
+    e = launch_behind(l.e4m3 ? kda_attn_shared_few_kernel<true> : kda_attn_shared_few_kernel<false>, dim3((unsigned)grid), kThreads, sizeof(Smem),
+                      stream, a, maps.k_decode, maps.v_decode, err_word);
     if (e != cudaSuccess) return e;
     if (has_many) {
         many.B = io.groups;
@@ -680,10 +660,8 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     out.gate = io.gate;
     const long long rows = (long long)io.B * l.Hq;
     const bool wide = rows <= kWideRows;
-    cfg = beside(attr, (unsigned)(wide ? rows : (rows + 7) / 8), 256, 0, stream);
-    e = cudaLaunchKernelEx(&cfg, wide ? kda_attn_shared_join_kernel<true> : kda_attn_shared_join_kernel<false>, a, out);
-    count_launches(1);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_behind(wide ? kda_attn_shared_join_kernel<true> : kda_attn_shared_join_kernel<false>, dim3((unsigned)(wide ? rows : (rows + 7) / 8)),
+                         256, 0, stream, a, out);
 }
 
 }  // namespace kda

@@ -8,6 +8,8 @@
 // take the same chunk at about the same time, so that all but one read of it come from
 // L2: 256 sequences of 64 heads with bf16 states into other buffers, 1,021 MB, 151 us.
 #include "beam_internal.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
 
 namespace kda {
 namespace {
@@ -19,6 +21,7 @@ constexpr int kCopy = kThreads * kLoads * 16;
 __global__ void __launch_bounds__(kThreads) kda_beam_reorder_kernel(const BeamReorderIO io, int chunks0, int* err) {
     const int b = (int)(blockIdx.x % (unsigned)io.B);
     int chunk = (int)(blockIdx.x / (unsigned)io.B);
+    ptx::griddep_wait();
     const int from = io.rows[b];
     if (from == -1 || (io.in_place && from == b)) return;
     // In place, a sequence that moves away may be gone before it is read.
@@ -47,9 +50,7 @@ cudaError_t launch_beam_reorder(const BeamReorderIO& io, const DeviceInfo&, int*
     const long long chunks0 = (io.bytes[0] + kCopy - 1) / kCopy, chunks1 = (io.bytes[1] + kCopy - 1) / kCopy;
     const long long grid = (chunks0 + chunks1) * io.B;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kda_beam_reorder_kernel<<<(unsigned)grid, kThreads, 0, stream>>>(io, (int)chunks0, err_word);
-    count_launches(1);
-    return cudaGetLastError();
+    return launch_behind(kda_beam_reorder_kernel, dim3((unsigned)grid), kThreads, 0, stream, io, (int)chunks0, err_word);
 }
 
 }  // namespace kda

@@ -41,6 +41,7 @@
 
 #include "attn_mma.cuh"
 #include "beam_internal.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace kda {
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
     __shared__ uint16_t s_again[kThreads];
     // The join's CTAs may come now where SMs have room for them, else at the last segment's end: beside rows
     // they cost more than they save (64 rows of 50257 18.2 us instead of 13.0, 4 of 32000 7.7 instead of 8.2).
+    ptx::griddep_wait();
     if (a.early) ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.io.num;
     const long long last = a.deal.first(blockIdx.x + 1LL);
@@ -789,10 +791,8 @@ cudaError_t launch_beam_select(const BeamSelectIO& io, const DeviceInfo& dev, cu
     Part* p = static_cast<Part*>(io.workspace);
     uint64_t* lists = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(io.workspace) + parts_bytes(parts_of(io, d)));
     const RowsArgs r{io, d, p, lists, d.ctas <= dev.sm_count};
-    if (io.bf16) kda_beam_rows_kernel<true><<<(unsigned)d.ctas, kThreads, 0, stream>>>(r);
-    else kda_beam_rows_kernel<false><<<(unsigned)d.ctas, kThreads, 0, stream>>>(r);
-    count_launches(1);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_behind(io.bf16 ? kda_beam_rows_kernel<true> : kda_beam_rows_kernel<false>, dim3((unsigned)d.ctas), kThreads, 0,
+                                        stream, r);
     if (e != cudaSuccess) return e;
     const uint64_t segments = (uint64_t)io.beams * most;
     // Threads for all candidates, kJoinPer each at most.
@@ -800,19 +800,8 @@ cudaError_t launch_beam_select(const BeamSelectIO& io, const DeviceInfo& dev, cu
     while (threads < kJoinThreads && segments * io.num > (uint64_t)kJoinPer * threads) threads *= 2;
     const JoinArgs j{io, d, most, (int)((segments * io.num + threads - 1) / threads),
                      (uint32_t)(((1ull << 31) + segments - 1) / segments), (uint32_t)(((1ull << 31) + most - 1) / most), p, lists};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)io.groups);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     auto join = threads == kThreads ? kda_beam_join_kernel<kThreads> : threads == 512 ? kda_beam_join_kernel<512> : kda_beam_join_kernel<kJoinThreads>;
-    e = cudaLaunchKernelEx(&cfg, join, j);
-    count_launches(1);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_behind(join, dim3((unsigned)io.groups), threads, 0, stream, j);
 }
 
 }  // namespace kda
