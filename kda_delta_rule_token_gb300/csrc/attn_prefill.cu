@@ -233,10 +233,15 @@ __device__ __forceinline__ void next_part(const PrefillArgs& a, const Ctl& ctl, 
         if ((int)blockIdx.x >= sc.ctas) return;
         const long long from = sc.all * blockIdx.x / sc.ctas, to = sc.all * (blockIdx.x + 1) / sc.ctas;
         if (c.k < 0) {
-            int lo = 0, hi = a.io.B - 1;   // the last group whose segments begin at or before `from`
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (a.io.group_start[mid] <= from) lo = mid; else hi = mid - 1;
+            // The last group whose segments begin at or before `from`; the warp's lanes look together.
+            const int lane = threadIdx.x & 31;
+            int lo = 0, n = a.io.B;
+            while (n > 1) {
+                const int step = (n + 31) >> 5;
+                const uint32_t begun = __ballot_sync(0xffffffffu, lane * step < n && a.io.group_start[lo + min(lane * step, n)] <= from);
+                const int k = 31 - __clz((int)begun);
+                lo += k * step;
+                n = min(step, n - k * step);
             }
             c.k = lo;
             c.unit = from;
