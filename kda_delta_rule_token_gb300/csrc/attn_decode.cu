@@ -231,7 +231,8 @@ __device__ __noinline__ void mend_rows(const DecodeArgs& a, long long left, int 
     }
 }
 
-template <bool kE4m3, int kRowTiles>
+// kShared: the whole of kda_attn_decode_shared where it passes over its groups.
+template <bool kE4m3, int kRowTiles, bool kShared>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<kRowTiles>())
 kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, int* err) {
@@ -252,6 +253,7 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
     uint64_t* empty = sm.empty + group * kDepth; // the group's other warp has read the stage
     uint8_t* ring = sm.ring + group * kDepth * kStageBytes;
 
+    if (kShared) ptx::griddep_wait();   // the first kernel of its call, launched behind other work
     ptx::griddep_launch_dependents();
     if (lane == 0 && lead)
         for (int s = 0; s < kDepth; ++s) {
@@ -771,11 +773,15 @@ kda_attn_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_consta
 // the CTA that holds the first part (search: the blockIdx.x-th of those that
 // hold one), blockIdx.y over query rows, four channels per lane.  Few parts: a
 // warp per row.  Many: the eight warps share a row's.
-__global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, int ctas, bool search) {
+template <bool kShared>
+__global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, int ctas, bool search, int* err) {
     __shared__ float4 s_acc[8][32];
     __shared__ float s_ref[8], s_sum[8];
     __shared__ uint32_t s_used[kJoinCtas / 32];
     ptx::griddep_wait();
+    if (kShared && blockIdx.x == 0 && blockIdx.y == 0)
+        for (int g = (int)threadIdx.x; g < a.io.check_groups; g += 256)
+            if (bad_offsets(a.io.check_cu, g, a.io.B)) atomicOr(err, kErrAttnIndex);
     int first = (int)blockIdx.x;
     if (search) {
         for (int i = (int)threadIdx.x; i < kJoinCtas; i += 256) {
@@ -852,9 +858,9 @@ __global__ void __launch_bounds__(256) kda_attn_join_kernel(const DecodeArgs a, 
 
 std::atomic<bool> g_attr_done[64];
 
-template <bool kE4m3, int kRowTiles>
+template <bool kE4m3, int kRowTiles, bool kShared>
 cudaError_t set_smem() {
-    return cudaFuncSetAttribute(kda_attn_decode_kernel<kE4m3, kRowTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(kda_attn_decode_kernel<kE4m3, kRowTiles, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)sizeof(Smem<kRowTiles>));
 }
 
@@ -876,10 +882,14 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
                                  int* err_word, cudaStream_t stream, bool beside) {
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
-        cudaError_t e = set_smem<false, 1>();
-        if (e == cudaSuccess) e = set_smem<false, 2>();
-        if (e == cudaSuccess) e = set_smem<true, 1>();
-        if (e == cudaSuccess) e = set_smem<true, 2>();
+        cudaError_t e = set_smem<false, 1, false>();
+        if (e == cudaSuccess) e = set_smem<false, 2, false>();
+        if (e == cudaSuccess) e = set_smem<true, 1, false>();
+        if (e == cudaSuccess) e = set_smem<true, 2, false>();
+        if (e == cudaSuccess) e = set_smem<false, 1, true>();
+        if (e == cudaSuccess) e = set_smem<false, 2, true>();
+        if (e == cudaSuccess) e = set_smem<true, 1, true>();
+        if (e == cudaSuccess) e = set_smem<true, 2, true>();
         if (e != cudaSuccess) return e;
         g_attr_done[dev.device].store(true, std::memory_order_release);
     }
@@ -905,8 +915,8 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
     const bool two = most_rows > 16;
     const int ctas = dev.sm_count * (two ? ctas_per_sm<2>() : ctas_per_sm<1>());
     const int grid = (int)(most < ctas ? most : ctas);
-    auto kernel = l.e4m3 ? (two ? kda_attn_decode_kernel<true, 2> : kda_attn_decode_kernel<true, 1>)
-                         : (two ? kda_attn_decode_kernel<false, 2> : kda_attn_decode_kernel<false, 1>);
+    auto kernel = l.e4m3 ? (two ? kda_attn_decode_kernel<true, 2, false> : kda_attn_decode_kernel<true, 1, false>)
+                         : (two ? kda_attn_decode_kernel<false, 2, false> : kda_attn_decode_kernel<false, 1, false>);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -917,9 +927,12 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = beside ? 1 : 0;
+    if (io.check_groups)
+        kernel = l.e4m3 ? (two ? kda_attn_decode_kernel<true, 2, true> : kda_attn_decode_kernel<true, 1, true>)
+                        : (two ? kda_attn_decode_kernel<false, 2, true> : kda_attn_decode_kernel<false, 1, true>);
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, maps.k_decode, maps.v_decode, err_word);
     count_launches(1);
-    if (e != cudaSuccess || grid == 1) return e;   // one CTA leaves no parts
+    if (e != cudaSuccess || (grid == 1 && !io.check_groups)) return e;   // one CTA leaves no parts
     // More than eight parts to a request and head, whose rows a CTA joins one
     // after another: CTAs for those that hold a first part only, and more of them
     // over the rows (one request of 30000 keys and 32 / 8 heads, 8 tokens: 65 -> 45 us,
@@ -933,7 +946,7 @@ cudaError_t launch_attn_few_rows(const AttnLayer& l, const AttnMaps& maps, const
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kda_attn_join_kernel, a, grid, search);
+    e = cudaLaunchKernelEx(&cfg, io.check_groups ? kda_attn_join_kernel<true> : kda_attn_join_kernel<false>, a, grid, search, err_word);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

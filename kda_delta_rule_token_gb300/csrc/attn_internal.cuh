@@ -121,7 +121,15 @@ struct AttnIO {
     const long long* group_start;    // [B + 1] units of work before the group's, none for one that is not its own
     const int* group_pairs;          // [B] pairs of token tiles before the group's
     int2* parts;                     // [pairs][Hkv] (out) first part's slot, -1 if there is but one, and last part's
+    // Offsets of groups that the few-row kernel's join looks over: kda_attn_decode_shared where it passes over them.
+    int check_groups;
+    const int* check_cu;             // [check_groups + 1]
 };
+
+// Whether group g's requests are none that there are, or out of order.
+__device__ __forceinline__ bool bad_offsets(const int* cu, int g, int B) {
+    return cu[g] < 0 || cu[g + 1] < cu[g] || cu[g + 1] > B;
+}
 
 struct AttnSharedIO {
     int B, groups;

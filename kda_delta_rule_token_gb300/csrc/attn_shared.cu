@@ -165,10 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(cons
         to0 = io.cu_groups[warp + 1];
         len0 = io.prefix_lens[warp];
     }
-    for (int g = tid; g < io.groups; g += kPlanThreads) {
-        const int from = io.cu_groups[g], to = io.cu_groups[g + 1];
-        bad |= from < 0 || to < from || to > io.B;
-    }
+    for (int g = tid; g < io.groups; g += kPlanThreads) bad |= bad_offsets(io.cu_groups, g, io.B);
     for (int b = tid; b < io.B; b += kPlanThreads) group_of[b] = -1;
     bad = __syncthreads_or(bad);
     if (bad && tid == 0) atomicOr(err, kErrAttnIndex);
@@ -263,18 +260,6 @@ __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(cons
         a.start[count] = total;
         a.many_start[io.groups] = many_total;
     }
-}
-
-// The check of the offsets alone.
-__global__ void __launch_bounds__(256) kda_attn_shared_check_kernel(const AttnSharedIO io, int* err) {
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();   // (now that the inputs are there, which the next kernel does not wait for)
-    bool bad = false;
-    for (int g = threadIdx.x; g < io.groups; g += 256) {
-        const int from = io.cu_groups[g], to = io.cu_groups[g + 1];
-        bad |= from < 0 || to < from || to > io.B;
-    }
-    if (bad) atomicOr(err, kErrAttnIndex);
 }
 
 // Where the notes on an item's parts begin.
@@ -591,10 +576,9 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     carve(a, many, io.workspace, l, io.B, dev);
     // A block table too narrow for so many bytes of keys and values, were all of its pages full and nothing
     // shared: kda_attn_decode's kernels, whose two launches take less than four do (four requests of 600
-    // tokens, 32 / 8 heads, 9.7 MB at most: 10.5 us and 13.5; 24 MB are 3.5 us of the copy rate).
+    // tokens, 32 / 8 heads, 9.7 MB at most: 9.6 us and 13.5; 24 MB are 3.5 us of the copy rate).
     constexpr long long kSmall = 24LL << 20;
     if (!io.groups || ((long long)io.B * l.Hkv * io.max_pages << l.page_shift) * kHeadDim * (l.e4m3 ? 2 : 4) <= kSmall) {
-        if (io.groups && (e = launch_behind(kda_attn_shared_check_kernel, dim3(1), 256, 0, stream, io, err_word)) != cudaSuccess) return e;
         AttnIO d{};
         d.B = d.N = io.B;
         d.q = io.q;
@@ -607,6 +591,8 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
         d.lse = io.lse;
         d.workspace = a.decode;
         d.drop = io.drop;
+        d.check_groups = io.groups;
+        d.check_cu = io.cu_groups;
         return launch_attn_few_rows(l, maps, d, dev, err_word, stream, io.groups > 0);
     }
     a.io = io;

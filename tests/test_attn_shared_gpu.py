@@ -196,6 +196,15 @@ def test_offsets_that_are_not_ascending(cu):
     layer.done()
 
 
+@pytest.mark.parametrize("cu,status", [([0, 1], kda.KDA_OK), ([0, 2], kda.KDA_ERR_INVALID_ARG), ([-1, 1], kda.KDA_ERR_INVALID_ARG)])
+def test_offsets_of_a_call_of_one_cta(cu, status):
+    layer = Layer(1, 1, 16)
+    fill(layer, [10], narrow=True)
+    layer.groups = [(cu[0], cu[1], 5)]
+    verify(layer, queries(layer, 1), [10], status=status)
+    layer.done()
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("n", [4, 70])
