@@ -130,7 +130,7 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long* s_w
     }
     if (lane == 31) s_warp[warp] = x;
     __syncthreads();
-    long long w = s_warp[lane];
+    long long w = lane < (int)(blockDim.x >> 5) ? s_warp[lane] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, w, d);
@@ -150,12 +150,12 @@ __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(cons
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const AttnSharedIO& io = a.io;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
     const int shift = max(a.page_shift, a.tile_shift), most = io.max_pages << a.page_shift;
     int* group_of = io.B <= kNear ? s_group : a.group_of;
     int* group_len = io.B <= kNear ? s_len : a.group_len;   // (no more groups than requests)
     const int count = io.groups + io.B;
-    const int per = (count + kPlanThreads - 1) / kPlanThreads, i0 = min(count, tid * per), i1 = min(count, i0 + per);
+    const int per = (count + threads - 1) / threads, i0 = min(count, tid * per), i1 = min(count, i0 + per);
     bool bad = false;
     // What this thread's first item and this warp's first group need, on the way beside the offsets.
     const int kv0 = i0 < i1 && i0 >= io.groups ? io.kv_lens[i0 - io.groups] : 0;
@@ -165,11 +165,11 @@ __global__ void __launch_bounds__(kPlanThreads) kda_attn_shared_plan_kernel(cons
         to0 = io.cu_groups[warp + 1];
         len0 = io.prefix_lens[warp];
     }
-    for (int g = tid; g < io.groups; g += kPlanThreads) bad |= bad_offsets(io.cu_groups, g, io.B);
-    for (int b = tid; b < io.B; b += kPlanThreads) group_of[b] = -1;
+    for (int g = tid; g < io.groups; g += threads) bad |= bad_offsets(io.cu_groups, g, io.B);
+    for (int b = tid; b < io.B; b += threads) group_of[b] = -1;
     bad = __syncthreads_or(bad);
     if (bad && tid == 0) atomicOr(err, kErrAttnIndex);
-    for (int g = warp; g < io.groups; g += kPlanThreads / 32) {
+    for (int g = warp; g < io.groups; g += threads / 32) {
         const bool near = g == warp;
         const int from = bad ? 0 : near ? from0 : io.cu_groups[g], to = bad ? 0 : near ? to0 : io.cu_groups[g + 1];
         const int len = min(max(near ? len0 : io.prefix_lens[g], 0), most) >> shift << shift;
@@ -617,7 +617,10 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     a.v_scale = l.v_scale;
     const int grid = dev.sm_count * kCtasPerSm;
     a.warps = grid * kWarps;
-    if ((e = launch_behind(kda_attn_shared_plan_kernel, dim3(1), kPlanThreads, 0, stream, a, err_word)) != cudaSuccess) return e;
+    // A thread for each request and group, a warp for each group: no more meet than have something to do.
+    int threads = 128;
+    while (threads < kPlanThreads && (threads < io.B + io.groups || threads < 32LL * io.groups)) threads *= 2;
+    if ((e = launch_behind(kda_attn_shared_plan_kernel, dim3(1), threads, 0, stream, a, err_word)) != cudaSuccess) return e;
     e = launch_behind(l.e4m3 ? kda_attn_shared_few_kernel<true> : kda_attn_shared_few_kernel<false>, dim3((unsigned)grid), kThreads, sizeof(Smem),
                       stream, a, maps.k_decode, maps.v_decode, err_word);
     if (e != cudaSuccess) return e;
