@@ -25,11 +25,11 @@
 //    who had the first and the last one noted it.
 //
 // Measured (a kernel's share: what the call takes longer when it is launched twice): 32 prompts of up
-// to 4,100 tokens with 1 to 30 requests each, 32 / 8 heads, bf16, 534 MB: 123 us, 0.64 of
+// to 4,100 tokens with 1 to 30 requests each, 32 / 8 heads, bf16, 534 MB: 122 us, 0.65 of
 // the copy rate (the few-row kernel 53 us and the tensor core kernel about 57, 5 TB/s each; plan
-// 5, join 7).  64 requests behind 8,192 tokens, 65 MB: 38 us (plan 4, few-row kernel 9,
-// tensor core kernel 15, join 9, whose 20 MB of parts come from L2; kda_attn_decode: 178 us); of
-// the tensor core kernel's 15 its 3 or 4 key tiles take 4, the parts' way out 4.  256 requests of 64 heads
+// 5, join 7).  64 requests behind 8,192 tokens, 65 MB: 36 us (plan 3, few-row kernel 9,
+// tensor core kernel 15, join 7, whose 20 MB of parts come from L2; kda_attn_decode: 178 us); of
+// the tensor core kernel's 15 its 3 or 4 key tiles take 6, the parts' way out 3 (6.4 TB/s).  256 requests of 64 heads
 // behind four documents of up to 16,300 tokens in e4m3, 128 GFLOP: 131 us (plan 6, few-row kernel
 // 17, tensor core kernel about 97, join 11).  The requests' own keys in the decode's kernel,
 // where four warps share a request's tiles and meet at its end: 15 us slower.  Queries and
@@ -465,15 +465,18 @@ kda_attn_shared_few_kernel(const __grid_constant__ Args a, const __grid_constant
         for (int i = used; i < issued; ++i) ptx::mbar_wait_timed(&full[i % kStages], (uint32_t)(i / kStages) & 1u);
 }
 
-// Rows of the join that get a CTA each, whose warps share the parts.
+// Rows of the join that get a CTA each, whose warps share the parts (64 samples, 2,048 rows of 20 parts: eight
+// warps 37.9 us of the call, four and two 35.9; 8,192 rows and 16,384 of few parts, a warp each 122 and 131, four
+// 126 and 144).
 constexpr int kWideRows = 4096;
+constexpr int kSplit = 4;
 
-// kWide: a CTA per row, its eight warps taking parts in turn; else a warp per row.  Four
+// kWide: a CTA per row, its warps taking parts in turn; else a warp per row.  Four
 // channels per lane.
 template <bool kWide>
 __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_constant__ Args a, const AttnIO out) {
-    __shared__ float4 s_acc[8][32];
-    __shared__ float s_ref[8], s_sum[8];
+    __shared__ float4 s_acc[kSplit][32];
+    __shared__ float s_ref[kSplit], s_sum[kSplit];
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = a.io.groups;
     const uint32_t rows = (uint32_t)a.io.B * a.Hq, row = kWide ? blockIdx.x : blockIdx.x * 8 + warp;
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_
     // behind it up to the last one's.
     auto add_parts = [&](int2 note, const float* slots, size_t slot_floats, size_t refs, int r, uint32_t at) {
         if (note.x < 0) {   // finished: its lse, and a sum of 1
-            if (!kWide || (nth++ & 7) == warp) {
+            if (!kWide || (nth++ & (kSplit - 1)) == warp) {
                 const float l = a.lse[at];
                 add(l * kLog2e, l == -INFINITY ? 0.f : l == l ? 1.f : l, *reinterpret_cast<const float4*>(a.o + (size_t)at * kHeadDim + 4 * lane), 1.f);
             }
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_
         }
         const int parts = (note.y >> 1) - (note.x >> 1) + 1;
 #pragma unroll 4
-        for (int p = kWide ? (warp - nth) & 7 : 0; p < parts; p += kWide ? 8 : 1) {
+        for (int p = kWide ? (warp - nth) & (kSplit - 1) : 0; p < parts; p += kWide ? kSplit : 1) {
             const float* s = slots + (size_t)(p ? (note.x & ~1) + 2 * p : note.x) * slot_floats;
             const float2 rl = *reinterpret_cast<const float2*>(s + refs + 2 * r);
             add(rl.x, rl.y, *reinterpret_cast<const float4*>(s + (size_t)r * kHeadDim + 4 * lane), vs);
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_
         __syncthreads();
         if (warp) return;
 #pragma unroll
-        for (int w = 1; w < 8; ++w) add(s_ref[w], s_sum[w], s_acc[w][lane], 1.f);
+        for (int w = 1; w < kSplit; ++w) add(s_ref[w], s_sum[w], s_acc[w][lane], 1.f);
     }
     const float n = sum != 0.f ? 1.f / sum : 0.f;
     mma::store4(out, (size_t)row * kHeadDim + 4 * lane, make_float4(acc.x * n, acc.y * n, acc.z * n, acc.w * n), sum != 0.f);
@@ -650,7 +653,7 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     const long long rows = (long long)io.B * l.Hq;
     const bool wide = rows <= kWideRows;
     return launch_behind(wide ? kda_attn_shared_join_kernel<true> : kda_attn_shared_join_kernel<false>, dim3((unsigned)(wide ? rows : (rows + 7) / 8)),
-                         256, 0, stream, a, out);
+                         wide ? 32 * kSplit : 256, 0, stream, a, out);
 }
 
 }  // namespace kda
