@@ -6,7 +6,7 @@
 // are wanted if that is partly full; a request that does not go on lets go of its
 // pages, and those that nobody holds any more are free.  What moves is the table
 // (8 bytes an entry), 8 bytes for each page whose holders change, and the copies'
-// rows.  The bookkeeping is bound by the latency of two dependent launches: the
+// rows.  The bookkeeping is bound by the latency of two steps: the
 // table's new entries follow from the old ones alone, but which page a copy gets
 // from how many pages are released before it.
 //
@@ -17,14 +17,16 @@
 //    count by one atomic, and the last holder's lane notes the page if nobody is
 //    left.  A column is one warp's, in the order of the requests, so what is noted
 //    does not depend on scheduling.
-//  * kda_attn_fork_pages_kernel: puts the columns' freed pages on the stack one
-//    after another and hands the stack's end out to the copies.
+//  * put_pages: puts the columns' freed pages on the stack one after another and hands the
+//    stack's end out to the copies.  The CTAs of tables of up to 256 columns are a cluster
+//    and meet at its barrier in between (a launch less: 2.5 us of the host's time, the GPU's is the
+//    same); wider ones take a second, dependent launch.
 //
 // kda_attn_copy_pages_kernel copies rows, bound by HBM or by its launch.
 //
 // Four requests of 1,100 tokens: 6.6 us, and 1.6 for one layer's copies; 256 of 8,000
 // in pages of 128, a quarter of which ends: 15.6 us (the chain of loads and the
-// atomics of one column after another) and 4.4 (16 MB).  The host's calls take 10 and 4 us.
+// atomics of one column after another) and 4.4 (16 MB).  The host's calls take 8 and 4 us.
 #include <atomic>
 
 #include "attn_internal.cuh"
@@ -38,6 +40,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCols = 32;            // columns of the table per CTA
 constexpr int kColsPerWarp = kCols / kWarps;
+constexpr int kMostCluster = 8;      // CTAs that may meet in one launch
 
 // Workspace: pages that each column frees, requests that want a copy, in order,
 // and their number, the columns' freed pages.
@@ -56,6 +59,86 @@ __device__ __forceinline__ int length_of(const AttnForkIO& io, int b, int shift)
     return min(max(io.kv_lens[b], 0), io.max_pages << shift);
 }
 
+// The columns' freed pages onto the stack, one column after another, and its end to the copies; by the CTAs of the columns.
+__device__ __forceinline__ void put_pages(const AttnForkIO& io, int shift, int num_pages, int* err) {
+    __shared__ int s_before[kWarps], s_all[kWarps];
+    const Space ws = space_of(io.workspace, io.B, io.max_pages);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int col0 = blockIdx.x * kCols;
+    // Pages freed by the columns before this CTA's, and by all.
+    int before = 0, all = 0;
+    for (int c = tid; c < io.max_pages; c += kThreads) {
+        const int n = ws.freed[c];
+        all += n;
+        if (c < col0) before += n;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (lane == 0) {
+        s_before[warp] = before;
+        s_all[warp] = all;
+    }
+    __syncthreads();
+    before = all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        before += s_before[w];
+        all += s_all[w];
+    }
+    const int count = min(max(io.free_count[0], 0), io.free_capacity);
+    const int wants = ws.wants[0];
+
+    // Copy `nth` gets the page.
+    auto give = [&](int nth, int page) {
+        const int b = ws.wanting[nth], r = io.rows[b], len = length_of(io, r, shift), col = len >> shift;
+        const int from = io.block_table[(size_t)r * io.max_pages + col];
+        if ((unsigned)page >= (unsigned)num_pages || (unsigned)from >= (unsigned)num_pages) atomicOr(err, kErrAttnIndex);
+        io.new_table[(size_t)b * io.max_pages + col] = page;
+        io.copy_src[b] = from;
+        io.copy_dst[b] = page;
+        io.copy_rows[b] = len & ((1 << shift) - 1);
+    };
+
+    // This CTA's columns, a warp for each in turn: freed page k goes onto the stack, and to copy all - 1 - k.
+    int mine = col0 + lane < io.max_pages ? ws.freed[col0 + lane] : 0, upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+    }
+    for (int c = warp; c < kCols; c += kWarps) {
+        const int n = __shfl_sync(0xffffffffu, mine, c), from = before + __shfl_sync(0xffffffffu, upto, c) - n;
+        for (int i = lane; i < n; i += 32) {
+            const int page = ws.pages[(size_t)(col0 + c) * io.B + i], k = from + i;
+            io.page_refs[page] = 0;
+            if (count + k < io.free_capacity) io.free_pages[count + k] = page;
+            else atomicOr(err, kErrAttnIndex);
+            if (all - 1 - k < wants) give(all - 1 - k, page);
+        }
+    }
+    if (blockIdx.x) return;
+    // Copies beyond the freed pages get those that were free before; the last may get none.
+    for (int nth = all + tid; nth < wants; nth += kThreads)
+        if (nth - all < count) give(nth, io.free_pages[count - 1 - (nth - all)]);
+    // These hold nothing: each by a warp.
+    const int served = (int)min((long long)wants, (long long)all + count);
+    for (int nth = served + warp; nth < wants; nth += kWarps) {
+        const int b = ws.wanting[nth], r = io.rows[b], whole = length_of(io, r, shift) >> shift;
+        for (int c = lane; c < whole; c += 32) {
+            const int page = io.block_table[(size_t)r * io.max_pages + c];
+            if ((unsigned)page < (unsigned)num_pages) atomicSub(&io.page_refs[page], 1);
+        }
+        if (lane == 0) io.new_lens[b] = 0;
+    }
+    if (tid == 0) {
+        io.info[0] = all;
+        io.info[1] = served;
+        io.info[2] = min(count + all, io.free_capacity) - served;
+        io.info[3] = wants - served;
+    }
+}
+
+// kAll: the grid's x is a cluster, and what the columns free is put away here too.
+template <bool kAll>
 __global__ void __launch_bounds__(kThreads) kda_attn_fork_kernel(const AttnForkIO io, int shift, int num_pages, int* err) {
     extern __shared__ int s_dyn[];
     int* s_children = s_dyn;             // [B] requests that go on from request b
@@ -85,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) kda_attn_fork_kernel(const AttnForkI
     }
     __syncthreads();
 
-    if (blockIdx.x == 0 && blockIdx.y == gridDim.y - 1) {
+    if (blockIdx.x == 0 && blockIdx.y == (kAll ? 0 : gridDim.y - 1)) {
         if (bad) atomicOr(err, kErrAttnIndex);
         // Lengths, and the requests that want a copy, in their order.
         const int per = (io.B + kThreads - 1) / kThreads, b0 = min(io.B, tid * per), b1 = min(io.B, b0 + per);
@@ -195,84 +278,17 @@ __global__ void __launch_bounds__(kThreads) kda_attn_fork_kernel(const AttnForkI
 #pragma unroll
         for (int c = 0; c < kColsPerWarp; ++c)
             if (col0 + warp * kColsPerWarp + c < io.max_pages) ws.freed[col0 + warp * kColsPerWarp + c] = freed[c];
+    if (kAll) {
+        __threadfence();
+        __syncthreads();
+        ptx::cluster_sync();
+        put_pages(io, shift, num_pages, err);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads) kda_attn_fork_pages_kernel(const AttnForkIO io, int shift, int num_pages, int* err) {
-    __shared__ int s_before[kWarps], s_all[kWarps];
     ptx::griddep_wait();
-    const Space ws = space_of(io.workspace, io.B, io.max_pages);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int col0 = blockIdx.x * kCols;
-    // Pages freed by the columns before this CTA's, and by all.
-    int before = 0, all = 0;
-    for (int c = tid; c < io.max_pages; c += kThreads) {
-        const int n = ws.freed[c];
-        all += n;
-        if (c < col0) before += n;
-    }
-    before = __reduce_add_sync(0xffffffffu, before);
-    all = __reduce_add_sync(0xffffffffu, all);
-    if (lane == 0) {
-        s_before[warp] = before;
-        s_all[warp] = all;
-    }
-    __syncthreads();
-    before = all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        before += s_before[w];
-        all += s_all[w];
-    }
-    const int count = min(max(io.free_count[0], 0), io.free_capacity);
-    const int wants = ws.wants[0];
-
-    // Copy `nth` gets the page.
-    auto give = [&](int nth, int page) {
-        const int b = ws.wanting[nth], r = io.rows[b], len = length_of(io, r, shift), col = len >> shift;
-        const int from = io.block_table[(size_t)r * io.max_pages + col];
-        if ((unsigned)page >= (unsigned)num_pages || (unsigned)from >= (unsigned)num_pages) atomicOr(err, kErrAttnIndex);
-        io.new_table[(size_t)b * io.max_pages + col] = page;
-        io.copy_src[b] = from;
-        io.copy_dst[b] = page;
-        io.copy_rows[b] = len & ((1 << shift) - 1);
-    };
-
-    // This CTA's columns, a warp for each in turn: freed page k goes onto the stack, and to copy all - 1 - k.
-    int mine = col0 + lane < io.max_pages ? ws.freed[col0 + lane] : 0, upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += y;
-    }
-    for (int c = warp; c < kCols; c += kWarps) {
-        const int n = __shfl_sync(0xffffffffu, mine, c), from = before + __shfl_sync(0xffffffffu, upto, c) - n;
-        for (int i = lane; i < n; i += 32) {
-            const int page = ws.pages[(size_t)(col0 + c) * io.B + i], k = from + i;
-            io.page_refs[page] = 0;
-            if (count + k < io.free_capacity) io.free_pages[count + k] = page;
-            else atomicOr(err, kErrAttnIndex);
-            if (all - 1 - k < wants) give(all - 1 - k, page);
-        }
-    }
-    if (blockIdx.x) return;
-    // Copies beyond the freed pages get those that were free before; the last may get none.
-    for (int nth = all + tid; nth < wants; nth += kThreads)
-        if (nth - all < count) give(nth, io.free_pages[count - 1 - (nth - all)]);
-    // These hold nothing: each by a warp.
-    const int served = (int)min((long long)wants, (long long)all + count);
-    for (int nth = served + warp; nth < wants; nth += kWarps) {
-        const int b = ws.wanting[nth], r = io.rows[b], whole = length_of(io, r, shift) >> shift;
-        for (int c = lane; c < whole; c += 32) {
-            const int page = io.block_table[(size_t)r * io.max_pages + c];
-            if ((unsigned)page < (unsigned)num_pages) atomicSub(&io.page_refs[page], 1);
-        }
-        if (lane == 0) io.new_lens[b] = 0;
-    }
-    if (tid == 0) {
-        io.info[0] = all;
-        io.info[1] = served;
-        io.info[2] = min(count + all, io.free_capacity) - served;
-        io.info[3] = wants - served;
-    }
+    put_pages(io, shift, num_pages, err);
 }
 
 // rows x 128 values of one head's keys or values, from page src to page dst.
@@ -316,8 +332,9 @@ cudaError_t launch_attn_fork(const AttnLayer& l, const AttnForkIO& io, const Dev
                              cudaStream_t stream) {
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     if (!g_attr_done[dev.device].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(kda_attn_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   KDA_ATTN_MAX_PLAN_REQUESTS * 8);
+        cudaError_t e = cudaFuncSetAttribute(kda_attn_fork_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, KDA_ATTN_MAX_PLAN_REQUESTS * 8);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kda_attn_fork_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, KDA_ATTN_MAX_PLAN_REQUESTS * 8);
         if (e != cudaSuccess) return e;
         g_attr_done[dev.device].store(true, std::memory_order_release);
     }
@@ -326,8 +343,11 @@ cudaError_t launch_attn_fork(const AttnLayer& l, const AttnForkIO& io, const Dev
     int over = (int)((dev.sm_count + cols - 1) / cols);
     const int most = (io.B + kWarps - 1) / kWarps;
     if (over > most) over = most;
-    const cudaError_t e = launch_behind(kda_attn_fork_kernel, dim3(cols, (unsigned)over), kThreads, (size_t)io.B * 8, stream, io, l.page_shift,
-                                        l.num_pages, err_word);
+    const dim3 grid(cols, (unsigned)over);
+    if (cols <= (unsigned)kMostCluster)
+        return launch_clusters_behind(kda_attn_fork_kernel<true>, grid, (int)cols, kThreads, (size_t)io.B * 8, stream, io, l.page_shift, l.num_pages,
+                                      err_word);
+    const cudaError_t e = launch_behind(kda_attn_fork_kernel<false>, grid, kThreads, (size_t)io.B * 8, stream, io, l.page_shift, l.num_pages, err_word);
     if (e != cudaSuccess) return e;
     return launch_behind(kda_attn_fork_pages_kernel, dim3(cols), kThreads, 0, stream, io, l.page_shift, l.num_pages, err_word);
 }

@@ -14,22 +14,31 @@
 
 namespace kda {
 
+// `cluster`: CTAs of a cluster along the grid's x.
 template <class... Params, class... Args>
-cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args&&... args) {
-    cudaLaunchAttribute attr[1];
+cudaError_t launch_clusters_behind(void (*kernel)(Params...), dim3 grid, int cluster, int threads, size_t smem, cudaStream_t stream, Args&&... args) {
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
     count_launches(1);
     if (e != cudaSuccess) cudaGetLastError();   // returned, not left for others to find
     return e;
+}
+
+template <class... Params, class... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args&&... args) {
+    return launch_clusters_behind(kernel, grid, 1, threads, smem, stream, std::forward<Args>(args)...);
 }
 
 }  // namespace kda

@@ -120,7 +120,7 @@ class Model:
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
-@pytest.mark.parametrize("B,width,seed", [(1, 1, 0), (2, 3, 1), (4, 40, 2), (9, 33, 3), (33, 70, 4), (70, 5, 5), (256, 9, 6), (300, 34, 7)])
+@pytest.mark.parametrize("B,width,seed", [(1, 1, 0), (2, 3, 1), (4, 40, 2), (9, 33, 3), (33, 70, 4), (70, 5, 5), (256, 9, 6), (300, 34, 7), (6, 256, 8), (6, 257, 9)])
 def test_requests_that_grow_and_fork(B, width, page, seed):
     m = Model(B, width, page, B * width, seed)
     layer = Layer(m.pages, page=page)
