@@ -29,7 +29,7 @@
 // Measured (both launches, inputs in HBM but for what L2 kept of them): 512 rows of
 // 131072 logits in fp32, 268 MB, 53 us, of which the rows take 47 (5.7 TB/s, 0.84
 // of the copy rate): looks at the largest logits, 3000 cycles each, which other CTAs of the SM
-// cover in part.  128 rows of 131071 in bf16, 33 MB, 22 us: one or two looks to a CTA's 8 tiles.  Four rows of
+// cover in part.  128 rows of 131071 in bf16, 33 MB, 21 us: a look to a CTA's 8 tiles and the join.  Four rows of
 // 32000, 7.7 us: two launches, and in the join a chain of loads, 64-bit arithmetic and instructions
 // that no CTA before has fetched.  What runs once per segment or CTA is short for the same reason (the list
 // ranked by loops written out 2 us more, the join with 16 candidates to a thread 1 us).  A look every four tiles 57 us; before that, the bound found bit
@@ -51,7 +51,7 @@ constexpr int kThreads = 256;
 constexpr int kPer = 16;               // logits of a thread per tile
 constexpr int kTile = kThreads * kPer;
 constexpr int kSub = 8;                // tiles between two looks at the largest logits
-static_assert(kSub * kPer % 64 == 0, "four logits of a thread for each lane of half a warp");
+static_assert(64 % kPer == 0 && kPer % 4 == 0, "four logits of a thread for each lane of half a warp");
 constexpr int kList = 768;             // candidates that a CTA holds
 constexpr int kThin = 256;             // more than these are brought down to num
 static_assert(kThin + KDA_BEAM_MAX_NUM <= kList, "room for num candidates");
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
 
     if (begin < end) load(begin);
     for (int t0 = begin, t1; t0 < end; t0 = t1) {
-        t1 = min(t0 + kSub, end);
+        t1 = end - t0 <= kSub + 2 ? end : t0 + kSub;   // (the head and the tail are no look of their own)
         const float sum0 = sum, low0 = low;
         float scale0 = 1.f, most;
         uint32_t bound, top;
@@ -387,10 +387,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
             low = l0;
         }
         __syncthreads();
-        constexpr int kTurns = kSub * kPer / 64;
-        const int i_mine = 4 * (lane & 15) % kPer;
-        for (int k = tid / 16; k < total * kTurns; k += kThreads / 16) {
-            const int thread = s_again[k / kTurns], t_mine = t0 + (k % kTurns * 64 + 4 * (lane & 15)) / kPer;
+        const int i_mine = 4 * (lane & 15) % kPer, turns = ((t1 - t0) * kPer + 63) / 64;
+        for (int k = tid / 16; k < total * turns; k += kThreads / 16) {
+            const int turn = k / total, thread = s_again[k - turn * total], t_mine = t0 + (turn * 64 + 4 * (lane & 15)) / kPer;
             const uint8_t* mine_at = base + (long long)token(t_mine, i_mine, 0) * kBytes;
             float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (t_mine < t1 && there(t_mine, i_mine, thread)) {
