@@ -90,7 +90,8 @@ struct Args {
     void* decode;            // of kda_attn_decode's kernels
     float* o;                // [2 B][Hq][128] results over the prefix, then of own keys
     float* lse;              // [2 B][Hq]
-    int warps;
+    int warps;               // of the few-row kernel
+    int many_ctas;
 };
 
 size_t carve(Args& a, AttnIO& many, void* workspace, const AttnLayer& l, int B, const DeviceInfo& dev) {
@@ -496,10 +497,11 @@ __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_
         acc.w = acc.w * e + v.w * df;
     };
     const float vs = a.v_scale ? a.v_scale[h] : 1.f;
-    int nth = 0;   // parts so far: kWide, part p is warp p % 8's
+    int nth = 0;   // parts so far: kWide, part p is warp p % kSplit's
     // Parts from the noted slots, two slots to a worker: the first part's, then the first slot of each worker
     // behind it up to the last one's.
-    auto add_parts = [&](int2 note, const float* slots, size_t slot_floats, size_t refs, int r, uint32_t at) {
+    // A worker whose wait ran out left no note: what stands there instead is followed nowhere.
+    auto add_parts = [&](int2 note, const float* slots, int workers, size_t slot_floats, size_t refs, int r, uint32_t at) {
         if (note.x < 0) {   // finished: its lse, and a sum of 1
             if (!kWide || (nth++ & (kSplit - 1)) == warp) {
                 const float l = a.lse[at];
@@ -507,6 +509,7 @@ __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_
             }
             return;
         }
+        if ((unsigned)note.y >= 2u * workers) return;
         const int parts = (note.y >> 1) - (note.x >> 1) + 1;
 #pragma unroll 4
         for (int p = kWide ? (warp - nth) & (kSplit - 1) : 0; p < parts; p += kWide ? kSplit : 1) {
@@ -534,9 +537,9 @@ __global__ void __launch_bounds__(256) kda_attn_shared_join_kernel(const __grid_
             row_in = side * 128 + (in - side * a.tokens) * a.G + head;
         }
     }
-    if (own) add_parts(own_note, a.slots, kSlotFloats, kRows * kHeadDim, head % kRows, rows + row);
+    if (own) add_parts(own_note, a.slots, a.warps, kSlotFloats, kRows * kHeadDim, head % kRows, rows + row);
     if (g >= 0)
-        add_parts(note, many ? a.many_slots : a.slots, many ? 2 * 128 * (kHeadDim + 2) : kSlotFloats, (many ? 2 * 128 : kRows) * kHeadDim, row_in, row);
+        add_parts(note, many ? a.many_slots : a.slots, many ? a.many_ctas : a.warps, many ? 2 * 128 * (kHeadDim + 2) : kSlotFloats, (many ? 2 * 128 : kRows) * kHeadDim, row_in, row);
     if (kWide) {
         s_acc[warp][lane] = acc;
         if (lane == 0) {
@@ -620,6 +623,7 @@ cudaError_t launch_attn_shared(const AttnLayer& l, const AttnMaps& maps, const A
     a.v_scale = l.v_scale;
     const int grid = dev.sm_count * kCtasPerSm;
     a.warps = grid * kWarps;
+    a.many_ctas = dev.sm_count;
     // A thread for each request and group, a warp for each group: no more meet than have something to do.
     int threads = 128;
     while (threads < kPlanThreads && (threads < io.B + io.groups || threads < 32LL * io.groups)) threads *= 2;

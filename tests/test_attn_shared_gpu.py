@@ -409,6 +409,32 @@ def test_refusals():
     layer.done()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,held", [(5, 0x3C), (40, 0x3C), (40, 0), (40, 0xFF)])
+def test_a_copy_that_never_comes(n, held, e4m3, monkeypatch):
+    """The bounded waits on it run out, whatever the workspace held: reported once, nothing written outside, and the
+    device works on."""
+    spans, lens = [(0, n, 300)], [320 + b for b in range(n)]
+
+    def layer_of():
+        layer = Layer(8, 2, 16, e4m3)
+        fill(layer, lens)
+        share(layer, spans, lens)
+        return layer
+
+    monkeypatch.setenv("KDA_FAULT_INJECT", "attn_drop")
+    layer = layer_of()
+    monkeypatch.delenv("KDA_FAULT_INJECT")
+    ws = Guard((kda.kda_attn_shared_workspace_bytes(layer.attn, n),), torch.uint8, fill=held)
+    attend(layer, queries(layer, n), lens, ws=ws)
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_ERR_TIMEOUT
+    assert kda.kda_attn_sync_status(layer.attn) == kda.KDA_OK
+    layer.done()
+    again = layer_of()
+    verify(again, queries(again, n), lens)
+    again.done()
+
+
 def test_injected_launch_failure(monkeypatch):
     for name in ("attn_decode_shared", "all"):
         monkeypatch.setenv("KDA_FAULT_INJECT", name)
