@@ -57,7 +57,8 @@ KDA_API size_t kda_beam_select_workspace_bytes(const kda_ctx *ctx, int groups, i
  *   out_scores [groups][num] fp32, out_tokens [groups][num] int32,
  *   out_rows   [groups][num] int32: r of the beam that goes on
  *   workspace kda_beam_select_workspace_bytes bytes, 16-byte aligned
- * fp32 and int32 arrays are 4-byte aligned.  groups == 0 is a no-op.  beams from 1
+ * fp32 and int32 arrays are 4-byte aligned; no output may overlap an input.  groups == 0
+ * is a no-op.  beams from 1
  * to 64 (more, or a larger num: KDA_ERR_UNSUPPORTED), beams * vocab below 2^31,
  * groups * beams up to 2^30.  The result does not depend on the order in which
  * parts of the work end.

@@ -359,6 +359,29 @@ def test_reorder_errors_into_other_buffers():
     assert torch.equal(other_inner[0][1], left)
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_reorder_many_sequences(in_place, bf16):
+    """More than are listed at a time, with an error among them."""
+    B = 5001
+    S = torch.randint(0, 2 ** 15, (B, 1, D, D), device=DEV, dtype=torch.int16 if bf16 else torch.int32)
+    conv = torch.randn(B, 3, 3 * D, device=DEV)
+    rows = [b - 1 if b % 7 == 1 else -1 if b % 7 == 3 else b for b in range(B)]
+    rows[4500] = B
+    if not in_place:
+        rows[2], rows[5000] = 4999, 0
+    S_out, conv_out = (S, conv) if in_place else (torch.zeros_like(S), torch.zeros_like(conv))
+    old, old_conv = S_out.clone(), conv_out.clone()
+    stays = torch.tensor([r in (-1, B) for r in rows], device=DEV)
+    at = torch.tensor([0 if r in (-1, B) else r for r in rows], device=DEV)
+    want = torch.where(stays[:, None, None, None], old, S[at])
+    want_conv = torch.where(stays[:, None, None], old_conv, conv[at])
+    with Ctx() as ctx:
+        kda.kda_beam_reorder(ctx, B, torch.tensor(rows, dtype=torch.int32, device=DEV), S, conv, S_out=S_out, conv_out=conv_out)
+        assert kda.kda_sync_status(ctx) == kda.KDA_ERR_INVALID_ARG
+    assert torch.equal(S_out, want) and torch.equal(conv_out, want_conv)
+
+
 def test_reorder_beyond_4_gib():
     B, H = 300, 256
     S = torch.zeros(B, H, D, D, device=DEV)
