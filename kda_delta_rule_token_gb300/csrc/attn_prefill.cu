@@ -406,17 +406,16 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
         ctl.dead = 0;
         ctl.busiest = 0;
         ctl.kissued = ctl.vissued = ctl.raws = 0;
-        joins(a.io.workspace)[blockIdx.x].m = 0;
+        if (!kShared) joins(a.io.workspace)[blockIdx.x].m = 0;
     }
     Sched sc;
     if (kShared) {
-        // (Beside the few-row kernel, whose start has waited for the plan.)
+        // The plan's sums, and what the work before the call wrote, are only sure to be seen behind this
+        // kernel's own wait: that the few-row kernel before it has waited for the plan does not reach here.
+        ptx::griddep_wait();
         sc.all = a.io.group_start[a.io.B];
         sc.ctas = (int)min((long long)gridDim.x, sc.all);
-        if ((int)blockIdx.x >= sc.ctas) {
-            ptx::griddep_wait();   // ends after it
-            return;
-        }
+        if ((int)blockIdx.x >= sc.ctas) return;
         if (warp == kWarpMma) tc::alloc(&ctl.tmem, 512);
     } else {
         // Segments of all requests.
@@ -1051,7 +1050,6 @@ kda_attn_prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap
     }
     __syncthreads();
     if (warp == kWarpMma) tc::dealloc(tm, 512);
-    if (kShared) ptx::griddep_wait();
 }
 
 // Joins the parts of segments cut between CTAs, a warp per row, four channels

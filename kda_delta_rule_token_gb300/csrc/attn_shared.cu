@@ -18,8 +18,8 @@
 //    of tiles, copied by TMA ahead of their use across the ends of requests, and no warp
 //    waits for another.
 //  * the prompts' tensor core kernel (attn_prefill.cu), without a causal edge: prefixes of
-//    more rows, cut into equal ranges of key tiles for all SMs.  Its CTAs start as
-//    the few-row kernel's end.
+//    more rows, cut into equal ranges of key tiles for all SMs.  Its CTAs come as the few-row
+//    kernel's end, and wait for all of it before they look at the plan.
 //  * the join: a warp per row, or a CTA where rows are few.  What one warp (or CTA) had
 //    of a row alone came to the workspace as a finished result, what several had as parts;
 //    who had the first and the last one noted it.
@@ -315,7 +315,7 @@ kda_attn_shared_few_kernel(const __grid_constant__ Args a, const __grid_constant
     if (tid == 0) sm.dead = 0;
     ptx::fence_mbar_init();
     __syncthreads();
-    ptx::griddep_wait();               // the plan; the launch behind this one needs it too
+    ptx::griddep_wait();               // the plan
     ptx::griddep_launch_dependents();
 
     const int count = a.io.groups + a.io.B;

@@ -1,0 +1,29 @@
+"""Kernels that come while the work before them still runs (programmatic dependent launch), by their source: what
+they may have read too early shows in no result for as long as it happens to be there already."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kda_delta_rule_token_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def body(text, kernel):
+    """What stands between the braces of a __global__ function."""
+    at = re.search(r"__global__[^{;]*\b%s\s*\([^{;]*\{" % kernel, text).end()
+    depth, end = 1, at
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[end], 0)
+        end += 1
+    return text[at:end - 1]
+
+
+def test_the_tensor_core_kernel_waits_before_it_reads_the_plan():
+    """Its launch behind the few-row kernel does not bring it what the plan, two launches before, wrote."""
+    text = body(source("attn_prefill.cu"), "kda_attn_prefill_kernel")
+    shared = text[text.index("if (kShared) {"):]
+    assert shared.index("griddep_wait();") < shared.index("group_start[")
+    assert "a.io" not in text[:text.index("if (kShared) {")].replace("if (!kShared) joins(a.io.workspace)", "")
