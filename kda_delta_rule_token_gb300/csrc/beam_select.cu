@@ -556,7 +556,8 @@ template <int kMost>
 __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) {
     __shared__ double s_from[KDA_BEAM_MAX_BEAMS];   // a score is (logit - most) + from
     __shared__ double s_most[KDA_BEAM_MAX_BEAMS];
-    __shared__ int s_first[KDA_BEAM_MAX_BEAMS], s_segments[KDA_BEAM_MAX_BEAMS];   // (none of a beam at its end)
+    __shared__ int s_first[KDA_BEAM_MAX_BEAMS], s_segments[KDA_BEAM_MAX_BEAMS];
+    __shared__ bool s_done[KDA_BEAM_MAX_BEAMS];     // at its end: its segments hold anything
     __shared__ Groups s_group;
     __shared__ Choice s_best[kMost], s_bound;
     __shared__ Choice s_list[kJoinList];
@@ -572,10 +573,11 @@ __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) 
         const long long row = (long long)g * K + k;
         const int from = a.deal.cta_of(row * a.deal.per_row), to = a.deal.cta_of((row + 1) * a.deal.per_row - 1);
         s_first[k] = (int)row + from;
-        s_segments[k] = done && done[k] ? 0 : to - from + 1;
+        s_segments[k] = to - from + 1;
     }
     __syncthreads();
     ptx::griddep_wait();
+    const bool ended = done && tid < K && done[tid];   // (under way beside the lists)
 
     // This thread's share of the segments' lists, taken as all first candidates, then all second ones,
     // ..., in turns by the groups of threads of the bound below: each group has some of every beam.
@@ -595,10 +597,13 @@ __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) 
         }
     }
 
+    if (tid < K) s_done[tid] = ended;
+    __syncthreads();
+
     // The beams' sums of exp(x - most).  Where one is NaN, the beam has nothing to offer.
     for (int k = warp; k < K; k += threads / 32) {
         const int here = s_segments[k];
-        if (here == 0) continue;
+        if (s_done[k]) continue;
         const Part* p = a.parts + s_first[k];
         const uint64_t* l = a.lists + (size_t)s_first[k] * n;
         // Up to 32 parts and 64 candidates at once: one latency for all of them.
@@ -648,11 +653,11 @@ __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) 
             // Of NaN the key tells nothing.
             const bool number = ((uint64_t)__double_as_longlong(score) << 1) <= 0xffe0000000000000ull;
             const uint64_t key = key_of(score);
-            mine[j] = Choice{own[j] && number && key > kLowestKey ? key : 0,
+            mine[j] = Choice{own[j] && !s_done[k] && number && key > kLowestKey ? key : 0,
                              (uint32_t)k * (uint32_t)a.io.vocab + (uint32_t)token_of(own[j])};
         } else {
             mine[j] = Choice{0, 0};
-            if (done && tid < K && done[tid] && scores[tid] > -INFINITY)
+            if (ended && scores[tid] > -INFINITY)
                 mine[j] = Choice{key_of(scores[tid]), (uint32_t)tid * (uint32_t)a.io.vocab + (uint32_t)a.io.end_token};
         }
         if (better(mine[j], best)) best = mine[j];

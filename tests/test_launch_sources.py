@@ -3,7 +3,11 @@ they may have read too early shows in no result for as long as it happens to be 
 import os
 import re
 
+import pytest
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kda_delta_rule_token_gb300", "csrc")
+# Memory that a call's arguments or its workspace name, read (or written) by an index, or a member array of one.
+ACCESS = re.compile(r"\b(?:io|a|g|done|scores|group_of|group_len)(?:\.\w+)*\s*\[|->\w+\s*\[|atomic\w+\((?:&?io|&?a\.|err)")
 
 
 def source(name):
@@ -19,6 +23,23 @@ def body(text, kernel):
         depth += {"{": 1, "}": -1}.get(text[end], 0)
         end += 1
     return text[at:end - 1]
+
+
+def kernels(name):
+    return re.findall(r"__global__[^{;]*?\b(kda_\w+)\s*\(", source(name))
+
+
+FILES = ["beam_select.cu", "beam_reorder.cu", "attn_fork.cu", "attn_shared.cu"]
+
+
+def test_there_are_such_kernels():
+    assert sum(len(kernels(f)) for f in FILES) >= 9
+
+
+@pytest.mark.parametrize("file,kernel", [(f, k) for f in FILES for k in kernels(f)])
+def test_nothing_is_read_before_the_wait(file, kernel):
+    before, wait, _ = body(source(file), kernel).partition("griddep_wait();")
+    assert wait and not ACCESS.findall(before)
 
 
 def test_the_tensor_core_kernel_waits_before_it_reads_the_plan():
