@@ -189,6 +189,14 @@ __device__ __forceinline__ uint32_t group_bound(uint32_t best, int num, Groups& 
     return sm.bound;
 }
 
+// 16 bytes of the logits.  (Behind the wait for the work that writes them, so an ordinary load; written out, as
+// the compiler's own costs three registers more than a thread has.)
+__device__ __forceinline__ uint4 load16(const uint4* from) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(from));
+    return v;
+}
+
 // How the tiles are dealt: row r's are units [r * per_row, (r + 1) * per_row), CTA c
 // has units [units * c / ctas, units * (c + 1) / ctas).  Segments are numbered
 // r + c, which no two share.
@@ -267,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
         }
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
-            if (there(t, j * kVec, tid)) raw[j] = __ldg(body + (t * kLoads + j) * kThreads + tid);
+            if (there(t, j * kVec, tid)) raw[j] = load16(body + (t * kLoads + j) * kThreads + tid);
     };
     float x[kPer];
     auto unpack = [&](int t) {

@@ -42,6 +42,13 @@ def test_nothing_is_read_before_the_wait(file, kernel):
     assert wait and not ACCESS.findall(before)
 
 
+def test_no_loads_of_what_is_constant():
+    """Loads that may come from a cache which is not kept in step want memory that no one writes while the kernel
+    lives; what a kernel reads that comes early may be written until its wait is over."""
+    for file in FILES + ["attn_prefill.cu", "attn_decode.cu", "attn_rows.cuh"]:
+        assert not re.search(r"__ldg|\.nc\b", source(file)), file
+
+
 def test_the_tensor_core_kernel_waits_before_it_reads_the_plan():
     """Its launch behind the few-row kernel does not bring it what the plan, two launches before, wrote."""
     text = body(source("attn_prefill.cu"), "kda_attn_prefill_kernel")
