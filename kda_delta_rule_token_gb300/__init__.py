@@ -480,6 +480,22 @@ def _words(t, name, count, size=4):
     raise ValueError(f"{name} must have {count} dense elements of {size} bytes: shape {tuple(t.shape)}, strides {t.stride()}, {t.dtype}")
 
 
+_kinds = {}   # of torch's types: 1 what the library takes as bf16, 0 as fp32; found on first use
+
+
+def _bf16(t, name):
+    """Whether a tensor is bf16 (or its raw view), or fp32.  Others, fp16 among them, are refused: the library
+    would take them for one of these."""
+    kind = _kinds.get(t.dtype)
+    if kind is None:
+        if not _kinds:
+            import torch
+            _kinds.update({torch.float32: 0, torch.bfloat16: 1, torch.int16: 1, torch.uint16: 1})
+            return _bf16(t, name)
+        raise ValueError(f"{name} must be fp32 or bf16 (or bf16's raw view): {t.dtype}")
+    return kind
+
+
 def kda_beam_select_workspace_bytes(ctx, groups, beams, vocab, num) -> int:
     return int(load().kda_beam_select_workspace_bytes(ctx, int(groups), int(beams), int(vocab), int(num)))
 
@@ -488,12 +504,14 @@ def kda_beam_select(ctx, groups, beams, logits, scores, num, out_scores, out_tok
                     done=None, end_token=0, keep_places=False, workspace_bytes=0, stream=None) -> None:
     """The num best continuations of every group (kda_beam.h).  logits [groups * beams, vocab]: fp32 or bf16
     (or its raw view), rows at any stride; done: bytes or truth values."""
-    if logits.dim() != 2 or logits.shape[0] < groups * beams or (logits.stride(1) != 1 and logits.shape[1] != 1):
-        raise ValueError(f"logits must be [{groups * beams}, vocab] with dense rows: shape {tuple(logits.shape)}, "
-                         f"strides {logits.stride()}")
-    vocab = logits.shape[1]
-    stride = logits.stride(0) if logits.shape[0] > 1 else vocab   # of one row any stride will do
-    _check(load().kda_beam_select(ctx, int(groups), int(beams), vocab, _p(logits), int(logits.element_size() == 2), stride,
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [{groups * beams}, vocab]: shape {tuple(logits.shape)}")
+    (rows, vocab), (stride, step) = logits.shape, logits.stride()
+    if rows < groups * beams or (step != 1 and vocab != 1):
+        raise ValueError(f"logits must be [{groups * beams}, vocab] with dense rows: shape {(rows, vocab)}, strides {(stride, step)}")
+    if rows == 1:
+        stride = vocab   # of one row any stride will do
+    _check(load().kda_beam_select(ctx, int(groups), int(beams), vocab, logits.data_ptr(), _bf16(logits, "logits"), stride,
                                   _words(scores, "scores", groups * beams), _words(done, "done", groups * beams, 1),
                                   int(end_token), int(num), 1 if keep_places else 0,
                                   _words(out_scores, "out_scores", groups * num), _words(out_tokens, "out_tokens", groups * num),
