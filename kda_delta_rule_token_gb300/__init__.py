@@ -265,7 +265,7 @@ def kda_prefill_varlen(ctx, B, cu_seqlens, total_T, q, k, v, z, beta_logit, gate
 def _nbytes(buf, given):
     if buf is None or isinstance(buf, int) or given:
         return int(given)
-    return buf.numel() * buf.element_size()
+    return buf.nbytes
 
 
 def kda_bind_lowrank(ctx, hidden, rank, W_fa, W_fb, W_bp) -> None:
@@ -426,10 +426,14 @@ def kda_attn_shared_workspace_bytes(attn, B) -> int:
 def kda_attn_decode_shared(attn, B, q, block_table, kv_lens, groups, cu_groups, prefix_lens, o, workspace, *, max_pages=None,
                            gate_logit=None, o_f32=None, lse=None, workspace_bytes=0, stream=None) -> None:
     """kda_attn_decode where group g's requests, cu_groups[g] to cu_groups[g + 1] - 1, share their first prefix_lens[g] keys."""
-    _check(load().kda_attn_decode_shared(attn, B, _dense(q, "q"), _p(block_table), _pitch(block_table, max_pages), _p(kv_lens),
-                                         int(groups), _dense(cu_groups, "cu_groups"), _dense(prefix_lens, "prefix_lens"),
-                                         _dense(gate_logit, "gate_logit"), _dense(o, "o"), _is_f32(o, o_f32), _dense(lse, "lse"),
-                                         _p(workspace), _nbytes(workspace, workspace_bytes), _stream(stream)),
+    f32 = _is_f32(o, o_f32)
+    table, pitch = _table(block_table, "block_table", B, max_pages)
+    offsets = groups if 0 < groups <= B else -1   # (no offsets of no groups, or of so many that the library refuses the call)
+    _check(load().kda_attn_decode_shared(attn, B, _values(q, "q", B, 1), table, pitch,
+                                         _words(kv_lens, "kv_lens", B), int(groups), _words(cu_groups, "cu_groups", offsets + 1),
+                                         _words(prefix_lens, "prefix_lens", offsets), _values(gate_logit, "gate_logit", B, 0),
+                                         _values(o, "o", B, 1 - f32), f32, _words(lse, "lse", B), _p(workspace),
+                                         _nbytes(workspace, workspace_bytes), _stream(stream)),
            "kda_attn_decode_shared")
 
 
@@ -494,6 +498,24 @@ def _bf16(t, name):
             return _bf16(t, name)
         raise ValueError(f"{name} must be fp32 or bf16 (or bf16's raw view): {t.dtype}")
     return kind
+
+
+def _values(t, name, B, bf16):
+    """The address of a dense tensor of at least B rows, bf16 (or its raw view) or fp32."""
+    if t is None or t.__class__ is int:
+        return t
+    if _bf16(t, name) == bf16 and t.is_contiguous() and t.shape[0] >= B:
+        return t.data_ptr()
+    raise ValueError(f"{name} must have {B} dense rows of {'bf16' if bf16 else 'fp32'}: shape {tuple(t.shape)}, strides {t.stride()}, {t.dtype}")
+
+
+def _table(t, name, B, given):
+    """The address of an int32 block table of at least B rows, and its pitch (_pitch)."""
+    if t.__class__ is int:
+        return t, int(given)
+    if t.element_size() != 4 or (t.shape[0] < B and t.dim() == 2):
+        raise ValueError(f"{name} must have {B} rows of int32: shape {tuple(t.shape)}, {t.dtype}")
+    return t.data_ptr(), _pitch(t, given)
 
 
 def kda_beam_select_workspace_bytes(ctx, groups, beams, vocab, num) -> int:

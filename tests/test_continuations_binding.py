@@ -18,3 +18,37 @@ def test_select_takes_both_types_and_the_raw_view(rec):  # noqa: F811
     for dtype in (torch.float32, BF, torch.int16, torch.uint16):
         select(torch.zeros(6, 50).to(dtype))
     assert [a[5] for _, a in rec.calls] == [0, 1, 1, 1]
+
+
+def shared(B=3, **change):
+    args = dict(q=torch.zeros(3, 4, D, dtype=BF), block_table=ints(3, 7), kv_lens=ints(3), groups=2, cu_groups=ints(3),
+                prefix_lens=ints(2), o=torch.zeros(3, 4, D, dtype=BF))
+    args.update(change)
+    kda.kda_attn_decode_shared(1, B, **args, workspace=16, workspace_bytes=1 << 30, stream=0)
+
+
+LONG = torch.int64
+
+
+@pytest.mark.parametrize("change", [
+    dict(cu_groups=torch.zeros(3, dtype=LONG)), dict(prefix_lens=torch.zeros(2, dtype=LONG)), dict(kv_lens=torch.zeros(3, dtype=LONG)),
+    dict(block_table=torch.zeros(3, 7, dtype=LONG)), dict(cu_groups=ints(2)), dict(prefix_lens=ints(1)), dict(kv_lens=ints(2)),
+    dict(block_table=ints(2, 7)), dict(q=torch.zeros(3, 4, D)), dict(q=torch.zeros(3, 4, D, dtype=torch.float16)),
+    dict(q=torch.zeros(2, 4, D, dtype=BF)), dict(o=torch.zeros(3, 4, D, dtype=torch.float16)), dict(o=torch.zeros(3, 4, D), o_f32=False),
+    dict(o_f32=True), dict(o=torch.zeros(2, 4, D, dtype=BF)), dict(o=torch.zeros(3, 4, D, dtype=torch.float64)),
+    dict(gate_logit=torch.zeros(3, 4, D, dtype=BF)), dict(gate_logit=torch.zeros(2, 4, D)), dict(lse=torch.zeros(3, 4, dtype=torch.float64)),
+    dict(lse=torch.zeros(2))])
+def test_shared_decode_refuses_types_and_short_tensors(rec, change):  # noqa: F811
+    with pytest.raises(ValueError):
+        shared(**change)
+    assert not rec.calls
+
+
+def test_shared_decode_takes_what_it_may_be_given(rec):  # noqa: F811
+    shared()
+    shared(q=torch.zeros(5, 4, D, dtype=torch.int16), o=torch.zeros(4, 4, D), gate_logit=torch.zeros(3, 4, D), lse=torch.zeros(3, 4))
+    shared(q=16, o=16, o_f32=True, kv_lens=16, block_table=16, cu_groups=16, prefix_lens=16, max_pages=9)
+    shared(groups=0, cu_groups=None, prefix_lens=None, block_table=ints(3, 20)[:, 3:7])
+    shared(groups=5)     # for the library to refuse
+    shared(B=-1)
+    assert [a[11] for _, a in rec.calls] == [0, 1, 1, 0, 0, 0] and [a[4] for _, a in rec.calls][2:4] == [9, 20]
