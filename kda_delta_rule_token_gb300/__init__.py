@@ -543,12 +543,21 @@ def kda_beam_select(ctx, groups, beams, logits, scores, num, out_scores, out_tok
 
 def kda_beam_reorder(ctx, B, rows, S, conv_state, *, S_out=None, conv_out=None, stream=None) -> None:
     """S[b], conv_state[b] <- S[rows[b]], conv_state[rows[b]] in place, or into S_out and conv_out (kda_beam.h)."""
-    S_out, conv_out = S if S_out is None else S_out, conv_state if conv_out is None else conv_out
-    if S_out.element_size() != S.element_size():
-        raise ValueError(f"S is {S.dtype}, S_out {S_out.dtype}")
-    _check(load().kda_beam_reorder(ctx, int(B), _words(rows, "rows", B), _dense(S, "S"), _dense(conv_state, "conv_state"),
-                                   _dense(S_out, "S_out"), _dense(conv_out, "conv_out"), int(S.element_size() == 2),
+    size = S.element_size()
+    if size not in (2, 4):
+        raise ValueError(f"S must be fp32 or bf16: {S.dtype}")
+    S_at, conv_at = _sequences(S, "S", B, size), _sequences(conv_state, "conv_state", B, 4)
+    _check(load().kda_beam_reorder(ctx, int(B), _words(rows, "rows", B), S_at, conv_at,
+                                   S_at if S_out is None else _sequences(S_out, "S_out", B, size),
+                                   conv_at if conv_out is None else _sequences(conv_out, "conv_out", B, 4), int(size == 2),
                                    _stream(stream)), "kda_beam_reorder")
+
+
+def _sequences(t, name, B, size):
+    """The address of a dense tensor of at least B sequences' values of `size` bytes."""
+    if t.element_size() == size and t.is_contiguous() and t.shape[0] >= B:
+        return t.data_ptr()
+    raise ValueError(f"{name} must hold {B} dense sequences of values of {size} bytes: shape {tuple(t.shape)}, strides {t.stride()}, {t.dtype}")
 
 
 def kda_testing_bounded_wait(ctx, limit_us, stream=None) -> None:

@@ -52,3 +52,16 @@ def test_shared_decode_takes_what_it_may_be_given(rec):  # noqa: F811
     shared(groups=5)     # for the library to refuse
     shared(B=-1)
     assert [a[11] for _, a in rec.calls] == [0, 1, 1, 0, 0, 0] and [a[4] for _, a in rec.calls][2:4] == [9, 20]
+
+
+@pytest.mark.parametrize("change", [
+    dict(S=torch.zeros(2, 1, D, D)), dict(conv_state=torch.zeros(2, 3, 3 * D)), dict(S=torch.zeros(3, 1, D, D, dtype=torch.float64)),
+    dict(conv_state=torch.zeros(3, 3, 3 * D, dtype=BF)), dict(S_out=torch.zeros(2, 1, D, D), conv_out=torch.zeros(3, 3, 3 * D)),
+    dict(S_out=torch.zeros(3, 1, D, D), conv_out=torch.zeros(2, 3, 3 * D)),
+    dict(S_out=torch.zeros(3, 1, D, D), conv_out=torch.zeros(3, 3, 3 * D, dtype=torch.float64)), dict(conv_state=torch.zeros(3, 3 * D, 3).transpose(1, 2))])
+def test_reorder_refuses_short_tensors_and_other_types(rec, change):  # noqa: F811
+    args = dict(S=torch.zeros(3, 1, D, D), conv_state=torch.zeros(3, 3, 3 * D))
+    args.update(change)
+    with pytest.raises(ValueError):
+        kda.kda_beam_reorder(1, 3, ints(3), args.pop("S"), args.pop("conv_state"), stream=0, **args)
+    assert not rec.calls
