@@ -454,12 +454,13 @@ def kda_attn_fork(attn, B, rows, kv_lens, block_table, page_refs, free_pages, fr
                   workspace_bytes=0, stream=None) -> None:
     """Requests take over one another's pages (kda_attn.h).  Both tables have rows of the same pitch."""
     cap = free_pages.numel() if free_capacity is None else int(free_capacity)
-    pitch = _pitch(block_table, max_pages)
-    if max_pages is None and new_table.stride() != block_table.stride() and _pitch(new_table, None) != pitch:
-        raise ValueError(f"rows of block_table are {pitch} apart, those of new_table {_pitch(new_table, None)}")
-    _check(load().kda_attn_fork(attn, B, _words(rows, "rows", B), _words(kv_lens, "kv_lens", B), _p(block_table), pitch,
+    old, pitch = _table(block_table, "block_table", B, max_pages)
+    new, new_pitch = _table(new_table, "new_table", B, max_pages)
+    if new_pitch != pitch:
+        raise ValueError(f"rows of block_table are {pitch} apart, those of new_table {new_pitch}")
+    _check(load().kda_attn_fork(attn, B, _words(rows, "rows", B), _words(kv_lens, "kv_lens", B), old, pitch,
                                 _words(page_refs, "page_refs", 0), _words(free_pages, "free_pages", cap), cap,
-                                _p(free_count), _p(new_table), _words(new_lens, "new_lens", B),
+                                _words(free_count, "free_count", 1), new, _words(new_lens, "new_lens", B),
                                 _words(copy_src, "copy_src", B), _words(copy_dst, "copy_dst", B),
                                 _words(copy_rows, "copy_rows", B), _words(info, "info", 4), _p(workspace),
                                 _nbytes(workspace, workspace_bytes), _stream(stream)), "kda_attn_fork")

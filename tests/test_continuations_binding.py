@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import kda_delta_rule_token_gb300 as kda
-from test_continuations_abi import BF, D, ints, lib, rec, select  # noqa: F401
+from test_continuations_abi import BF, D, fork, ints, lib, rec, select  # noqa: F401
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.float64, torch.int32, torch.int64, torch.uint8])
@@ -65,3 +65,18 @@ def test_reorder_refuses_short_tensors_and_other_types(rec, change):  # noqa: F8
     with pytest.raises(ValueError):
         kda.kda_beam_reorder(1, 3, ints(3), args.pop("S"), args.pop("conv_state"), stream=0, **args)
     assert not rec.calls
+
+
+@pytest.mark.parametrize("change", [
+    dict(block_table=torch.zeros(3, 7, dtype=LONG)), dict(new_table=torch.zeros(3, 7, dtype=LONG)), dict(free_count=torch.zeros(1, dtype=LONG)),
+    dict(block_table=ints(2, 7)), dict(new_table=ints(2, 7)), dict(free_count=ints(0))])
+def test_fork_refuses_types_and_short_tensors(rec, change):  # noqa: F811
+    with pytest.raises(ValueError):
+        fork(**change)
+    assert not rec.calls
+
+
+def test_fork_takes_addresses(rec):  # noqa: F811
+    fork(block_table=16, new_table=32, free_count=48, max_pages=7)
+    fork(block_table=ints(5, 7), new_table=ints(4, 7), free_count=ints(3))
+    assert [(a[4], a[5], a[10]) for _, a in rec.calls[:1]] == [(16, 7, 32)] and len(rec.calls) == 2
