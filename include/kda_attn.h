@@ -196,7 +196,7 @@ KDA_API size_t kda_attn_fork_workspace_bytes(const kda_attn_ctx *ctx, int B, int
  * int32 arrays are 4-byte aligned; no output may alias an input but those marked
  * (in, out).  A page id outside the cache is copied as it is and counted nowhere; it,
  * a page that more requests let go of than hold it, and a free list without room for
- * the freed pages (which are lost) are errors.  B == 0 is a no-op.  B above
+ * the freed pages that no copy takes (which are lost) are errors.  B == 0 is a no-op.  B above
  * KDA_ATTN_MAX_PLAN_REQUESTS: KDA_ERR_UNSUPPORTED.
  */
 KDA_API kda_status kda_attn_fork(kda_attn_ctx *ctx, int B, const int32_t *rows, const int32_t *kv_lens,

@@ -110,9 +110,10 @@ __device__ __forceinline__ void put_pages(const AttnForkIO& io, int shift, int n
         for (int i = lane; i < n; i += 32) {
             const int page = ws.pages[(size_t)(col0 + c) * io.B + i], k = from + i;
             io.page_refs[page] = 0;
+            const bool taken = all - 1 - k < wants;
             if (count + k < io.free_capacity) io.free_pages[count + k] = page;
-            else atomicOr(err, kErrAttnIndex);
-            if (all - 1 - k < wants) give(all - 1 - k, page);
+            else if (!taken) atomicOr(err, kErrAttnIndex);   // lost
+            if (taken) give(all - 1 - k, page);
         }
     }
     if (blockIdx.x) return;
@@ -132,7 +133,7 @@ __device__ __forceinline__ void put_pages(const AttnForkIO& io, int shift, int n
     if (tid == 0) {
         io.info[0] = all;
         io.info[1] = served;
-        io.info[2] = min(count + all, io.free_capacity) - served;
+        io.info[2] = (int)min((long long)count + all - served, (long long)io.free_capacity);
         io.info[3] = wants - served;
     }
 }
