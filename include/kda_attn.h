@@ -254,7 +254,11 @@ KDA_API size_t kda_attn_shared_workspace_bytes(const kda_attn_ctx *ctx, int B);
  * (beams, samples of one prompt: the block tables that kda_attn_fork makes).  Every
  * request's table row names all of its pages, as ever, and the results are
  * those of kda_attn_decode up to rounding; the groups say what need not be read more
- * than once.
+ * than once.  What a group's rows per key head (requests * Hq / Hkv) decide is how the
+ * softmax weights of its prefix are rounded: over a bf16 cache, in calls of more than 32 such
+ * rows (B * Hq / Hkv), those of groups of more than 16 to bf16 once, as kda_attn_prefill
+ * rounds them (2^-8 of each weight, o is off by up to that of the weighted sum of |v|);
+ * all others as kda_attn_decode (2^-16, over an e4m3 cache 2^-11).
  *   groups      0 to B
  *   cu_groups   [groups + 1] int32, ascending from 0 or more to B or less: group g is
  *               requests cu_groups[g] to cu_groups[g + 1] - 1; requests of no group share
