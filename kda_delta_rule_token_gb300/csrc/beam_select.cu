@@ -767,7 +767,7 @@ constexpr int kSegmentCost = 5;        // tiles
 Deal deal_of(int groups, int beams, int vocab, int num, const DeviceInfo& dev, int& most) {
     const long long rows = (long long)groups * beams;
     Deal d;
-    d.per_row = (vocab + kTile - 1) / kTile;
+    d.per_row = (int)(((long long)vocab + kTile - 1) / kTile);   // (vocab may be 2^31 - 1)
     d.units = rows * d.per_row;
     long long ctas = (long long)kCtasPerSm * dev.sm_count;
     if (ctas > d.units) ctas = d.units;
