@@ -37,7 +37,9 @@ KDA_API size_t kda_beam_select_workspace_bytes(const kda_ctx *ctx, int groups, i
  * and the num highest of a group's beams * vocab scores are returned, highest
  * first, of equal ones those of the lower beam, then of the lower token, first.
  * A score that is NaN (a row with a NaN or +infinite logit, or whose logits are
- * all -infinity) counts as -infinity.  Scores are compared in 64 bits; the sums
+ * all -infinity) counts as -infinity.  Scores of different beams are compared in
+ * 64 bits, those of one beam as its logits are: the larger logit has the higher score
+ * also where 64 bits hold the two for equal (beyond scores[g][k] of 1e9 or so).  The sums
  * of a row's num largest terms are taken in 64 bits too, those of its other terms
  * in fp32.
  *   logits    [groups * beams][vocab] fp32, or bf16 if logits_bf16 is nonzero,

@@ -531,10 +531,12 @@ __global__ void __launch_bounds__(kThreads, 4) kda_beam_rows_kernel(const RowsAr
 }
 
 // A continuation: its score in the order of unsigned numbers (64-bit comparisons of
-// floating numbers run at a sixty-fourth of the rate), and beam * vocab + token.
+// floating numbers run at a sixty-fourth of the rate), and what decides between equal ones, the lower
+// beam, the larger logit (whose score is the higher one by what 64 bits do not hold), the lower token:
+// the beam's complement, the logit's order and the token's complement, 64 bits at most
+// since beams * vocab is below 2^31.
 struct __align__(16) Choice {
-    uint64_t key;
-    uint32_t at;
+    uint64_t key, low;
 };
 constexpr uint64_t kLowestKey = 0x000fffffffffffffull;   // -infinity's
 __device__ __forceinline__ uint64_t key_of(double score) {
@@ -546,7 +548,7 @@ __device__ __forceinline__ double score_of(uint64_t key) {
     return __longlong_as_double((long long)(key ^ ((key >> 63) ? 1ull << 63 : ~0ull)));
 }
 __device__ __forceinline__ bool better(const Choice& a, const Choice& b) {
-    return (a.key > b.key) | ((a.key == b.key) & (a.at < b.at));   // no branch: loops over it are bound by its latency
+    return (a.key > b.key) | ((a.key == b.key) & (a.low > b.low));   // no branch: loops over it are bound by its latency
 }
 
 struct JoinArgs {
@@ -554,6 +556,7 @@ struct JoinArgs {
     Deal deal;
     int most;            // segments of a row
     int rounds;          // candidates of a thread
+    int beam_bits, token_bits;
     uint32_t per_segments, per_most;   // 2^31 over K * most and over most, rounded up: quotients of numbers below 2^12
     const Part* parts;
     const uint64_t* lists;
@@ -575,6 +578,12 @@ __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) 
     const int g = blockIdx.x, K = a.io.beams, n = a.io.num, S = a.most;
     const uint8_t* done = a.io.done ? a.io.done + (size_t)g * K : nullptr;
     const float* scores = a.io.scores + (size_t)g * K;
+    const uint32_t beam_mask = (1u << a.beam_bits) - 1, token_mask = (1u << a.token_bits) - 1;
+    auto low_of = [&](int beam, uint64_t c) {   // of candidate c
+        return (uint64_t)(beam_mask - beam) << (32 + a.token_bits) | (c >> 32) << a.token_bits | ((uint32_t)c & token_mask);
+    };
+    auto beam_at = [&](uint64_t low) { return (int)(beam_mask - (uint32_t)(low >> (32 + a.token_bits))); };
+    auto token_at = [&](uint64_t low) { return (int)(token_mask - ((uint32_t)low & token_mask)); };
     if (tid == 0) s_held = 0;
     if (tid < K) {
         const int k = tid;
@@ -651,7 +660,7 @@ __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) 
 
     // The continuations above -infinity; the last is that of a beam at its end.
     Choice mine[kJoinPer + 1];
-    Choice best{0, 0xffffffffu};
+    Choice best{0, 0};
 #pragma unroll
     for (int j = 0; j <= kJoinPer; ++j) {
         if (j >= a.rounds && j < kJoinPer) continue;
@@ -661,18 +670,17 @@ __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) 
             // Of NaN the key tells nothing.
             const bool number = ((uint64_t)__double_as_longlong(score) << 1) <= 0xffe0000000000000ull;
             const uint64_t key = key_of(score);
-            mine[j] = Choice{own[j] && !s_done[k] && number && key > kLowestKey ? key : 0,
-                             (uint32_t)k * (uint32_t)a.io.vocab + (uint32_t)token_of(own[j])};
+            mine[j] = Choice{own[j] && !s_done[k] && number && key > kLowestKey ? key : 0, low_of(k, own[j])};
         } else {
             mine[j] = Choice{0, 0};
             if (ended && scores[tid] > -INFINITY)
-                mine[j] = Choice{key_of(scores[tid]), (uint32_t)tid * (uint32_t)a.io.vocab + (uint32_t)a.io.end_token};
+                mine[j] = Choice{key_of(scores[tid]), low_of(tid, candidate(0.f, a.io.end_token))};
         }
         if (better(mine[j], best)) best = mine[j];
     }
     // A bound that num of them reach, as in the rows' kernel; of equal scores all pass.
     uint32_t top;
-    Choice bound{max((uint64_t)group_bound((uint32_t)(best.key >> 32), n, s_group, &top, kMost / kGroups) << 32, (uint64_t)1), 0xffffffffu};
+    Choice bound{max((uint64_t)group_bound((uint32_t)(best.key >> 32), n, s_group, &top, kMost / kGroups) << 32, (uint64_t)1), 0};
     for (;;) {
         int count = 0;
 #pragma unroll
@@ -689,7 +697,7 @@ __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) 
         s_best[tid] = best;
         if (tid == 0) {
             s_held = 0;
-            s_bound = Choice{1, 0xffffffffu};
+            s_bound = Choice{1, 0};
         }
         __syncthreads();
         int above = 0;
@@ -712,15 +720,16 @@ __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) 
     if (warp == 0 && chosen < n) {
         int m = chosen;
         for (uint32_t at = 0; m < n; ++at) {
+            const int beam = (int)(at / (uint32_t)a.io.vocab), token = (int)(at % (uint32_t)a.io.vocab);
             bool used = false;
-            for (int i = lane; i < chosen; i += 32) used |= s_sorted[i].at == at;
+            for (int i = lane; i < chosen; i += 32) used |= beam_at(s_sorted[i].low) == beam && token_at(s_sorted[i].low) == token;
             if (__any_sync(0xffffffffu, used)) continue;
-            if (lane == 0) s_sorted[m] = Choice{kLowestKey, at};
+            if (lane == 0) s_sorted[m] = Choice{kLowestKey, low_of(beam, candidate(0.f, token))};
             ++m;
         }
     }
     __syncthreads();
-    if (tid < n) s_beam[tid] = (int)(s_sorted[tid].at / (uint32_t)a.io.vocab);
+    if (tid < n) s_beam[tid] = beam_at(s_sorted[tid].low);
     __syncthreads();
 
     if (tid < n) {
@@ -752,7 +761,7 @@ __global__ void __launch_bounds__(kMost) kda_beam_join_kernel(const JoinArgs a) 
         }
         const size_t out = (size_t)g * n + place;
         a.io.out_scores[out] = (float)score_of(s_sorted[tid].key);
-        a.io.out_tokens[out] = (int)(s_sorted[tid].at % (uint32_t)a.io.vocab);
+        a.io.out_tokens[out] = token_at(s_sorted[tid].low);
         a.io.out_rows[out] = g * K + beam;
     }
 }
@@ -810,7 +819,12 @@ cudaError_t launch_beam_select(const BeamSelectIO& io, const DeviceInfo& dev, cu
     // Threads for all candidates, kJoinPer each at most.
     int threads = kThreads;
     while (threads < kJoinThreads && segments * io.num > (uint64_t)kJoinPer * threads) threads *= 2;
-    const JoinArgs j{io, d, most, (int)((segments * io.num + threads - 1) / threads),
+    auto bits = [](int n) {   // of numbers below n
+        int b = 0;
+        while (1LL << b < n) ++b;
+        return b;
+    };
+    const JoinArgs j{io, d, most, (int)((segments * io.num + threads - 1) / threads), bits(io.beams), bits(io.vocab),
                      (uint32_t)(((1ull << 31) + segments - 1) / segments), (uint32_t)(((1ull << 31) + most - 1) / most), p, lists};
     auto join = threads == kThreads ? kda_beam_join_kernel<kThreads> : threads == 512 ? kda_beam_join_kernel<512> : kda_beam_join_kernel<kJoinThreads>;
     return launch_behind(join, dim3((unsigned)io.groups), threads, 0, stream, j);

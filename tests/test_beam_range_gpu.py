@@ -36,3 +36,51 @@ def test_largest_vocabulary(bf16):
     for got, value in zip(s[0].tolist(), want.values()):
         exact = value - math.log(total)
         assert abs(got - exact) <= SLACK + 2.0 ** -23 * abs(exact)
+
+
+@pytest.mark.parametrize("far", [1e30, -1e30, 3e38, -3e38])
+@pytest.mark.parametrize("K,V,num", [(1, 5000, 4), (3, 1000, 8), (2, 3, 5), (5, 40000, 64)])
+def test_scores_far_from_zero(K, V, num, far):
+    """All 64-bit scores of a group are equal there: the lower beam's come first, of a beam those of the larger logits,
+    of equal logits the lower tokens, however many parts the row was cut into."""
+    x, scores = make(2, K, V, seed=K + V)
+    x[:, V // 2] = x[:, 0]                   # equal logits as well
+    scores[:] = far
+    with Ctx() as ctx:
+        s, t, r = select(ctx, x, scores, num)
+    assert bool((s == scores[0, 0]).all())
+    for g in range(2):
+        want = []
+        for k in range(K):
+            best = x[g * K + k].double().sort(descending=True, stable=True).indices[:num]
+            want += [(g * K + k, v) for v in best.tolist()]
+        assert list(zip(r[g].tolist(), t[g].tolist())) == want[:num]
+
+
+def test_marks_of_beams_that_do_not_count():
+    """Scores of -1e30 for all beams but one, and a vocabulary with few open tokens: the beam that counts first, then the
+    others by their own logits."""
+    x, scores = make(1, 3, 600, seed=4)
+    x[:, 4:] = -math.inf
+    scores[:] = -1e30
+    scores[0, 0] = -2.0
+    with Ctx() as ctx:
+        s, t, r = select(ctx, x, scores, 7)
+    y = beam_ref.scores64(x, scores, None, 0)
+    assert r[0].tolist() == [0] * 4 + [1] * 3
+    assert t[0, 4:].tolist() == x[1, :4].sort(descending=True).indices[:3].tolist()
+    assert t[0, :4].tolist() == y[0, 0].sort(descending=True, stable=True).indices[:4].tolist()
+    assert bool((s[0, 4:] == scores[0, 1]).all())
+
+
+@pytest.mark.parametrize("K,V,num", [(1, 9000, 4), (3, 30000, 8), (4, 4097, 33)])
+def test_logits_closer_than_scores(K, V, num):
+    """Logits about 0 that differ by less than 64 bits of a score hold: the largest ones all the same."""
+    gen = torch.Generator(device=DEV).manual_seed(V)
+    x = torch.randn(2 * K, V, generator=gen, device=DEV) * 1e-25
+    scores = -torch.arange(2 * K, device=DEV, dtype=torch.float32).view(2, K)   # beams that are far apart
+    with Ctx() as ctx:
+        s, t, r = select(ctx, x, scores, num)
+    for g in range(2):
+        best = x[g * K].sort(descending=True, stable=True).indices[:num]
+        assert t[g].tolist() == best.tolist() and r[g].tolist() == [g * K] * num
