@@ -186,7 +186,8 @@ KDA_API size_t kda_attn_fork_workspace_bytes(const kda_attn_ctx *ctx, int B, int
  *               later) adds 1.  A page is held at one and the same place of all rows that
  *               hold it, and a partly full one by one request.
  *   free_pages  [free_capacity] int32 (in, out), free_count [1] int32 (in): the stack, as
- *               for kda_attn_plan; entries from free_count on may be written
+ *               for kda_attn_plan; entries from free_count on may be written.  free_count
+ *               may be info + 2: a captured step carries on with what it left
  *   new_table   [B][max_pages] int32 (out), new_lens [B] int32 (out): not the old ones.
  *               Entries past a request's pages are not written.
  *   copy_src, copy_dst, copy_rows  [B] int32 (out)
@@ -194,7 +195,7 @@ KDA_API size_t kda_attn_fork_workspace_bytes(const kda_attn_ctx *ctx, int B, int
  *               on with free_count = info[2]), requests refused
  *   workspace   kda_attn_fork_workspace_bytes bytes, 16-byte aligned
  * int32 arrays are 4-byte aligned; no output may alias an input but those marked
- * (in, out).  A page id outside the cache is copied as it is and counted nowhere; it,
+ * (in, out), and info free_count.  A page id outside the cache is copied as it is and counted nowhere; it,
  * a page that more requests let go of than hold it, and a free list without room for
  * the freed pages that no copy takes (which are lost) are errors.  B == 0 is a no-op.  B above
  * KDA_ATTN_MAX_PLAN_REQUESTS: KDA_ERR_UNSUPPORTED.

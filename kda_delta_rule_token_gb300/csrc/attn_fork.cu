@@ -43,7 +43,8 @@ constexpr int kColsPerWarp = kCols / kWarps;
 constexpr int kMostCluster = 8;      // CTAs that may meet in one launch
 
 // Workspace: pages that each column frees, requests that want a copy, in order,
-// and their number, the columns' freed pages.
+// their number and that of the pages on the stack (which info may come to stand in the
+// place of), the columns' freed pages.
 struct Space {
     int* freed;      // [max_pages]
     int* wanting;    // [B]
@@ -84,8 +85,7 @@ __device__ __forceinline__ void put_pages(const AttnForkIO& io, int shift, int n
         before += s_before[w];
         all += s_all[w];
     }
-    const int count = min(max(io.free_count[0], 0), io.free_capacity);
-    const int wants = ws.wants[0];
+    const int wants = ws.wants[0], count = ws.wants[1];
 
     // Copy `nth` gets the page.
     auto give = [&](int nth, int page) {
@@ -201,7 +201,10 @@ __global__ void __launch_bounds__(kThreads) kda_attn_fork_kernel(const AttnForkI
         int at = upto - mine;
         for (int b = b0; b < b1; ++b)
             if (wants(b)) ws.wanting[at++] = b;
-        if (tid == 0) ws.wants[0] = all;
+        if (tid == 0) {
+            ws.wants[0] = all;
+            ws.wants[1] = min(max(io.free_count[0], 0), io.free_capacity);
+        }
     }
 
     // New rows: the pages of the one that the request goes on from, but for a copy of its own.
