@@ -24,8 +24,8 @@
 //
 // kda_attn_copy_pages_kernel copies rows, bound by HBM or by its launch.
 //
-// Four requests of 1,100 tokens: 6.6 us, and 1.6 for one layer's copies; 256 of 8,000
-// in pages of 128, a quarter of which ends: 15.6 us (the chain of loads and the
+// Four requests of 1,100 tokens: 6.9 us, and 1.6 for one layer's copies; 256 of 8,000
+// in pages of 128, a quarter of which ends: 16.2 us (the chain of loads and the
 // atomics of one column after another) and 4.4 (16 MB).  The host's calls take 8 and 4 us.
 #include <atomic>
 

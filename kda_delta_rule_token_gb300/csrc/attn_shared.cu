@@ -25,13 +25,15 @@
 //    who had the first and the last one noted it.
 //
 // Measured (a kernel's share: what the call takes longer when it is launched twice): 32 prompts of up
-// to 4,100 tokens with 1 to 30 requests each, 32 / 8 heads, bf16, 534 MB: 122 us, 0.65 of
+// to 4,100 tokens with 1 to 30 requests each, 32 / 8 heads, bf16, 534 MB: 127 us, 0.62 of
 // the copy rate (the few-row kernel 53 us and the tensor core kernel about 57, 5 TB/s each; plan
-// 5, join 7).  64 requests behind 8,192 tokens, 65 MB: 36 us (plan 3, few-row kernel 9,
+// 5, join 7).  64 requests behind 8,192 tokens, 65 MB: 38 us (plan 3, few-row kernel 9,
 // tensor core kernel 15, join 7, whose 20 MB of parts come from L2; kda_attn_decode: 178 us); of
 // the tensor core kernel's 15 its 3 or 4 key tiles take 6, the parts' way out 3 (6.4 TB/s).  256 requests of 64 heads
-// behind four documents of up to 16,300 tokens in e4m3, 128 GFLOP: 131 us (plan 6, few-row kernel
-// 17, tensor core kernel about 97, join 11).  The requests' own keys in the decode's kernel,
+// behind four documents of up to 16,300 tokens in e4m3, 128 GFLOP: 135 us (plan 6, few-row kernel
+// 17, tensor core kernel about 97, join 11).  What is left of each sum, 5, 2 and 4 us, the tensor core
+// kernel waits for the last CTAs of the few-row kernel; that its own set-up comes before that wait
+// changes nothing (127.2, 37.2 and 134.5 us).  The requests' own keys in the decode's kernel,
 // where four warps share a request's tiles and meet at its end: 15 us slower.  Queries and
 // requests brought near ahead of their use, more tiles per warp: no faster.  The join with
 // several rows of a request per CTA, their places found once: 1 to 5 us slower.

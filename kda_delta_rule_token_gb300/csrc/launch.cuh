@@ -1,9 +1,11 @@
 // A launch whose CTAs may come while the kernel before it in the stream still ends
 // (programmatic dependent launch).  Every kernel that is launched so waits for the one before
-// (ptx::griddep_wait) before it reads or writes anything, or is launched behind one of
-// the same call that has, and ends after it.  The first kernels of the calls for several
-// continuations are launched so too: calls in a row, between other work, take 2 to 3 us less each
-// (64 sequences reordered 18.4 -> 15.8 us, 64 samples' attention 46.6 -> 44.1).
+// (ptx::griddep_wait) before it reads or writes memory that others use.  The wait is each kernel's own: what
+// the kernel before it has waited for reaches it by that kernel's end alone, so that all
+// of a call's kernels, and the next call's first one, see what came before them.  The first kernels
+// of the calls for several continuations are launched so too: calls in a row, between other work, took
+// 2 to 3 us less each when that came in (64 sequences reordered 18.4 -> 15.8 us, 14.6 now; 64 samples'
+// attention 46.6 -> 44.1, 42.6 now).
 #pragma once
 
 #include <cuda_runtime.h>
