@@ -30,7 +30,7 @@
 // 131072 logits in fp32, 268 MB, 53 us, of which the rows take 47 (5.7 TB/s, 0.84
 // of the copy rate): looks at the largest logits, 3000 cycles each, which other CTAs of the SM
 // cover in part.  128 rows of 131071 in bf16, 33 MB, 21 us: a look to a CTA's 8 tiles and the join.  Four rows of
-// 32000, 7.7 us: two launches, and in the join a chain of loads, 64-bit arithmetic and instructions
+// 32000, 7.5 us: two launches, and in the join a chain of loads, 64-bit arithmetic and instructions
 // that no CTA before has fetched.  What runs once per segment or CTA is short for the same reason (the list
 // ranked by loops written out 2 us more, the join with 16 candidates to a thread 1 us).  A look every four tiles 57 us; before that, the bound found bit
 // by bit 65 instead of 62, threads looked at again by their own warps 59.7 instead of 57.6, by quarters of
